@@ -6,7 +6,9 @@ no fast-math.
 """
 from __future__ import annotations
 
+import concurrent.futures
 import glob
+import hashlib
 import os
 import shutil
 import subprocess
@@ -17,6 +19,7 @@ LIB = os.path.join(HERE, "libfpstok.so")
 MICROBENCH_SRC = os.path.join(HERE, "microbench", "fp32_rate.cu")
 MICROBENCH_LIB = os.path.join(HERE, "libfpstok_microbench.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
+OBJ = os.path.join(HERE, "_build")
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-fmad=false",
@@ -48,14 +51,36 @@ def stale() -> bool:
 
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
-    """Compile every ``csrc/*.cu`` into ``libfpstok.so`` (in-tree) when stale."""
+    """Compile every ``csrc/*.cu`` into ``libfpstok.so`` (in-tree) when stale:
+    one object per file, several at a time, an object again only when its
+    source, a header or the command line changed."""
     if not force and not stale():
         return LIB
+    os.makedirs(OBJ, exist_ok=True)
+    headers = [p for p in deps() if not p.endswith(".cu")]
+    common = hashlib.sha256()
+    for p in headers:
+        common.update(open(p, "rb").read())
+
+    def compile_one(src):
+        cmd = [nvcc(), *[f for f in NVCC_FLAGS if f != "-shared"], *extra, "-I", INCLUDE, "-c", src]
+        h = common.copy()
+        h.update(open(src, "rb").read() + "\0".join(cmd).encode())
+        obj = os.path.join(OBJ, f"{os.path.basename(src)[:-3]}.{h.hexdigest()[:16]}.o")
+        if force or not os.path.exists(obj):
+            tmp = obj + f".tmp{os.getpid()}"
+            if verbose:
+                print(" ".join(cmd))
+            subprocess.check_call([*cmd, "-o", tmp])
+            for old in glob.glob(os.path.join(OBJ, os.path.basename(src)[:-3] + ".*.o")):
+                os.remove(old)
+            os.replace(tmp, obj)
+        return obj
+
+    with concurrent.futures.ThreadPoolExecutor(os.cpu_count() or 1) as pool:
+        objects = list(pool.map(compile_one, sources()))
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc(), *NVCC_FLAGS, *extra, "-I", INCLUDE, *sources(), "-o", tmp]
-    if verbose:
-        print(" ".join(cmd))
-    subprocess.check_call(cmd)
+    subprocess.check_call([nvcc(), *NVCC_FLAGS, *objects, "-o", tmp])
     os.replace(tmp, LIB)
     return LIB
 
