@@ -26,6 +26,12 @@ FPS_ASSIGN_KNN = 1
 FPS_MAX_K = 256
 FPS_MAX_KNN = 128
 FPS_MAX_F = 64
+FPS_DTYPE_F32 = 0
+FPS_DTYPE_BF16 = 1
+FPS_DTYPE_F16 = 2
+FPS_MAX_ROTARY_DIM = 256
+FPS_MAX_ROTARY_AXES = 8
+FPS_MAX_ATTENTION_DIM = 128
 
 # (name, restype, argtypes) of every exported symbol, mirroring fpstok.h.
 SIGNATURES = [
@@ -52,6 +58,11 @@ SIGNATURES = [
     ("fps_pack_workspace_bytes", SZ, []),
     ("fps_pack_tokens", I, [P, I, P, P, I, I, P, P, P, P, SZ, P]),
     ("fps_unpack_tokens", I, [P, I, I64, P, I, I, P, P, SZ, P]),
+    ("fps_rotary_table_init", I, [P, P, I, ctypes.c_double, P, I]),
+    ("fps_rotary", I, [P, P, I, I64, I, I, I64, I64, I64, I64, P, I64, P, I, P]),
+    ("fps_attention_workspace_bytes", SZ, [P, I]),
+    ("fps_attention", I, [P, P, P, P, SZ, P]),
+    ("fps_attention_backward", I, [P, P, P, P, I64, I64, P, P, P, P, SZ, P]),
     ("fps_device_status", I, [P, P, ctypes.POINTER(I)]),
     ("fps_status_string", ctypes.c_char_p, [I]),
     ("fps_launch_count", ctypes.c_uint64, []),
@@ -67,6 +78,25 @@ class FpsOpts(ctypes.Structure):
 
     _fields_ = [("K", I), ("assign_mode", I), ("k", I), ("lloyd_iters", I), ("charge_col", I),
                 ("force_schedule", I), ("max_event_hint", I), ("axis_scale", ctypes.c_float * 4)]
+
+
+class RotaryTableStruct(ctypes.Structure):
+    """``fps_rotary_table`` of fpstok.h."""
+
+    _fields_ = [("pairs", I), ("axes", I), ("interleaved", I),
+                ("turns_hi", ctypes.c_float * (FPS_MAX_ROTARY_DIM // 2)),
+                ("turns_lo", ctypes.c_float * (FPS_MAX_ROTARY_DIM // 2)),
+                ("axis", ctypes.c_ubyte * (FPS_MAX_ROTARY_DIM // 2))]
+
+
+class AttentionArgs(ctypes.Structure):
+    """``fps_attention_args`` of fpstok.h."""
+
+    _fields_ = [("q", P), ("k", P), ("v", P), ("dtype", I), ("heads", I), ("kv_heads", I), ("head_dim", I),
+                ("n_q", I64), ("n_kv", I64), ("q_token_stride", I64), ("q_head_stride", I64),
+                ("k_token_stride", I64), ("k_head_stride", I64), ("v_token_stride", I64), ("v_head_stride", I64),
+                ("q_offsets", P), ("kv_offsets", P), ("events", I), ("scale", ctypes.c_float), ("causal", I),
+                ("window", I64), ("sinks", I64), ("max_tokens", I), ("zero_tail", I)]
 
 
 _lib = None

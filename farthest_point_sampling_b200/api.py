@@ -485,6 +485,266 @@ def segment_mean(feats: torch.Tensor, offsets: Optional[torch.Tensor], K: int,
     return _SegmentMean.apply(feats, offsets, K, token_id, knn_idx)
 
 
+class RotaryTable:
+    """Frequencies of :func:`rotary_embed` (C ``fps_rotary_table``), kept on the host.
+
+    Axis a owns ``axis_dims[a]`` (even) consecutive values of a head, that is
+    ``n = axis_dims[a] / 2`` pairs; pair i of it turns by ``axis_scale[a] *
+    base ** (-i / n)`` radians per unit of ``positions[:, a]``.  Pairs are
+    values ``(p, p + pairs)`` of the head, or ``(2p, 2p + 1)`` with
+    ``interleaved``."""
+
+    def __init__(self, axis_dims, base: float = 10000.0, axis_scale=None, interleaved: bool = False):
+        dims = [int(d) for d in axis_dims]
+        if not dims:
+            raise ValueError("axis_dims must name at least one axis")
+        scale = None
+        if axis_scale is not None:
+            w = [float(v) for v in axis_scale]
+            if len(w) != len(dims):
+                raise ValueError("axis_scale must hold one weight per axis")
+            scale = (ctypes.c_double * len(w))(*w)
+        self.c = _lib.RotaryTableStruct()
+        st = _lib.load().fps_rotary_table_init(ctypes.byref(self.c), (ctypes.c_int * len(dims))(*dims), len(dims),
+                                               float(base), scale, int(bool(interleaved)))
+        _lib.check(st, "fps_rotary_table_init")
+
+    @property
+    def axes(self) -> int:
+        return self.c.axes
+
+    @property
+    def pairs(self) -> int:
+        return self.c.pairs
+
+
+_DTYPES = {torch.float32: _lib.FPS_DTYPE_F32, torch.bfloat16: _lib.FPS_DTYPE_BF16, torch.float16: _lib.FPS_DTYPE_F16}
+
+
+def _need_rows(t: torch.Tensor, name: str, dtypes, device: Optional[torch.device] = None):
+    """A [rows, heads, D] tensor of one of ``dtypes`` whose heads are contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be one of {[str(d) for d in dtypes]}, got {t.dtype} (no implicit conversion)")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [rows, heads, D], got shape {tuple(t.shape)}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"the values of a head of {name} must be contiguous")
+
+
+def _strides(t: torch.Tensor):
+    """Row and head strides in elements; the stride of an axis of one entry is
+    free in torch, so a contiguous one stands in for it."""
+    n, h, d = t.shape
+    head = t.stride(1) if h > 1 else d
+    return (t.stride(0) if n > 1 else max(h * d, head * h)), head
+
+
+def rotary_embed(x: torch.Tensor, positions: torch.Tensor, table: RotaryTable, inverse: bool = False,
+                 out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """C ``fps_rotary``: the heads ``x [T, H, D]`` (float32, bfloat16 or
+    float16; rows and heads may be strided, e.g. the query and key heads of a
+    fused projection) turned by their positions ``[T, axes]`` (float32, e.g.
+    the packed centroids).  ``out`` may be ``x`` itself (in place).  With
+    ``inverse`` the turn goes back.  Not recorded by autograd: see
+    :func:`apply_rotary`."""
+    dev = _cuda_device(x)
+    _need_rows(x, "x", _DTYPES)
+    if not isinstance(table, RotaryTable):
+        raise TypeError("table must be a RotaryTable")
+    if not isinstance(positions, torch.Tensor) or positions.dtype != torch.float32:
+        raise TypeError("positions must be a float32 tensor (no implicit conversion)")
+    T, H, D = x.shape
+    if positions.device != dev or tuple(positions.shape) != (T, table.axes):
+        raise ValueError(f"positions must be [{T}, {table.axes}] on {dev}, got {tuple(positions.shape)} on {positions.device}")
+    if (table.axes > 1 and positions.stride(1) != 1) or (T > 1 and positions.stride(0) < table.axes):
+        raise ValueError("the coordinates of a position must be contiguous")
+    if 2 * table.pairs > D:
+        raise ValueError(f"the table turns {2 * table.pairs} values, a head has {D}")
+    if H < 1:
+        raise ValueError("x must have at least one head")
+    if out is None:
+        out = torch.empty((T, H, D), dtype=x.dtype, device=dev)
+    else:
+        _need_rows(out, "out", (x.dtype,), dev)
+        if out.shape != x.shape:
+            raise ValueError("out must have the shape of x")
+    (xt, xh), (yt, yh) = _strides(x), _strides(out)
+    with torch.cuda.device(dev):
+        st = _lib.load().fps_rotary(_ptr(x), _ptr(out), _DTYPES[x.dtype], T, H, D, xt, xh, yt, yh, _ptr(positions),
+                                    positions.stride(0) if T > 1 else table.axes, ctypes.byref(table.c),
+                                    int(bool(inverse)), _stream(dev))
+    _lib.check(st, "fps_rotary")
+    return out
+
+
+class _Rotary(torch.autograd.Function):
+    """The rotation is orthogonal, so its gradient is the inverse rotation."""
+
+    @staticmethod
+    def forward(ctx, x, positions, table):
+        ctx.save_for_backward(positions)
+        ctx.table = table
+        return rotary_embed(x, positions, table)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad):
+        (positions,) = ctx.saved_tensors
+        return rotary_embed(_dense_heads(grad), positions, ctx.table, inverse=True), None, None
+
+
+def apply_rotary(x: torch.Tensor, positions: torch.Tensor, table: RotaryTable) -> torch.Tensor:
+    """:func:`rotary_embed` that autograd differentiates with respect to ``x``
+    (positions are taken as constants)."""
+    if positions.requires_grad:
+        raise ValueError("apply_rotary has no gradient with respect to positions")
+    return _Rotary.apply(x, positions, table)
+
+
+def _dense_heads(t: torch.Tensor) -> torch.Tensor:
+    """A gradient as autograd hands it over (any strides) with rows the kernels read."""
+    ok = t.stride(2) == 1 and t.stride(1) >= t.shape[2] and t.stride(0) >= t.shape[2] and t.stride(1) % 8 == 0 and \
+        t.stride(0) % 8 == 0 and t.data_ptr() % 16 == 0
+    return t if ok else t.contiguous()
+
+
+def _attention_args(q, k, v, tok_offsets, kv_offsets, scale, causal, window, sinks, max_tokens):
+    dev = _cuda_device(q)
+    half = (torch.bfloat16, torch.float16)
+    _need_rows(q, "q", half)
+    _need_rows(k, "k", (q.dtype,), dev)
+    _need_rows(v, "v", (q.dtype,), dev)
+    if k.shape != v.shape or k.shape[2] != q.shape[2]:
+        raise ValueError(f"k and v must have one shape and the head size of q, got {tuple(q.shape)}, {tuple(k.shape)}, {tuple(v.shape)}")
+    if q.shape[1] < 1 or k.shape[1] < 1 or q.shape[1] % k.shape[1]:
+        raise ValueError(f"the query heads must be a multiple of the key heads, got {q.shape[1]} and {k.shape[1]}")
+    if q.shape[2] % 8 or not 8 <= q.shape[2] <= _lib.FPS_MAX_ATTENTION_DIM:
+        raise ValueError(f"the head size must be a multiple of 8 up to {_lib.FPS_MAX_ATTENTION_DIM}, got {q.shape[2]}")
+    if kv_offsets is None:
+        if q.shape[0] != k.shape[0]:
+            raise ValueError("q and k must have the same rows unless kv_offsets is given")
+        kv_offsets = tok_offsets
+    _need(tok_offsets, "tok_offsets", torch.int64, 1, dev)
+    _need(kv_offsets, "kv_offsets", torch.int64, 1, dev)
+    if tok_offsets.numel() < 1 or tok_offsets.numel() != kv_offsets.numel():
+        raise ValueError("tok_offsets and kv_offsets must both be [B + 1]")
+    strides = []
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        st = _strides(t)
+        if t.numel() and (t.data_ptr() % 16 or any(x <= 0 or x % 8 for x in st)):
+            raise ValueError(f"{name} must start on 16 bytes, with row and head strides that are positive multiples of 8")
+        strides += st
+    window, sinks = int(window), int(sinks)
+    if window < -1 or sinks < 0:
+        raise ValueError("window must be -1 or more and sinks 0 or more")
+    scale = q.shape[2] ** -0.5 if scale is None else float(scale)
+    if not 0.0 < scale < float("inf"):
+        raise ValueError("scale must be positive and finite")
+    a = _lib.AttentionArgs()
+    a.q, a.k, a.v = q.data_ptr(), k.data_ptr(), v.data_ptr()
+    a.dtype, a.heads, a.kv_heads, a.head_dim = _DTYPES[q.dtype], q.shape[1], k.shape[1], q.shape[2]
+    a.n_q, a.n_kv = q.shape[0], k.shape[0]
+    (a.q_token_stride, a.q_head_stride, a.k_token_stride, a.k_head_stride, a.v_token_stride, a.v_head_stride) = strides
+    a.q_offsets, a.kv_offsets, a.events = tok_offsets.data_ptr(), kv_offsets.data_ptr(), tok_offsets.numel() - 1
+    a.scale, a.causal, a.window, a.sinks = scale, int(bool(causal)), min(window, 1 << 40), min(sinks, 1 << 40)
+    a.max_tokens = min(int(max_tokens), 2**31 - 1)
+    return a, dev
+
+
+def attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, tok_offsets: torch.Tensor,
+                      kv_offsets: Optional[torch.Tensor] = None, scale: Optional[float] = None, causal: bool = False,
+                      window: int = -1, sinks: int = 0, max_tokens: int = 0, need_lse: bool = True,
+                      workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None):
+    """C ``fps_attention``: returns ``(out [n_q, H, D], lse [H, n_q])`` (lse
+    None without ``need_lse``); see :func:`packed_attention`.  Rows of a given
+    ``out`` that belong to no event are left as they were; in a new one they
+    are 0."""
+    a, dev = _attention_args(q, k, v, tok_offsets, kv_offsets, scale, causal, window, sinks, max_tokens)
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        a.zero_tail = 1
+    else:
+        _need(out, "out", q.dtype, 3, dev)
+        if out.shape != q.shape or out.data_ptr() % 16:
+            raise ValueError("out must have the shape of q and start on 16 bytes")
+    lib = _lib.load()
+    lse = None
+    if need_lse:  # rows of no event read as a query that sees nothing
+        lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=dev)
+    ws = _workspace(lib.fps_attention_workspace_bytes(ctypes.byref(a), 0), dev, workspace)
+    with torch.cuda.device(dev):
+        st = lib.fps_attention(ctypes.byref(a), _ptr(out), _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(), _stream(dev))
+    _lib.check(st, "fps_attention")
+    return out, lse
+
+
+def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
+                       lse: torch.Tensor, tok_offsets: torch.Tensor, kv_offsets: Optional[torch.Tensor] = None,
+                       scale: Optional[float] = None, causal: bool = False, window: int = -1, sinks: int = 0,
+                       max_tokens: int = 0, workspace: Optional[torch.Tensor] = None):
+    """C ``fps_attention_backward``: ``(dq, dk, dv)`` given the forward's
+    ``out`` and ``lse``.  Gradient rows that belong to no event are 0."""
+    a, dev = _attention_args(q, k, v, tok_offsets, kv_offsets, scale, causal, window, sinks, max_tokens)
+    _need(out, "out", q.dtype, 3, dev)
+    _need(lse, "lse", torch.float32, 2, dev)
+    _need_rows(dout, "dout", (q.dtype,), dev)
+    if out.shape != q.shape or dout.shape != q.shape or tuple(lse.shape) != (q.shape[1], q.shape[0]):
+        raise ValueError("out and dout must have the shape of q, and lse [H, n_q]")
+    dt, dh = _strides(dout)
+    if dout.numel() and (dout.data_ptr() % 16 or dt <= 0 or dh <= 0 or dt % 8 or dh % 8 or out.data_ptr() % 16):
+        raise ValueError("dout and out must start on 16 bytes, with dout's strides positive multiples of 8")
+    dq, dk, dv = (torch.empty(t.shape, dtype=q.dtype, device=dev) for t in (q, k, v))
+    lib = _lib.load()
+    ws = _workspace(lib.fps_attention_workspace_bytes(ctypes.byref(a), 1), dev, workspace)
+    with torch.cuda.device(dev):
+        st = lib.fps_attention_backward(ctypes.byref(a), _ptr(out), _ptr(lse), _ptr(dout), dt, dh, _ptr(dq), _ptr(dk),
+                                        _ptr(dv), _ptr(ws), ws.numel() * ws.element_size(), _stream(dev))
+    _lib.check(st, "fps_attention_backward")
+    return dq, dk, dv
+
+
+class _PackedAttention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, tok_offsets, kv_offsets, opts):
+        out, lse = attention_forward(q, k, v, tok_offsets, kv_offsets, **opts)
+        ctx.save_for_backward(q, k, v, out, lse, tok_offsets, kv_offsets)
+        ctx.opts = opts
+        return out
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dout):
+        q, k, v, out, lse, tok_offsets, kv_offsets = ctx.saved_tensors
+        dq, dk, dv = attention_backward(_dense_heads(dout), q, k, v, out, lse, tok_offsets, kv_offsets, **ctx.opts)
+        return dq, dk, dv, None, None, None
+
+
+def packed_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, tok_offsets: torch.Tensor,
+                     kv_offsets: Optional[torch.Tensor] = None, scale: Optional[float] = None, causal: bool = False,
+                     window: int = -1, sinks: int = 0, max_tokens: int = 0) -> torch.Tensor:
+    """Attention within each packed event (the layout of :func:`pack_tokens`),
+    differentiable with respect to ``q``, ``k`` and ``v``.
+
+    ``q [n_q, H, D]``, ``k`` and ``v [n_kv, H_kv, D]`` in bfloat16 or float16
+    (H a multiple of H_kv: shared key heads); rows and heads may be strided.
+    ``tok_offsets [B + 1]`` delimits the events; ``kv_offsets`` when the keys
+    have rows of their own (e.g. one summary query per event).  Query i of nq
+    stands at position ``p = i + nk - nq`` of its event's nk keys and sees key
+    j when ``(|p - j| <= window, or window is -1, or j < sinks) and (j <= p if
+    causal)``; a query that sees none returns 0.  ``scale`` defaults to
+    ``D ** -0.5``.  ``max_tokens``: an upper bound on the tokens of an event
+    (e.g. the K of the tokenizer), 0 when unknown; it selects kernels.
+    Returns ``[n_q, H, D]``; rows behind the last event are 0."""
+    opts = dict(scale=scale, causal=causal, window=window, sinks=sinks, max_tokens=max_tokens)
+    if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in (q, k, v)):
+        return _PackedAttention.apply(q, k, v, tok_offsets, kv_offsets, opts)
+    return attention_forward(q, k, v, tok_offsets, kv_offsets, need_lse=False, **opts)[0]
+
+
 def device_status(workspace: torch.Tensor) -> None:
     """Reads the device-side status word of a workspace (synchronises the
     current stream) and raises ``FpsError`` if a check failed."""

@@ -1,0 +1,52 @@
+// Attention over packed events: the call as the kernels see it, and their
+// launchers.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/fpstok.h"
+
+namespace fpstok {
+
+struct WsHeader;
+
+// Visibility of one event: query i of nq stands at p = i + nk - nq and sees
+// key j when (|p - j| <= window, or window < 0, or j < sinks) and
+// (j <= p if causal).
+struct AttnMask {
+  int causal;
+  int window;  // clamped to 2^30; -1 = unlimited
+  int sinks;
+};
+
+struct AttnCall {
+  const void* q;
+  const void* k;
+  const void* v;
+  int dtype;
+  int64_t n_q, n_kv;
+  int heads, kv_heads, group, D;
+  int64_t q_token, q_head, k_token, k_head, v_token, v_head;
+  const int64_t* q_offsets;
+  const int64_t* kv_offsets;
+  int B;
+  float scale;
+  AttnMask mask;
+  int max_tokens;
+  int zero_tail;
+  void* out;   // [n_q, heads, D]
+  float* lse;  // [heads, n_q]
+  // backward
+  const void* dout;
+  int64_t do_token, do_head;
+  void* dq;
+  void* dk;
+  void* dv;
+};
+
+size_t attention_workspace_bytes(int64_t n_q, int64_t n_kv, int B, int heads, int kv_heads, int D, bool backward);
+cudaError_t launch_attention(const AttnCall& c, void* workspace, cudaStream_t s);
+cudaError_t launch_attention_backward(const AttnCall& c, void* workspace, cudaStream_t s);
+
+}  // namespace fpstok

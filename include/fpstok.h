@@ -341,6 +341,113 @@ int fps_pack_tokens(const float *src, int D, const int64_t *offsets, const int32
 int fps_unpack_tokens(const float *src, int D, int64_t n_tok, const int64_t *tok_offsets, int B, int K,
                       float *dst, void *workspace, size_t workspace_bytes, fps_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Transformer operators on packed tokens (graphnet PR #923, "What is added":
+ * 4D rotary embedding; packed attention with a block mask).
+ *
+ * Element types of these calls. */
+#define FPS_DTYPE_F32 0
+#define FPS_DTYPE_BF16 1
+#define FPS_DTYPE_F16 2
+
+#define FPS_MAX_ROTARY_DIM 256
+#define FPS_MAX_ROTARY_AXES 8
+
+/*
+ * Rotary positions over several coordinate axes.  Pair p of a head belongs
+ * to axis a(p) and has the frequency w_p in radians per coordinate unit; with
+ * theta = positions[t, a(p)] * w_p,
+ *   y1 = x1 cos(theta) - x2 sin(theta),  y2 = x2 cos(theta) + x1 sin(theta).
+ * Pair p is values (p, p + pairs) of the head, or (2p, 2p + 1) when
+ * interleaved; values from 2 * pairs on are copied.  Computed in float32 from
+ * angles reduced to one turn with the product held to about 48 bits, each
+ * output rounded once to its type.
+ */
+typedef struct fps_rotary_table { /* a host struct; filled by fps_rotary_table_init */
+    int pairs, axes, interleaved;
+    float turns_hi[FPS_MAX_ROTARY_DIM / 2]; /* w_p / 2 pi = turns_hi + turns_lo */
+    float turns_lo[FPS_MAX_ROTARY_DIM / 2];
+    unsigned char axis[FPS_MAX_ROTARY_DIM / 2];
+} fps_rotary_table;
+
+/* Axis a owns axis_dims[a] (even, >= 0) consecutive values, that is
+ * n = axis_dims[a] / 2 pairs, with w = axis_scale[a] * base^(-i / n) for its
+ * pair i (axis_scale NULL: 1).  base > 0 and every axis_scale finite, at least
+ * one pair, 2 * pairs <= FPS_MAX_ROTARY_DIM, axes <= FPS_MAX_ROTARY_AXES. */
+int fps_rotary_table_init(fps_rotary_table *table, const int *axis_dims, int axes, double base,
+                          const double *axis_scale, int interleaved);
+
+/*
+ * x, y: [T, H, D] of `dtype`, values of a head contiguous, the other strides
+ * in elements.  y may be x with the same strides (in place); otherwise they
+ * do not overlap.  positions: float32 [T, table->axes], rows position_stride
+ * floats apart.  inverse != 0 turns by -theta: the gradient of the forward.
+ * 2 * pairs <= D <= FPS_MAX_ROTARY_DIM.  No workspace.
+ */
+int fps_rotary(const void *x, void *y, int dtype, int64_t T, int H, int D, int64_t x_token_stride,
+               int64_t x_head_stride, int64_t y_token_stride, int64_t y_head_stride, const float *positions,
+               int64_t position_stride, const fps_rotary_table *table, int inverse, fps_stream_t stream);
+
+#define FPS_MAX_ATTENTION_DIM 128
+
+/*
+ * Attention of packed events.  Event b holds queries q_offsets[b] ..
+ * q_offsets[b + 1] - 1 and keys kv_offsets[b] .. kv_offsets[b + 1] - 1 (the
+ * offsets of fps_pack_tokens; both may be one array).  Query i of nq stands
+ * at position p = i + nk - nq of its event's nk keys and sees key j when
+ *   (|p - j| <= window, or window < 0, or j < sinks) and (j <= p if causal).
+ * out_i = sum_j softmax_j(scale * q_i . k_j) v_j over the keys it sees; a
+ * query that sees no key gets out = 0 and lse = -inf.  Query head h reads
+ * key/value head h / (heads / kv_heads).
+ *
+ * q [n_q, heads, D], k and v [n_kv, kv_heads, D] of `dtype` (BF16 or F16),
+ * values of a head contiguous, the other strides in elements.  D is a multiple
+ * of 8, at most FPS_MAX_ATTENTION_DIM; pointers are 16-byte aligned and
+ * strides positive multiples of 8 elements.  out [n_q, heads, D] and the
+ * gradients (like q, k, v) are contiguous and 16-byte aligned.  lse float32
+ * [heads, n_q]: log of the softmax sum, natural logarithm.
+ *
+ * Scores, the running maximum and sum, outputs and gradients accumulate in
+ * float32; softmax weights and score gradients are rounded to `dtype` for
+ * their matrix products; every output is rounded once.
+ *
+ * Rows of out and lse that belong to no event (behind q_offsets[events]) are
+ * left as they were, or out rows set to 0 when zero_tail is set; gradient
+ * rows that belong to no event are set to 0.  Non-finite values of one event
+ * do not reach another; within an event they may reach rows that do not see
+ * them.
+ */
+typedef struct fps_attention_args {
+    const void *q, *k, *v;
+    int dtype;
+    int heads, kv_heads, head_dim;
+    int64_t n_q, n_kv;
+    int64_t q_token_stride, q_head_stride;
+    int64_t k_token_stride, k_head_stride;
+    int64_t v_token_stride, v_head_stride;
+    const int64_t *q_offsets, *kv_offsets; /* int64 [events + 1] */
+    int events;
+    float scale;    /* finite, > 0 */
+    int causal;     /* 0 or 1 */
+    int64_t window; /* keys on each side, -1 = unlimited */
+    int64_t sinks;  /* first keys of an event that every query may see, >= 0 */
+    int max_tokens; /* upper bound on the queries and keys of any event, 0 = unknown; an event above it
+                       is reported by fps_device_status() and its rows are not valid */
+    int zero_tail;
+} fps_attention_args;
+
+/* Workspace bytes of the two calls below for these sizes (pointers are not read). */
+size_t fps_attention_workspace_bytes(const fps_attention_args *args, int backward);
+/* lse may be NULL when no gradient follows. */
+int fps_attention(const fps_attention_args *args, void *out, float *lse, void *workspace, size_t workspace_bytes,
+                  fps_stream_t stream);
+/* The gradients of sum(dout * out) with respect to q, k and v, given the
+ * forward's out and lse.  dout [n_q, heads, D] with its own strides, aligned
+ * like q.  The order of every sum is fixed: the same call gives the same bits. */
+int fps_attention_backward(const fps_attention_args *args, const void *out, const float *lse, const void *dout,
+                           int64_t dout_token_stride, int64_t dout_head_stride, void *dq, void *dk, void *dv,
+                           void *workspace, size_t workspace_bytes, fps_stream_t stream);
+
 /* Reads (and clears) the device-side status word in `workspace`; synchronises
  * `stream`.  Returns FPS_OK or FPS_ERR_DEVICE; *detail (optional) receives the
  * recorded reason (see FPS_DEV_* below). */

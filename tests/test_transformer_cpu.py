@@ -1,0 +1,119 @@
+"""Refusals of the packed-token transformer operators, found on the host before
+any launch: none of these calls reaches a GPU."""
+import ctypes
+import math
+
+import pytest
+
+import farthest_point_sampling_b200 as fps
+from farthest_point_sampling_b200 import _lib
+
+torch = pytest.importorskip("torch")
+X = ctypes.c_void_p(256)
+
+
+def test_rotary_table():
+    t = fps.RotaryTable((4, 0, 6), base=100.0, axis_scale=(2.0, 1.0, -0.5))
+    assert t.axes == 3 and t.pairs == 5 and list(t.c.axis[:5]) == [0, 0, 2, 2, 2]
+    want = [2.0, 2.0 * 100 ** -0.5, -0.5, -0.5 * 100 ** (-1 / 3), -0.5 * 100 ** (-2 / 3)]
+    for p, w in enumerate(want):
+        # a float pair holds the float64 value to 2^-48
+        assert abs(t.c.turns_hi[p] + t.c.turns_lo[p] - w / (2 * math.pi)) <= 2.0 ** -47 * abs(w)
+    for bad in (dict(axis_dims=(3,)), dict(axis_dims=(0, 0)), dict(axis_dims=(-2, 4)), dict(axis_dims=(4,), base=0.0),
+                dict(axis_dims=(4,), base=float("nan")), dict(axis_dims=(4,), axis_scale=(float("inf"),)),
+                dict(axis_dims=(258,)), dict(axis_dims=(2,) * 9), dict(axis_dims=(4,), axis_scale=(1e300,))):
+        with pytest.raises(fps.FpsError):
+            fps.RotaryTable(**bad)
+    with pytest.raises(ValueError):
+        fps.RotaryTable(())
+    with pytest.raises(ValueError):
+        fps.RotaryTable((4, 4), axis_scale=(1.0,))
+
+
+def test_rotary_argument_errors():
+    lib = fps.load_library()
+    t = fps.RotaryTable((4, 4)).c
+
+    def call(x=X, y=X, dtype=1, T=5, H=2, D=16, xs=(32, 16), ys=(32, 16), pos=X, ps=2, table=t):
+        return lib.fps_rotary(x, y, dtype, T, H, D, *xs, *ys, pos, ps, ctypes.byref(table) if table is not None else None, 0, None)
+
+    assert call(dtype=3) == _lib.FPS_ERR_ARG
+    assert call(T=-1) == _lib.FPS_ERR_ARG
+    assert call(H=0) == _lib.FPS_ERR_ARG
+    assert call(D=6) == _lib.FPS_ERR_ARG  # fewer values than the table turns
+    assert call(D=512) == _lib.FPS_ERR_TOO_LARGE
+    assert call(T=1 << 30) == _lib.FPS_ERR_TOO_LARGE
+    assert call(table=None) == _lib.FPS_ERR_ARG
+    assert call(pos=None) == _lib.FPS_ERR_ARG
+    assert call(x=None) == _lib.FPS_ERR_ARG
+    assert call(x=ctypes.c_void_p(257)) == _lib.FPS_ERR_ARG
+    assert call(ps=1) == _lib.FPS_ERR_ARG
+    assert call(xs=(64, 16)) == _lib.FPS_ERR_ARG  # in place with other strides
+    assert call(ys=(32, 8), y=ctypes.c_void_p(4096)) == _lib.FPS_ERR_ARG  # heads of y overlap
+    assert call(T=0) == _lib.FPS_OK
+    broken = _lib.RotaryTableStruct.from_buffer_copy(t)
+    broken.axis[3] = 7
+    assert call(table=broken) == _lib.FPS_ERR_ARG
+
+
+def _args(**kw):
+    a = _lib.AttentionArgs()
+    base = dict(q=256, k=256, v=256, dtype=1, heads=4, kv_heads=2, head_dim=64, n_q=10, n_kv=10, q_token_stride=256,
+                q_head_stride=64, k_token_stride=128, k_head_stride=64, v_token_stride=128, v_head_stride=64, q_offsets=256,
+                kv_offsets=256, events=2, scale=0.125, causal=0, window=-1, sinks=0, max_tokens=0, zero_tail=0)
+    base.update(kw)
+    for name, value in base.items():
+        setattr(a, name, value)
+    return a
+
+
+def test_attention_argument_errors():
+    lib = fps.load_library()
+    ws = lib.fps_attention_workspace_bytes(ctypes.byref(_args()), 0)
+    wsb = lib.fps_attention_workspace_bytes(ctypes.byref(_args()), 1)
+    assert ws > 0 and wsb > 0
+
+    def both(code, **kw):
+        a = _args(**kw)
+        assert lib.fps_attention(ctypes.byref(a), X, X, X, 1 << 40, None) == code, kw
+        assert lib.fps_attention_backward(ctypes.byref(a), X, X, X, 256, 64, X, X, X, X, 1 << 40, None) == code, kw
+
+    for kw in (dict(dtype=0), dict(heads=3), dict(heads=0), dict(kv_heads=0), dict(head_dim=12), dict(head_dim=0), dict(n_q=-1),
+               dict(n_kv=-1), dict(events=-1), dict(max_tokens=-1), dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")),
+               dict(scale=float("inf")), dict(causal=2), dict(window=-2), dict(sinks=-1), dict(q=0), dict(k=0), dict(v=0),
+               dict(q=264), dict(q_offsets=0), dict(kv_offsets=0), dict(q_token_stride=0), dict(q_head_stride=0),
+               dict(k_token_stride=100), dict(v_head_stride=-64)):
+        both(_lib.FPS_ERR_ARG, **kw)
+    for kw in (dict(head_dim=136), dict(n_q=1 << 30), dict(n_kv=1 << 31), dict(heads=1 << 17, kv_heads=1),
+               dict(n_q=(1 << 30) - 1, heads=4096, kv_heads=1)):
+        both(_lib.FPS_ERR_TOO_LARGE, **kw)
+    a = _args()
+    ref = ctypes.byref(a)
+    assert lib.fps_attention(None, X, X, X, ws, None) == _lib.FPS_ERR_ARG
+    assert lib.fps_attention(ref, None, X, X, ws, None) == _lib.FPS_ERR_ARG
+    assert lib.fps_attention(ref, ctypes.c_void_p(264), X, X, ws, None) == _lib.FPS_ERR_ARG
+    assert lib.fps_attention(ref, X, X, X, ws - 1, None) == _lib.FPS_ERR_WORKSPACE
+    assert lib.fps_attention(ref, X, X, None, ws, None) == _lib.FPS_ERR_WORKSPACE
+    assert lib.fps_attention(ref, X, X, ctypes.c_void_p(128), ws, None) == _lib.FPS_ERR_WORKSPACE
+    bw = lib.fps_attention_backward
+    assert bw(ref, X, None, X, 256, 64, X, X, X, X, wsb, None) == _lib.FPS_ERR_ARG
+    assert bw(ref, X, X, X, 256, 60, X, X, X, X, wsb, None) == _lib.FPS_ERR_ARG
+    assert bw(ref, X, X, X, 256, 64, X, None, X, X, wsb, None) == _lib.FPS_ERR_ARG
+    assert bw(ref, X, X, X, 256, 64, X, X, X, X, wsb - 1, None) == _lib.FPS_ERR_WORKSPACE
+
+
+def test_binding_refusals():
+    t = fps.RotaryTable((4, 4))
+    x = torch.zeros((3, 2, 16))
+    with pytest.raises(ValueError, match="CUDA"):
+        fps.rotary_embed(x, torch.zeros((3, 2)), t)
+    with pytest.raises(ValueError, match="CUDA"):
+        fps.apply_rotary(x, torch.zeros((3, 2)), t)
+    with pytest.raises(ValueError, match="gradient"):
+        fps.apply_rotary(x, torch.zeros((3, 2), requires_grad=True), t)
+    off = torch.tensor([0, 3])
+    h = x.to(torch.bfloat16)
+    for call in (lambda: fps.packed_attention(h, h, h, off), lambda: fps.attention_forward(h, h, h, off),
+                 lambda: fps.attention_backward(h, h, h, h, h, torch.zeros((2, 3)), off)):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
