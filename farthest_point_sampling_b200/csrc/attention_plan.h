@@ -1,0 +1,28 @@
+// The tile lists of an attention call, and the tensor maps of its inputs.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "attention.h"
+
+namespace fpstok {
+
+struct TileItem;
+
+// WsHeader::n_items of the two lists.
+constexpr int kQueryTiles = 0;
+constexpr int kKeyTiles = 1;
+
+// Fills `queries` (and `keys` when not NULL) with the tiles of every event in
+// order, their counts in hdr->n_items, and resets the call's status words.
+// An event longer than max_tokens is recorded and gets no tiles; inconsistent
+// offsets are recorded and end the lists.
+cudaError_t launch_attention_plan(const AttnCall& c, WsHeader* hdr, TileItem* queries, TileItem* keys, cudaStream_t s);
+
+// Map of a [rows, heads, D] 16-bit tensor for boxes of 64 rows x one head x
+// 64 values, 128-byte swizzled; what lies outside reads as zeros.
+bool attention_map(CUtensorMap* map, const void* base, bool bf16, int64_t rows, int heads, int D, int64_t token_stride,
+                   int64_t head_stride);
+
+}  // namespace fpstok

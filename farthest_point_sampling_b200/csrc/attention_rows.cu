@@ -64,51 +64,6 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-template <typename T>
-__global__ void k_attn_row(const AttnCall c, WsHeader* hdr) {
-  const int lane = threadIdx.x & 31;
-  const int64_t w = (int64_t)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
-  if (w >= c.n_q * c.heads) return;
-  const int64_t r = w / c.heads;
-  const int h = (int)(w - r * c.heads);
-  T* out = static_cast<T*>(c.out) + (r * c.heads + h) * c.D;
-  const int b = event_of(c.q_offsets, c.B, r);
-  Span sp;
-  if (b >= 0) sp = span_of(c, b, hdr);
-  if (b < 0 || !sp.ok) {
-    if (c.zero_tail)
-      for (int d = lane; d < c.D; d += 32) st(out + d, 0.f);
-    return;
-  }
-  const T* q = static_cast<const T*>(c.q) + r * c.q_token + h * c.q_head;
-  const int64_t p = r - sp.q0 + sp.nk - sp.nq;
-  float qv[4], o[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) qv[i] = lane + 32 * i < c.D ? ld(q + lane + 32 * i) * c.scale : 0.f;
-  float m = -INFINITY, l = 0.f;
-  for (int64_t j = 0; j < sp.nk; ++j) {
-    if (!sees(c.mask, p, j)) continue;
-    const T* k = static_cast<const T*>(c.k) + (sp.k0 + j) * c.k_token + (h / c.group) * c.k_head;
-    const T* v = static_cast<const T*>(c.v) + (sp.k0 + j) * c.v_token + (h / c.group) * c.v_head;
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (lane + 32 * i < c.D) s = fmaf(qv[i], ld(k + lane + 32 * i), s);
-    s = warp_sum(s);
-    const float mn = fmaxf(m, s);
-    const float f = mn == -INFINITY ? 0.f : expf(m - mn), e = mn == -INFINITY ? 0.f : expf(s - mn);
-    l = fmaf(l, f, e);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (lane + 32 * i < c.D) o[i] = fmaf(o[i], f, e * ld(v + lane + 32 * i));
-    m = mn;
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (lane + 32 * i < c.D) st(out + lane + 32 * i, l > 0.f ? o[i] / l : (l == 0.f ? 0.f : l));
-  if (lane == 0 && c.lse) c.lse[(int64_t)h * c.n_q + r] = l == 0.f ? -INFINITY : m + logf(l);
-}
-
 // dq of one (query, head); delta recomputed where needed.
 template <typename T>
 __global__ void k_attn_row_dq(const AttnCall c, WsHeader* hdr) {
@@ -246,18 +201,10 @@ unsigned row_blocks(int64_t rows) { return (unsigned)((rows + kRowWarps - 1) / k
 
 }  // namespace
 
-size_t attention_workspace_bytes(int64_t, int64_t, int, int, int, int, bool) { return 256; }
+size_t attention_workspace_bytes(int64_t n_q, int64_t, int B, int, int, int, bool) { return attention_forward_bytes(n_q, B); }
 
 cudaError_t launch_attention(const AttnCall& c, void* workspace, cudaStream_t s) {
-  WsHeader* hdr = static_cast<WsHeader*>(workspace);
-  cudaError_t e = check(c, hdr, s);
-  if (e != cudaSuccess || c.n_q == 0) return e;
-  count_launch();
-  if (c.dtype == FPS_DTYPE_BF16)
-    k_attn_row<__nv_bfloat16><<<row_blocks(c.n_q * c.heads), 32 * kRowWarps, 0, s>>>(c, hdr);
-  else
-    k_attn_row<__half><<<row_blocks(c.n_q * c.heads), 32 * kRowWarps, 0, s>>>(c, hdr);
-  return cudaGetLastError();
+  return launch_attention_forward(c, workspace, s);
 }
 
 cudaError_t launch_attention_backward(const AttnCall& c, void* workspace, cudaStream_t s) {

@@ -1,0 +1,116 @@
+// What the attention kernels share: the tile list, the key tiles a query tile
+// sees and the visibility of one row.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <math.h>
+
+#include "attention.h"
+#include "common.cuh"
+
+namespace fpstok {
+
+constexpr int kTile = 128;  // rows of a query or key tile: one TMEM lane each
+
+// One tile of an event: its rows are t * kTile .. of the event's queries (or
+// keys, in the key list).
+struct TileItem {
+  int q0, nq, k0, nk;  // the event's first query row, queries, first key row, keys
+  int t;
+  int pad[3];
+};
+
+// Tiles of both lists: sum of ceil(n_b / kTile) <= n / kTile + B.
+__host__ __device__ inline int64_t max_tiles(int64_t n, int B) { return n / kTile + B; }
+
+// Visible keys of the query at position p of nk keys: [0, s) and [lo, hi).
+struct RowSpan {
+  int lo, hi, s;
+};
+__device__ __forceinline__ RowSpan row_span(const AttnMask& m, int p, int nk) {
+  RowSpan r;
+  r.lo = 0;
+  r.hi = nk;
+  r.s = 0;
+  if (m.window >= 0) {
+    r.lo = max(0, p - m.window);
+    r.hi = min(nk, p + m.window + 1);
+    r.s = min(m.sinks, nk);
+  }
+  if (m.causal) {
+    r.hi = min(r.hi, p + 1);
+    r.s = min(r.s, p + 1);
+  }
+  r.hi = max(r.hi, r.lo);
+  r.s = max(r.s, 0);
+  return r;
+}
+
+// Key tiles that some query at positions p0 .. p1 sees: `before` tiles from 0
+// on (sinks), then the tiles from `first` on; `count` in all.
+struct KeyTiles {
+  int before, first, count;
+  __device__ __forceinline__ int tile(int j) const { return j < before ? j : j - before + first; }
+};
+__device__ __forceinline__ KeyTiles key_tiles(const AttnMask& m, int p0, int p1, int nk) {
+  const RowSpan a = row_span(m, p0, nk), b = row_span(m, p1, nk);
+  const int hi = max(a.hi, b.hi), lo = min(a.lo, b.lo), s = max(a.s, b.s);
+  KeyTiles k;
+  int first = lo / kTile, end = hi > lo ? (hi + kTile - 1) / kTile : first;
+  const int sink = (s + kTile - 1) / kTile;
+  if (end == first) {  // no window: the sinks alone
+    k.before = 0;
+    k.first = 0;
+    k.count = sink;
+    return k;
+  }
+  if (sink >= first) {
+    if (sink > 0) first = 0;
+    end = max(end, sink);
+    k.before = 0;
+  } else {
+    k.before = sink;
+  }
+  k.first = first;
+  k.count = k.before + end - first;
+  return k;
+}
+
+// Whether some pair of the queries p0 .. p1 and the keys k0 .. k1 - 1 is hidden.
+__device__ __forceinline__ bool tile_masked(const AttnMask& m, int p0, int p1, int k0, int k1) {
+  if (m.causal && k1 - 1 > p0) return true;
+  return m.window >= 0 && k1 > m.sinks && (p1 - k0 > m.window || k1 - 1 - p0 > m.window);
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack16<__nv_bfloat16>(float lo, float hi) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+template <>
+__device__ __forceinline__ uint32_t pack16<__half>(float lo, float hi) {
+  __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Rows [first, n) of a [n, row_values] 16-bit tensor to 0, over the whole grid.
+__device__ __forceinline__ void zero_rows(void* base, int64_t first, int64_t n, int64_t row_values) {
+  if (first < 0 || first >= n) return;
+  uint4* p = reinterpret_cast<uint4*>(static_cast<char*>(base) + first * row_values * 2);
+  const int64_t total = (n - first) * row_values / 8;
+  for (int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; e < total; e += (int64_t)gridDim.x * blockDim.x)
+    p[e] = make_uint4(0, 0, 0, 0);
+}
+
+}  // namespace fpstok

@@ -460,6 +460,9 @@ int fps_device_status(void *workspace, fps_stream_t stream, int *detail);
 /* A cluster FPS kernel gave up waiting for its peers' candidates (a bounded
  * wait ran out); that launch's results are not valid. */
 #define FPS_DEV_EXCHANGE_TIMEOUT 5
+/* An attention kernel gave up waiting for a tile (a bounded wait ran out); that
+ * launch's results are not valid. */
+#define FPS_DEV_WAIT_TIMEOUT 6
 
 /*
  * Test hook of the cluster schedules' bounded exchange wait (host side only;
