@@ -45,11 +45,10 @@ struct AttnCall {
   void* dv;
 };
 
-size_t attention_workspace_bytes(int64_t n_q, int64_t n_kv, int B, int heads, int kv_heads, int D, bool backward);
-// The tensor-core kernels (attention_forward.cu) and their workspace.
+// Workspace bytes of a call of these sizes.
 size_t attention_forward_bytes(int64_t n_q, int B);
+size_t attention_backward_bytes(int64_t n_q, int64_t n_kv, int B, int heads);
 cudaError_t launch_attention_forward(const AttnCall& c, void* workspace, cudaStream_t s);
-cudaError_t launch_attention(const AttnCall& c, void* workspace, cudaStream_t s);
 cudaError_t launch_attention_backward(const AttnCall& c, void* workspace, cudaStream_t s);
 
 }  // namespace fpstok

@@ -71,7 +71,7 @@ __device__ __forceinline__ FwdItem fwd_item(const FwdArgs& a, int item) {
   w.row0 = w.e.t * kTile;
   w.rows = min(kTile, w.e.nq - w.row0);
   w.p0 = w.row0 + w.e.nk - w.e.nq;
-  w.keys = key_tiles(a.mask, w.p0, w.p0 + w.rows - 1, w.e.nk);
+  w.keys = key_tiles<kTile>(a.mask, w.p0, w.p0 + w.rows - 1, w.e.nk);
   return w;
 }
 

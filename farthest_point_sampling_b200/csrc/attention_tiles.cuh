@@ -47,18 +47,19 @@ __device__ __forceinline__ RowSpan row_span(const AttnMask& m, int p, int nk) {
   return r;
 }
 
-// Key tiles that some query at positions p0 .. p1 sees: `before` tiles from 0
-// on (sinks), then the tiles from `first` on; `count` in all.
+// Key tiles of kSize keys that some query at positions p0 .. p1 sees: `before`
+// tiles from 0 on (sinks), then the tiles from `first` on; `count` in all.
 struct KeyTiles {
   int before, first, count;
   __device__ __forceinline__ int tile(int j) const { return j < before ? j : j - before + first; }
 };
+template <int kSize>
 __device__ __forceinline__ KeyTiles key_tiles(const AttnMask& m, int p0, int p1, int nk) {
   const RowSpan a = row_span(m, p0, nk), b = row_span(m, p1, nk);
   const int hi = max(a.hi, b.hi), lo = min(a.lo, b.lo), s = max(a.s, b.s);
   KeyTiles k;
-  int first = lo / kTile, end = hi > lo ? (hi + kTile - 1) / kTile : first;
-  const int sink = (s + kTile - 1) / kTile;
+  int first = lo / kSize, end = hi > lo ? (hi + kSize - 1) / kSize : first;
+  const int sink = (s + kSize - 1) / kSize;
   if (end == first) {  // no window: the sinks alone
     k.before = 0;
     k.first = 0;
@@ -75,6 +76,21 @@ __device__ __forceinline__ KeyTiles key_tiles(const AttnMask& m, int p0, int p1,
   k.first = first;
   k.count = k.before + end - first;
   return k;
+}
+
+// Positions of the queries that see key j, as [lo, hi], unclipped.
+struct ColumnSpan {
+  int lo, hi;
+};
+__device__ __forceinline__ ColumnSpan column_span(const AttnMask& m, int j) {
+  ColumnSpan c;
+  c.lo = m.causal ? j : -(1 << 30);
+  c.hi = 1 << 30;
+  if (m.window >= 0 && j >= m.sinks) {
+    c.lo = max(c.lo, j - m.window);
+    c.hi = min(c.hi, j + m.window);
+  }
+  return c;
 }
 
 // Whether some pair of the queries p0 .. p1 and the keys k0 .. k1 - 1 is hidden.

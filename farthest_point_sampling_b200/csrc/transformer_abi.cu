@@ -13,7 +13,7 @@ namespace {
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 int from_cuda(cudaError_t e) { return e == cudaSuccess ? FPS_OK : FPS_ERR_CUDA; }
-constexpr int64_t kMaxRows = (int64_t)1 << 30;  // positions, and positions plus a window, fit 32 bits
+constexpr int64_t kMaxRows = (int64_t)1 << 29;  // positions, their differences and a window more fit 32 bits
 constexpr int64_t kMaxStride = (int64_t)1 << 38;  // elements; a TMA stride is below 2^40 bytes
 
 // Sizes only: enough to compute a workspace.
@@ -140,8 +140,8 @@ int fps_rotary(const void* x, void* y, int dtype, int64_t T, int H, int D, int64
 
 size_t fps_attention_workspace_bytes(const fps_attention_args* args, int backward) {
   if (check_attention_sizes(args)) return 0;
-  return attention_workspace_bytes(args->n_q, args->n_kv, args->events, args->heads, args->kv_heads, args->head_dim,
-                                   backward != 0);
+  return backward ? attention_backward_bytes(args->n_q, args->n_kv, args->events, args->heads)
+                  : attention_forward_bytes(args->n_q, args->events);
 }
 
 int fps_attention(const fps_attention_args* args, void* out, float* lse, void* workspace, size_t workspace_bytes,
@@ -154,7 +154,7 @@ int fps_attention(const fps_attention_args* args, void* out, float* lse, void* w
   if (!workspace || workspace_bytes < need || !aligned(workspace, 256)) return FPS_ERR_WORKSPACE;
   c.out = out;
   c.lse = lse;
-  return from_cuda(launch_attention(c, workspace, reinterpret_cast<cudaStream_t>(stream)));
+  return from_cuda(launch_attention_forward(c, workspace, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int fps_attention_backward(const fps_attention_args* args, const void* out, const float* lse, const void* dout,

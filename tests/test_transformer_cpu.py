@@ -42,7 +42,7 @@ def test_rotary_argument_errors():
     assert call(H=0) == _lib.FPS_ERR_ARG
     assert call(D=6) == _lib.FPS_ERR_ARG  # fewer values than the table turns
     assert call(D=512) == _lib.FPS_ERR_TOO_LARGE
-    assert call(T=1 << 30) == _lib.FPS_ERR_TOO_LARGE
+    assert call(T=1 << 29) == _lib.FPS_ERR_TOO_LARGE
     assert call(table=None) == _lib.FPS_ERR_ARG
     assert call(pos=None) == _lib.FPS_ERR_ARG
     assert call(x=None) == _lib.FPS_ERR_ARG
@@ -84,8 +84,8 @@ def test_attention_argument_errors():
                dict(q=264), dict(q_offsets=0), dict(kv_offsets=0), dict(q_token_stride=0), dict(q_head_stride=0),
                dict(k_token_stride=100), dict(v_head_stride=-64)):
         both(_lib.FPS_ERR_ARG, **kw)
-    for kw in (dict(head_dim=136), dict(n_q=1 << 30), dict(n_kv=1 << 31), dict(heads=1 << 17, kv_heads=1),
-               dict(n_q=(1 << 30) - 1, heads=4096, kv_heads=1)):
+    for kw in (dict(head_dim=136), dict(n_q=1 << 29), dict(n_kv=1 << 31), dict(heads=1 << 17, kv_heads=1),
+               dict(n_q=(1 << 29) - 1, heads=4096, kv_heads=1)):
         both(_lib.FPS_ERR_TOO_LARGE, **kw)
     a = _args()
     ref = ctypes.byref(a)
