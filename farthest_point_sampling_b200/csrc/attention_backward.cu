@@ -76,7 +76,7 @@ struct BwdItem {
   int h;           // head (queries kernel) or key head
   int row0, rows;  // kept rows: first in its event, how many
   int shift;       // nk - nq: position of query 0
-  KeyTiles tiles;  // streamed tiles of one head
+  KeyTiles<kStream> tiles;  // streamed tiles of one head
   int count;       // streamed tiles in all
 };
 template <bool kKeys>
@@ -95,9 +95,10 @@ __device__ __forceinline__ BwdItem bwd_item(const BwdArgs& a, int item) {
     const ColumnSpan first = column_span(a.mask, w.row0), last = column_span(a.mask, w.row0 + w.rows - 1);
     const int lo = min(max(min(first.lo, last.lo) - w.shift, 0), w.e.nq);
     const int hi = min(max(max(first.hi, last.hi) - w.shift + 1, 0), w.e.nq);
-    w.tiles.before = 0;
-    w.tiles.first = lo / kStream;
-    w.tiles.count = hi > lo ? (hi + kStream - 1) / kStream - w.tiles.first : 0;
+    w.tiles.before = w.tiles.s = 0;
+    w.tiles.first = lo & ~15;
+    w.tiles.end = hi;
+    w.tiles.count = hi > lo ? (hi - w.tiles.first + kStream - 1) / kStream : 0;
     w.count = w.tiles.count * a.group;
   } else {
     w.tiles = key_tiles<kStream>(a.mask, w.row0 + w.shift, w.row0 + w.rows - 1 + w.shift, w.e.nk);
@@ -116,12 +117,12 @@ __device__ __forceinline__ StreamTile stream_tile(const BwdArgs& a, const BwdIte
   if constexpr (kKeys) {
     const int m = t / w.tiles.count;
     s.head = w.h * a.group + m;
-    s.row0 = w.tiles.tile(t - m * w.tiles.count) * kStream;
-    s.rows = min(kStream, w.e.nq - s.row0);
+    s.row0 = w.tiles.start(t - m * w.tiles.count);
+    s.rows = w.tiles.extent(t - m * w.tiles.count);
   } else {
     s.head = w.h / a.group;
-    s.row0 = w.tiles.tile(t) * kStream;
-    s.rows = min(kStream, w.e.nk - s.row0);
+    s.row0 = w.tiles.start(t);
+    s.rows = w.tiles.extent(t);
   }
   return s;
 }
@@ -390,7 +391,7 @@ __global__ void __launch_bounds__(BwdShape<DP, kGroups, kKeys>::kThreads, BwdSha
         // kept rows k0 .. and streamed rows against one another: which pairs are hidden
         const int qp0 = (kKeys ? s.row0 : w.row0) + w.shift, qn = kKeys ? s.rows : w.rows;
         const int kk0 = kKeys ? w.row0 : s.row0, kn = kKeys ? w.rows : s.rows;
-        const bool masked = s.rows < kStream || tile_masked(a.mask, qp0, qp0 + qn - 1, kk0, kk0 + kn);
+        const bool masked = (s.rows & 31) != 0 || tile_masked(a.mask, qp0, qp0 + qn - 1, kk0, kk0 + kn);
         int from, width, sink = 0;
         if constexpr (kKeys) {
           const int p = s.row0 + w.shift;  // position of the tile's first query

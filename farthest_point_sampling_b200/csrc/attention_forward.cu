@@ -31,7 +31,8 @@ namespace fpstok {
 namespace {
 
 constexpr int kSoftmaxWarps = 4;
-constexpr int kFwdThreads = 32 * (kSoftmaxWarps + 2);
+constexpr int kFwdThreads = 256;  // the softmax warp group, and one of a loading and an issuing warp (two idle)
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 40;  // a thread's share after the split; launched with 128 each
 constexpr int kPanel = kTile * 128;  // bytes of a 128-row panel of 64 values
 constexpr uint32_t kTmemColumns = 256;
 constexpr uint32_t kColO = 128;  // S (and P over it) in columns 0 .. 127
@@ -61,18 +62,21 @@ struct FwdArgs {
 struct FwdItem {
   TileItem e;
   int h, row0, rows, p0;  // head; first query of the tile in its event, queries of the tile, position of the first
-  KeyTiles keys;
+  KeyTiles<kTile> keys;
 };
-__device__ __forceinline__ FwdItem fwd_item(const FwdArgs& a, int item) {
+__device__ __forceinline__ FwdItem fwd_item(const FwdArgs& a, int item, const TileItem& e) {
   FwdItem w;
-  const int tile = item / a.heads;
-  w.h = item - tile * a.heads;
-  w.e = a.items[tile];
+  w.h = item % a.heads;
+  w.e = e;
   w.row0 = w.e.t * kTile;
   w.rows = min(kTile, w.e.nq - w.row0);
   w.p0 = w.row0 + w.e.nk - w.e.nq;
   w.keys = key_tiles<kTile>(a.mask, w.p0, w.p0 + w.rows - 1, w.e.nk);
   return w;
+}
+// Every role reads the list entry of its next item while it works on one.
+__device__ __forceinline__ TileItem fwd_entry(const FwdArgs& a, int item, int n_items) {
+  return a.items[item < n_items ? item / a.heads : 0];
 }
 
 // Scores of 32 columns from column c0 of the tile on: those outside [from,
@@ -100,15 +104,15 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_bar + 16);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   const uint32_t bars = smem_u32(s_bar);
-  const uint32_t q_full = bars, q_empty = bars + 16, k_full = bars + 32, k_empty = bars + 48, v_full = bars + 64,
-                 v_empty = bars + 80, s_full = bars + 96, p_ready = bars + 104, o_full = bars + 112;
+  const uint32_t q_full = bars, k_full = bars + 16, k_empty = bars + 32, v_full = bars + 48, v_empty = bars + 64,
+                 s_full = bars + 80, o_full = bars + 88, drain = bars + 96, p_ready = bars + 104, q_empty = bars + 112;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 12; ++i) mbar_init(bars + 8 * i, 1);
-    mbar_init(s_full, 1);
+    for (int i = 0; i < 13; ++i) mbar_init(bars + 8 * i, 1);
     mbar_init(p_ready, 32 * kSoftmaxWarps);
-    mbar_init(o_full, 1);
+    mbar_init(q_empty, 32 * kSoftmaxWarps);
+    mbar_init(q_empty + 8, 32 * kSoftmaxWarps);
     *s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     tma_prefetch_map(&map_q);
@@ -123,65 +127,66 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int n_items = a.hdr->n_items[kQueryTiles] * a.heads;
 
-  if (warp == kSoftmaxWarps) {
-    // ------------------------------------------------ loads
-    if (lane == 0) {
+  if (warp >= kSoftmaxWarps) {
+    regs_down<kOtherRegs>();
+    if (warp == kSoftmaxWarps && lane == 0) {
+      // ------------------------------------------------ loads
       int n = 0, nq = 0;  // key tiles and query tiles loaded so far
-      for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
-        const FwdItem w = fwd_item(a, item);
+      bool ok = true;
+      TileItem next = fwd_entry(a, blockIdx.x, n_items);
+      for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x) {
+        const FwdItem w = fwd_item(a, item, next);
+        next = fwd_entry(a, item + gridDim.x, n_items);
         if (w.keys.count == 0) continue;
         const int qs = nq % Sh::kStages;
-        if (nq >= Sh::kStages && !mbar_wait(q_empty + 8 * qs, ((nq / Sh::kStages) - 1) & 1, s_abort)) break;
+        if (nq >= Sh::kStages && !(ok = mbar_wait(q_empty + 8 * qs, ((nq / Sh::kStages) - 1) & 1, s_abort))) break;
         const int q_boxes = (w.rows + 63) / 64;
-        mbar_expect(q_full + 8 * qs, q_boxes * 64 * 128 * Sh::kPanels);
+        mbar_expect(q_full + 8 * qs, q_boxes * 8192 * Sh::kPanels);
         for (int p = 0; p < Sh::kPanels; ++p)
           for (int i = 0; i < q_boxes; ++i)
             tma_load(smem_u32(s_q) + qs * Sh::kTileBytes + p * kPanel + i * 8192, &map_q, q_full + 8 * qs, p * 64, w.h,
                      w.e.q0 + w.row0 + i * 64);
         ++nq;
         const int g = w.h / a.group;
-        bool ok = true;
-        for (int j = 0; j < w.keys.count && ok; ++j, ++n) {
+        for (int j = 0; j < w.keys.count; ++j, ++n) {
           const int st = n % Sh::kStages;
           const uint32_t round = ((n / Sh::kStages) - 1) & 1;
-          const int k0 = w.keys.tile(j) * kTile;
-          const int boxes = (min(kTile, w.e.nk - k0) + 63) / 64;
-          const uint32_t bytes = boxes * 64 * 128 * Sh::kPanels;
+          const int boxes = (w.keys.extent(j) + 63) / 64;
+          const int krow = w.e.k0 + w.keys.start(j);
           if (n >= Sh::kStages && !(ok = mbar_wait(k_empty + 8 * st, round, s_abort))) break;
-          mbar_expect(k_full + 8 * st, bytes);
+          mbar_expect(k_full + 8 * st, boxes * 8192 * Sh::kPanels);
           for (int p = 0; p < Sh::kPanels; ++p)
             for (int i = 0; i < boxes; ++i)
               tma_load(smem_u32(s_k) + st * Sh::kTileBytes + p * kPanel + i * 8192, &map_k, k_full + 8 * st, p * 64, g,
-                       w.e.k0 + k0 + i * 64);
+                       krow + i * 64);
           if (n >= Sh::kStages && !(ok = mbar_wait(v_empty + 8 * st, round, s_abort))) break;
-          mbar_expect(v_full + 8 * st, bytes);
+          mbar_expect(v_full + 8 * st, boxes * 8192 * Sh::kPanels);
           for (int p = 0; p < Sh::kPanels; ++p)
             for (int i = 0; i < boxes; ++i)
               tma_load(smem_u32(s_v) + st * Sh::kTileBytes + p * kPanel + i * 8192, &map_v, v_full + 8 * st, p * 64, g,
-                       w.e.k0 + k0 + i * 64);
+                       krow + i * 64);
         }
-        if (!ok) break;
       }
       // after a wait that gave up: this thread's copies still in flight land first
       if (*s_abort) {
         volatile int none = 0;
         for (int i = 0; i < Sh::kStages; ++i) {
-          const int lq = nq - 1 - i, lk = n - 1 - i;
+          const int lq = nq - 1 - i, lk = n - i;  // tile n may have its keys loading, not its values
           if (lq >= 0) mbar_wait(q_full + 8 * (lq % Sh::kStages), (lq / Sh::kStages) & 1, &none);
           if (lk >= 0) mbar_wait(k_full + 8 * (lk % Sh::kStages), (lk / Sh::kStages) & 1, &none);
-          if (lk >= 0) mbar_wait(v_full + 8 * (lk % Sh::kStages), (lk / Sh::kStages) & 1, &none);
+          if (lk >= 1) mbar_wait(v_full + 8 * ((lk - 1) % Sh::kStages), ((lk - 1) / Sh::kStages) & 1, &none);
         }
       }
-    }
-  } else if (warp == kSoftmaxWarps + 1) {
-    // ------------------------------------------------ products
-    if (lane == 0) {
+    } else if (warp == kSoftmaxWarps + 1 && lane == 0) {
+      // ------------------------------------------------ products
       int n = 0, nq = 0;
-      const int k_steps = (a.D + 15) / 16;
-      const uint32_t pv_desc = mma_desc(kBf16, false, true, k_steps * 16);
+      const int d_steps = (a.D + 15) / 16;
+      const uint32_t pv_desc = mma_desc(kBf16, false, true, d_steps * 16);
       bool ok = true;
+      TileItem next = fwd_entry(a, blockIdx.x, n_items);
       for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x) {
-        const FwdItem w = fwd_item(a, item);
+        const FwdItem w = fwd_item(a, item, next);
+        next = fwd_entry(a, item + gridDim.x, n_items);
         if (w.keys.count == 0) continue;
         const int qs = nq % Sh::kStages;
         const uint32_t q_addr = smem_u32(s_q) + qs * Sh::kTileBytes;
@@ -189,7 +194,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
         for (int j = 0; j <= w.keys.count; ++j) {
           if (j > 0) {  // O += P V of tile j - 1
             const int m = n + j - 1, st = m % Sh::kStages;
-            const int steps = (min(kTile, w.e.nk - w.keys.tile(j - 1) * kTile) + 15) / 16;
+            const int steps = (w.keys.extent(j - 1) + 15) / 16;
             if (!(ok = mbar_wait(v_full + 8 * st, (m / Sh::kStages) & 1, s_abort))) break;
             if (!(ok = mbar_wait(p_ready, m & 1, s_abort))) break;
             tc_fence_after();
@@ -201,18 +206,17 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
           }
           if (j < w.keys.count) {  // S = Q K^T of tile j; over P, which the product before has read
             const int m = n + j, st = m % Sh::kStages;
-            const int cols = (min(kTile, w.e.nk - w.keys.tile(j) * kTile) + 15) / 16 * 16;
+            const int cols = (w.keys.extent(j) + 15) / 16 * 16;
             if (!(ok = mbar_wait(k_full + 8 * st, (m / Sh::kStages) & 1, s_abort))) break;
             tc_fence_after();
             const uint32_t k_addr = smem_u32(s_k) + st * Sh::kTileBytes;
             const uint32_t qk_desc = mma_desc(kBf16, false, false, cols);
-            for (int ks = 0; ks < k_steps; ++ks) {
+            for (int ks = 0; ks < d_steps; ++ks) {
               const uint32_t at = (ks >> 2) * kPanel + (ks & 3) * 32;
               mma_ss(tmem, smem_desc(q_addr + at, kPanel), smem_desc(k_addr + at, kPanel), qk_desc, ks > 0);
             }
             mma_commit(k_empty + 8 * st);
             mma_commit(s_full);
-            if (j == w.keys.count - 1) mma_commit(q_empty + 8 * qs);
           }
         }
         if (!ok) break;
@@ -221,65 +225,87 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
       }
       if (*s_abort) {  // products in flight end before TMEM is freed
         volatile int none = 0;
-        mbar_init(bars + 120, 1);
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        mma_commit(bars + 120);
-        mbar_wait(bars + 120, 0, &none);
+        mma_commit(drain);
+        mbar_wait(drain, 0, &none);
       }
     }
   } else {
     // ------------------------------------------------ softmax
-    int n = 0, done = 0;  // key tiles and items so far
+    regs_up<kSoftmaxRegs>();
+    int n = 0, nq = 0;  // key tiles and query tiles so far
     const int row = threadIdx.x;
     const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
+    const float2 scale2 = make_float2(a.scale_log2, a.scale_log2);
     bool ok = true;
+    TileItem next = fwd_entry(a, blockIdx.x, n_items);
     for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x) {
-      const FwdItem w = fwd_item(a, item);
+      const FwdItem w = fwd_item(a, item, next);
+      next = fwd_entry(a, item + gridDim.x, n_items);
       const int64_t qrow = (int64_t)w.e.q0 + w.row0 + row;
-      const int p = w.p0 + row;
-      const RowSpan span = row_span(a.mask, p, w.e.nk);
+      T* out = static_cast<T*>(a.out) + ((int64_t)(w.e.q0 + w.row0 + warp * 32) * a.heads + w.h) * a.D;
+      const int warp_rows = min(32, w.rows - warp * 32);
+      if (w.keys.count == 0) {  // nothing to see
+        for (int r = lane; r < warp_rows; r += 32) {
+          for (int c = 0; c < a.D; c += 8)
+            *reinterpret_cast<uint4*>(out + (int64_t)r * a.heads * a.D + c) = make_uint4(0, 0, 0, 0);
+          if (a.lse) a.lse[(int64_t)w.h * a.n_q + qrow] = -INFINITY;
+        }
+        continue;
+      }
+      const RowSpan span = row_span(a.mask, w.p0 + row, w.e.nk);
+      // keys that some row of this warp sees
+      const RowSpan warp_lo = row_span(a.mask, w.p0 + warp * 32, w.e.nk);
+      const RowSpan warp_hi = row_span(a.mask, w.p0 + min(warp * 32 + 31, w.rows - 1), w.e.nk);
       float m_used = -INFINITY, l = 0.f;
       for (int j = 0; j < w.keys.count; ++j, ++n) {
         const int st = n % Sh::kStages;
-        const int k0 = w.keys.tile(j) * kTile;
-        const int valid = min(kTile, w.e.nk - k0);
-        const int odd = valid & 15;
+        const int k0 = w.keys.start(j), extent = w.keys.extent(j);
+        const int odd = extent & 15;
         if (odd) {
-          // Keys past the event's last inside the product's step of 16: their
+          // Keys past the tile's last inside the product's step of 16: their
           // weights are 0, and their values must be finite for 0 to stay 0.
           if (!(ok = mbar_wait(v_full + 8 * st, (n / Sh::kStages) & 1, s_abort))) break;
           uint8_t* v_tile = s_v + st * Sh::kTileBytes;
           for (int e = threadIdx.x; e < (16 - odd) * 8 * Sh::kPanels; e += 32 * kSoftmaxWarps) {
-            const int r = valid + e / (8 * Sh::kPanels), c = e % (8 * Sh::kPanels);
+            const int r = extent + e / (8 * Sh::kPanels), c = e % (8 * Sh::kPanels);
             *reinterpret_cast<uint4*>(v_tile + (c >> 3) * kPanel + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
           }
           fence_async_smem();
         }
+        // 32-column chunks of the tile that some row of the warp sees
+        int act = 0;
+#pragma unroll
+        for (int c = 0; c < kTile / 32; ++c) {
+          const int first = k0 + 32 * c, last = k0 + min(32 * c + 31, extent - 1);
+          if (32 * c < extent && warp_rows > 0 &&
+              ((last >= warp_lo.lo && first < warp_hi.hi) || first < warp_hi.s))
+            act |= 1 << c;
+        }
+        const bool masked = (extent & 31) != 0 || tile_masked(a.mask, w.p0, w.p0 + w.rows - 1, k0, k0 + extent);
         if (!(ok = mbar_wait(s_full, n & 1, s_abort))) break;
         tc_fence_after();
-        // S is read from TMEM twice, 32 columns at a time with the next 32 on
-        // their way: once for the row's maximum, once for the weights.
-        const bool masked = valid < kTile || tile_masked(a.mask, w.p0, w.p0 + w.rows - 1, k0, k0 + valid);
-        const int from = span.lo - k0, width = min(span.hi - k0, valid) - from, sink = min(span.s - k0, valid);
-        const int chunks = (valid + 31) >> 5;
-        float s[2][32];
-        tmem_ld32(lanes, reinterpret_cast<uint32_t*>(s[0]));
+        float s[kTile];
+#pragma unroll
+        for (int c = 0; c < kTile / 32; ++c)
+          if (act >> c & 1) tmem_ld32(lanes + 32 * c, reinterpret_cast<uint32_t*>(s + 32 * c));
+#pragma unroll
+        for (int c = 0; c < kTile / 32; ++c) tmem_wait_ld32(reinterpret_cast<uint32_t*>(s + 32 * c));
+        if (masked) {
+          const int from = span.lo - k0, width = min(span.hi - k0, extent) - from, sink = min(span.s - k0, extent);
+#pragma unroll
+          for (int c = 0; c < kTile / 32; ++c)
+            if (act >> c & 1) hide(s + 32 * c, 32 * c, from, width, sink);
+        }
         float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
         for (int c = 0; c < kTile / 32; ++c)
-          if (c < chunks) {
-            tmem_wait_ld32(reinterpret_cast<uint32_t*>(s[c & 1]));
-            if (c + 1 < kTile / 32 && c + 1 < chunks)
-              tmem_ld32(lanes + 32 * (c + 1), reinterpret_cast<uint32_t*>(s[(c + 1) & 1]));
-            float* v = s[c & 1];
-            if (masked) hide(v, 32 * c, from, width, sink);
+          if (act >> c & 1) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              m0 = max3f(m0, v[i], v[i + 1]);
-              m1 = max3f(m1, v[i + 2], v[i + 3]);
+            for (int i = 32 * c; i < 32 * c + 32; i += 4) {
+              m0 = max3f(m0, s[i], s[i + 1]);
+              m1 = max3f(m1, s[i + 2], s[i + 3]);
             }
           }
-        tmem_ld32(lanes, reinterpret_cast<uint32_t*>(s[0]));
         const float top = fmaxf(m0, m1);
         if (j == 0) {
           m_used = top;
@@ -302,66 +328,72 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
           }
         }
         const float base = m_used == -INFINITY ? 0.f : m_used * a.scale_log2;
-        float l0 = 0.f, l1 = 0.f;
+        const float2 base2 = make_float2(-base, -base);
+        float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int c = 0; c < kTile / 32; ++c)
-          if (c < chunks) {
-            tmem_wait_ld32(reinterpret_cast<uint32_t*>(s[c & 1]));
-            if (c + 1 < kTile / 32 && c + 1 < chunks)
-              tmem_ld32(lanes + 32 * (c + 1), reinterpret_cast<uint32_t*>(s[(c + 1) & 1]));
-            float* v = s[c & 1];
-            if (masked) hide(v, 32 * c, from, width, sink);
-            uint32_t pk[16];
+        for (int c = 0; c < kTile / 32; ++c) {
+          uint32_t pk[16];
+          if (act >> c & 1) {
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
-              const float e0 = exp2_approx(fmaf(v[i], a.scale_log2, -base));
-              const float e1 = exp2_approx(fmaf(v[i + 1], a.scale_log2, -base));
-              l0 += e0;
-              l1 += e1;
-              pk[i / 2] = pack16<T>(e0, e1);
+              float2 e = fma2(make_float2(s[32 * c + i], s[32 * c + i + 1]), scale2, base2);
+              e.x = exp2_approx(e.x);
+              e.y = exp2_approx(e.y);
+              sum = add2(sum, e);
+              pk[i / 2] = pack16<T>(e.x, e.y);
             }
-            tmem_st16(lanes + 16 * c, pk);  // columns whose S this pass has read already
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) pk[i] = 0;
           }
-        l += l0 + l1;
+          if (32 * c < extent) tmem_st16(lanes + 16 * c, pk);
+        }
+        l += sum.x + sum.y;
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(p_ready);
       }
       if (!ok) break;
-      const bool live = row < w.rows;
-      T* out = static_cast<T*>(a.out) + (qrow * a.heads + w.h) * a.D;
-      if (w.keys.count) {
-        if (!(ok = mbar_wait(o_full, done & 1, s_abort))) break;
-        ++done;
-        tc_fence_after();
-      }
-      const float inv = w.keys.count == 0 || l == 0.f ? 0.f : 1.f / l;
+      const int qs = nq % Sh::kStages;
+      if (!(ok = mbar_wait(o_full, nq & 1, s_abort))) break;
+      ++nq;
+      tc_fence_after();
+      // O / l to the item's query tile in shared memory, which no product
+      // reads any more, then to memory with whole rows per instruction; a
+      // warp only touches its own rows.
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      uint8_t* stage = s_q + qs * Sh::kTileBytes;
 #pragma unroll
       for (int c = 0; c < DP; c += 32) {
         uint32_t o[32];
-        if (w.keys.count) {
-          tmem_ld32(lanes + kColO + c, o);
-          tmem_wait_ld32(o);
-        } else {
+        tmem_ld32(lanes + kColO + c, o);
+        tmem_wait_ld32(o);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = 0;
-        }
-        if (live) {
+        for (int i = 0; i < 32; i += 8) {
+          uint4 v;
+          uint32_t* pv = reinterpret_cast<uint32_t*>(&v);
 #pragma unroll
-          for (int i = 0; i < 32; i += 8)
-            if (c + i < a.D) {
-              uint4 v;
-              uint32_t* pv = reinterpret_cast<uint32_t*>(&v);
-#pragma unroll
-              for (int q = 0; q < 4; ++q)
-                pv[q] = pack16<T>(l == 0.f ? 0.f : __uint_as_float(o[i + 2 * q]) * inv,
-                                  l == 0.f ? 0.f : __uint_as_float(o[i + 2 * q + 1]) * inv);
-              *reinterpret_cast<uint4*>(out + c + i) = v;
-            }
+          for (int q = 0; q < 4; ++q)
+            pv[q] = l == 0.f ? 0u
+                             : pack16<T>(__uint_as_float(o[i + 2 * q]) * inv, __uint_as_float(o[i + 2 * q + 1]) * inv);
+          const int k = (c + i) / 8;
+          *reinterpret_cast<uint4*>(stage + (k >> 3) * kPanel + row * 128 + (((k & 7) ^ (row & 7)) << 4)) = v;
         }
       }
       tc_fence_before();
-      if (live && a.lse) a.lse[(int64_t)w.h * a.n_q + qrow] = l == 0.f ? -INFINITY : fmaf(m_used, a.scale, logf(l));
+      __syncwarp();
+      constexpr int kRowsAtOnce = 32 / (DP / 8);
+      const int chunk = lane % (DP / 8);
+      if (chunk * 8 < a.D)
+        for (int r = lane / (DP / 8); r < warp_rows; r += kRowsAtOnce) {
+          const int rr = warp * 32 + r;
+          *reinterpret_cast<uint4*>(out + (int64_t)r * a.heads * a.D + chunk * 8) = *reinterpret_cast<const uint4*>(
+              stage + (chunk >> 3) * kPanel + rr * 128 + (((chunk & 7) ^ (rr & 7)) << 4));
+        }
+      if (lane < warp_rows && a.lse)
+        a.lse[(int64_t)w.h * a.n_q + qrow] = l == 0.f ? -INFINITY : fmaf(m_used, a.scale, logf(l));
+      fence_async_smem();  // these reads and writes before the next tile's load
+      mbar_arrive(q_empty + 8 * qs);
     }
   }
   if (a.zero_tail) zero_rows(a.out, a.B > 0 ? a.q_offsets[a.B] : 0, a.n_q, (int64_t)a.heads * a.D);

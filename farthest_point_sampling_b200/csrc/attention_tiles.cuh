@@ -47,34 +47,32 @@ __device__ __forceinline__ RowSpan row_span(const AttnMask& m, int p, int nk) {
   return r;
 }
 
-// Key tiles of kSize keys that some query at positions p0 .. p1 sees: `before`
-// tiles from 0 on (sinks), then the tiles from `first` on; `count` in all.
+// Key tiles of kSize keys that some query at positions p0 .. p1 sees: first
+// `before` tiles over the sinks [0, s), then tiles from key `first` (a
+// multiple of 16) up to `end`.  A tile holds the keys from start(j) on,
+// extent(j) of them.
+template <int kSize>
 struct KeyTiles {
-  int before, first, count;
-  __device__ __forceinline__ int tile(int j) const { return j < before ? j : j - before + first; }
+  int before, first, end, s, count;
+  __device__ __forceinline__ int start(int j) const { return j < before ? j * kSize : first + (j - before) * kSize; }
+  __device__ __forceinline__ int extent(int j) const { return min(kSize, (j < before ? s : end) - start(j)); }
 };
 template <int kSize>
-__device__ __forceinline__ KeyTiles key_tiles(const AttnMask& m, int p0, int p1, int nk) {
+__device__ __forceinline__ KeyTiles<kSize> key_tiles(const AttnMask& m, int p0, int p1, int nk) {
   const RowSpan a = row_span(m, p0, nk), b = row_span(m, p1, nk);
-  const int hi = max(a.hi, b.hi), lo = min(a.lo, b.lo), s = max(a.s, b.s);
-  KeyTiles k;
-  int first = lo / kSize, end = hi > lo ? (hi + kSize - 1) / kSize : first;
-  const int sink = (s + kSize - 1) / kSize;
-  if (end == first) {  // no window: the sinks alone
-    k.before = 0;
+  KeyTiles<kSize> k;
+  k.s = max(a.s, b.s);
+  k.end = max(a.hi, b.hi);
+  k.first = min(a.lo, b.lo) & ~15;
+  if (k.end <= k.first) {  // no window: the sinks alone
     k.first = 0;
-    k.count = sink;
-    return k;
+    k.end = k.s;
+  } else if (k.s > 0 && k.s + kSize > k.first) {  // sinks that reach the window's tiles, or nearly: one run of tiles
+    k.first = 0;
+    k.end = max(k.end, k.s);
   }
-  if (sink >= first) {
-    if (sink > 0) first = 0;
-    end = max(end, sink);
-    k.before = 0;
-  } else {
-    k.before = sink;
-  }
-  k.first = first;
-  k.count = k.before + end - first;
+  k.before = k.first > 0 ? (k.s + kSize - 1) / kSize : 0;
+  k.count = k.before + (k.end - k.first + kSize - 1) / kSize;
   return k;
 }
 
@@ -116,6 +114,19 @@ __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// a * b + c of two values at once.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(d)
+      : "l"(pack2(a.x, a.y)), "l"(pack2(b.x, b.y)), "l"(pack2(c.x, c.y)));
+  return make_float2(lo2(d), hi2(d));
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  const uint64_t d = add2(pack2(a.x, a.y), pack2(b.x, b.y));
+  return make_float2(lo2(d), hi2(d));
 }
 
 constexpr float kLog2e = 1.4426950408889634f;
