@@ -80,12 +80,10 @@ struct BwdItem {
   int count;       // streamed tiles in all
 };
 template <bool kKeys>
-__device__ __forceinline__ BwdItem bwd_item(const BwdArgs& a, int item) {
+__device__ __forceinline__ BwdItem bwd_item(const BwdArgs& a, int h, const TileItem& e) {
   BwdItem w;
-  const int heads = kKeys ? a.kv_heads : a.heads;
-  const int tile = item / heads;
-  w.h = item - tile * heads;
-  w.e = a.items[tile];
+  w.h = h;
+  w.e = e;
   w.row0 = w.e.t * kTile;
   w.rows = min(kTile, (kKeys ? w.e.nk : w.e.nq) - w.row0);
   w.shift = w.e.nk - w.e.nq;
@@ -209,15 +207,19 @@ __global__ void __launch_bounds__(BwdShape<DP, kGroups, kKeys>::kThreads, BwdSha
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int n_items = a.hdr->n_items[kKeys ? kKeyTiles : kQueryTiles] * (kKeys ? a.kv_heads : a.heads);
+  // every role walks the block's items, and reads the next one's entry while it works on one
+  ItemWalk walk(kKeys ? a.kv_heads : a.heads, a.hdr->n_items[kKeys ? kKeyTiles : kQueryTiles]);
+  TileItem next = a.items[walk.more() ? walk.tile : 0];
 
   if (warp == kLoadWarp) {
     // ------------------------------------------------ loads
     if (lane == 0) {
       int n = 0, nk = 0;  // streamed and kept tiles loaded so far
       bool ok = true;
-      for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x) {
-        const BwdItem w = bwd_item<kKeys>(a, item);
+      while (walk.more() && ok) {
+        const BwdItem w = bwd_item<kKeys>(a, walk.h, next);
+        walk.advance();
+        if (walk.more()) next = a.items[walk.tile];
         if (w.count == 0) continue;
         const int ks = nk % Sh::kKept;
         if (nk >= Sh::kKept && !(ok = mbar_wait(kept_empty + 8 * ks, ((nk / Sh::kKept) - 1) & 1, s_abort))) break;
@@ -261,11 +263,13 @@ __global__ void __launch_bounds__(BwdShape<DP, kGroups, kKeys>::kThreads, BwdSha
       const int d_steps = (a.D + 15) / 16;
       const uint32_t out_desc = mma_desc(kBf16, false, true, d_steps * 16);
       bool ok = true;
-      for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x) {
-        const BwdItem w = bwd_item<kKeys>(a, item);
+      while (walk.more() && ok) {
+        const BwdItem w = bwd_item<kKeys>(a, walk.h, next);
+        walk.advance();
+        if (walk.more()) next = a.items[walk.tile];
         if (w.count == 0) continue;
         const int ks = nk % Sh::kKept;
-        const uint32_t kept = smem_u32(s_kept) + 2 * ks * Sh::kKeptBytes;
+        const uint32_t kept = smem_desc(smem_u32(s_kept) + 2 * ks * Sh::kKeptBytes, kPanel);
         if (!(ok = mbar_wait(kept_full + 8 * ks, (nk / Sh::kKept) & 1, s_abort))) break;
         for (int t = 0; t < w.count + kGroups - 1; ++t) {
           if (t < w.count) {  // scores of tile t, over the P and dS that the products before have read
@@ -275,12 +279,15 @@ __global__ void __launch_bounds__(BwdShape<DP, kGroups, kKeys>::kThreads, BwdSha
             if (!(ok = mbar_wait(ring_full + 8 * st, (m / Sh::kRing) & 1, s_abort))) break;
             tc_fence_after();
             const uint32_t desc = mma_desc(kBf16, false, false, cols);
+            const uint32_t from = smem_desc(ring, kStreamPanel);
+#pragma unroll
             for (int x = 0; x < 2; ++x)
-              for (int k = 0; k < d_steps; ++k)
-                mma_ss(tmem + g * 128 + x * 64,
-                       smem_desc(kept + x * Sh::kKeptBytes + (k >> 2) * kPanel + (k & 3) * 32, kPanel),
-                       smem_desc(ring + x * Sh::kStreamBytes + (k >> 2) * kStreamPanel + (k & 3) * 32, kStreamPanel),
-                       desc, k > 0);
+#pragma unroll
+              for (int k = 0; k < DP / 16; ++k)
+                if (k < d_steps)
+                  mma_ss(tmem + g * 128 + x * 64,
+                         kept + ((x * Sh::kKeptBytes + (k >> 2) * kPanel + (k & 3) * 32) >> 4),
+                         from + ((x * Sh::kStreamBytes + (k >> 2) * kStreamPanel + (k & 3) * 32) >> 4), desc, k > 0);
             mma_commit(score_full + 8 * g);
           }
           const int u = t - (kGroups - 1);
@@ -291,13 +298,18 @@ __global__ void __launch_bounds__(BwdShape<DP, kGroups, kKeys>::kThreads, BwdSha
             if (u == 0 && nk > 0 && !(ok = mbar_wait(acc_empty, (nk - 1) & 1, s_abort))) break;
             if (!(ok = mbar_wait(ready + 8 * g, (m / kGroups) & 1, s_abort))) break;
             tc_fence_after();
-            if constexpr (kKeys)
-              for (int k = 0; k < steps; ++k)  // dV += P^T dO
-                mma_ts(tmem + Sh::kColAcc + DP, tmem + g * 128 + k * 8,
-                       smem_desc(ring + Sh::kStreamBytes + k * 2048, kStreamPanel), out_desc, u > 0 || k > 0);
-            for (int k = 0; k < steps; ++k)  // dK += dS^T Q, or dQ += dS K
-              mma_ts(tmem + Sh::kColAcc, tmem + g * 128 + 64 + k * 8, smem_desc(ring + k * 2048, kStreamPanel), out_desc,
-                     u > 0 || k > 0);
+            const uint32_t from = smem_desc(ring, kStreamPanel);
+            if constexpr (kKeys) {  // dV += P^T dO
+#pragma unroll
+              for (int k = 0; k < kStream / 16; ++k)
+                if (k < steps)
+                  mma_ts(tmem + Sh::kColAcc + DP, tmem + g * 128 + k * 8, from + (Sh::kStreamBytes >> 4) + k * 128,
+                         out_desc, k > 0 || u > 0);
+            }
+#pragma unroll
+            for (int k = 0; k < kStream / 16; ++k)  // dK += dS^T Q, or dQ += dS K
+              if (k < steps)
+                mma_ts(tmem + Sh::kColAcc, tmem + g * 128 + 64 + k * 8, from + k * 128, out_desc, k > 0 || u > 0);
             mma_commit(ring_empty + 8 * st);
             if (u == w.count - 1) {
               mma_commit(kept_empty + 8 * ks);
@@ -324,8 +336,10 @@ __global__ void __launch_bounds__(BwdShape<DP, kGroups, kKeys>::kThreads, BwdSha
     float* col = s_col + g * 256;
     int n = 0, nk = 0;
     bool ok = true;
-    for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x) {
-      const BwdItem w = bwd_item<kKeys>(a, item);
+    while (walk.more() && ok) {
+      const BwdItem w = bwd_item<kKeys>(a, walk.h, next);
+      walk.advance();
+      if (walk.more()) next = a.items[walk.tile];
       const bool live = row < w.rows;
       RowSpan rs = {0, 0, 0};
       ColumnSpan cs = {0, 0};

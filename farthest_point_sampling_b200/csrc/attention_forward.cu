@@ -32,7 +32,7 @@ namespace {
 
 constexpr int kSoftmaxWarps = 4;
 constexpr int kFwdThreads = 256;  // the softmax warp group, and one of a loading and an issuing warp (two idle)
-constexpr int kSoftmaxRegs = 208, kOtherRegs = 40;  // a thread's share after the split; launched with 128 each
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 48;  // a thread's share after the split; launched with 128 each
 constexpr int kPanel = kTile * 128;  // bytes of a 128-row panel of 64 values
 constexpr uint32_t kTmemColumns = 256;
 constexpr uint32_t kColO = 128;  // S (and P over it) in columns 0 .. 127
@@ -64,9 +64,9 @@ struct FwdItem {
   int h, row0, rows, p0;  // head; first query of the tile in its event, queries of the tile, position of the first
   KeyTiles<kTile> keys;
 };
-__device__ __forceinline__ FwdItem fwd_item(const FwdArgs& a, int item, const TileItem& e) {
+__device__ __forceinline__ FwdItem fwd_item(const FwdArgs& a, int h, const TileItem& e) {
   FwdItem w;
-  w.h = item % a.heads;
+  w.h = h;
   w.e = e;
   w.row0 = w.e.t * kTile;
   w.rows = min(kTile, w.e.nq - w.row0);
@@ -74,19 +74,12 @@ __device__ __forceinline__ FwdItem fwd_item(const FwdArgs& a, int item, const Ti
   w.keys = key_tiles<kTile>(a.mask, w.p0, w.p0 + w.rows - 1, w.e.nk);
   return w;
 }
-// Every role reads the list entry of its next item while it works on one.
-__device__ __forceinline__ TileItem fwd_entry(const FwdArgs& a, int item, int n_items) {
-  return a.items[item < n_items ? item / a.heads : 0];
-}
 
-// Scores of 32 columns from column c0 of the tile on: those outside [from,
-// from + width) and not below sink to -inf.
-__device__ __forceinline__ void hide(float* s, int c0, int from, int width, int sink) {
-#pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    const int c = c0 + i;
-    if (!((c >= from && c - from < width) || c < sink)) s[i] = -INFINITY;
-  }
+// Bits lo .. hi - 1 of a word, bounds clipped to 0 .. 32.
+__device__ __forceinline__ uint32_t bits(int lo, int hi) {
+  lo = max(lo, 0);
+  hi = min(hi, 32);
+  return hi <= lo ? 0u : (0xffffffffu >> (32 - hi)) & (0xffffffffu << lo);
 }
 
 template <typename T, int DP>
@@ -125,7 +118,9 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int n_items = a.hdr->n_items[kQueryTiles] * a.heads;
+  // every role walks the block's items, and reads the next one's entry while it works on one
+  ItemWalk walk(a.heads, a.hdr->n_items[kQueryTiles]);
+  TileItem next = a.items[walk.more() ? walk.tile : 0];
 
   if (warp >= kSoftmaxWarps) {
     regs_down<kOtherRegs>();
@@ -133,16 +128,18 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
       // ------------------------------------------------ loads
       int n = 0, nq = 0;  // key tiles and query tiles loaded so far
       bool ok = true;
-      TileItem next = fwd_entry(a, blockIdx.x, n_items);
-      for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x) {
-        const FwdItem w = fwd_item(a, item, next);
-        next = fwd_entry(a, item + gridDim.x, n_items);
+      while (walk.more() && ok) {
+        const FwdItem w = fwd_item(a, walk.h, next);
+        walk.advance();
+        if (walk.more()) next = a.items[walk.tile];
         if (w.keys.count == 0) continue;
         const int qs = nq % Sh::kStages;
         if (nq >= Sh::kStages && !(ok = mbar_wait(q_empty + 8 * qs, ((nq / Sh::kStages) - 1) & 1, s_abort))) break;
         const int q_boxes = (w.rows + 63) / 64;
         mbar_expect(q_full + 8 * qs, q_boxes * 8192 * Sh::kPanels);
+#pragma unroll 1
         for (int p = 0; p < Sh::kPanels; ++p)
+#pragma unroll 1
           for (int i = 0; i < q_boxes; ++i)
             tma_load(smem_u32(s_q) + qs * Sh::kTileBytes + p * kPanel + i * 8192, &map_q, q_full + 8 * qs, p * 64, w.h,
                      w.e.q0 + w.row0 + i * 64);
@@ -155,13 +152,17 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
           const int krow = w.e.k0 + w.keys.start(j);
           if (n >= Sh::kStages && !(ok = mbar_wait(k_empty + 8 * st, round, s_abort))) break;
           mbar_expect(k_full + 8 * st, boxes * 8192 * Sh::kPanels);
+#pragma unroll 1
           for (int p = 0; p < Sh::kPanels; ++p)
+#pragma unroll 1
             for (int i = 0; i < boxes; ++i)
               tma_load(smem_u32(s_k) + st * Sh::kTileBytes + p * kPanel + i * 8192, &map_k, k_full + 8 * st, p * 64, g,
                        krow + i * 64);
           if (n >= Sh::kStages && !(ok = mbar_wait(v_empty + 8 * st, round, s_abort))) break;
           mbar_expect(v_full + 8 * st, boxes * 8192 * Sh::kPanels);
+#pragma unroll 1
           for (int p = 0; p < Sh::kPanels; ++p)
+#pragma unroll 1
             for (int i = 0; i < boxes; ++i)
               tma_load(smem_u32(s_v) + st * Sh::kTileBytes + p * kPanel + i * 8192, &map_v, v_full + 8 * st, p * 64, g,
                        krow + i * 64);
@@ -183,13 +184,13 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
       const int d_steps = (a.D + 15) / 16;
       const uint32_t pv_desc = mma_desc(kBf16, false, true, d_steps * 16);
       bool ok = true;
-      TileItem next = fwd_entry(a, blockIdx.x, n_items);
-      for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x) {
-        const FwdItem w = fwd_item(a, item, next);
-        next = fwd_entry(a, item + gridDim.x, n_items);
+      while (walk.more() && ok) {
+        const FwdItem w = fwd_item(a, walk.h, next);
+        walk.advance();
+        if (walk.more()) next = a.items[walk.tile];
         if (w.keys.count == 0) continue;
         const int qs = nq % Sh::kStages;
-        const uint32_t q_addr = smem_u32(s_q) + qs * Sh::kTileBytes;
+        const uint32_t q = smem_desc(smem_u32(s_q) + qs * Sh::kTileBytes, kPanel);
         if (!(ok = mbar_wait(q_full + 8 * qs, (nq / Sh::kStages) & 1, s_abort))) break;
         for (int j = 0; j <= w.keys.count; ++j) {
           if (j > 0) {  // O += P V of tile j - 1
@@ -198,9 +199,10 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
             if (!(ok = mbar_wait(v_full + 8 * st, (m / Sh::kStages) & 1, s_abort))) break;
             if (!(ok = mbar_wait(p_ready, m & 1, s_abort))) break;
             tc_fence_after();
-            const uint32_t v_addr = smem_u32(s_v) + st * Sh::kTileBytes;
-            for (int ks = 0; ks < steps; ++ks)
-              mma_ts(tmem + kColO, tmem + ks * 8, smem_desc(v_addr + ks * 2048, kPanel), pv_desc, j > 1 || ks > 0);
+            const uint32_t v = smem_desc(smem_u32(s_v) + st * Sh::kTileBytes, kPanel);
+#pragma unroll
+            for (int ks = 0; ks < kTile / 16; ++ks)
+              if (ks < steps) mma_ts(tmem + kColO, tmem + ks * 8, v + ks * 128, pv_desc, ks > 0 || j > 1);
             mma_commit(v_empty + 8 * st);
             if (j == w.keys.count) mma_commit(o_full);
           }
@@ -209,11 +211,12 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
             const int cols = (w.keys.extent(j) + 15) / 16 * 16;
             if (!(ok = mbar_wait(k_full + 8 * st, (m / Sh::kStages) & 1, s_abort))) break;
             tc_fence_after();
-            const uint32_t k_addr = smem_u32(s_k) + st * Sh::kTileBytes;
+            const uint32_t k = smem_desc(smem_u32(s_k) + st * Sh::kTileBytes, kPanel);
             const uint32_t qk_desc = mma_desc(kBf16, false, false, cols);
-            for (int ks = 0; ks < d_steps; ++ks) {
-              const uint32_t at = (ks >> 2) * kPanel + (ks & 3) * 32;
-              mma_ss(tmem, smem_desc(q_addr + at, kPanel), smem_desc(k_addr + at, kPanel), qk_desc, ks > 0);
+#pragma unroll
+            for (int ks = 0; ks < DP / 16; ++ks) {
+              const uint32_t at = ((ks >> 2) * kPanel + (ks & 3) * 32) >> 4;
+              if (ks < d_steps) mma_ss(tmem, q + at, k + at, qk_desc, ks > 0);
             }
             mma_commit(k_empty + 8 * st);
             mma_commit(s_full);
@@ -237,10 +240,10 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
     const float2 scale2 = make_float2(a.scale_log2, a.scale_log2);
     bool ok = true;
-    TileItem next = fwd_entry(a, blockIdx.x, n_items);
-    for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x) {
-      const FwdItem w = fwd_item(a, item, next);
-      next = fwd_entry(a, item + gridDim.x, n_items);
+    while (walk.more() && ok) {
+      const FwdItem w = fwd_item(a, walk.h, next);
+      walk.advance();
+      if (walk.more()) next = a.items[walk.tile];
       const int64_t qrow = (int64_t)w.e.q0 + w.row0 + row;
       T* out = static_cast<T*>(a.out) + ((int64_t)(w.e.q0 + w.row0 + warp * 32) * a.heads + w.h) * a.D;
       const int warp_rows = min(32, w.rows - warp * 32);
@@ -294,7 +297,12 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
           const int from = span.lo - k0, width = min(span.hi - k0, extent) - from, sink = min(span.s - k0, extent);
 #pragma unroll
           for (int c = 0; c < kTile / 32; ++c)
-            if (act >> c & 1) hide(s + 32 * c, 32 * c, from, width, sink);
+            if (act >> c & 1) {
+              const uint32_t see = bits(from - 32 * c, from + width - 32 * c) | bits(0, sink - 32 * c);
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (!(see >> i & 1)) s[32 * c + i] = -INFINITY;
+            }
         }
         float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
@@ -382,18 +390,26 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
       }
       tc_fence_before();
       __syncwarp();
-      constexpr int kRowsAtOnce = 32 / (DP / 8);
-      const int chunk = lane % (DP / 8);
-      if (chunk * 8 < a.D)
-        for (int r = lane / (DP / 8); r < warp_rows; r += kRowsAtOnce) {
-          const int rr = warp * 32 + r;
-          *reinterpret_cast<uint4*>(out + (int64_t)r * a.heads * a.D + chunk * 8) = *reinterpret_cast<const uint4*>(
-              stage + (chunk >> 3) * kPanel + rr * 128 + (((chunk & 7) ^ (rr & 7)) << 4));
-        }
-      if (lane < warp_rows && a.lse)
-        a.lse[(int64_t)w.h * a.n_q + qrow] = l == 0.f ? -INFINITY : fmaf(m_used, a.scale, logf(l));
+      constexpr int kChunks = DP / 8, kRowsAtOnce = 32 / kChunks;
+      const int chunk = lane % kChunks, first = lane / kChunks;
+      uint4 v[kChunks];
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) {
+        const int rr = warp * 32 + first + i * kRowsAtOnce;
+        v[i] = *reinterpret_cast<const uint4*>(stage + (chunk >> 3) * kPanel + rr * 128 +
+                                               (((chunk & 7) ^ (rr & 7)) << 4));
+      }
       fence_async_smem();  // these reads and writes before the next tile's load
       mbar_arrive(q_empty + 8 * qs);
+      if (chunk * 8 < a.D) {
+        const int64_t row_values = (int64_t)a.heads * a.D;
+        T* to = out + first * row_values + chunk * 8;
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i)
+          if (first + i * kRowsAtOnce < warp_rows) *reinterpret_cast<uint4*>(to + i * kRowsAtOnce * row_values) = v[i];
+      }
+      if (lane < warp_rows && a.lse)
+        a.lse[(int64_t)w.h * a.n_q + qrow] = l == 0.f ? -INFINITY : fmaf(m_used, a.scale, logf(l));
     }
   }
   if (a.zero_tail) zero_rows(a.out, a.B > 0 ? a.q_offsets[a.B] : 0, a.n_q, (int64_t)a.heads * a.D);

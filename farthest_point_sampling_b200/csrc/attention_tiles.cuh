@@ -21,6 +21,27 @@ struct TileItem {
   int pad[3];
 };
 
+// A block's walk over (tile, head) items, heads first: `step` items at a time
+// without a division.
+struct ItemWalk {
+  int tile, h, step_tiles, step_heads, heads, n_tiles;
+  __device__ __forceinline__ ItemWalk(int heads_, int n_tiles_) : heads(heads_), n_tiles(n_tiles_) {
+    tile = blockIdx.x / heads;
+    h = blockIdx.x - tile * heads;
+    step_tiles = gridDim.x / heads;
+    step_heads = gridDim.x - step_tiles * heads;
+  }
+  __device__ __forceinline__ bool more() const { return tile < n_tiles; }
+  __device__ __forceinline__ void advance() {
+    tile += step_tiles;
+    h += step_heads;
+    if (h >= heads) {
+      h -= heads;
+      ++tile;
+    }
+  }
+};
+
 // Tiles of both lists: sum of ceil(n_b / kTile) <= n / kTile + B.
 __host__ __device__ inline int64_t max_tiles(int64_t n, int B) { return n / kTile + B; }
 

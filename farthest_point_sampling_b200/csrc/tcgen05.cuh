@@ -38,13 +38,13 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
 // has given up (*abort), it returns false and the caller leaves its loop.
 constexpr int kWaitPolls = 1 << 21;
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
-  if (mbar_try(bar, parity)) return true;
-  for (int i = 0; i < kWaitPolls; ++i) {
-    if (mbar_try(bar, parity)) return true;
-    if ((i & 63) == 63 && *abort) return false;
-  }
-  *abort = 1;
-  return false;
+#pragma unroll 1
+  for (int i = 0; !mbar_try(bar, parity); ++i)
+    if (i == kWaitPolls || *abort) {
+      *abort = 1;
+      return false;
+    }
+  return true;
 }
 
 // Registers of a warp group (all its warps execute this).  The shares of a
@@ -148,11 +148,13 @@ __device__ __forceinline__ void tmem_wait_ld16(uint32_t* r) {
 
 // Shared-memory operand in 128-byte swizzled panels: rows of 128 bytes (64
 // 16-bit values), 8-row groups 1024 bytes apart, panels of 64 values
-// `panel_bytes` apart.  Read along the rows (K-major) a step of 16 values is
-// 32 bytes; read across them (MN-major) a step of 16 rows is 2048 bytes.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t panel_bytes) {
-  return (uint64_t)((addr & 0x3ffff) >> 4) | ((uint64_t)(panel_bytes >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+// `panel_bytes` apart.  The low word of its descriptor holds the address and
+// the panel stride in units of 16 bytes, so a step adds bytes / 16 to it: 2
+// for 16 values along the rows (K-major), 128 for 16 rows (MN-major); the
+// high word is the same for all.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t smem_desc(uint32_t addr, uint32_t panel_bytes) {
+  return (addr >> 4) | ((panel_bytes >> 4) << 16);
 }
 
 // Instruction descriptor: 16-bit operands, float32 accumulator, M = 128.
@@ -161,20 +163,22 @@ __host__ __device__ constexpr uint32_t mma_desc(bool bf16, bool a_mn, bool b_mn,
          ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
-// D[tmem] (+)= A[smem] B[smem], by one thread.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+// D[tmem] (+)= A[smem] B[smem], by one thread; a and b are low descriptor words.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(kDescHigh)
       : "memory");
 }
 // D[tmem] (+)= A[tmem] B[smem].
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "mov.b64 y, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(kDescHigh)
       : "memory");
 }
 // Arrives on `bar` once every tcgen05 operation this thread issued before is done.
