@@ -6,13 +6,14 @@
 //   P = exp2(c S - c m),  l <- l f + sum P,  O <- O f + P V,  f = exp2(c (m_old - m)),
 // c = scale log2(e), and the output is O / l, lse = m scale + ln l.
 //
-// A block is six warps: one thread loads Q, K and V tiles with TMA, one issues
-// the tcgen05 products, and four warps do the softmax with one query row per
-// thread (a TMEM lane), so no row crosses threads.  S goes to TMEM, P comes
-// back over it as 16-bit operand A of the second product, O stays in TMEM
-// until the item ends.  Two blocks share an SM: while one's softmax runs, the
-// other's products do.  Blocks are persistent; the loader runs ahead into the
-// next items.
+// A block is ten warps: one thread loads Q, K and V tiles with TMA, one issues
+// the tcgen05 products, and eight warps do the softmax with two threads per
+// query row (a TMEM lane), each for half of a tile's keys; they exchange the
+// row's maximum once per tile and its sum once per item.  S goes to TMEM, P
+// comes back over it as 16-bit operand A of the second product, O stays in
+// TMEM until the item ends.  Two blocks share an SM: while one's softmax runs,
+// the other's products do.  Blocks are persistent; the loader runs ahead into
+// the next items.
 //
 // Rounding: P is rounded to the input type for P V; l sums the unrounded
 // values.  O is rescaled only when m grows by more than 8 / log2 units, which
@@ -30,20 +31,13 @@ namespace fpstok {
 
 namespace {
 
-constexpr int kSoftmaxWarps = 4;
-constexpr int kFwdThreads = 256;  // the softmax warp group, and one of a loading and an issuing warp (two idle)
-constexpr int kSoftmaxRegs = 208, kOtherRegs = 48;  // a thread's share after the split; launched with 128 each
+constexpr int kSoftmaxWarps = 8;
+constexpr int kSoftmaxThreads = 32 * kSoftmaxWarps;
+constexpr int kFwdThreads = kSoftmaxThreads + 64;
+constexpr int kHalf = kTile / 2;  // keys of a tile that one of a row's two threads takes
 constexpr int kPanel = kTile * 128;  // bytes of a 128-row panel of 64 values
 constexpr uint32_t kTmemColumns = 256;
 constexpr uint32_t kColO = 128;  // S (and P over it) in columns 0 .. 127
-
-template <int DP>
-struct FwdShape {
-  static constexpr int kPanels = DP / 64;
-  static constexpr int kStages = DP == 64 ? 2 : 1;  // of Q, K and V each: 96 KB either way, two blocks per SM
-  static constexpr uint32_t kTileBytes = kPanels * kPanel;
-  static constexpr size_t kSmem = 1024 + 3 * kStages * kTileBytes + 256;
-};
 
 struct FwdArgs {
   int64_t n_q;
@@ -58,22 +52,39 @@ struct FwdArgs {
   WsHeader* hdr;
 };
 
-// What every role of the block computes alike for one item.
+// One work item as the loading thread hands it to the others, through a ring
+// in shared memory.
 struct FwdItem {
-  TileItem e;
-  int h, row0, rows, p0;  // head; first query of the tile in its event, queries of the tile, position of the first
+  int count;            // key tiles; -1 ends the work
+  int h;                // head
+  int q_row, rows, p0;  // first query row, queries of the tile, position of the first
+  int k_row, nk;        // the event's first key row, its keys
   KeyTiles<kTile> keys;
 };
+constexpr int kItemRing = 2;
+template <bool kMasked>
 __device__ __forceinline__ FwdItem fwd_item(const FwdArgs& a, int h, const TileItem& e) {
   FwdItem w;
   w.h = h;
-  w.e = e;
-  w.row0 = w.e.t * kTile;
-  w.rows = min(kTile, w.e.nq - w.row0);
-  w.p0 = w.row0 + w.e.nk - w.e.nq;
-  w.keys = key_tiles<kTile>(a.mask, w.p0, w.p0 + w.rows - 1, w.e.nk);
+  w.q_row = e.q0 + e.t * kTile;
+  w.rows = min(kTile, e.nq - e.t * kTile);
+  w.p0 = e.t * kTile + e.nk - e.nq;
+  w.k_row = e.k0;
+  w.nk = e.nk;
+  w.keys = kMasked ? key_tiles<kTile>(a.mask, w.p0, w.p0 + w.rows - 1, e.nk)
+                   : KeyTiles<kTile>{0, 0, e.nk, 0, (e.nk + kTile - 1) / kTile};
+  w.count = w.keys.count;
   return w;
 }
+
+template <int DP>
+struct FwdShape {
+  static constexpr int kPanels = DP / 64;
+  static constexpr int kStages = DP == 64 ? 2 : 1;  // of Q, K and V each: 96 KB either way, two blocks per SM
+  static constexpr uint32_t kTileBytes = kPanels * kPanel;
+  static constexpr size_t kSmem =
+      1024 + 3 * kStages * kTileBytes + 4 * kTile * sizeof(float) + kItemRing * sizeof(FwdItem) + 256;
+};
 
 // Bits lo .. hi - 1 of a word, bounds clipped to 0 .. 32.
 __device__ __forceinline__ uint32_t bits(int lo, int hi) {
@@ -82,7 +93,8 @@ __device__ __forceinline__ uint32_t bits(int lo, int hi) {
   return hi <= lo ? 0u : (0xffffffffu >> (32 - hi)) & (0xffffffffu << lo);
 }
 
-template <typename T, int DP>
+// kMasked: a causal or windowed call; without, every query sees its whole event.
+template <typename T, int DP, bool kMasked>
 __global__ void __launch_bounds__(kFwdThreads, 2)
     k_attn_forward(const FwdArgs a, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                    const __grid_constant__ CUtensorMap map_v) {
@@ -93,19 +105,23 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
   uint8_t* s_q = s_base;
   uint8_t* s_k = s_q + Sh::kStages * Sh::kTileBytes;
   uint8_t* s_v = s_k + Sh::kStages * Sh::kTileBytes;
-  uint64_t* s_bar = reinterpret_cast<uint64_t*>(s_v + Sh::kStages * Sh::kTileBytes);
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_bar + 16);
+  float* s_pair = reinterpret_cast<float*>(s_v + Sh::kStages * Sh::kTileBytes);  // [parity][half][row]
+  FwdItem* s_item = reinterpret_cast<FwdItem*>(s_pair + 4 * kTile);
+  uint64_t* s_bar = reinterpret_cast<uint64_t*>(s_item + kItemRing);
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_bar + 24);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   const uint32_t bars = smem_u32(s_bar);
   const uint32_t q_full = bars, k_full = bars + 16, k_empty = bars + 32, v_full = bars + 48, v_empty = bars + 64,
-                 s_full = bars + 80, o_full = bars + 88, drain = bars + 96, p_ready = bars + 104, q_empty = bars + 112;
+                 s_full = bars + 80, o_full = bars + 88, drain = bars + 96, item_full = bars + 104,
+                 item_empty = bars + 120, p_ready = bars + 136, q_empty = bars + 144, pair = bars + 160;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 13; ++i) mbar_init(bars + 8 * i, 1);
-    mbar_init(p_ready, 32 * kSoftmaxWarps);
-    mbar_init(q_empty, 32 * kSoftmaxWarps);
-    mbar_init(q_empty + 8, 32 * kSoftmaxWarps);
+    for (int i = 0; i < 15; ++i) mbar_init(bars + 8 * i, 1);
+    for (int i = 0; i < kItemRing; ++i) mbar_init(item_empty + 8 * i, kSoftmaxThreads + 1);
+    mbar_init(p_ready, kSoftmaxThreads);
+    for (int i = 0; i < 2; ++i) mbar_init(q_empty + 8 * i, kSoftmaxThreads);
+    for (int i = 0; i < 4; ++i) mbar_init(pair + 8 * i, 64);
     *s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     tma_prefetch_map(&map_q);
@@ -118,84 +134,96 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  // every role walks the block's items, and reads the next one's entry while it works on one
-  ItemWalk walk(a.heads, a.hdr->n_items[kQueryTiles]);
-  TileItem next = a.items[walk.more() ? walk.tile : 0];
 
-  if (warp >= kSoftmaxWarps) {
-    regs_down<kOtherRegs>();
-    if (warp == kSoftmaxWarps && lane == 0) {
-      // ------------------------------------------------ loads
-      int n = 0, nq = 0;  // key tiles and query tiles loaded so far
-      bool ok = true;
-      while (walk.more() && ok) {
-        const FwdItem w = fwd_item(a, walk.h, next);
+  if (warp == kSoftmaxWarps) {
+    // ------------------------------------------------ items and loads
+    if (lane == 0) {
+      ItemWalk walk(a.heads, a.hdr->n_items[kQueryTiles]);
+      TileItem next = a.items[walk.more() ? walk.tile : 0];
+      int i = 0, n = 0, nq = 0;  // items handed out, key tiles and query tiles loaded so far
+      for (bool more = true; more; ++i) {
+        const int slot = i % kItemRing;
+        if (i >= kItemRing && !mbar_wait(item_empty + 8 * slot, ((i / kItemRing) - 1) & 1, s_abort)) break;
+        more = walk.more();
+        if (!more) {
+          s_item[slot].count = -1;
+          mbar_arrive(item_full + 8 * slot);
+          break;
+        }
+        const FwdItem w = fwd_item<kMasked>(a, walk.h, next);
         walk.advance();
         if (walk.more()) next = a.items[walk.tile];
-        if (w.keys.count == 0) continue;
+        s_item[slot] = w;
+        mbar_arrive(item_full + 8 * slot);
+        if (w.count == 0) continue;
         const int qs = nq % Sh::kStages;
-        if (nq >= Sh::kStages && !(ok = mbar_wait(q_empty + 8 * qs, ((nq / Sh::kStages) - 1) & 1, s_abort))) break;
+        if (nq >= Sh::kStages && !mbar_wait(q_empty + 8 * qs, ((nq / Sh::kStages) - 1) & 1, s_abort)) break;
         const int q_boxes = (w.rows + 63) / 64;
         mbar_expect(q_full + 8 * qs, q_boxes * 8192 * Sh::kPanels);
 #pragma unroll 1
-        for (int p = 0; p < Sh::kPanels; ++p)
-#pragma unroll 1
-          for (int i = 0; i < q_boxes; ++i)
-            tma_load(smem_u32(s_q) + qs * Sh::kTileBytes + p * kPanel + i * 8192, &map_q, q_full + 8 * qs, p * 64, w.h,
-                     w.e.q0 + w.row0 + i * 64);
+        for (int b = 0; b < q_boxes; ++b)
+#pragma unroll
+          for (int p = 0; p < Sh::kPanels; ++p)
+            tma_load(smem_u32(s_q) + qs * Sh::kTileBytes + p * kPanel + b * 8192, &map_q, q_full + 8 * qs, p * 64, w.h,
+                     w.q_row + b * 64);
         ++nq;
         const int g = w.h / a.group;
-        for (int j = 0; j < w.keys.count; ++j, ++n) {
+        for (int j = 0; j < w.count; ++j, ++n) {
           const int st = n % Sh::kStages;
           const uint32_t round = ((n / Sh::kStages) - 1) & 1;
           const int boxes = (w.keys.extent(j) + 63) / 64;
-          const int krow = w.e.k0 + w.keys.start(j);
-          if (n >= Sh::kStages && !(ok = mbar_wait(k_empty + 8 * st, round, s_abort))) break;
+          const int krow = w.k_row + w.keys.start(j);
+          if (n >= Sh::kStages && !(more = mbar_wait(k_empty + 8 * st, round, s_abort))) break;
           mbar_expect(k_full + 8 * st, boxes * 8192 * Sh::kPanels);
 #pragma unroll 1
-          for (int p = 0; p < Sh::kPanels; ++p)
-#pragma unroll 1
-            for (int i = 0; i < boxes; ++i)
-              tma_load(smem_u32(s_k) + st * Sh::kTileBytes + p * kPanel + i * 8192, &map_k, k_full + 8 * st, p * 64, g,
-                       krow + i * 64);
-          if (n >= Sh::kStages && !(ok = mbar_wait(v_empty + 8 * st, round, s_abort))) break;
+          for (int b = 0; b < boxes; ++b)
+#pragma unroll
+            for (int p = 0; p < Sh::kPanels; ++p)
+              tma_load(smem_u32(s_k) + st * Sh::kTileBytes + p * kPanel + b * 8192, &map_k, k_full + 8 * st, p * 64, g,
+                       krow + b * 64);
+          if (n >= Sh::kStages && !(more = mbar_wait(v_empty + 8 * st, round, s_abort))) break;
           mbar_expect(v_full + 8 * st, boxes * 8192 * Sh::kPanels);
 #pragma unroll 1
-          for (int p = 0; p < Sh::kPanels; ++p)
-#pragma unroll 1
-            for (int i = 0; i < boxes; ++i)
-              tma_load(smem_u32(s_v) + st * Sh::kTileBytes + p * kPanel + i * 8192, &map_v, v_full + 8 * st, p * 64, g,
-                       krow + i * 64);
+          for (int b = 0; b < boxes; ++b)
+#pragma unroll
+            for (int p = 0; p < Sh::kPanels; ++p)
+              tma_load(smem_u32(s_v) + st * Sh::kTileBytes + p * kPanel + b * 8192, &map_v, v_full + 8 * st, p * 64, g,
+                       krow + b * 64);
         }
       }
       // after a wait that gave up: this thread's copies still in flight land first
       if (*s_abort) {
         volatile int none = 0;
-        for (int i = 0; i < Sh::kStages; ++i) {
-          const int lq = nq - 1 - i, lk = n - i;  // tile n may have its keys loading, not its values
+        for (int b = 0; b < Sh::kStages; ++b) {
+          const int lq = nq - 1 - b, lk = n - b;  // tile n may have its keys loading, not its values
           if (lq >= 0) mbar_wait(q_full + 8 * (lq % Sh::kStages), (lq / Sh::kStages) & 1, &none);
           if (lk >= 0) mbar_wait(k_full + 8 * (lk % Sh::kStages), (lk / Sh::kStages) & 1, &none);
           if (lk >= 1) mbar_wait(v_full + 8 * ((lk - 1) % Sh::kStages), ((lk - 1) / Sh::kStages) & 1, &none);
         }
       }
-    } else if (warp == kSoftmaxWarps + 1 && lane == 0) {
-      // ------------------------------------------------ products
+    }
+  } else if (warp == kSoftmaxWarps + 1) {
+    // ------------------------------------------------ products
+    if (lane == 0) {
       int n = 0, nq = 0;
       const int d_steps = (a.D + 15) / 16;
       const uint32_t pv_desc = mma_desc(kBf16, false, true, d_steps * 16);
       bool ok = true;
-      while (walk.more() && ok) {
-        const FwdItem w = fwd_item(a, walk.h, next);
-        walk.advance();
-        if (walk.more()) next = a.items[walk.tile];
-        if (w.keys.count == 0) continue;
+      for (int i = 0; ok; ++i) {
+        const int slot = i % kItemRing;
+        if (!(ok = mbar_wait(item_full + 8 * slot, (i / kItemRing) & 1, s_abort))) break;
+        const int count = s_item[slot].count;
+        const KeyTiles<kTile> keys = s_item[slot].keys;
+        mbar_arrive(item_empty + 8 * slot);
+        if (count < 0) break;
+        if (count == 0) continue;
         const int qs = nq % Sh::kStages;
         const uint32_t q = smem_desc(smem_u32(s_q) + qs * Sh::kTileBytes, kPanel);
         if (!(ok = mbar_wait(q_full + 8 * qs, (nq / Sh::kStages) & 1, s_abort))) break;
-        for (int j = 0; j <= w.keys.count; ++j) {
+        for (int j = 0; j <= count; ++j) {
           if (j > 0) {  // O += P V of tile j - 1
             const int m = n + j - 1, st = m % Sh::kStages;
-            const int steps = (w.keys.extent(j - 1) + 15) / 16;
+            const int steps = (keys.extent(j - 1) + 15) / 16;
             if (!(ok = mbar_wait(v_full + 8 * st, (m / Sh::kStages) & 1, s_abort))) break;
             if (!(ok = mbar_wait(p_ready, m & 1, s_abort))) break;
             tc_fence_after();
@@ -204,11 +232,11 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
             for (int ks = 0; ks < kTile / 16; ++ks)
               if (ks < steps) mma_ts(tmem + kColO, tmem + ks * 8, v + ks * 128, pv_desc, ks > 0 || j > 1);
             mma_commit(v_empty + 8 * st);
-            if (j == w.keys.count) mma_commit(o_full);
+            if (j == count) mma_commit(o_full);
           }
-          if (j < w.keys.count) {  // S = Q K^T of tile j; over P, which the product before has read
+          if (j < count) {  // S = Q K^T of tile j; over P, which the product before has read
             const int m = n + j, st = m % Sh::kStages;
-            const int cols = (w.keys.extent(j) + 15) / 16 * 16;
+            const int cols = (keys.extent(j) + 15) / 16 * 16;
             if (!(ok = mbar_wait(k_full + 8 * st, (m / Sh::kStages) & 1, s_abort))) break;
             tc_fence_after();
             const uint32_t k = smem_desc(smem_u32(s_k) + st * Sh::kTileBytes, kPanel);
@@ -222,8 +250,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
             mma_commit(s_full);
           }
         }
-        if (!ok) break;
-        n += w.keys.count;
+        n += count;
         ++nq;
       }
       if (*s_abort) {  // products in flight end before TMEM is freed
@@ -234,87 +261,102 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     }
   } else {
     // ------------------------------------------------ softmax
-    regs_up<kSoftmaxRegs>();
-    int n = 0, nq = 0;  // key tiles and query tiles so far
-    const int row = threadIdx.x;
-    const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
-    const float2 scale2 = make_float2(a.scale_log2, a.scale_log2);
+    int n = 0, nq = 0, x = 0;  // key tiles, query tiles and exchanges so far
+    const int half = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
     bool ok = true;
-    while (walk.more() && ok) {
-      const FwdItem w = fwd_item(a, walk.h, next);
-      walk.advance();
-      if (walk.more()) next = a.items[walk.tile];
-      const int64_t qrow = (int64_t)w.e.q0 + w.row0 + row;
-      T* out = static_cast<T*>(a.out) + ((int64_t)(w.e.q0 + w.row0 + warp * 32) * a.heads + w.h) * a.D;
-      const int warp_rows = min(32, w.rows - warp * 32);
-      if (w.keys.count == 0) {  // nothing to see
-        for (int r = lane; r < warp_rows; r += 32) {
-          for (int c = 0; c < a.D; c += 8)
-            *reinterpret_cast<uint4*>(out + (int64_t)r * a.heads * a.D + c) = make_uint4(0, 0, 0, 0);
-          if (a.lse) a.lse[(int64_t)w.h * a.n_q + qrow] = -INFINITY;
-        }
-        continue;
-      }
-      const RowSpan span = row_span(a.mask, w.p0 + row, w.e.nk);
-      // keys that some row of this warp sees
-      const RowSpan warp_lo = row_span(a.mask, w.p0 + warp * 32, w.e.nk);
-      const RowSpan warp_hi = row_span(a.mask, w.p0 + min(warp * 32 + 31, w.rows - 1), w.e.nk);
+    // The other thread's value of this row.  Two buffers: a thread writes one
+    // again only after both have been past the exchange in between.
+    const auto exchange = [&](float v, float* other) {
+      float* at = s_pair + (x & 1) * 2 * kTile + row;
+      at[half * kTile] = v;
+      mbar_arrive(pair + 8 * quarter);
+      if (!mbar_wait(pair + 8 * quarter, x & 1, s_abort)) return false;
+      *other = at[(half ^ 1) * kTile];
+      ++x;
+      return true;
+    };
+    for (int i = 0; ok; ++i) {
+      const int slot = i % kItemRing;
+      if (!(ok = mbar_wait(item_full + 8 * slot, (i / kItemRing) & 1, s_abort))) break;
+      const FwdItem& w = s_item[slot];  // read where it is needed: it stays until this thread lets go of the slot
+      const int count = w.count;
+      if (count < 0) break;
+      const int warp_rows = min(32, w.rows - quarter * 32);
       float m_used = -INFINITY, l = 0.f;
-      for (int j = 0; j < w.keys.count; ++j, ++n) {
-        const int st = n % Sh::kStages;
+      for (int j = 0; j < count; ++j, ++n) {
         const int k0 = w.keys.start(j), extent = w.keys.extent(j);
         const int odd = extent & 15;
         if (odd) {
           // Keys past the tile's last inside the product's step of 16: their
           // weights are 0, and their values must be finite for 0 to stay 0.
+          const int st = n % Sh::kStages;
           if (!(ok = mbar_wait(v_full + 8 * st, (n / Sh::kStages) & 1, s_abort))) break;
           uint8_t* v_tile = s_v + st * Sh::kTileBytes;
-          for (int e = threadIdx.x; e < (16 - odd) * 8 * Sh::kPanels; e += 32 * kSoftmaxWarps) {
+#pragma unroll 1
+          for (int e = threadIdx.x; e < (16 - odd) * 8 * Sh::kPanels; e += kSoftmaxThreads) {
             const int r = extent + e / (8 * Sh::kPanels), c = e % (8 * Sh::kPanels);
             *reinterpret_cast<uint4*>(v_tile + (c >> 3) * kPanel + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
           }
           fence_async_smem();
         }
-        // 32-column chunks of the tile that some row of the warp sees
-        int act = 0;
+        // this thread's two 32-key chunks: which of them some row of the warp
+        // sees, and what this row sees there
+        const int c0 = half * kHalf;
+        bool act[2];
+        bool masked = (extent & 31) != 0;
+        uint32_t see[2];
 #pragma unroll
-        for (int c = 0; c < kTile / 32; ++c) {
-          const int first = k0 + 32 * c, last = k0 + min(32 * c + 31, extent - 1);
-          if (32 * c < extent && warp_rows > 0 &&
-              ((last >= warp_lo.lo && first < warp_hi.hi) || first < warp_hi.s))
-            act |= 1 << c;
+        for (int c = 0; c < 2; ++c) {
+          act[c] = c0 + 32 * c < extent && warp_rows > 0;
+          see[c] = bits(0, extent - c0 - 32 * c);
         }
-        const bool masked = (extent & 31) != 0 || tile_masked(a.mask, w.p0, w.p0 + w.rows - 1, k0, k0 + extent);
-        if (!(ok = mbar_wait(s_full, n & 1, s_abort))) break;
-        tc_fence_after();
-        float s[kTile];
+        if constexpr (kMasked) {
+          if (tile_masked(a.mask, w.p0, w.p0 + w.rows - 1, k0, k0 + extent)) {
+            masked = true;
+            const RowSpan lo = row_span(a.mask, w.p0 + quarter * 32, w.nk);
+            const RowSpan hi = row_span(a.mask, w.p0 + min(quarter * 32 + 31, w.rows - 1), w.nk);
+            const RowSpan own = row_span(a.mask, w.p0 + row, w.nk);
 #pragma unroll
-        for (int c = 0; c < kTile / 32; ++c)
-          if (act >> c & 1) tmem_ld32(lanes + 32 * c, reinterpret_cast<uint32_t*>(s + 32 * c));
-#pragma unroll
-        for (int c = 0; c < kTile / 32; ++c) tmem_wait_ld32(reinterpret_cast<uint32_t*>(s + 32 * c));
-        if (masked) {
-          const int from = span.lo - k0, width = min(span.hi - k0, extent) - from, sink = min(span.s - k0, extent);
-#pragma unroll
-          for (int c = 0; c < kTile / 32; ++c)
-            if (act >> c & 1) {
-              const uint32_t see = bits(from - 32 * c, from + width - 32 * c) | bits(0, sink - 32 * c);
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (!(see >> i & 1)) s[32 * c + i] = -INFINITY;
-            }
-        }
-        float m0 = -INFINITY, m1 = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < kTile / 32; ++c)
-          if (act >> c & 1) {
-#pragma unroll
-            for (int i = 32 * c; i < 32 * c + 32; i += 4) {
-              m0 = max3f(m0, s[i], s[i + 1]);
-              m1 = max3f(m1, s[i + 2], s[i + 3]);
+            for (int c = 0; c < 2; ++c) {
+              const int first = k0 + c0 + 32 * c;
+              act[c] = act[c] && ((first + 31 >= lo.lo && first < hi.hi) || first < hi.s);
+              see[c] &= bits(own.lo - first, own.hi - first) | bits(0, own.s - first);
             }
           }
-        const float top = fmaxf(m0, m1);
+        }
+        if (!(ok = mbar_wait(s_full, n & 1, s_abort))) break;
+        tc_fence_after();
+        float s[kHalf];
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          tmem_ld32(lanes + c0 + 32 * c, reinterpret_cast<uint32_t*>(s + 32 * c));
+        tmem_wait_ld32(reinterpret_cast<uint32_t*>(s));
+        tmem_wait_ld32(reinterpret_cast<uint32_t*>(s + 32));
+        if (masked) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            if (act[c]) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (!(see[c] >> k & 1)) s[32 * c + k] = -INFINITY;
+            }
+        }
+        float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          if (act[c]) {
+#pragma unroll
+            for (int k = 32 * c; k < 32 * c + 32; k += 8) {
+              m0 = max3f(m0, s[k], s[k + 1]);
+              m1 = max3f(m1, s[k + 2], s[k + 3]);
+              m2 = max3f(m2, s[k + 4], s[k + 5]);
+              m3 = max3f(m3, s[k + 6], s[k + 7]);
+            }
+          }
+        float top = fmaxf(max3f(m0, m1, m2), m3), theirs;
+        if (!(ok = exchange(top, &theirs))) break;
+        top = fmaxf(top, theirs);
         if (j == 0) {
           m_used = top;
         } else {
@@ -325,36 +367,37 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
             if (grow) m_used = top;
             l *= f;
 #pragma unroll 1
-            for (int c = 0; c < DP; c += 16) {
-              uint32_t o[16];
-              tmem_ld16(lanes + kColO + c, o);
-              tmem_wait_ld16(o);
+            for (int c = half * (DP / 2); c < (half + 1) * (DP / 2); c += 8) {
+              uint32_t o[8];
+              tmem_ld8(lanes + kColO + c, o);
+              tmem_wait_ld8(o);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-              tmem_st16(lanes + kColO + c, o);
+              for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+              tmem_st8(lanes + kColO + c, o);
             }
           }
         }
         const float base = m_used == -INFINITY ? 0.f : m_used * a.scale_log2;
-        const float2 base2 = make_float2(-base, -base);
+        const float2 base2 = make_float2(-base, -base), scale2 = make_float2(a.scale_log2, a.scale_log2);
         float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int c = 0; c < kTile / 32; ++c) {
+        for (int c = 0; c < 2; ++c) {
           uint32_t pk[16];
-          if (act >> c & 1) {
+          if (act[c]) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              float2 e = fma2(make_float2(s[32 * c + i], s[32 * c + i + 1]), scale2, base2);
+            for (int k = 0; k < 32; k += 2) {
+              float2 e = fma2(make_float2(s[32 * c + k], s[32 * c + k + 1]), scale2, base2);
               e.x = exp2_approx(e.x);
               e.y = exp2_approx(e.y);
               sum = add2(sum, e);
-              pk[i / 2] = pack16<T>(e.x, e.y);
+              pk[k / 2] = pack16<T>(e.x, e.y);
             }
           } else {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) pk[i] = 0;
+            for (int k = 0; k < 16; ++k) pk[k] = 0;
           }
-          if (32 * c < extent) tmem_st16(lanes + 16 * c, pk);
+          // over scores that both threads have read before the exchange
+          if (c0 + 32 * c < extent) tmem_st16(lanes + (c0 + 32 * c) / 2, pk);
         }
         l += sum.x + sum.y;
         tmem_wait_st();
@@ -362,54 +405,70 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
         mbar_arrive(p_ready);
       }
       if (!ok) break;
+      const int64_t first_row = (int64_t)w.q_row + quarter * 32;
+      T* out = static_cast<T*>(a.out) + (first_row * a.heads + w.h) * a.D;
+      float* lse = a.lse && half == 0 ? a.lse + (int64_t)w.h * a.n_q + first_row : nullptr;
+      const int64_t row_values = (int64_t)a.heads * a.D;
+      mbar_arrive(item_empty + 8 * slot);
+      if (count == 0) {  // nothing to see
+        if (half == 0 && lane < warp_rows) {
+#pragma unroll 1
+          for (int c = 0; c < a.D; c += 8)
+            *reinterpret_cast<uint4*>(out + lane * row_values + c) = make_uint4(0, 0, 0, 0);
+          if (lse) lse[lane] = -INFINITY;
+        }
+        continue;
+      }
+      float theirs;
+      if (!(ok = exchange(l, &theirs))) break;
+      l += theirs;
       const int qs = nq % Sh::kStages;
       if (!(ok = mbar_wait(o_full, nq & 1, s_abort))) break;
       ++nq;
       tc_fence_after();
-      // O / l to the item's query tile in shared memory, which no product
-      // reads any more, then to memory with whole rows per instruction; a
-      // warp only touches its own rows.
+      // O / l, half of the columns each, to the item's query tile in shared
+      // memory, which no product reads any more, then to memory with whole
+      // sectors of 8 or 4 rows per instruction; a warp reads only what it wrote.
       const float inv = l == 0.f ? 0.f : 1.f / l;
       uint8_t* stage = s_q + qs * Sh::kTileBytes;
+      constexpr int kCols = DP / 2;
 #pragma unroll
-      for (int c = 0; c < DP; c += 32) {
+      for (int c = 0; c < kCols; c += 32) {
         uint32_t o[32];
-        tmem_ld32(lanes + kColO + c, o);
+        tmem_ld32(lanes + kColO + half * kCols + c, o);
         tmem_wait_ld32(o);
 #pragma unroll
-        for (int i = 0; i < 32; i += 8) {
+        for (int k = 0; k < 32; k += 8) {
           uint4 v;
           uint32_t* pv = reinterpret_cast<uint32_t*>(&v);
 #pragma unroll
           for (int q = 0; q < 4; ++q)
             pv[q] = l == 0.f ? 0u
-                             : pack16<T>(__uint_as_float(o[i + 2 * q]) * inv, __uint_as_float(o[i + 2 * q + 1]) * inv);
-          const int k = (c + i) / 8;
-          *reinterpret_cast<uint4*>(stage + (k >> 3) * kPanel + row * 128 + (((k & 7) ^ (row & 7)) << 4)) = v;
+                             : pack16<T>(__uint_as_float(o[k + 2 * q]) * inv, __uint_as_float(o[k + 2 * q + 1]) * inv);
+          const int at = (half * kCols + c + k) / 8;
+          *reinterpret_cast<uint4*>(stage + (at >> 3) * kPanel + row * 128 + (((at & 7) ^ (row & 7)) << 4)) = v;
         }
       }
       tc_fence_before();
       __syncwarp();
-      constexpr int kChunks = DP / 8, kRowsAtOnce = 32 / kChunks;
-      const int chunk = lane % kChunks, first = lane / kChunks;
+      constexpr int kChunks = kCols / 8, kRowsAtOnce = 32 / kChunks;
+      const int chunk = half * kChunks + lane % kChunks, first = lane / kChunks;
       uint4 v[kChunks];
 #pragma unroll
-      for (int i = 0; i < kChunks; ++i) {
-        const int rr = warp * 32 + first + i * kRowsAtOnce;
-        v[i] = *reinterpret_cast<const uint4*>(stage + (chunk >> 3) * kPanel + rr * 128 +
+      for (int k = 0; k < kChunks; ++k) {
+        const int rr = quarter * 32 + first + k * kRowsAtOnce;
+        v[k] = *reinterpret_cast<const uint4*>(stage + (chunk >> 3) * kPanel + rr * 128 +
                                                (((chunk & 7) ^ (rr & 7)) << 4));
       }
       fence_async_smem();  // these reads and writes before the next tile's load
       mbar_arrive(q_empty + 8 * qs);
       if (chunk * 8 < a.D) {
-        const int64_t row_values = (int64_t)a.heads * a.D;
         T* to = out + first * row_values + chunk * 8;
 #pragma unroll
-        for (int i = 0; i < kChunks; ++i)
-          if (first + i * kRowsAtOnce < warp_rows) *reinterpret_cast<uint4*>(to + i * kRowsAtOnce * row_values) = v[i];
+        for (int k = 0; k < kChunks; ++k)
+          if (first + k * kRowsAtOnce < warp_rows) *reinterpret_cast<uint4*>(to + k * kRowsAtOnce * row_values) = v[k];
       }
-      if (lane < warp_rows && a.lse)
-        a.lse[(int64_t)w.h * a.n_q + qrow] = l == 0.f ? -INFINITY : fmaf(m_used, a.scale, logf(l));
+      if (lse && lane < warp_rows) lse[lane] = l == 0.f ? -INFINITY : fmaf(m_used, a.scale, logf(l));
     }
   }
   if (a.zero_tail) zero_rows(a.out, a.B > 0 ? a.q_offsets[a.B] : 0, a.n_q, (int64_t)a.heads * a.D);
@@ -438,7 +497,7 @@ FwdWorkspace carve_forward(void* base, int64_t n_q, int B) {
   return w;
 }
 
-template <typename T, int DP>
+template <typename T, int DP, bool kMasked>
 cudaError_t run_forward(const AttnCall& c, const FwdWorkspace& ws, cudaStream_t s) {
   cudaError_t e = launch_attention_plan(c, ws.hdr, ws.items, nullptr, s);
   if (e != cudaSuccess || c.n_q == 0) return e;
@@ -464,7 +523,7 @@ cudaError_t run_forward(const AttnCall& c, const FwdWorkspace& ws, cudaStream_t 
   a.zero_tail = c.zero_tail;
   a.items = ws.items;
   a.hdr = ws.hdr;
-  const auto kernel = k_attn_forward<T, DP>;
+  const auto kernel = k_attn_forward<T, DP, kMasked>;
   constexpr int smem = (int)FwdShape<DP>::kSmem;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -484,15 +543,20 @@ cudaError_t run_forward(const AttnCall& c, const FwdWorkspace& ws, cudaStream_t 
   return cudaLaunchKernelEx(&cfg, kernel, a, map_q, map_k, map_v);
 }
 
+template <typename T>
+cudaError_t run_type(const AttnCall& c, const FwdWorkspace& ws, cudaStream_t s) {
+  if (c.mask.causal || c.mask.window >= 0)
+    return c.D <= 64 ? run_forward<T, 64, true>(c, ws, s) : run_forward<T, 128, true>(c, ws, s);
+  return c.D <= 64 ? run_forward<T, 64, false>(c, ws, s) : run_forward<T, 128, false>(c, ws, s);
+}
+
 }  // namespace
 
 size_t attention_forward_bytes(int64_t n_q, int B) { return carve_forward(nullptr, n_q, B).bytes; }
 
 cudaError_t launch_attention_forward(const AttnCall& c, void* workspace, cudaStream_t s) {
   const FwdWorkspace ws = carve_forward(workspace, c.n_q, c.B);
-  if (c.dtype == FPS_DTYPE_BF16)
-    return c.D <= 64 ? run_forward<__nv_bfloat16, 64>(c, ws, s) : run_forward<__nv_bfloat16, 128>(c, ws, s);
-  return c.D <= 64 ? run_forward<__half, 64>(c, ws, s) : run_forward<__half, 128>(c, ws, s);
+  return c.dtype == FPS_DTYPE_BF16 ? run_type<__nv_bfloat16>(c, ws, s) : run_type<__half>(c, ws, s);
 }
 
 }  // namespace fpstok
