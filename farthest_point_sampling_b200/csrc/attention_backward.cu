@@ -52,6 +52,7 @@ struct BwdArgs {
   void* d2;      // dV
   const int64_t* offsets;  // of the kept rows
   int B;
+  bool sectors;  // every gradient row starts on a 32-byte sector, and ends on one
   const TileItem* items;
   WsHeader* hdr;
 };
@@ -136,30 +137,14 @@ __device__ __forceinline__ float2 unpack16<__half>(uint32_t v) {
   return __half22float2(*reinterpret_cast<__half2*>(&v));
 }
 
-// One accumulator row of DP columns to global memory, scaled and rounded.
+// One gradient row from its accumulator, or zeros where no tile was seen.
 template <typename T, int DP>
-__device__ __forceinline__ void store_row(uint32_t acc, bool filled, bool live, float f, T* to, int D) {
+__device__ __forceinline__ void gradient_row(uint32_t acc, bool filled, bool live, float f, T* to, int D, bool sectors) {
+  if (filled) {
+    store_row<T, DP>(acc, live, f, to, D, sectors);
+  } else if (live) {
 #pragma unroll 1
-  for (int c = 0; c < DP; c += 32) {
-    uint32_t o[32];
-    if (filled) {
-      tmem_ld32(acc + c, o);
-      tmem_wait_ld32(o);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) o[i] = 0;
-    }
-    if (!live) continue;
-#pragma unroll
-    for (int i = 0; i < 32; i += 8)
-      if (c + i < D) {
-        uint4 v;
-        uint32_t* pv = reinterpret_cast<uint32_t*>(&v);
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          pv[q] = pack16<T>(__uint_as_float(o[i + 2 * q]) * f, __uint_as_float(o[i + 2 * q + 1]) * f);
-        *reinterpret_cast<uint4*>(to + c + i) = v;
-      }
+    for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4*>(to + c) = make_uint4(0, 0, 0, 0);
   }
 }
 
@@ -471,9 +456,9 @@ __global__ void __launch_bounds__(BwdShape<DP, kGroups, kKeys>::kThreads, BwdSha
       }
       const int64_t at = (((int64_t)(kKeys ? w.e.k0 : w.e.q0) + w.row0 + row) * (kKeys ? a.kv_heads : a.heads) + w.h) * a.D;
       if (kGroups == 1 || g == 0)
-        store_row<T, DP>(lanes + Sh::kColAcc, w.count > 0, live, a.scale, static_cast<T*>(a.d1) + at, a.D);
+        gradient_row<T, DP>(lanes + Sh::kColAcc, w.count > 0, live, a.scale, static_cast<T*>(a.d1) + at, a.D, a.sectors);
       if (kKeys && g == kGroups - 1)
-        store_row<T, DP>(lanes + Sh::kColAcc + DP, w.count > 0, live, 1.f, static_cast<T*>(a.d2) + at, a.D);
+        gradient_row<T, DP>(lanes + Sh::kColAcc + DP, w.count > 0, live, 1.f, static_cast<T*>(a.d2) + at, a.D, a.sectors);
       if (w.count) {
         tc_fence_before();
         mbar_arrive(acc_empty);
@@ -571,6 +556,8 @@ cudaError_t run_backward(const AttnCall& c, const BwdWorkspace& ws, cudaStream_t
   a.delta = ws.delta;
   a.B = c.B;
   a.hdr = ws.hdr;
+  a.sectors = ((reinterpret_cast<uintptr_t>(c.dq) | reinterpret_cast<uintptr_t>(c.dk) | reinterpret_cast<uintptr_t>(c.dv)) &
+               31) == 0 && c.D % 16 == 0;
   if (c.n_q > 0) {
     a.d1 = c.dq;
     a.d2 = nullptr;

@@ -48,6 +48,7 @@ struct FwdArgs {
   float* lse;
   const int64_t* q_offsets;
   int B, zero_tail;
+  bool sectors;  // every row of out starts on a 32-byte sector, and ends on one
   const TileItem* items;
   WsHeader* hdr;
 };
@@ -120,7 +121,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     for (int i = 0; i < 15; ++i) mbar_init(bars + 8 * i, 1);
     for (int i = 0; i < kItemRing; ++i) mbar_init(item_empty + 8 * i, kSoftmaxThreads + 1);
     mbar_init(p_ready, kSoftmaxThreads);
-    for (int i = 0; i < 2; ++i) mbar_init(q_empty + 8 * i, kSoftmaxThreads);
+    for (int i = 0; i < 2; ++i) mbar_init(q_empty + 8 * i, 1);
     for (int i = 0; i < 4; ++i) mbar_init(pair + 8 * i, 64);
     *s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -248,6 +249,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
             }
             mma_commit(k_empty + 8 * st);
             mma_commit(s_full);
+            if (j == count - 1) mma_commit(q_empty + 8 * qs);
           }
         }
         n += count;
@@ -422,53 +424,29 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
       float theirs;
       if (!(ok = exchange(l, &theirs))) break;
       l += theirs;
-      const int qs = nq % Sh::kStages;
       if (!(ok = mbar_wait(o_full, nq & 1, s_abort))) break;
       ++nq;
       tc_fence_after();
-      // O / l, half of the columns each, to the item's query tile in shared
-      // memory, which no product reads any more, then to memory with whole
-      // sectors of 8 or 4 rows per instruction; a warp reads only what it wrote.
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      uint8_t* stage = s_q + qs * Sh::kTileBytes;
+      // O / l, half of the columns each.  Where no row saw a key O may hold
+      // what masked infinities left, so those rows are cleared, not scaled.
       constexpr int kCols = DP / 2;
+      const bool live = lane < warp_rows;
+      if (__any_sync(kFull, l == 0.f) && kMasked) {
+#pragma unroll 1
+        for (int c = half * kCols; c < (half + 1) * kCols; c += 8) {
+          uint32_t o[8];
+          tmem_ld8(lanes + kColO + c, o);
+          tmem_wait_ld8(o);
 #pragma unroll
-      for (int c = 0; c < kCols; c += 32) {
-        uint32_t o[32];
-        tmem_ld32(lanes + kColO + half * kCols + c, o);
-        tmem_wait_ld32(o);
-#pragma unroll
-        for (int k = 0; k < 32; k += 8) {
-          uint4 v;
-          uint32_t* pv = reinterpret_cast<uint32_t*>(&v);
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            pv[q] = l == 0.f ? 0u
-                             : pack16<T>(__uint_as_float(o[k + 2 * q]) * inv, __uint_as_float(o[k + 2 * q + 1]) * inv);
-          const int at = (half * kCols + c + k) / 8;
-          *reinterpret_cast<uint4*>(stage + (at >> 3) * kPanel + row * 128 + (((at & 7) ^ (row & 7)) << 4)) = v;
+          for (int k = 0; k < 8; ++k) o[k] = l == 0.f ? 0u : o[k];
+          tmem_st8(lanes + kColO + c, o);
         }
+        tmem_wait_st();
       }
+      store_row<T, kCols>(lanes + kColO + half * kCols, live, l == 0.f ? 0.f : rcp_approx(l),
+                          out + lane * row_values + half * kCols, a.D - half * kCols, a.sectors);
       tc_fence_before();
-      __syncwarp();
-      constexpr int kChunks = kCols / 8, kRowsAtOnce = 32 / kChunks;
-      const int chunk = half * kChunks + lane % kChunks, first = lane / kChunks;
-      uint4 v[kChunks];
-#pragma unroll
-      for (int k = 0; k < kChunks; ++k) {
-        const int rr = quarter * 32 + first + k * kRowsAtOnce;
-        v[k] = *reinterpret_cast<const uint4*>(stage + (chunk >> 3) * kPanel + rr * 128 +
-                                               (((chunk & 7) ^ (rr & 7)) << 4));
-      }
-      fence_async_smem();  // these reads and writes before the next tile's load
-      mbar_arrive(q_empty + 8 * qs);
-      if (chunk * 8 < a.D) {
-        T* to = out + first * row_values + chunk * 8;
-#pragma unroll
-        for (int k = 0; k < kChunks; ++k)
-          if (first + k * kRowsAtOnce < warp_rows) *reinterpret_cast<uint4*>(to + k * kRowsAtOnce * row_values) = v[k];
-      }
-      if (lse && lane < warp_rows) lse[lane] = l == 0.f ? -INFINITY : fmaf(m_used, a.scale, logf(l));
+      if (lse && live) lse[lane] = l == 0.f ? -INFINITY : fmaf(m_used, a.scale, log2_approx(l) * kLn2);
     }
   }
   if (a.zero_tail) zero_rows(a.out, a.B > 0 ? a.q_offsets[a.B] : 0, a.n_q, (int64_t)a.heads * a.D);
@@ -521,6 +499,7 @@ cudaError_t run_forward(const AttnCall& c, const FwdWorkspace& ws, cudaStream_t 
   a.q_offsets = c.q_offsets;
   a.B = c.B;
   a.zero_tail = c.zero_tail;
+  a.sectors = reinterpret_cast<uintptr_t>(c.out) % 32 == 0 && c.D % 16 == 0;
   a.items = ws.items;
   a.hdr = ws.hdr;
   const auto kernel = k_attn_forward<T, DP, kMasked>;

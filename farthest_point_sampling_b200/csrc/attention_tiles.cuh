@@ -8,6 +8,7 @@
 
 #include "attention.h"
 #include "common.cuh"
+#include "tcgen05.cuh"
 
 namespace fpstok {
 
@@ -150,7 +151,53 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return make_float2(lo2(d), hi2(d));
 }
 
+__device__ __forceinline__ float log2_approx(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// One row's kCols float32 accumulator columns from TMEM to memory, times f,
+// rounded: whole 32-byte sectors per thread where rows start on them, else 16
+// bytes.  Rows past the tile's read TMEM like the others (a warp reads as
+// one) and store nothing; columns from D on are not part of the row.
+template <typename T, int kCols>
+__device__ __forceinline__ void store_row(uint32_t acc, bool live, float f, T* to, int cols, bool sectors) {
+#pragma unroll
+  for (int c = 0; c < kCols; c += 32) {
+    uint32_t o[32];
+    tmem_ld32(acc + c, o);
+    tmem_wait_ld32(o);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const uint64_t v = mul2(pack2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), pack2(f, f));
+      o[i] = pack16<T>(lo2(v), hi2(v));
+    }
+    if (!live) continue;
+    if (sectors) {
+#pragma unroll
+      for (int i = 0; i < 16; i += 8)
+        if (c + 2 * i < cols)
+          asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to + c + 2 * i), "r"(o[i]),
+                       "r"(o[i + 1]), "r"(o[i + 2]), "r"(o[i + 3]), "r"(o[i + 4]), "r"(o[i + 5]), "r"(o[i + 6]),
+                       "r"(o[i + 7])
+                       : "memory");
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; i += 4)
+        if (c + 2 * i < cols)
+          *reinterpret_cast<uint4*>(to + c + 2 * i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+    }
+  }
+}
 
 // Rows [first, n) of a [n, row_values] 16-bit tensor to 0, over the whole grid.
 __device__ __forceinline__ void zero_rows(void* base, int64_t first, int64_t n, int64_t row_values) {

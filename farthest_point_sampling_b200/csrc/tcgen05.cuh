@@ -22,21 +22,24 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
 __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
+// A poll sleeps in hardware for up to kWaitNs; polled without that, the waits
+// took half of the softmax warps' issue slots.
+constexpr uint32_t kWaitNs = 20000;
+constexpr int kWaitPolls = 100000;  // 2 s
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
-      : "r"(bar), "r"(parity)
+      : "r"(bar), "r"(parity), "r"(kWaitNs)
       : "memory");
   return ok != 0;
 }
 
 // Every wait ends: after kWaitPolls polls, or once another warp of the block
 // has given up (*abort), it returns false and the caller leaves its loop.
-constexpr int kWaitPolls = 1 << 21;
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
 #pragma unroll 1
   for (int i = 0; !mbar_try(bar, parity); ++i)
