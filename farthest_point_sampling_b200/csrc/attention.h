@@ -12,13 +12,14 @@ namespace fpstok {
 struct WsHeader;
 
 // Visibility of one event: query i of nq stands at p = i + nk - nq and sees
-// key j when (|p - j| <= window, or window < 0, or j < sinks) and
-// (j <= p if causal).
+// key j when p - left <= j <= p + right, or when j < sinks and (not causal or
+// j <= p).  Unlimited sides are kFar, beyond every position.
 struct AttnMask {
   int causal;
-  int window;  // clamped to 2^30; -1 = unlimited
+  int left, right;
   int sinks;
 };
+constexpr int kFar = 1 << 29;
 
 struct AttnCall {
   const void* q;

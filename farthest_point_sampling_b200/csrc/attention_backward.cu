@@ -92,7 +92,7 @@ __device__ __forceinline__ BwdItem bwd_item(const BwdArgs& a, int h, const TileI
     // queries that see some key of the tile: the first key's lower and the
     // last key's upper bound; a tile with a sink in it is seen to the end
     const ColumnSpan first = column_span(a.mask, w.row0), last = column_span(a.mask, w.row0 + w.rows - 1);
-    const int lo = min(max(min(first.lo, last.lo) - w.shift, 0), w.e.nq);
+    const int lo = min(max(first.lo - w.shift, 0), w.e.nq);
     const int hi = min(max(max(first.hi, last.hi) - w.shift + 1, 0), w.e.nq);
     w.tiles.before = w.tiles.s = 0;
     w.tiles.first = lo & ~15;
@@ -326,13 +326,11 @@ __global__ void __launch_bounds__(BwdShape<DP, kGroups, kKeys>::kThreads, BwdSha
       walk.advance();
       if (walk.more()) next = a.items[walk.tile];
       const bool live = row < w.rows;
-      RowSpan rs = {0, 0, 0};
       ColumnSpan cs = {0, 0};
       float lse2 = 0.f, delta = 0.f;
       if constexpr (kKeys) {
         cs = column_span(a.mask, w.row0 + row);
       } else if (w.count) {
-        rs = row_span(a.mask, w.row0 + row + w.shift, w.e.nk);
         // D of this thread's query: dO from its tile, O from memory
         const int ks = nk % Sh::kKept;
         if (!(ok = mbar_wait(kept_full + 8 * ks, (nk / Sh::kKept) & 1, s_abort))) break;
@@ -387,20 +385,6 @@ __global__ void __launch_bounds__(BwdShape<DP, kGroups, kKeys>::kThreads, BwdSha
         }
         if (!(ok = mbar_wait(score_full + 8 * g, visit & 1, s_abort))) break;
         tc_fence_after();
-        // kept rows k0 .. and streamed rows against one another: which pairs are hidden
-        const int qp0 = (kKeys ? s.row0 : w.row0) + w.shift, qn = kKeys ? s.rows : w.rows;
-        const int kk0 = kKeys ? w.row0 : s.row0, kn = kKeys ? w.rows : s.rows;
-        const bool masked = (s.rows & 31) != 0 || tile_masked(a.mask, qp0, qp0 + qn - 1, kk0, kk0 + kn);
-        int from, width, sink = 0;
-        if constexpr (kKeys) {
-          const int p = s.row0 + w.shift;  // position of the tile's first query
-          from = max(cs.lo - p, 0);
-          width = min(cs.hi - p + 1, s.rows) - from;
-        } else {
-          from = rs.lo - s.row0;
-          width = min(rs.hi - s.row0, s.rows) - from;
-          sink = min(rs.s - s.row0, s.rows);
-        }
 #pragma unroll 1
         for (int c = 0; c < kStream; c += 32) {
           if (c >= s.rows) break;
@@ -428,12 +412,27 @@ __global__ void __launch_bounds__(BwdShape<DP, kGroups, kKeys>::kThreads, BwdSha
             y[i + 2] = x[i + 2] * (y[i + 2] - de.z);
             y[i + 3] = x[i + 3] * (y[i + 3] - de.w);
           }
-          if (masked) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int k = c + i;
-              if (!((k >= from && k - from < width) || (!kKeys && k < sink))) x[i] = y[i] = 0.f;
+          // which pairs of the warp's kept rows and these 32 streamed rows see one another
+          bool whole = c + 32 <= s.rows;
+          uint32_t see = bits(0, s.rows - c);
+          const int r0 = w.row0 + (warp & 3) * 32, c0 = s.row0 + c;
+          if constexpr (kKeys) {
+            const int p = c0 + w.shift;
+            if (!all_seen(a.mask, p, p + 31, r0)) {
+              whole = false;
+              see &= bits(cs.lo - p, cs.hi + 1 - p);
             }
+          } else {
+            const int p = r0 + w.shift;
+            if (!all_seen(a.mask, p, p + 31, c0)) {
+              whole = false;
+              see &= seen_keys(a.mask, p + lane, c0);
+            }
+          }
+          if (!whole) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!(see >> i & 1)) x[i] = y[i] = 0.f;
           }
           uint32_t pk[16];
           if constexpr (kKeys) {

@@ -87,13 +87,6 @@ struct FwdShape {
       1024 + 3 * kStages * kTileBytes + 4 * kTile * sizeof(float) + kItemRing * sizeof(FwdItem) + 256;
 };
 
-// Bits lo .. hi - 1 of a word, bounds clipped to 0 .. 32.
-__device__ __forceinline__ uint32_t bits(int lo, int hi) {
-  lo = max(lo, 0);
-  hi = min(hi, 32);
-  return hi <= lo ? 0u : (0xffffffffu >> (32 - hi)) & (0xffffffffu << lo);
-}
-
 // kMasked: a causal or windowed call; without, every query sees its whole event.
 template <typename T, int DP, bool kMasked>
 __global__ void __launch_bounds__(kFwdThreads, 2)
@@ -303,27 +296,22 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
           fence_async_smem();
         }
         // this thread's two 32-key chunks: which of them some row of the warp
-        // sees, and what this row sees there
+        // sees, and, unless all its rows see all of one, what this row sees
         const int c0 = half * kHalf;
-        bool act[2];
-        bool masked = (extent & 31) != 0;
+        bool act[2], whole[2];
         uint32_t see[2];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          act[c] = c0 + 32 * c < extent && warp_rows > 0;
-          see[c] = bits(0, extent - c0 - 32 * c);
-        }
-        if constexpr (kMasked) {
-          if (tile_masked(a.mask, w.p0, w.p0 + w.rows - 1, k0, k0 + extent)) {
-            masked = true;
-            const RowSpan lo = row_span(a.mask, w.p0 + quarter * 32, w.nk);
-            const RowSpan hi = row_span(a.mask, w.p0 + min(quarter * 32 + 31, w.rows - 1), w.nk);
-            const RowSpan own = row_span(a.mask, w.p0 + row, w.nk);
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const int first = k0 + c0 + 32 * c;
-              act[c] = act[c] && ((first + 31 >= lo.lo && first < hi.hi) || first < hi.s);
-              see[c] &= bits(own.lo - first, own.hi - first) | bits(0, own.s - first);
+          const int at = c0 + 32 * c;
+          act[c] = at < extent && warp_rows > 0;
+          whole[c] = at + 32 <= extent;
+          see[c] = bits(0, extent - at);
+          if constexpr (kMasked) {
+            const int pa = w.p0 + quarter * 32, pb = pa + warp_rows - 1;
+            act[c] = act[c] && some_seen(a.mask, pa, pb, k0 + at);
+            if (!all_seen(a.mask, pa, pb, k0 + at)) {
+              whole[c] = false;
+              see[c] &= seen_keys(a.mask, pa + lane, k0 + at);
             }
           }
         }
@@ -335,15 +323,13 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
           tmem_ld32(lanes + c0 + 32 * c, reinterpret_cast<uint32_t*>(s + 32 * c));
         tmem_wait_ld32(reinterpret_cast<uint32_t*>(s));
         tmem_wait_ld32(reinterpret_cast<uint32_t*>(s + 32));
-        if (masked) {
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
-            if (act[c]) {
+        for (int c = 0; c < 2; ++c)
+          if (act[c] && !whole[c]) {
 #pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (!(see[c] >> k & 1)) s[32 * c + k] = -INFINITY;
-            }
-        }
+            for (int k = 0; k < 32; ++k)
+              if (!(see[c] >> k & 1)) s[32 * c + k] = -INFINITY;
+          }
         float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
 #pragma unroll
         for (int c = 0; c < 2; ++c)
@@ -524,7 +510,7 @@ cudaError_t run_forward(const AttnCall& c, const FwdWorkspace& ws, cudaStream_t 
 
 template <typename T>
 cudaError_t run_type(const AttnCall& c, const FwdWorkspace& ws, cudaStream_t s) {
-  if (c.mask.causal || c.mask.window >= 0)
+  if (c.mask.causal || c.mask.left < kFar)
     return c.D <= 64 ? run_forward<T, 64, true>(c, ws, s) : run_forward<T, 128, true>(c, ws, s);
   return c.D <= 64 ? run_forward<T, 64, false>(c, ws, s) : run_forward<T, 128, false>(c, ws, s);
 }

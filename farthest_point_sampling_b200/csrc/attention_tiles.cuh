@@ -46,27 +46,9 @@ struct ItemWalk {
 // Tiles of both lists: sum of ceil(n_b / kTile) <= n / kTile + B.
 __host__ __device__ inline int64_t max_tiles(int64_t n, int B) { return n / kTile + B; }
 
-// Visible keys of the query at position p of nk keys: [0, s) and [lo, hi).
-struct RowSpan {
-  int lo, hi, s;
-};
-__device__ __forceinline__ RowSpan row_span(const AttnMask& m, int p, int nk) {
-  RowSpan r;
-  r.lo = 0;
-  r.hi = nk;
-  r.s = 0;
-  if (m.window >= 0) {
-    r.lo = max(0, p - m.window);
-    r.hi = min(nk, p + m.window + 1);
-    r.s = min(m.sinks, nk);
-  }
-  if (m.causal) {
-    r.hi = min(r.hi, p + 1);
-    r.s = min(r.s, p + 1);
-  }
-  r.hi = max(r.hi, r.lo);
-  r.s = max(r.s, 0);
-  return r;
+// Sinks that the query at position p of nk keys sees: keys 0 .. n - 1.
+__device__ __forceinline__ int sinks_of(const AttnMask& m, int p) {
+  return m.causal ? min(m.sinks, p + 1) : m.sinks;
 }
 
 // Key tiles of kSize keys that some query at positions p0 .. p1 sees: first
@@ -81,11 +63,10 @@ struct KeyTiles {
 };
 template <int kSize>
 __device__ __forceinline__ KeyTiles<kSize> key_tiles(const AttnMask& m, int p0, int p1, int nk) {
-  const RowSpan a = row_span(m, p0, nk), b = row_span(m, p1, nk);
   KeyTiles<kSize> k;
-  k.s = max(a.s, b.s);
-  k.end = max(a.hi, b.hi);
-  k.first = min(a.lo, b.lo) & ~15;
+  k.s = max(min(sinks_of(m, p1), nk), 0);
+  k.end = min(nk, p1 + m.right + 1);
+  k.first = max(0, p0 - m.left) & ~15;
   if (k.end <= k.first) {  // no window: the sinks alone
     k.first = 0;
     k.end = k.s;
@@ -98,25 +79,39 @@ __device__ __forceinline__ KeyTiles<kSize> key_tiles(const AttnMask& m, int p0, 
   return k;
 }
 
-// Positions of the queries that see key j, as [lo, hi], unclipped.
+// Positions of the queries that see key j, as [lo, hi].
 struct ColumnSpan {
   int lo, hi;
 };
 __device__ __forceinline__ ColumnSpan column_span(const AttnMask& m, int j) {
   ColumnSpan c;
-  c.lo = m.causal ? j : -(1 << 30);
-  c.hi = 1 << 30;
-  if (m.window >= 0 && j >= m.sinks) {
-    c.lo = max(c.lo, j - m.window);
-    c.hi = min(c.hi, j + m.window);
+  c.lo = j - m.right;
+  c.hi = j + m.left;
+  if (j < m.sinks) {
+    c.hi = kFar;
+    if (!m.causal) c.lo = -kFar;
   }
   return c;
 }
 
-// Whether some pair of the queries p0 .. p1 and the keys k0 .. k1 - 1 is hidden.
-__device__ __forceinline__ bool tile_masked(const AttnMask& m, int p0, int p1, int k0, int k1) {
-  if (m.causal && k1 - 1 > p0) return true;
-  return m.window >= 0 && k1 > m.sinks && (p1 - k0 > m.window || k1 - 1 - p0 > m.window);
+// Bits lo .. hi - 1 of a word, bounds clipped to 0 .. 32.
+__device__ __forceinline__ uint32_t bits(int lo, int hi) {
+  lo = max(lo, 0);
+  hi = min(hi, 32);
+  return hi <= lo ? 0u : (0xffffffffu >> (32 - hi)) & (0xffffffffu << lo);
+}
+
+// The keys k .. k + 31 against the queries at positions pa .. pb: whether some
+// pair sees one another, and whether every pair does.
+__device__ __forceinline__ bool some_seen(const AttnMask& m, int pa, int pb, int k) {
+  return (k + 31 >= pa - m.left && k <= pb + m.right) || k < sinks_of(m, pb);
+}
+__device__ __forceinline__ bool all_seen(const AttnMask& m, int pa, int pb, int k) {
+  return (k >= pb - m.left && k + 31 <= pa + m.right) || k + 31 < sinks_of(m, pa);
+}
+// Those of the keys k .. k + 31 that the query at position p sees.
+__device__ __forceinline__ uint32_t seen_keys(const AttnMask& m, int p, int k) {
+  return bits(p - m.left - k, p + m.right + 1 - k) | bits(0, sinks_of(m, p) - k);
 }
 
 template <typename T>

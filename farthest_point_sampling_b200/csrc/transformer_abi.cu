@@ -13,7 +13,7 @@ namespace {
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 int from_cuda(cudaError_t e) { return e == cudaSuccess ? FPS_OK : FPS_ERR_CUDA; }
-constexpr int64_t kMaxRows = (int64_t)1 << 29;  // positions, their differences and a window more fit 32 bits
+constexpr int64_t kMaxRows = kFar;  // positions, their differences and a window more fit 32 bits
 constexpr int64_t kMaxStride = (int64_t)1 << 38;  // elements; a TMA stride is below 2^40 bytes
 
 // Sizes only: enough to compute a workspace.
@@ -68,10 +68,11 @@ int make_call(const fps_attention_args* a, AttnCall* c) {
   c->kv_offsets = a->kv_offsets;
   c->B = a->events;
   c->scale = a->scale;
-  // positions stay below kMaxRows: a wider window sees everything
+  // positions stay below kMaxRows = kFar: a wider window sees everything
   c->mask.causal = a->causal;
-  c->mask.window = a->window >= kMaxRows ? -1 : (int)a->window;
-  c->mask.sinks = (int)(a->sinks >= kMaxRows ? kMaxRows : a->sinks);
+  c->mask.left = a->window < 0 || a->window >= kMaxRows ? kFar : (int)a->window;
+  c->mask.right = a->causal ? 0 : c->mask.left;
+  c->mask.sinks = c->mask.left == kFar ? 0 : (int)(a->sinks >= kMaxRows ? kMaxRows : a->sinks);
   c->max_tokens = a->max_tokens;
   c->zero_tail = a->zero_tail;
   return FPS_OK;
