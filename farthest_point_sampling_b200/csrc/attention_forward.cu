@@ -6,14 +6,13 @@
 //   P = exp2(c S - c m),  l <- l f + sum P,  O <- O f + P V,  f = exp2(c (m_old - m)),
 // c = scale log2(e), and the output is O / l, lse = m scale + ln l.
 //
-// A block is ten warps: one thread loads Q, K and V tiles with TMA, one issues
-// the tcgen05 products, and eight warps do the softmax with two threads per
-// query row (a TMEM lane), each for half of a tile's keys; they exchange the
-// row's maximum once per tile and its sum once per item.  S goes to TMEM, P
-// comes back over it as 16-bit operand A of the second product, O stays in
-// TMEM until the item ends.  Two blocks share an SM: while one's softmax runs,
-// the other's products do.  Blocks are persistent; the loader runs ahead into
-// the next items.
+// A block is six warps: one thread loads Q, K and V tiles with TMA, one issues
+// the tcgen05 products, and four warps do the softmax with one query row (a
+// TMEM lane) per thread, its scores in registers, so that no row crosses
+// threads.  S goes to TMEM, P comes back over it as 16-bit operand A of the
+// second product, O stays in TMEM until the item ends.  Two blocks share an
+// SM: while one's softmax runs, the other's products do.  Blocks are
+// persistent; the loader runs ahead into the next items.
 //
 // Rounding: P is rounded to the input type for P V; l sums the unrounded
 // values.  O is rescaled only when m grows by more than 8 / log2 units, which
@@ -31,10 +30,9 @@ namespace fpstok {
 
 namespace {
 
-constexpr int kSoftmaxWarps = 8;
+constexpr int kSoftmaxWarps = 4;
 constexpr int kSoftmaxThreads = 32 * kSoftmaxWarps;
 constexpr int kFwdThreads = kSoftmaxThreads + 64;
-constexpr int kHalf = kTile / 2;  // keys of a tile that one of a row's two threads takes
 constexpr int kPanel = kTile * 128;  // bytes of a 128-row panel of 64 values
 constexpr uint32_t kTmemColumns = 256;
 constexpr uint32_t kColO = 128;  // S (and P over it) in columns 0 .. 127
@@ -84,7 +82,7 @@ struct FwdShape {
   static constexpr int kStages = DP == 64 ? 2 : 1;  // of Q, K and V each: 96 KB either way, two blocks per SM
   static constexpr uint32_t kTileBytes = kPanels * kPanel;
   static constexpr size_t kSmem =
-      1024 + 3 * kStages * kTileBytes + 4 * kTile * sizeof(float) + kItemRing * sizeof(FwdItem) + 256;
+      1024 + 3 * kStages * kTileBytes + kItemRing * sizeof(FwdItem) + 256;
 };
 
 // kMasked: a causal or windowed call; without, every query sees its whole event.
@@ -99,15 +97,14 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
   uint8_t* s_q = s_base;
   uint8_t* s_k = s_q + Sh::kStages * Sh::kTileBytes;
   uint8_t* s_v = s_k + Sh::kStages * Sh::kTileBytes;
-  float* s_pair = reinterpret_cast<float*>(s_v + Sh::kStages * Sh::kTileBytes);  // [parity][half][row]
-  FwdItem* s_item = reinterpret_cast<FwdItem*>(s_pair + 4 * kTile);
+  FwdItem* s_item = reinterpret_cast<FwdItem*>(s_v + Sh::kStages * Sh::kTileBytes);
   uint64_t* s_bar = reinterpret_cast<uint64_t*>(s_item + kItemRing);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_bar + 24);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   const uint32_t bars = smem_u32(s_bar);
   const uint32_t q_full = bars, k_full = bars + 16, k_empty = bars + 32, v_full = bars + 48, v_empty = bars + 64,
                  s_full = bars + 80, o_full = bars + 88, drain = bars + 96, item_full = bars + 104,
-                 item_empty = bars + 120, p_ready = bars + 136, q_empty = bars + 144, pair = bars + 160;
+                 item_empty = bars + 120, p_ready = bars + 136, q_empty = bars + 144;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -115,7 +112,6 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     for (int i = 0; i < kItemRing; ++i) mbar_init(item_empty + 8 * i, kSoftmaxThreads + 1);
     mbar_init(p_ready, kSoftmaxThreads);
     for (int i = 0; i < 2; ++i) mbar_init(q_empty + 8 * i, 1);
-    for (int i = 0; i < 4; ++i) mbar_init(pair + 8 * i, 64);
     *s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     tma_prefetch_map(&map_q);
@@ -256,28 +252,16 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     }
   } else {
     // ------------------------------------------------ softmax
-    int n = 0, nq = 0, x = 0;  // key tiles, query tiles and exchanges so far
-    const int half = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
-    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+    int n = 0, nq = 0;  // key tiles and query tiles so far
+    const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
     bool ok = true;
-    // The other thread's value of this row.  Two buffers: a thread writes one
-    // again only after both have been past the exchange in between.
-    const auto exchange = [&](float v, float* other) {
-      float* at = s_pair + (x & 1) * 2 * kTile + row;
-      at[half * kTile] = v;
-      mbar_arrive(pair + 8 * quarter);
-      if (!mbar_wait(pair + 8 * quarter, x & 1, s_abort)) return false;
-      *other = at[(half ^ 1) * kTile];
-      ++x;
-      return true;
-    };
     for (int i = 0; ok; ++i) {
       const int slot = i % kItemRing;
       if (!(ok = mbar_wait(item_full + 8 * slot, (i / kItemRing) & 1, s_abort))) break;
       const FwdItem& w = s_item[slot];  // read where it is needed: it stays until this thread lets go of the slot
       const int count = w.count;
       if (count < 0) break;
-      const int warp_rows = min(32, w.rows - quarter * 32);
+      const int warp_rows = min(32, w.rows - warp * 32);
       float m_used = -INFINITY, l = 0.f;
       for (int j = 0; j < count; ++j, ++n) {
         const int k0 = w.keys.start(j), extent = w.keys.extent(j);
@@ -295,19 +279,19 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
           }
           fence_async_smem();
         }
-        // this thread's two 32-key chunks: which of them some row of the warp
+        // the tile's 32-key chunks: which of them some row of the warp
         // sees, and, unless all its rows see all of one, what this row sees
-        const int c0 = half * kHalf;
-        bool act[2], whole[2];
-        uint32_t see[2];
+        constexpr int kChunks = kTile / 32;
+        bool act[kChunks], whole[kChunks];
+        uint32_t see[kChunks];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int at = c0 + 32 * c;
+        for (int c = 0; c < kChunks; ++c) {
+          const int at = 32 * c;
           act[c] = at < extent && warp_rows > 0;
           whole[c] = at + 32 <= extent;
           see[c] = bits(0, extent - at);
           if constexpr (kMasked) {
-            const int pa = w.p0 + quarter * 32, pb = pa + warp_rows - 1;
+            const int pa = w.p0 + warp * 32, pb = pa + warp_rows - 1;
             act[c] = act[c] && some_seen(a.mask, pa, pb, k0 + at);
             if (!all_seen(a.mask, pa, pb, k0 + at)) {
               whole[c] = false;
@@ -317,14 +301,14 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
         }
         if (!(ok = mbar_wait(s_full, n & 1, s_abort))) break;
         tc_fence_after();
-        float s[kHalf];
+        float s[kTile];
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-          tmem_ld32(lanes + c0 + 32 * c, reinterpret_cast<uint32_t*>(s + 32 * c));
-        tmem_wait_ld32(reinterpret_cast<uint32_t*>(s));
-        tmem_wait_ld32(reinterpret_cast<uint32_t*>(s + 32));
+        for (int c = 0; c < kChunks; ++c)
+          tmem_ld32(lanes + 32 * c, reinterpret_cast<uint32_t*>(s + 32 * c));
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
+        for (int c = 0; c < kChunks; ++c) tmem_wait_ld32(reinterpret_cast<uint32_t*>(s + 32 * c));
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
           if (act[c] && !whole[c]) {
 #pragma unroll
             for (int k = 0; k < 32; ++k)
@@ -332,7 +316,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
           }
         float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
+        for (int c = 0; c < kChunks; ++c)
           if (act[c]) {
 #pragma unroll
             for (int k = 32 * c; k < 32 * c + 32; k += 8) {
@@ -342,9 +326,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
               m3 = max3f(m3, s[k + 6], s[k + 7]);
             }
           }
-        float top = fmaxf(max3f(m0, m1, m2), m3), theirs;
-        if (!(ok = exchange(top, &theirs))) break;
-        top = fmaxf(top, theirs);
+        const float top = fmaxf(max3f(m0, m1, m2), m3);
         if (j == 0) {
           m_used = top;
         } else {
@@ -355,7 +337,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
             if (grow) m_used = top;
             l *= f;
 #pragma unroll 1
-            for (int c = half * (DP / 2); c < (half + 1) * (DP / 2); c += 8) {
+            for (int c = 0; c < DP; c += 8) {
               uint32_t o[8];
               tmem_ld8(lanes + kColO + c, o);
               tmem_wait_ld8(o);
@@ -369,7 +351,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
         const float2 base2 = make_float2(-base, -base), scale2 = make_float2(a.scale_log2, a.scale_log2);
         float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        for (int c = 0; c < kChunks; ++c) {
           uint32_t pk[16];
           if (act[c]) {
 #pragma unroll
@@ -384,8 +366,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
 #pragma unroll
             for (int k = 0; k < 16; ++k) pk[k] = 0;
           }
-          // over scores that both threads have read before the exchange
-          if (c0 + 32 * c < extent) tmem_st16(lanes + (c0 + 32 * c) / 2, pk);
+          if (32 * c < extent) tmem_st16(lanes + 16 * c, pk);
         }
         l += sum.x + sum.y;
         tmem_wait_st();
@@ -393,13 +374,13 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
         mbar_arrive(p_ready);
       }
       if (!ok) break;
-      const int64_t first_row = (int64_t)w.q_row + quarter * 32;
+      const int64_t first_row = (int64_t)w.q_row + warp * 32;
       T* out = static_cast<T*>(a.out) + (first_row * a.heads + w.h) * a.D;
-      float* lse = a.lse && half == 0 ? a.lse + (int64_t)w.h * a.n_q + first_row : nullptr;
+      float* lse = a.lse ? a.lse + (int64_t)w.h * a.n_q + first_row : nullptr;
       const int64_t row_values = (int64_t)a.heads * a.D;
       mbar_arrive(item_empty + 8 * slot);
       if (count == 0) {  // nothing to see
-        if (half == 0 && lane < warp_rows) {
+        if (lane < warp_rows) {
 #pragma unroll 1
           for (int c = 0; c < a.D; c += 8)
             *reinterpret_cast<uint4*>(out + lane * row_values + c) = make_uint4(0, 0, 0, 0);
@@ -407,19 +388,15 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
         }
         continue;
       }
-      float theirs;
-      if (!(ok = exchange(l, &theirs))) break;
-      l += theirs;
       if (!(ok = mbar_wait(o_full, nq & 1, s_abort))) break;
       ++nq;
       tc_fence_after();
-      // O / l, half of the columns each.  Where no row saw a key O may hold
+      // O / l.  Where no row saw a key O may hold
       // what masked infinities left, so those rows are cleared, not scaled.
-      constexpr int kCols = DP / 2;
       const bool live = lane < warp_rows;
       if (__any_sync(kFull, l == 0.f) && kMasked) {
 #pragma unroll 1
-        for (int c = half * kCols; c < (half + 1) * kCols; c += 8) {
+        for (int c = 0; c < DP; c += 8) {
           uint32_t o[8];
           tmem_ld8(lanes + kColO + c, o);
           tmem_wait_ld8(o);
@@ -429,8 +406,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
         }
         tmem_wait_st();
       }
-      store_row<T, kCols>(lanes + kColO + half * kCols, live, l == 0.f ? 0.f : rcp_approx(l),
-                          out + lane * row_values + half * kCols, a.D - half * kCols, a.sectors);
+      store_row<T, DP>(lanes + kColO, live, l == 0.f ? 0.f : rcp_approx(l), out + lane * row_values, a.D, a.sectors);
       tc_fence_before();
       if (lse && live) lse[lane] = l == 0.f ? -INFINITY : fmaf(m_used, a.scale, log2_approx(l) * kLn2);
     }
