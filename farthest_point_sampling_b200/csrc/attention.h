@@ -47,8 +47,8 @@ struct AttnCall {
 };
 
 // Workspace bytes of a call of these sizes.
-size_t attention_forward_bytes(int64_t n_q, int B);
-size_t attention_backward_bytes(int64_t n_q, int64_t n_kv, int B, int heads);
+size_t attention_forward_bytes(const AttnCall& c);
+size_t attention_backward_bytes(const AttnCall& c);
 cudaError_t launch_attention_forward(const AttnCall& c, void* workspace, cudaStream_t s);
 cudaError_t launch_attention_backward(const AttnCall& c, void* workspace, cudaStream_t s);
 

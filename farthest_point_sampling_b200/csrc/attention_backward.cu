@@ -527,7 +527,10 @@ cudaError_t run(const BwdArgs& a, int64_t items, const CUtensorMap& k1, const CU
 
 template <typename T, int DP>
 cudaError_t run_backward(const AttnCall& c, const BwdWorkspace& ws, cudaStream_t s) {
-  cudaError_t e = launch_attention_plan(c, ws.hdr, ws.queries, ws.keys, s);
+  PlanLists lists = {};
+  lists.queries = ws.queries;
+  lists.keys = ws.keys;
+  cudaError_t e = launch_attention_plan(c, ws.hdr, lists, s);
   if (e != cudaSuccess) return e;
   const bool bf16 = std::is_same<T, __nv_bfloat16>::value;
   // without queries (or keys) no item has a tile of the other: their maps are not used
@@ -577,8 +580,8 @@ cudaError_t run_backward(const AttnCall& c, const BwdWorkspace& ws, cudaStream_t
 
 }  // namespace
 
-size_t attention_backward_bytes(int64_t n_q, int64_t n_kv, int B, int heads) {
-  return carve_backward(nullptr, n_q, n_kv, B, heads).bytes;
+size_t attention_backward_bytes(const AttnCall& c) {
+  return carve_backward(nullptr, c.n_q, c.n_kv, c.B, c.heads).bytes;
 }
 
 cudaError_t launch_attention_backward(const AttnCall& c, void* workspace, cudaStream_t s) {

@@ -20,6 +20,7 @@
 // range limits of both types.
 #include <type_traits>
 
+#include "attention_few.h"
 #include "attention_plan.h"
 #include "attention_tiles.cuh"
 #include "common.cuh"
@@ -422,25 +423,43 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
   if (threadIdx.x == 0 && *s_abort) record_error(a.hdr, kDevWaitTimeout);
 }
 
+// Whether a call looks for events with at most kFewRows query rows: when its
+// events have no more than that on average.
+bool few_rows(const AttnCall& c) { return c.B > 0 && c.n_q * c.group <= (int64_t)kFewRows * c.B; }
+
 struct FwdWorkspace {
   WsHeader* hdr;
   TileItem* items;
+  TileItem* units;
+  JoinItem* joins;
+  float* partial;
+  int chunk;
   size_t bytes;
 };
-FwdWorkspace carve_forward(void* base, int64_t n_q, int B) {
-  FwdWorkspace w;
+FwdWorkspace carve_forward(void* base, const AttnCall& c) {
+  FwdWorkspace w = {};
   char* p = static_cast<char*>(base);
+  size_t off = 256;
+  const auto take = [&](size_t bytes) {
+    char* at = p + off;
+    off = (off + bytes + 255) & ~(size_t)255;
+    return at;
+  };
   w.hdr = reinterpret_cast<WsHeader*>(p);
-  w.items = reinterpret_cast<TileItem*>(p + 256);
-  w.bytes = 256 + (size_t)(max_tiles(n_q, B) + 1) * sizeof(TileItem);
-  w.bytes = (w.bytes + 255) & ~(size_t)255;
+  w.items = reinterpret_cast<TileItem*>(take((max_tiles(c.n_q, c.B) + 1) * sizeof(TileItem)));
+  if (few_rows(c)) {
+    w.chunk = few_chunk(c.n_kv, c.kv_heads);
+    w.units = reinterpret_cast<TileItem*>(take((c.n_kv / w.chunk + c.B + 1) * sizeof(TileItem)));
+    w.joins = reinterpret_cast<JoinItem*>(take((c.n_kv / w.chunk + 1) * sizeof(JoinItem)));
+    w.partial = reinterpret_cast<float*>(take(few_partial_floats(c.n_kv, c.kv_heads, c.D, w.chunk) * sizeof(float)));
+  }
+  w.bytes = off;
   return w;
 }
 
 template <typename T, int DP, bool kMasked>
 cudaError_t run_forward(const AttnCall& c, const FwdWorkspace& ws, cudaStream_t s) {
-  cudaError_t e = launch_attention_plan(c, ws.hdr, ws.items, nullptr, s);
-  if (e != cudaSuccess || c.n_q == 0) return e;
+  cudaError_t e;
   const bool bf16 = std::is_same<T, __nv_bfloat16>::value;
   CUtensorMap map_q, map_k, map_v;
   if (!attention_map(&map_q, c.q, bf16, c.n_q, c.heads, c.D, c.q_token, c.q_head)) return cudaErrorInvalidValue;
@@ -493,10 +512,23 @@ cudaError_t run_type(const AttnCall& c, const FwdWorkspace& ws, cudaStream_t s) 
 
 }  // namespace
 
-size_t attention_forward_bytes(int64_t n_q, int B) { return carve_forward(nullptr, n_q, B).bytes; }
+size_t attention_forward_bytes(const AttnCall& c) { return carve_forward(nullptr, c).bytes; }
 
 cudaError_t launch_attention_forward(const AttnCall& c, void* workspace, cudaStream_t s) {
-  const FwdWorkspace ws = carve_forward(workspace, c.n_q, c.B);
+  const FwdWorkspace ws = carve_forward(workspace, c);
+  PlanLists lists = {};
+  lists.queries = ws.items;
+  if (few_rows(c)) {
+    lists.units = ws.units;
+    lists.joins = ws.joins;
+    lists.chunk = ws.chunk;
+  }
+  cudaError_t e = launch_attention_plan(c, ws.hdr, lists, s);
+  if (e != cudaSuccess || c.n_q == 0) return e;
+  if (lists.units) {
+    const FewPlan plan = {ws.chunk, ws.units, ws.joins, ws.partial};
+    if ((e = launch_attention_few(c, plan, ws.hdr, s)) != cudaSuccess) return e;
+  }
   return c.dtype == FPS_DTYPE_BF16 ? run_type<__nv_bfloat16>(c, ws, s) : run_type<__half>(c, ws, s);
 }
 

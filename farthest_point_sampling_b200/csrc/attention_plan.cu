@@ -3,6 +3,7 @@
 // length is bounded by rows / 128 + events.
 #include "attention_plan.h"
 
+#include "attention_few.h"
 #include "attention_tiles.cuh"
 #include "common.cuh"
 #include "internal.h"
@@ -38,26 +39,30 @@ __device__ __forceinline__ int block_scan(int v, int* s_warp, int* total) {
   return x - v + (warp ? s_warp[warp - 1] : 0);  // exclusive
 }
 
-// Block 0 makes the query list, block 1 the key list.  A pass takes 1024
-// events, one per thread: their tiles are counted and scanned, then all
-// threads write the pass's items, each finding its event by bisection in
-// shared memory, so that one long event does not keep one thread.
+enum PlanList { kPlanQueries, kPlanKeys, kPlanUnits };
+
+// One block per list.  A pass takes 1024 events, one per thread: their items
+// are counted and scanned, then all threads write the pass's items, each
+// finding its event by bisection in shared memory, so that one long event does
+// not keep one thread.
 __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const int64_t* __restrict__ q_off,
                                                             const int64_t* __restrict__ k_off, int B, int64_t n_q,
-                                                            int64_t n_kv, int max_tokens, WsHeader* hdr,
-                                                            TileItem* queries, TileItem* keys) {
+                                                            int64_t n_kv, int max_tokens, int group, AttnMask mask,
+                                                            WsHeader* hdr, const PlanLists lists) {
   asm volatile("griddepcontrol.launch_dependents;");
   __shared__ int s_warp[32];
-  __shared__ int s_start[kPlanThreads + 1];
+  __shared__ int s_start[kPlanThreads];
   __shared__ TileItem s_event[kPlanThreads];
   const int tid = threadIdx.x;
-  const bool key_list = blockIdx.x == 1;
-  TileItem* items = key_list ? keys : queries;
-  int base = 0, error = 0;
+  // blocks in the order queries, keys, units, without the lists that are not asked for
+  const int kind = blockIdx.x == 0 ? kPlanQueries : lists.keys && blockIdx.x == 1 ? kPlanKeys : kPlanUnits;
+  TileItem* items = kind == kPlanQueries ? lists.queries : kind == kPlanKeys ? lists.keys : lists.units;
+  int base = 0, slots = 0, joins = 0, error = 0;
   if (tid == 0 && B > 0 && (q_off[0] != 0 || k_off[0] != 0)) error = kDevBadOffsets;
   for (int b0 = 0; b0 < B; b0 += kPlanThreads) {
     const int b = b0 + tid;
-    int tiles = 0;
+    int n = 0, parts = 0;
+    TileItem e = {};
     if (b < B) {
       const int64_t q0 = q_off[b], q1 = q_off[b + 1], k0 = k_off[b], k1 = k_off[b + 1];
       if (q0 < 0 || k0 < 0 || q1 < q0 || k1 < k0 || q1 > n_q || k1 > n_kv) {
@@ -65,39 +70,58 @@ __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const int64_t* __res
       } else if (max_tokens > 0 && (q1 - q0 > max_tokens || k1 - k0 > max_tokens)) {
         error = error ? error : kDevTooLarge;
       } else {
-        s_event[tid] = TileItem{(int)q0, (int)(q1 - q0), (int)k0, (int)(k1 - k0), 0, {0, 0, 0}};
-        tiles = (int)(((key_list ? k1 - k0 : q1 - q0) + kTile - 1) / kTile);
+        e.q0 = (int)q0;
+        e.nq = (int)(q1 - q0);
+        e.k0 = (int)k0;
+        e.nk = (int)(k1 - k0);
+        const bool few = lists.units && (int64_t)e.nq * group <= kFewRows;
+        if (kind == kPlanQueries) {
+          n = few ? 0 : (e.nq + kTile - 1) / kTile;
+        } else if (kind == kPlanKeys) {
+          n = (e.nk + kTile - 1) / kTile;
+        } else if (few && e.nq > 0) {
+          n = max((few_span(mask, e.nq, e.nk).count() + lists.chunk - 1) / lists.chunk, 1);
+          parts = n > 1 ? n : 0;
+        }
       }
     }
     // A pass with bad offsets makes no items and ends the list: up to there
-    // offsets rise, which is what bounds the items of a list by max_tiles().
+    // offsets rise, which is what bounds the items of a list by its buffer.
     if (__syncthreads_or(error == kDevBadOffsets)) break;
     int total;
-    s_start[tid] = block_scan(tiles, s_warp, &total);
+    s_start[tid] = block_scan(n, s_warp, &total);
+    if (kind == kPlanUnits) {
+      int total_parts, total_joins;
+      const int slot = slots + block_scan(parts, s_warp, &total_parts);
+      const int join = joins + block_scan(parts > 0, s_warp, &total_joins);
+      e.pad[0] = n;
+      e.pad[1] = slot;
+      if (parts) lists.joins[join] = JoinItem{e.q0, e.nq, slot, parts};
+      slots += total_parts;
+      joins += total_joins;
+    }
+    s_event[tid] = e;
     __syncthreads();
-    for (int e = tid; e < total; e += kPlanThreads) {
-      int lo = 0, hi = kPlanThreads - 1;  // the last event of the pass that starts at or before e
+    for (int i = tid; i < total; i += kPlanThreads) {
+      int lo = 0, hi = kPlanThreads - 1;  // the last event of the pass that starts at or before i
       while (lo < hi) {
         const int m = (lo + hi + 1) >> 1;
-        if (s_start[m] <= e) lo = m; else hi = m - 1;
+        if (s_start[m] <= i) lo = m; else hi = m - 1;
       }
       TileItem it = s_event[lo];
-      it.t = e - s_start[lo];
-      items[base + e] = it;
+      it.t = i - s_start[lo];
+      items[base + i] = it;
     }
     base += total;
     __syncthreads();
   }
-  // one writer of the status word per block, the query block's after its reset
   error = __syncthreads_or(error == kDevBadOffsets) ? kDevBadOffsets : __syncthreads_or(error) ? kDevTooLarge : 0;
   if (tid == 0) {
-    hdr->n_items[key_list ? kKeyTiles : kQueryTiles] = base;
-    if (!key_list) {
+    hdr->n_items[kind == kPlanQueries ? kQueryTiles : kind == kPlanKeys ? kKeyTiles : kFewUnits] = base;
+    if (kind == kPlanUnits) hdr->n_items[kFewJoins] = joins;
+    if (kind == kPlanQueries) {  // every block sees the same errors; one writes the status word
       hdr->status = error;
       hdr->detail = 0;
-      hdr->next_item[0] = 0;
-      hdr->next_item[1] = 0;
-      hdr->next_item[2] = 0;
     }
   }
 }
@@ -120,11 +144,10 @@ EncodeTiled encode_tiled() {
 
 }  // namespace
 
-cudaError_t launch_attention_plan(const AttnCall& c, WsHeader* hdr, TileItem* queries, TileItem* keys,
-                                  cudaStream_t s) {
+cudaError_t launch_attention_plan(const AttnCall& c, WsHeader* hdr, const PlanLists& lists, cudaStream_t s) {
   count_launch();
-  k_attn_plan<<<keys ? 2 : 1, kPlanThreads, 0, s>>>(c.q_offsets, c.kv_offsets, c.B, c.n_q, c.n_kv, c.max_tokens, hdr,
-                                                    queries, keys);
+  k_attn_plan<<<1 + (lists.keys != nullptr) + (lists.units != nullptr), kPlanThreads, 0, s>>>(
+      c.q_offsets, c.kv_offsets, c.B, c.n_q, c.n_kv, c.max_tokens, c.group, c.mask, hdr, lists);
   return cudaGetLastError();
 }
 

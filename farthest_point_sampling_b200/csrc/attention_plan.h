@@ -9,16 +9,27 @@
 namespace fpstok {
 
 struct TileItem;
+struct JoinItem;
 
-// WsHeader::n_items of the two lists.
+// WsHeader::n_items of the lists.
 constexpr int kQueryTiles = 0;
 constexpr int kKeyTiles = 1;
+constexpr int kFewUnits = 2;
+constexpr int kFewJoins = 3;
 
-// Fills `queries` (and `keys` when not NULL) with the tiles of every event in
-// order, their counts in hdr->n_items, and resets the call's status words.
-// An event longer than max_tokens is recorded and gets no tiles; inconsistent
-// offsets are recorded and end the lists.
-cudaError_t launch_attention_plan(const AttnCall& c, WsHeader* hdr, TileItem* queries, TileItem* keys, cudaStream_t s);
+// The lists of one call; those that are NULL are not made.
+struct PlanLists {
+  TileItem* queries;  // tiles of 128 queries
+  TileItem* keys;     // tiles of 128 keys
+  TileItem* units;    // chunks of the events with at most kFewRows query rows, which then have no query tiles
+  JoinItem* joins;    // those of them with several chunks
+  int chunk;
+};
+
+// Fills the lists in event order, their counts in hdr->n_items, and resets the
+// call's status words.  An event longer than max_tokens is recorded and is in
+// no list; inconsistent offsets are recorded and end the lists.
+cudaError_t launch_attention_plan(const AttnCall& c, WsHeader* hdr, const PlanLists& lists, cudaStream_t s);
 
 // Map of a [rows, heads, D] 16-bit tensor for boxes of 64 rows x one head x
 // 64 values, 128-byte swizzled; what lies outside reads as zeros.

@@ -79,6 +79,21 @@ __device__ __forceinline__ KeyTiles<kSize> key_tiles(const AttnMask& m, int p0, 
   return k;
 }
 
+// The keys that some query of a whole event sees, counted through: the sinks,
+// then the window's.
+struct FewSpan {
+  int s, lo, hi;
+  __device__ __forceinline__ int count() const { return s + max(hi - lo, 0); }
+  __device__ __forceinline__ int key(int v) const { return v < s ? v : lo + (v - s); }
+};
+__device__ __forceinline__ FewSpan few_span(const AttnMask& m, int nq, int nk) {
+  FewSpan f;
+  f.s = max(min(sinks_of(m, nk - 1), nk), 0);
+  f.lo = max(max(0, nk - nq - m.left), f.s);
+  f.hi = min(nk, nk + m.right);
+  return f;
+}
+
 // Positions of the queries that see key j, as [lo, hi].
 struct ColumnSpan {
   int lo, hi;

@@ -35,8 +35,23 @@ bool row_strides_ok(int64_t token, int64_t head) {
   return token > 0 && head > 0 && token % 8 == 0 && head % 8 == 0 && token < kMaxStride && head < kMaxStride;
 }
 
-int make_call(const fps_attention_args* a, AttnCall* c) {
+int make_sizes(const fps_attention_args* a, AttnCall* c) {
   const int rc = check_attention_sizes(a);
+  if (rc) return rc;
+  *c = AttnCall{};
+  c->dtype = a->dtype;
+  c->n_q = a->n_q;
+  c->n_kv = a->n_kv;
+  c->heads = a->heads;
+  c->kv_heads = a->kv_heads;
+  c->group = a->heads / a->kv_heads;
+  c->D = a->head_dim;
+  c->B = a->events;
+  return FPS_OK;
+}
+
+int make_call(const fps_attention_args* a, AttnCall* c) {
+  const int rc = make_sizes(a, c);
   if (rc) return rc;
   if (!(a->scale > 0.f) || !std::isfinite(a->scale)) return FPS_ERR_ARG;
   if ((a->causal != 0 && a->causal != 1) || a->window < -1 || a->sinks < 0) return FPS_ERR_ARG;
@@ -47,17 +62,9 @@ int make_call(const fps_attention_args* a, AttnCall* c) {
                       !row_strides_ok(a->k_token_stride, a->k_head_stride) ||
                       !row_strides_ok(a->v_token_stride, a->v_head_stride)))
     return FPS_ERR_ARG;
-  *c = AttnCall{};
   c->q = a->q;
   c->k = a->k;
   c->v = a->v;
-  c->dtype = a->dtype;
-  c->n_q = a->n_q;
-  c->n_kv = a->n_kv;
-  c->heads = a->heads;
-  c->kv_heads = a->kv_heads;
-  c->group = a->heads / a->kv_heads;
-  c->D = a->head_dim;
   c->q_token = a->q_token_stride;
   c->q_head = a->q_head_stride;
   c->k_token = a->k_token_stride;
@@ -66,7 +73,6 @@ int make_call(const fps_attention_args* a, AttnCall* c) {
   c->v_head = a->v_head_stride;
   c->q_offsets = a->q_offsets;
   c->kv_offsets = a->kv_offsets;
-  c->B = a->events;
   c->scale = a->scale;
   // positions stay below kMaxRows = kFar: a wider window sees everything
   c->mask.causal = a->causal;
@@ -140,9 +146,9 @@ int fps_rotary(const void* x, void* y, int dtype, int64_t T, int H, int D, int64
 }
 
 size_t fps_attention_workspace_bytes(const fps_attention_args* args, int backward) {
-  if (check_attention_sizes(args)) return 0;
-  return backward ? attention_backward_bytes(args->n_q, args->n_kv, args->events, args->heads)
-                  : attention_forward_bytes(args->n_q, args->events);
+  AttnCall c;
+  if (make_sizes(args, &c)) return 0;
+  return backward ? attention_backward_bytes(c) : attention_forward_bytes(c);
 }
 
 int fps_attention(const fps_attention_args* args, void* out, float* lse, void* workspace, size_t workspace_bytes,
