@@ -15,12 +15,14 @@
 // one block in a fixed order, so the result does not depend on scheduling;
 // the price is that the scores are formed twice.
 //
-// Roles as in the forward kernel: a loading thread, an issuing thread, and
-// softmax warps with one kept row per thread; P and dS go back to TMEM as
-// 16-bit operand A.  TMEM holds kGroups stages of scores (128 columns each)
-// and the accumulators.  With 64-wide heads a block takes 256 columns and two
-// blocks share an SM; with 128-wide heads the keys kernel takes all 512 and
-// works on two stages at once with a warp group each.
+// Roles as in the forward kernel: a loading warp, an issuing thread, and two
+// groups of four softmax warps with one kept row per thread that take the
+// streamed tiles in turn, so that one group's softmax runs under the other's
+// products; P and dS go back to TMEM as 16-bit operand A.  TMEM holds two
+// stages of scores (128 columns each) and the accumulators, two sets of them
+// where they fit, so that a block goes on with the next item while it stores
+// one.  One block takes an SM; the products bound it, at 64 streamed rows by
+// the shared-memory reads of their two operands.
 //
 // Rounding: P and dS are rounded to the input type for their products.  D
 // comes from the rounded output, as the forward left it.
@@ -39,6 +41,9 @@ namespace {
 constexpr int kStream = 64;                   // rows of a streamed tile
 constexpr int kStreamPanel = kStream * 128;   // bytes of one of its 64-value panels
 constexpr int kPanel = kTile * 128;
+constexpr int kGroups = 2;                    // softmax groups, and stages of scores
+constexpr int kBwdThreads = 32 * (4 * kGroups + 2);
+constexpr int kItemRing = 2;
 
 struct BwdArgs {
   int64_t n_q, n_kv;
@@ -47,7 +52,7 @@ struct BwdArgs {
   float scale, scale_log2;
   const void* out;
   const float* lse;
-  float* delta;  // [heads, n_q], written by the queries kernel
+  float* rows;   // [2][heads, n_q]: -lse log2(e) and -D, written by the queries kernel for the keys kernel
   void* d1;      // dQ, or dK
   void* d2;      // dV
   const int64_t* offsets;  // of the kept rows
@@ -57,73 +62,66 @@ struct BwdArgs {
   WsHeader* hdr;
 };
 
-template <int DP, int kGroups, bool kKeys>
-struct BwdShape {
-  static constexpr int kPanels = DP / 64;
-  static constexpr uint32_t kKeptBytes = kPanels * kPanel;          // one kept tensor's tile
-  static constexpr uint32_t kStreamBytes = kPanels * kStreamPanel;  // one streamed tensor's tile
-  // 96 KB and two blocks per SM, or 192 KB and one
-  static constexpr int kKept = DP == 64 || kKeys ? 2 : 1;
-  static constexpr int kRing = DP == 64 || kKeys ? 2 : 1;
-  static constexpr int kThreads = 32 * (4 * kGroups + 2);
-  static constexpr uint32_t kColAcc = 128 * kGroups;
-  static constexpr uint32_t kColumns = kColAcc + (kKeys ? 2 : 1) * DP <= 256 ? 256 : 512;
-  static constexpr int kBlocks = kColumns == 256 ? 2 : 1;
-  static constexpr size_t kSmem = 1024 + 2 * (kKept * kKeptBytes + kRing * kStreamBytes) + kGroups * 1024 + 256;
-};
-
+// One work item as the loading warp hands it to the others.
 struct BwdItem {
-  TileItem e;
-  int h;           // head (queries kernel) or key head
-  int row0, rows;  // kept rows: first in its event, how many
-  int shift;       // nk - nq: position of query 0
-  KeyTiles<kStream> tiles;  // streamed tiles of one head
-  int count;       // streamed tiles in all
+  int count;            // streamed tiles of one head; -1 ends the work
+  int h;                // head (queries kernel) or key head
+  int kept_row, rows;   // first kept row, how many
+  int at;               // the first kept row in its event
+  int stream_row;       // the event's first streamed row
+  int shift;            // nk - nq: position of query 0
+  KeyTiles<kStream> tiles;
 };
 template <bool kKeys>
 __device__ __forceinline__ BwdItem bwd_item(const BwdArgs& a, int h, const TileItem& e) {
   BwdItem w;
   w.h = h;
-  w.e = e;
-  w.row0 = w.e.t * kTile;
-  w.rows = min(kTile, (kKeys ? w.e.nk : w.e.nq) - w.row0);
-  w.shift = w.e.nk - w.e.nq;
+  w.at = e.t * kTile;
+  w.kept_row = (kKeys ? e.k0 : e.q0) + w.at;
+  w.rows = min(kTile, (kKeys ? e.nk : e.nq) - w.at);
+  w.stream_row = kKeys ? e.q0 : e.k0;
+  w.shift = e.nk - e.nq;
   if constexpr (kKeys) {
     // queries that see some key of the tile: the first key's lower and the
     // last key's upper bound; a tile with a sink in it is seen to the end
-    const ColumnSpan first = column_span(a.mask, w.row0), last = column_span(a.mask, w.row0 + w.rows - 1);
-    const int lo = min(max(first.lo - w.shift, 0), w.e.nq);
-    const int hi = min(max(max(first.hi, last.hi) - w.shift + 1, 0), w.e.nq);
+    const ColumnSpan first = column_span(a.mask, w.at), last = column_span(a.mask, w.at + w.rows - 1);
+    const int lo = min(max(first.lo - w.shift, 0), e.nq);
+    const int hi = min(max(max(first.hi, last.hi) - w.shift + 1, 0), e.nq);
     w.tiles.before = w.tiles.s = 0;
     w.tiles.first = lo & ~15;
     w.tiles.end = hi;
     w.tiles.count = hi > lo ? (hi - w.tiles.first + kStream - 1) / kStream : 0;
-    w.count = w.tiles.count * a.group;
   } else {
-    w.tiles = key_tiles<kStream>(a.mask, w.row0 + w.shift, w.row0 + w.rows - 1 + w.shift, w.e.nk);
-    w.count = w.tiles.count;
+    w.tiles = key_tiles<kStream>(a.mask, w.at + w.shift, w.at + w.rows - 1 + w.shift, e.nk);
   }
+  w.count = w.tiles.count;
   return w;
 }
 
-// Streamed tile t of an item: the head its rows belong to, first row in the event, rows.
-struct StreamTile {
-  int head, row0, rows;
+template <int DP, bool kKeys>
+struct BwdShape {
+  static constexpr int kPanels = DP / 64;
+  static constexpr uint32_t kKeptBytes = kPanels * kPanel;          // one kept tensor's tile
+  static constexpr uint32_t kStreamBytes = kPanels * kStreamPanel;  // one streamed tensor's tile
+  // 64 KB of kept tiles, 96 or 128 KB of streamed ones
+  static constexpr int kKept = DP == 64 ? 2 : 1;
+  static constexpr int kRing = DP == 64 ? 6 : 4;
+  static constexpr uint32_t kColAcc = 128 * kGroups;
+  static constexpr uint32_t kAccColumns = (kKeys ? 2 : 1) * DP;
+  static constexpr int kAcc = kColAcc + 2 * kAccColumns <= 512 ? 2 : 1;
+  static constexpr uint32_t kColumns = 512;
+  static constexpr size_t kSmem = 1024 + 2 * (kKept * kKeptBytes + kRing * kStreamBytes) + kRing * 512 +
+                                  kItemRing * sizeof(BwdItem) + 512;
 };
-template <bool kKeys>
-__device__ __forceinline__ StreamTile stream_tile(const BwdArgs& a, const BwdItem& w, int t) {
-  StreamTile s;
-  if constexpr (kKeys) {
-    const int m = t / w.tiles.count;
-    s.head = w.h * a.group + m;
-    s.row0 = w.tiles.start(t - m * w.tiles.count);
-    s.rows = w.tiles.extent(t - m * w.tiles.count);
-  } else {
-    s.head = w.h / a.group;
-    s.row0 = w.tiles.start(t);
-    s.rows = w.tiles.extent(t);
-  }
-  return s;
+
+// 4 bytes from global to shared memory, asynchronously; zero where not real.
+__device__ __forceinline__ void copy4(uint32_t dst, const float* src, bool real) {
+  const int n = real ? 4 : 0;
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+// One arrival on `bar` when this thread's copies so far have landed.
+__device__ __forceinline__ void copy_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 template <typename T>
@@ -148,37 +146,46 @@ __device__ __forceinline__ void gradient_row(uint32_t acc, bool filled, bool liv
   }
 }
 
-template <typename T, int DP, int kGroups, bool kKeys>
-__global__ void __launch_bounds__(BwdShape<DP, kGroups, kKeys>::kThreads, BwdShape<DP, kGroups, kKeys>::kBlocks)
+template <typename T, int DP, bool kKeys>
+__global__ void __launch_bounds__(kBwdThreads, 1)
     k_attn_backward(const BwdArgs a, const __grid_constant__ CUtensorMap map_k1, const __grid_constant__ CUtensorMap map_k2,
                     const __grid_constant__ CUtensorMap map_s1, const __grid_constant__ CUtensorMap map_s2) {
-  using Sh = BwdShape<DP, kGroups, kKeys>;
+  using Sh = BwdShape<DP, kKeys>;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   constexpr int kLoadWarp = 4 * kGroups, kMmaWarp = kLoadWarp + 1;
   extern __shared__ uint8_t s_raw[];
   uint8_t* s_base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~(uintptr_t)1023);
-  // kept tiles (tensor 1 and 2 of a stage side by side), then the streamed ring
+  // kept tiles (tensor 1 and 2 of a stage side by side), then the streamed
+  // ring, then the ring's -lse and -D of 64 queries (keys kernel)
   uint8_t* s_kept = s_base;
   uint8_t* s_ring = s_kept + 2 * Sh::kKept * Sh::kKeptBytes;
-  float* s_col = reinterpret_cast<float*>(s_ring + 2 * Sh::kRing * Sh::kStreamBytes);  // [group][2][lse, D][64]
-  uint64_t* s_bar = reinterpret_cast<uint64_t*>(s_col + kGroups * 256);
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_bar + 18);
+  float* s_col = reinterpret_cast<float*>(s_ring + 2 * Sh::kRing * Sh::kStreamBytes);
+  BwdItem* s_item = reinterpret_cast<BwdItem*>(s_col + Sh::kRing * 128);
+  uint64_t* s_bar = reinterpret_cast<uint64_t*>(s_item + kItemRing);
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_bar + 32);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   const uint32_t bars = smem_u32(s_bar);
-  const uint32_t kept_full = bars, kept_empty = bars + 16, ring_full = bars + 32, ring_empty = bars + 48,
-                 score_full = bars + 64, ready = bars + 80, acc_full = bars + 96, acc_empty = bars + 104,
-                 drain = bars + 112, col_ready = bars + 120;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t kept_full = bars, kept_empty = bars + 16, score_full = bars + 32, acc_full = bars + 48,
+                 item_full = bars + 64, drain = bars + 80, item_empty = bars + 88, ready = bars + 104,
+                 acc_empty = bars + 120, ring_full = bars + 136, ring_empty = bars + 184;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 10; ++i) mbar_init(bars + 8 * i, 1);
-    mbar_init(ready, 128);
-    mbar_init(ready + 8, 128);
-    mbar_init(acc_full, 1);
-    mbar_init(acc_empty, 128 * kGroups);
-    mbar_init(drain, 1);
-    mbar_init(col_ready, 128);
-    mbar_init(col_ready + 8, 128);
+    for (const uint32_t b : {kept_full, score_full, acc_full, item_full, drain}) {
+      mbar_init(b, 1);
+      if (b != drain) mbar_init(b + 8, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(item_empty + 8 * i, 128 * kGroups + 1);
+      // in the queries kernel the softmax threads read the kept dO themselves
+      mbar_init(kept_empty + 8 * i, kKeys ? 1 : 1 + 128 * kGroups);
+      mbar_init(ready + 8 * i, 128);
+      mbar_init(acc_empty + 8 * i, 128 * kGroups);
+    }
+    for (int i = 0; i < Sh::kRing; ++i) {
+      mbar_init(ring_full + 8 * i, kKeys ? 33 : 1);  // the tiles, and in the keys kernel each lane's -lse and -D
+      mbar_init(ring_empty + 8 * i, 1);
+    }
     *s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     tma_prefetch_map(&map_k1);
@@ -190,280 +197,334 @@ __global__ void __launch_bounds__(BwdShape<DP, kGroups, kKeys>::kThreads, BwdSha
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *s_tmem;
+  const uint32_t tmem = uniform(*s_tmem);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  // every role walks the block's items, and reads the next one's entry while it works on one
-  ItemWalk walk(kKeys ? a.kv_heads : a.heads, a.hdr->n_items[kKeys ? kKeyTiles : kQueryTiles]);
-  TileItem next = a.items[walk.more() ? walk.tile : 0];
 
   if (warp == kLoadWarp) {
-    // ------------------------------------------------ loads
-    if (lane == 0) {
-      int n = 0, nk = 0;  // streamed and kept tiles loaded so far
-      bool ok = true;
-      while (walk.more() && ok) {
-        const BwdItem w = bwd_item<kKeys>(a, walk.h, next);
-        walk.advance();
-        if (walk.more()) next = a.items[walk.tile];
-        if (w.count == 0) continue;
-        const int ks = nk % Sh::kKept;
-        if (nk >= Sh::kKept && !(ok = mbar_wait(kept_empty + 8 * ks, ((nk / Sh::kKept) - 1) & 1, s_abort))) break;
-        const int boxes = (w.rows + 63) / 64;
-        const int row = (kKeys ? w.e.k0 : w.e.q0) + w.row0;
-        mbar_expect(kept_full + 8 * ks, 2 * boxes * 8192 * Sh::kPanels);
-        for (int p = 0; p < Sh::kPanels; ++p)
-          for (int i = 0; i < boxes; ++i) {
-            const uint32_t to = smem_u32(s_kept) + 2 * ks * Sh::kKeptBytes + p * kPanel + i * 8192;
-            tma_load(to, &map_k1, kept_full + 8 * ks, p * 64, w.h, row + i * 64);
-            tma_load(to + Sh::kKeptBytes, &map_k2, kept_full + 8 * ks, p * 64, w.h, row + i * 64);
-          }
-        ++nk;
-        for (int t = 0; t < w.count; ++t, ++n) {
-          const StreamTile s = stream_tile<kKeys>(a, w, t);
-          const int st = n % Sh::kRing;
-          if (n >= Sh::kRing && !(ok = mbar_wait(ring_empty + 8 * st, ((n / Sh::kRing) - 1) & 1, s_abort))) break;
-          const int srow = (kKeys ? w.e.q0 : w.e.k0) + s.row0;
-          mbar_expect(ring_full + 8 * st, 2 * Sh::kStreamBytes);
-          for (int p = 0; p < Sh::kPanels; ++p) {
-            const uint32_t to = smem_u32(s_ring) + 2 * st * Sh::kStreamBytes + p * kStreamPanel;
-            tma_load(to, &map_s1, ring_full + 8 * st, p * 64, s.head, srow);
-            tma_load(to + Sh::kStreamBytes, &map_s2, ring_full + 8 * st, p * 64, s.head, srow);
-          }
-        }
+    // ------------------------------------------------ items and loads
+    ItemWalk walk(kKeys ? a.kv_heads : a.heads, a.hdr->n_items[kKeys ? kKeyTiles : kQueryTiles]);
+    TileItem next = a.items[walk.more() ? walk.tile : 0];
+    int i = 0, n = 0, nk = 0;  // items handed out, streamed and kept tiles loaded so far
+    bool ok = true;
+    for (; ok; ++i) {
+      const int slot = i % kItemRing;
+      if (i >= kItemRing && !mbar_wait_warp(item_empty + 8 * slot, ((i / kItemRing) - 1) & 1, s_abort)) break;
+      if (!walk.more()) {
+        if (lane == 0) s_item[slot].count = -1;
+        __syncwarp();
+        mbar_arrive_one(item_full + 8 * slot);
+        break;
       }
-      // after a wait that gave up: this thread's copies still in flight land first
-      if (*s_abort) {
-        volatile int none = 0;
-        for (int i = 0; i < 2; ++i) {
-          const int lk = nk - 1 - i, ls = n - 1 - i;
-          if (lk >= 0 && i < Sh::kKept) mbar_wait(kept_full + 8 * (lk % Sh::kKept), (lk / Sh::kKept) & 1, &none);
-          if (ls >= 0 && i < Sh::kRing) mbar_wait(ring_full + 8 * (ls % Sh::kRing), (ls / Sh::kRing) & 1, &none);
+      const BwdItem w = bwd_item<kKeys>(a, walk.h, next);
+      walk.advance();
+      if (walk.more()) next = a.items[walk.tile];
+      if (lane == 0) s_item[slot] = w;
+      __syncwarp();
+      mbar_arrive_one(item_full + 8 * slot);
+      if (w.count == 0) continue;
+      const int ks = nk % Sh::kKept;
+      if (nk >= Sh::kKept && !mbar_wait_warp(kept_empty + 8 * ks, ((nk / Sh::kKept) - 1) & 1, s_abort)) break;
+      {
+        const int boxes = (w.rows + 63) / 64;
+        mbar_expect(kept_full + 8 * ks, 2 * boxes * 8192 * Sh::kPanels);
+#pragma unroll 1
+        for (int b = 0; b < boxes; ++b)
+#pragma unroll
+          for (int p = 0; p < Sh::kPanels; ++p) {
+            const uint32_t to = smem_u32(s_kept) + 2 * ks * Sh::kKeptBytes + p * kPanel + b * 8192;
+            tma_load(to, &map_k1, kept_full + 8 * ks, p * 64, w.h, w.kept_row + b * 64);
+            tma_load(to + Sh::kKeptBytes, &map_k2, kept_full + 8 * ks, p * 64, w.h, w.kept_row + b * 64);
+          }
+      }
+      ++nk;
+      const int head0 = kKeys ? w.h * a.group : w.h / a.group;
+#pragma unroll 1
+      for (int hd = 0; hd < (kKeys ? a.group : 1) && ok; ++hd)
+#pragma unroll 1
+        for (int j = 0; j < w.count; ++j, ++n) {
+          const int st = n % Sh::kRing;
+          if (n >= Sh::kRing && !(ok = mbar_wait_warp(ring_empty + 8 * st, ((n / Sh::kRing) - 1) & 1, s_abort))) break;
+          const int row = w.stream_row + w.tiles.start(j);
+          {
+            mbar_expect(ring_full + 8 * st, 2 * Sh::kStreamBytes);
+#pragma unroll
+            for (int p = 0; p < Sh::kPanels; ++p) {
+              const uint32_t to = smem_u32(s_ring) + 2 * st * Sh::kStreamBytes + p * kStreamPanel;
+              tma_load(to, &map_s1, ring_full + 8 * st, p * 64, head0 + hd, row);
+              tma_load(to + Sh::kStreamBytes, &map_s2, ring_full + 8 * st, p * 64, head0 + hd, row);
+            }
+          }
+          if constexpr (kKeys) {
+            const int extent = w.tiles.extent(j);
+            const float* from = a.rows + (int64_t)(head0 + hd) * a.n_q + row;
+            const uint32_t to = smem_u32(s_col + st * 128);
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+              for (int c = lane; c < kStream; c += 32)
+                copy4(to + (x * kStream + c) * 4, from + (c < extent ? (int64_t)x * a.heads * a.n_q + c : 0), c < extent);
+            copy_arrive(ring_full + 8 * st);
+          }
         }
+    }
+    // after a wait that gave up: the copies still in flight land first
+    if (__any_sync(kFull, *s_abort)) {
+      volatile int none = 0;
+      for (int b = 0; b < Sh::kRing; ++b) {
+        const int lk = nk - 1 - b, ls = n - 1 - b;
+        if (lk >= 0 && b < Sh::kKept) mbar_wait_warp(kept_full + 8 * (lk % Sh::kKept), (lk / Sh::kKept) & 1, &none);
+        if (ls >= 0) mbar_wait_warp(ring_full + 8 * (ls % Sh::kRing), (ls / Sh::kRing) & 1, &none);
       }
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------ products
-    if (lane == 0) {
-      int n = 0, nk = 0;
+    {
+      int m = 0, nk = 0;  // tiles and items with tiles so far
       const int d_steps = (a.D + 15) / 16;
       const uint32_t out_desc = mma_desc(kBf16, false, true, d_steps * 16);
       bool ok = true;
-      while (walk.more() && ok) {
-        const BwdItem w = bwd_item<kKeys>(a, walk.h, next);
-        walk.advance();
-        if (walk.more()) next = a.items[walk.tile];
-        if (w.count == 0) continue;
+      // The scores of a tile are issued before the gradients from the tile
+      // before it, which may be the last of the item before.
+      struct {
+        int tile, steps, item, kept;
+        bool first, last, held;
+      } p = {};
+      const auto gradients = [&]() {
+        const int st = p.tile % Sh::kRing, g = p.tile % kGroups, acc = p.item % Sh::kAcc;
+        if (p.first && p.item >= Sh::kAcc &&
+            !mbar_wait_warp(acc_empty + 8 * acc, ((p.item / Sh::kAcc) - 1) & 1, s_abort))
+          return false;
+        if (!mbar_wait_warp(ready + 8 * g, (p.tile / kGroups) & 1, s_abort)) return false;
+        tc_fence_after();
+        const uint32_t from = smem_desc(smem_u32(s_ring) + 2 * st * Sh::kStreamBytes, kStreamPanel);
+        const uint32_t to = tmem + Sh::kColAcc + acc * Sh::kAccColumns, scores = tmem + g * 128;
+        if constexpr (kKeys) {  // dV += P^T dO
+#pragma unroll
+          for (int k = 0; k < kStream / 16; ++k)
+            if (k < p.steps)
+              mma_ts(to + DP, scores + k * 8, from + (Sh::kStreamBytes >> 4) + k * 128, out_desc, k > 0 || !p.first);
+        }
+#pragma unroll
+        for (int k = 0; k < kStream / 16; ++k)  // dK += dS^T Q, or dQ += dS K
+          if (k < p.steps) mma_ts(to, scores + 64 + k * 8, from + k * 128, out_desc, k > 0 || !p.first);
+        mma_commit(ring_empty + 8 * st);
+        if (p.last) {
+          mma_commit(kept_empty + 8 * p.kept);
+          mma_commit(acc_full + 8 * acc);
+        }
+        return true;
+      };
+      for (int i = 0; ok; ++i) {
+        const int slot = i % kItemRing;
+        if (!(ok = mbar_wait_warp(item_full + 8 * slot, (i / kItemRing) & 1, s_abort))) break;
+        const int count = uniform(s_item[slot].count);
+        KeyTiles<kStream> tiles;
+        tiles.before = uniform(s_item[slot].tiles.before);
+        tiles.first = uniform(s_item[slot].tiles.first);
+        tiles.end = uniform(s_item[slot].tiles.end);
+        tiles.s = uniform(s_item[slot].tiles.s);
+        mbar_arrive_one(item_empty + 8 * slot);
+        if (count < 0) break;
+        if (count == 0) continue;
         const int ks = nk % Sh::kKept;
         const uint32_t kept = smem_desc(smem_u32(s_kept) + 2 * ks * Sh::kKeptBytes, kPanel);
-        if (!(ok = mbar_wait(kept_full + 8 * ks, (nk / Sh::kKept) & 1, s_abort))) break;
-        for (int t = 0; t < w.count + kGroups - 1; ++t) {
-          if (t < w.count) {  // scores of tile t, over the P and dS that the products before have read
-            const int m = n + t, st = m % Sh::kRing, g = m % kGroups;
-            const uint32_t ring = smem_u32(s_ring) + 2 * st * Sh::kStreamBytes;
-            const int cols = (stream_tile<kKeys>(a, w, t).rows + 15) / 16 * 16;
-            if (!(ok = mbar_wait(ring_full + 8 * st, (m / Sh::kRing) & 1, s_abort))) break;
+        // With one stage of kept tiles their load waits for the last item's gradients.
+        if (Sh::kKept == 1 && p.held) {
+          if (!(ok = gradients())) break;
+          p.held = false;
+        }
+        if (!(ok = mbar_wait_warp(kept_full + 8 * ks, (nk / Sh::kKept) & 1, s_abort))) break;
+        const int heads = kKeys ? a.group : 1;
+#pragma unroll 1
+        for (int hd = 0; hd < heads && ok; ++hd)
+#pragma unroll 1
+          for (int j = 0; j < count; ++j, ++m) {
+            const int st = m % Sh::kRing, g = m % kGroups;
+            if (!(ok = mbar_wait_warp(ring_full + 8 * st, (m / Sh::kRing) & 1, s_abort))) break;
             tc_fence_after();
-            const uint32_t desc = mma_desc(kBf16, false, false, cols);
-            const uint32_t from = smem_desc(ring, kStreamPanel);
+            const int steps = (tiles.extent(j) + 15) / 16;
+            const uint32_t desc = mma_desc(kBf16, false, false, steps * 16);
+            const uint32_t from = smem_desc(smem_u32(s_ring) + 2 * st * Sh::kStreamBytes, kStreamPanel);
+            // over the P and dS of two tiles before, which their products have read
 #pragma unroll
             for (int x = 0; x < 2; ++x)
 #pragma unroll
               for (int k = 0; k < DP / 16; ++k)
                 if (k < d_steps)
-                  mma_ss(tmem + g * 128 + x * 64,
-                         kept + ((x * Sh::kKeptBytes + (k >> 2) * kPanel + (k & 3) * 32) >> 4),
+                  mma_ss(tmem + g * 128 + x * 64, kept + ((x * Sh::kKeptBytes + (k >> 2) * kPanel + (k & 3) * 32) >> 4),
                          from + ((x * Sh::kStreamBytes + (k >> 2) * kStreamPanel + (k & 3) * 32) >> 4), desc, k > 0);
             mma_commit(score_full + 8 * g);
+            if (p.held && !(ok = gradients())) break;
+            p.tile = m;
+            p.steps = steps;
+            p.item = nk;
+            p.kept = ks;
+            p.first = hd == 0 && j == 0;
+            p.last = hd == heads - 1 && j == count - 1;
+            p.held = true;
           }
-          const int u = t - (kGroups - 1);
-          if (u >= 0) {  // gradients from tile u
-            const int m = n + u, st = m % Sh::kRing, g = m % kGroups;
-            const uint32_t ring = smem_u32(s_ring) + 2 * st * Sh::kStreamBytes;
-            const int steps = (stream_tile<kKeys>(a, w, u).rows + 15) / 16;
-            if (u == 0 && nk > 0 && !(ok = mbar_wait(acc_empty, (nk - 1) & 1, s_abort))) break;
-            if (!(ok = mbar_wait(ready + 8 * g, (m / kGroups) & 1, s_abort))) break;
-            tc_fence_after();
-            const uint32_t from = smem_desc(ring, kStreamPanel);
-            if constexpr (kKeys) {  // dV += P^T dO
-#pragma unroll
-              for (int k = 0; k < kStream / 16; ++k)
-                if (k < steps)
-                  mma_ts(tmem + Sh::kColAcc + DP, tmem + g * 128 + k * 8, from + (Sh::kStreamBytes >> 4) + k * 128,
-                         out_desc, k > 0 || u > 0);
-            }
-#pragma unroll
-            for (int k = 0; k < kStream / 16; ++k)  // dK += dS^T Q, or dQ += dS K
-              if (k < steps)
-                mma_ts(tmem + Sh::kColAcc, tmem + g * 128 + 64 + k * 8, from + k * 128, out_desc, k > 0 || u > 0);
-            mma_commit(ring_empty + 8 * st);
-            if (u == w.count - 1) {
-              mma_commit(kept_empty + 8 * ks);
-              mma_commit(acc_full);
-            }
-          }
-        }
-        if (!ok) break;
-        n += w.count;
         ++nk;
       }
-      if (*s_abort) {  // products in flight end before TMEM is freed
+      if (ok && p.held) gradients();
+      if (__any_sync(kFull, *s_abort)) {  // products in flight end before TMEM is freed
         volatile int none = 0;
         mma_commit(drain);
-        mbar_wait(drain, 0, &none);
+        mbar_wait_warp(drain, 0, &none);
       }
     }
   } else {
     // ------------------------------------------------ softmax and its gradient
-    const int g = warp >> 2;  // warp group: takes the tiles of its score stage
+    const int g = warp >> 2, quarter = warp & 3;  // warp group: takes the tiles of its score stage
     const int row = threadIdx.x & 127;
-    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
     const uint32_t scores = lanes + g * 128;
-    float* col = s_col + g * 256;
-    int n = 0, nk = 0;
+    int m = 0, nk = 0;
     bool ok = true;
-    while (walk.more() && ok) {
-      const BwdItem w = bwd_item<kKeys>(a, walk.h, next);
-      walk.advance();
-      if (walk.more()) next = a.items[walk.tile];
-      const bool live = row < w.rows;
-      ColumnSpan cs = {0, 0};
-      float lse2 = 0.f, delta = 0.f;
-      if constexpr (kKeys) {
-        cs = column_span(a.mask, w.row0 + row);
-      } else if (w.count) {
-        // D of this thread's query: dO from its tile, O from memory
-        const int ks = nk % Sh::kKept;
-        if (!(ok = mbar_wait(kept_full + 8 * ks, (nk / Sh::kKept) & 1, s_abort))) break;
-        if (live) {
-          const int64_t q = (int64_t)w.e.q0 + w.row0 + row;
-          const T* o = static_cast<const T*>(a.out) + (q * a.heads + w.h) * a.D;
-          const uint8_t* d = s_kept + (2 * ks + 1) * Sh::kKeptBytes + row * 128;
-          for (int c = 0; c < a.D / 8; ++c) {
-            const uint4 vo = *reinterpret_cast<const uint4*>(o + c * 8);
-            const uint4 vd = *reinterpret_cast<const uint4*>(d + (c >> 3) * kPanel + (((c & 7) ^ (row & 7)) << 4));
-            const uint32_t* po = reinterpret_cast<const uint32_t*>(&vo);
-            const uint32_t* pd = reinterpret_cast<const uint32_t*>(&vd);
+    for (int i = 0; ok; ++i) {
+      const int slot = i % kItemRing;
+      if (!(ok = mbar_wait(item_full + 8 * slot, (i / kItemRing) & 1, s_abort))) break;
+      const BwdItem& w = s_item[slot];  // read where it is needed: it stays until this thread lets go of the slot
+      const int count = w.count;
+      if (count < 0) break;
+      float lse2 = 0.f, delta = 0.f;  // -lse log2(e) and -D of this thread's query
+      if constexpr (!kKeys) {
+        if (count) {  // D: dO from its tile, O from memory
+          const int ks = nk % Sh::kKept;
+          if (!(ok = mbar_wait(kept_full + 8 * ks, (nk / Sh::kKept) & 1, s_abort))) break;
+          if (row < w.rows) {
+            const int64_t q = (int64_t)w.kept_row + row, at = (int64_t)w.h * a.n_q + q;
+            const T* o = static_cast<const T*>(a.out) + (q * a.heads + w.h) * a.D;
+            const uint8_t* d = s_kept + (2 * ks + 1) * Sh::kKeptBytes + row * 128;
+            for (int c = 0; c < a.D / 8; ++c) {
+              const uint4 vo = *reinterpret_cast<const uint4*>(o + c * 8);
+              const uint4 vd = *reinterpret_cast<const uint4*>(d + (c >> 3) * kPanel + (((c & 7) ^ (row & 7)) << 4));
+              const uint32_t* po = reinterpret_cast<const uint32_t*>(&vo);
+              const uint32_t* pd = reinterpret_cast<const uint32_t*>(&vd);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float2 x = unpack16<T>(po[i]), y = unpack16<T>(pd[i]);
-              delta = fmaf(x.x, y.x, fmaf(x.y, y.y, delta));
+              for (int k = 0; k < 4; ++k) {
+                const float2 x = unpack16<T>(po[k]), y = unpack16<T>(pd[k]);
+                delta = fmaf(x.x, y.x, fmaf(x.y, y.y, delta));
+              }
+            }
+            lse2 = -a.lse[at] * kLog2e;
+            delta = -delta;
+            if (g == 0) {
+              a.rows[at] = lse2;
+              a.rows[(int64_t)a.heads * a.n_q + at] = delta;
             }
           }
-          lse2 = a.lse[(int64_t)w.h * a.n_q + q] * kLog2e;
-          a.delta[(int64_t)w.h * a.n_q + q] = delta;
+          mbar_arrive(kept_empty + 8 * ks);
         }
       }
-      for (int t = 0; t < w.count; ++t) {
-        const int m = n + t;
-        if (m % kGroups != g) continue;
-        const StreamTile s = stream_tile<kKeys>(a, w, t);
-        const int visit = m / kGroups;
-        const float* c_lse = col + (visit & 1) * 128;
-        if constexpr (kKeys) {
-          // lse and D of the tile's queries, shared by the rows; one array
-          // per parity, so one barrier per tile is enough
-          const int64_t at = (int64_t)s.head * a.n_q + w.e.q0 + s.row0 + (row & 63);
-          float v = 0.f;
-          if ((row & 63) < s.rows) v = row < 64 ? a.lse[at] * kLog2e : a.delta[at];
-          col[(visit & 1) * 128 + row] = v;
-          mbar_arrive(col_ready + 8 * g);
-          if (!(ok = mbar_wait(col_ready + 8 * g, visit & 1, s_abort))) break;
-        }
-        const int odd = s.rows & 15;
-        if (odd) {
-          // Streamed rows past the event's last inside a product's step of 16:
-          // their P and dS are 0, and the rows must be finite for 0 to stay 0.
-          const int st = m % Sh::kRing;
-          if (!(ok = mbar_wait(ring_full + 8 * st, (m / Sh::kRing) & 1, s_abort))) break;
-          uint8_t* tile = s_ring + 2 * st * Sh::kStreamBytes;
-          constexpr int kTensors = kKeys ? 2 : 1;
-          for (int e = row; e < (16 - odd) * 8 * Sh::kPanels * kTensors; e += 128) {
-            const int c = e % (8 * Sh::kPanels * kTensors), r = s.rows + e / (8 * Sh::kPanels * kTensors);
-            *reinterpret_cast<uint4*>(tile + (c >> 3) * kStreamPanel + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-          }
-          fence_async_smem();
-        }
-        if (!(ok = mbar_wait(score_full + 8 * g, visit & 1, s_abort))) break;
-        tc_fence_after();
+      const int heads = kKeys ? a.group : 1;
 #pragma unroll 1
-        for (int c = 0; c < kStream; c += 32) {
-          if (c >= s.rows) break;
-          float x[32], y[32];
-          tmem_ld32(scores + c, reinterpret_cast<uint32_t*>(x));
-          tmem_ld32(scores + 64 + c, reinterpret_cast<uint32_t*>(y));
-          tmem_wait_ld32(reinterpret_cast<uint32_t*>(x));
-          tmem_wait_ld32(reinterpret_cast<uint32_t*>(y));
+      for (int hd = 0; hd < heads && ok; ++hd)
+#pragma unroll 1
+        for (int j = 0; j < count; ++j, ++m) {
+          if (m % kGroups != g) continue;
+          const int visit = m / kGroups, st = m % Sh::kRing;
+          const int extent = w.tiles.extent(j), odd = extent & 15;
+          if (kKeys || odd) {
+            // also where -lse and -D are read from
+            if (!(ok = mbar_wait(ring_full + 8 * st, (m / Sh::kRing) & 1, s_abort))) break;
+          }
+          if (odd) {
+            // Streamed rows past the tile's last inside a product's step of 16:
+            // their P and dS are 0, and the rows must be finite for 0 to stay 0.
+            uint8_t* tile = s_ring + 2 * st * Sh::kStreamBytes;
+            constexpr int kTensors = kKeys ? 2 : 1;
+#pragma unroll 1
+            for (int e = row; e < (16 - odd) * 8 * Sh::kPanels * kTensors; e += 128) {
+              const int c = e % (8 * Sh::kPanels * kTensors), r = extent + e / (8 * Sh::kPanels * kTensors);
+              *reinterpret_cast<uint4*>(tile + (c >> 3) * kStreamPanel + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_async_smem();
+          }
+          if (!(ok = mbar_wait(score_full + 8 * g, visit & 1, s_abort))) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < kStream; c += 32) {
+            if (c >= extent) break;
+            // which pairs of the warp's kept rows and these 32 streamed rows see one another
+            const int r0 = w.at + quarter * 32, c0 = w.tiles.start(j) + c;
+            const int pa = (kKeys ? c0 : r0) + w.shift, key = kKeys ? r0 : c0;
+            uint32_t p16[16], d16[16];
+            if (some_seen(a.mask, pa, pa + 31, key)) {
+              float x[32], y[32];
+              tmem_ld32(scores + c, reinterpret_cast<uint32_t*>(x));
+              tmem_ld32(scores + 64 + c, reinterpret_cast<uint32_t*>(y));
+              tmem_wait_ld32(reinterpret_cast<uint32_t*>(x));
+              tmem_wait_ld32(reinterpret_cast<uint32_t*>(y));
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            float4 le, de;
-            if constexpr (kKeys) {
-              le = *reinterpret_cast<const float4*>(c_lse + c + i);
-              de = *reinterpret_cast<const float4*>(c_lse + 64 + c + i);
+              for (int k = 0; k < 32; k += 4) {
+                float4 le = make_float4(lse2, lse2, lse2, lse2), de = make_float4(delta, delta, delta, delta);
+                if constexpr (kKeys) {
+                  le = *reinterpret_cast<const float4*>(s_col + st * 128 + c + k);
+                  de = *reinterpret_cast<const float4*>(s_col + st * 128 + kStream + c + k);
+                }
+                const float2 e0 = fma2(make_float2(x[k], x[k + 1]), make_float2(a.scale_log2, a.scale_log2), make_float2(le.x, le.y));
+                const float2 e1 = fma2(make_float2(x[k + 2], x[k + 3]), make_float2(a.scale_log2, a.scale_log2), make_float2(le.z, le.w));
+                x[k] = exp2_approx(e0.x);
+                x[k + 1] = exp2_approx(e0.y);
+                x[k + 2] = exp2_approx(e1.x);
+                x[k + 3] = exp2_approx(e1.y);
+                const uint64_t y0 = mul2(add2(pack2(y[k], y[k + 1]), pack2(de.x, de.y)), pack2(x[k], x[k + 1]));
+                const uint64_t y1 = mul2(add2(pack2(y[k + 2], y[k + 3]), pack2(de.z, de.w)), pack2(x[k + 2], x[k + 3]));
+                y[k] = lo2(y0);
+                y[k + 1] = hi2(y0);
+                y[k + 2] = lo2(y1);
+                y[k + 3] = hi2(y1);
+              }
+              if (c + 32 > extent || !all_seen(a.mask, pa, pa + 31, key)) {
+                uint32_t see = bits(0, extent - c);
+                if constexpr (kKeys) {
+                  const ColumnSpan s = column_span(a.mask, key + lane);
+                  see &= bits(s.lo - pa, s.hi + 1 - pa);
+                } else {
+                  see &= seen_keys(a.mask, pa + lane, key);
+                }
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                  if (!(see >> k & 1)) x[k] = y[k] = 0.f;
+              }
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                p16[k] = pack16<T>(x[2 * k], x[2 * k + 1]);
+                d16[k] = pack16<T>(y[2 * k], y[2 * k + 1]);
+              }
             } else {
-              le = make_float4(lse2, lse2, lse2, lse2);
-              de = make_float4(delta, delta, delta, delta);
-            }
-            x[i] = exp2_approx(fmaf(x[i], a.scale_log2, -le.x));
-            x[i + 1] = exp2_approx(fmaf(x[i + 1], a.scale_log2, -le.y));
-            x[i + 2] = exp2_approx(fmaf(x[i + 2], a.scale_log2, -le.z));
-            x[i + 3] = exp2_approx(fmaf(x[i + 3], a.scale_log2, -le.w));
-            y[i] = x[i] * (y[i] - de.x);
-            y[i + 1] = x[i + 1] * (y[i + 1] - de.y);
-            y[i + 2] = x[i + 2] * (y[i + 2] - de.z);
-            y[i + 3] = x[i + 3] * (y[i + 3] - de.w);
-          }
-          // which pairs of the warp's kept rows and these 32 streamed rows see one another
-          bool whole = c + 32 <= s.rows;
-          uint32_t see = bits(0, s.rows - c);
-          const int r0 = w.row0 + (warp & 3) * 32, c0 = s.row0 + c;
-          if constexpr (kKeys) {
-            const int p = c0 + w.shift;
-            if (!all_seen(a.mask, p, p + 31, r0)) {
-              whole = false;
-              see &= bits(cs.lo - p, cs.hi + 1 - p);
-            }
-          } else {
-            const int p = r0 + w.shift;
-            if (!all_seen(a.mask, p, p + 31, c0)) {
-              whole = false;
-              see &= seen_keys(a.mask, p + lane, c0);
-            }
-          }
-          if (!whole) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (!(see >> i & 1)) x[i] = y[i] = 0.f;
+              for (int k = 0; k < 16; ++k) p16[k] = d16[k] = 0;
+            }
+            if constexpr (kKeys) tmem_st16(scores + c / 2, p16);
+            tmem_st16(scores + 64 + c / 2, d16);
           }
-          uint32_t pk[16];
-          if constexpr (kKeys) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) pk[i] = pack16<T>(x[2 * i], x[2 * i + 1]);
-            tmem_st16(scores + c / 2, pk);
-          }
-#pragma unroll
-          for (int i = 0; i < 16; ++i) pk[i] = pack16<T>(y[2 * i], y[2 * i + 1]);
-          tmem_st16(scores + 64 + c / 2, pk);
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(ready + 8 * g);
         }
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(ready + 8 * g);
-      }
       if (!ok) break;
-      if (w.count) {
-        if (!(ok = mbar_wait(acc_full, nk & 1, s_abort))) break;
+      const bool live = row < w.rows;
+      const int64_t at = (((int64_t)w.kept_row + row) * (kKeys ? a.kv_heads : a.heads) + w.h) * a.D;
+      mbar_arrive(item_empty + 8 * slot);
+      const int acc = nk % Sh::kAcc;
+      if (count) {
+        if (!(ok = mbar_wait(acc_full + 8 * acc, (nk / Sh::kAcc) & 1, s_abort))) break;
         tc_fence_after();
       }
-      const int64_t at = (((int64_t)(kKeys ? w.e.k0 : w.e.q0) + w.row0 + row) * (kKeys ? a.kv_heads : a.heads) + w.h) * a.D;
-      if (kGroups == 1 || g == 0)
-        gradient_row<T, DP>(lanes + Sh::kColAcc, w.count > 0, live, a.scale, static_cast<T*>(a.d1) + at, a.D, a.sectors);
-      if (kKeys && g == kGroups - 1)
-        gradient_row<T, DP>(lanes + Sh::kColAcc + DP, w.count > 0, live, 1.f, static_cast<T*>(a.d2) + at, a.D, a.sectors);
-      if (w.count) {
+      // the groups share the stores: dK and dV, or half of dQ each
+      const uint32_t from = lanes + Sh::kColAcc + acc * Sh::kAccColumns;
+      if constexpr (kKeys)
+        gradient_row<T, DP>(from + g * DP, count > 0, live, g == 0 ? a.scale : 1.f,
+                            static_cast<T*>(g == 0 ? a.d1 : a.d2) + at, a.D, a.sectors);
+      else
+        gradient_row<T, DP / 2>(from + g * (DP / 2), count > 0, live, a.scale, static_cast<T*>(a.d1) + at + g * (DP / 2),
+                                a.D - g * (DP / 2), a.sectors);
+      if (count) {
         tc_fence_before();
-        mbar_arrive(acc_empty);
+        mbar_arrive(acc_empty + 8 * acc);
         ++nk;
       }
-      n += w.count;
     }
   }
   const int64_t first = a.B > 0 ? a.offsets[a.B] : 0;
@@ -483,7 +544,7 @@ __global__ void __launch_bounds__(BwdShape<DP, kGroups, kKeys>::kThreads, BwdSha
 struct BwdWorkspace {
   WsHeader* hdr;
   TileItem *queries, *keys;
-  float* delta;
+  float* rows;
   size_t bytes;
 };
 BwdWorkspace carve_backward(void* base, int64_t n_q, int64_t n_kv, int B, int heads) {
@@ -498,22 +559,22 @@ BwdWorkspace carve_backward(void* base, int64_t n_q, int64_t n_kv, int B, int he
   w.hdr = reinterpret_cast<WsHeader*>(p);
   w.queries = reinterpret_cast<TileItem*>(take((max_tiles(n_q, B) + 1) * sizeof(TileItem)));
   w.keys = reinterpret_cast<TileItem*>(take((max_tiles(n_kv, B) + 1) * sizeof(TileItem)));
-  w.delta = reinterpret_cast<float*>(take((size_t)n_q * heads * sizeof(float)));
+  w.rows = reinterpret_cast<float*>(take((size_t)n_q * heads * 2 * sizeof(float)));
   w.bytes = off;
   return w;
 }
 
-template <typename T, int DP, int kGroups, bool kKeys>
+template <typename T, int DP, bool kKeys>
 cudaError_t run(const BwdArgs& a, int64_t items, const CUtensorMap& k1, const CUtensorMap& k2, const CUtensorMap& s1,
                 const CUtensorMap& s2, cudaStream_t s) {
-  using Sh = BwdShape<DP, kGroups, kKeys>;
-  const auto kernel = k_attn_backward<T, DP, kGroups, kKeys>;
+  using Sh = BwdShape<DP, kKeys>;
+  const auto kernel = k_attn_backward<T, DP, kKeys>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sh::kSmem);
   if (e != cudaSuccess) return e;
-  const int64_t slots = (int64_t)device_info().sm_count * Sh::kBlocks;
+  const int64_t slots = device_info().sm_count;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(items < 1 ? 1 : items < slots ? items : slots));
-  cfg.blockDim = dim3(Sh::kThreads);
+  cfg.blockDim = dim3(kBwdThreads);
   cfg.dynamicSmemBytes = Sh::kSmem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -555,7 +616,7 @@ cudaError_t run_backward(const AttnCall& c, const BwdWorkspace& ws, cudaStream_t
   a.scale_log2 = c.scale * kLog2e;
   a.out = c.out;
   a.lse = c.lse;
-  a.delta = ws.delta;
+  a.rows = ws.rows;
   a.B = c.B;
   a.hdr = ws.hdr;
   a.sectors = ((reinterpret_cast<uintptr_t>(c.dq) | reinterpret_cast<uintptr_t>(c.dk) | reinterpret_cast<uintptr_t>(c.dv)) &
@@ -565,14 +626,14 @@ cudaError_t run_backward(const AttnCall& c, const BwdWorkspace& ws, cudaStream_t
     a.d2 = nullptr;
     a.offsets = c.q_offsets;
     a.items = ws.queries;
-    if ((e = run<T, DP, 1, false>(a, max_tiles(c.n_q, c.B) * c.heads, q, d, k, v, s)) != cudaSuccess) return e;
+    if ((e = run<T, DP, false>(a, max_tiles(c.n_q, c.B) * c.heads, q, d, k, v, s)) != cudaSuccess) return e;
   }
   if (c.n_kv > 0) {
     a.d1 = c.dk;
     a.d2 = c.dv;
     a.offsets = c.kv_offsets;
     a.items = ws.keys;
-    if ((e = run<T, DP, DP == 64 ? 1 : 2, true>(a, max_tiles(c.n_kv, c.B) * c.kv_heads, k, v, q, d, s)) != cudaSuccess)
+    if ((e = run<T, DP, true>(a, max_tiles(c.n_kv, c.B) * c.kv_heads, k, v, q, d, s)) != cudaSuccess)
       return e;
   }
   return cudaSuccess;

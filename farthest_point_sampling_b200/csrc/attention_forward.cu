@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
   const uint32_t q_full = bars, k_full = bars + 16, k_empty = bars + 32, v_full = bars + 48, v_empty = bars + 64,
                  s_full = bars + 80, o_full = bars + 88, drain = bars + 96, item_full = bars + 104,
                  item_empty = bars + 120, p_ready = bars + 136, q_empty = bars + 144;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 15; ++i) mbar_init(bars + 8 * i, 1);
@@ -123,32 +123,34 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *s_tmem;
+  const uint32_t tmem = uniform(*s_tmem);
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
   if (warp == kSoftmaxWarps) {
     // ------------------------------------------------ items and loads
-    if (lane == 0) {
+    {
       ItemWalk walk(a.heads, a.hdr->n_items[kQueryTiles]);
       TileItem next = a.items[walk.more() ? walk.tile : 0];
       int i = 0, n = 0, nq = 0;  // items handed out, key tiles and query tiles loaded so far
       for (bool more = true; more; ++i) {
         const int slot = i % kItemRing;
-        if (i >= kItemRing && !mbar_wait(item_empty + 8 * slot, ((i / kItemRing) - 1) & 1, s_abort)) break;
+        if (i >= kItemRing && !mbar_wait_warp(item_empty + 8 * slot, ((i / kItemRing) - 1) & 1, s_abort)) break;
         more = walk.more();
         if (!more) {
-          s_item[slot].count = -1;
-          mbar_arrive(item_full + 8 * slot);
+          if (lane == 0) s_item[slot].count = -1;
+          __syncwarp();
+          mbar_arrive_one(item_full + 8 * slot);
           break;
         }
         const FwdItem w = fwd_item<kMasked>(a, walk.h, next);
         walk.advance();
         if (walk.more()) next = a.items[walk.tile];
-        s_item[slot] = w;
-        mbar_arrive(item_full + 8 * slot);
+        if (lane == 0) s_item[slot] = w;
+        __syncwarp();
+        mbar_arrive_one(item_full + 8 * slot);
         if (w.count == 0) continue;
         const int qs = nq % Sh::kStages;
-        if (nq >= Sh::kStages && !mbar_wait(q_empty + 8 * qs, ((nq / Sh::kStages) - 1) & 1, s_abort)) break;
+        if (nq >= Sh::kStages && !mbar_wait_warp(q_empty + 8 * qs, ((nq / Sh::kStages) - 1) & 1, s_abort)) break;
         const int q_boxes = (w.rows + 63) / 64;
         mbar_expect(q_full + 8 * qs, q_boxes * 8192 * Sh::kPanels);
 #pragma unroll 1
@@ -164,7 +166,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
           const uint32_t round = ((n / Sh::kStages) - 1) & 1;
           const int boxes = (w.keys.extent(j) + 63) / 64;
           const int krow = w.k_row + w.keys.start(j);
-          if (n >= Sh::kStages && !(more = mbar_wait(k_empty + 8 * st, round, s_abort))) break;
+          if (n >= Sh::kStages && !(more = mbar_wait_warp(k_empty + 8 * st, round, s_abort))) break;
           mbar_expect(k_full + 8 * st, boxes * 8192 * Sh::kPanels);
 #pragma unroll 1
           for (int b = 0; b < boxes; ++b)
@@ -172,7 +174,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
             for (int p = 0; p < Sh::kPanels; ++p)
               tma_load(smem_u32(s_k) + st * Sh::kTileBytes + p * kPanel + b * 8192, &map_k, k_full + 8 * st, p * 64, g,
                        krow + b * 64);
-          if (n >= Sh::kStages && !(more = mbar_wait(v_empty + 8 * st, round, s_abort))) break;
+          if (n >= Sh::kStages && !(more = mbar_wait_warp(v_empty + 8 * st, round, s_abort))) break;
           mbar_expect(v_full + 8 * st, boxes * 8192 * Sh::kPanels);
 #pragma unroll 1
           for (int b = 0; b < boxes; ++b)
@@ -183,40 +185,44 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
         }
       }
       // after a wait that gave up: this thread's copies still in flight land first
-      if (*s_abort) {
+      if (__any_sync(kFull, *s_abort)) {
         volatile int none = 0;
         for (int b = 0; b < Sh::kStages; ++b) {
           const int lq = nq - 1 - b, lk = n - b;  // tile n may have its keys loading, not its values
-          if (lq >= 0) mbar_wait(q_full + 8 * (lq % Sh::kStages), (lq / Sh::kStages) & 1, &none);
-          if (lk >= 0) mbar_wait(k_full + 8 * (lk % Sh::kStages), (lk / Sh::kStages) & 1, &none);
-          if (lk >= 1) mbar_wait(v_full + 8 * ((lk - 1) % Sh::kStages), ((lk - 1) / Sh::kStages) & 1, &none);
+          if (lq >= 0) mbar_wait_warp(q_full + 8 * (lq % Sh::kStages), (lq / Sh::kStages) & 1, &none);
+          if (lk >= 0) mbar_wait_warp(k_full + 8 * (lk % Sh::kStages), (lk / Sh::kStages) & 1, &none);
+          if (lk >= 1) mbar_wait_warp(v_full + 8 * ((lk - 1) % Sh::kStages), ((lk - 1) / Sh::kStages) & 1, &none);
         }
       }
     }
   } else if (warp == kSoftmaxWarps + 1) {
     // ------------------------------------------------ products
-    if (lane == 0) {
+    {
       int n = 0, nq = 0;
       const int d_steps = (a.D + 15) / 16;
       const uint32_t pv_desc = mma_desc(kBf16, false, true, d_steps * 16);
       bool ok = true;
       for (int i = 0; ok; ++i) {
         const int slot = i % kItemRing;
-        if (!(ok = mbar_wait(item_full + 8 * slot, (i / kItemRing) & 1, s_abort))) break;
-        const int count = s_item[slot].count;
-        const KeyTiles<kTile> keys = s_item[slot].keys;
-        mbar_arrive(item_empty + 8 * slot);
+        if (!(ok = mbar_wait_warp(item_full + 8 * slot, (i / kItemRing) & 1, s_abort))) break;
+        const int count = uniform(s_item[slot].count);
+        KeyTiles<kTile> keys;
+        keys.before = uniform(s_item[slot].keys.before);
+        keys.first = uniform(s_item[slot].keys.first);
+        keys.end = uniform(s_item[slot].keys.end);
+        keys.s = uniform(s_item[slot].keys.s);
+        mbar_arrive_one(item_empty + 8 * slot);
         if (count < 0) break;
         if (count == 0) continue;
         const int qs = nq % Sh::kStages;
         const uint32_t q = smem_desc(smem_u32(s_q) + qs * Sh::kTileBytes, kPanel);
-        if (!(ok = mbar_wait(q_full + 8 * qs, (nq / Sh::kStages) & 1, s_abort))) break;
+        if (!(ok = mbar_wait_warp(q_full + 8 * qs, (nq / Sh::kStages) & 1, s_abort))) break;
         for (int j = 0; j <= count; ++j) {
           if (j > 0) {  // O += P V of tile j - 1
             const int m = n + j - 1, st = m % Sh::kStages;
             const int steps = (keys.extent(j - 1) + 15) / 16;
-            if (!(ok = mbar_wait(v_full + 8 * st, (m / Sh::kStages) & 1, s_abort))) break;
-            if (!(ok = mbar_wait(p_ready, m & 1, s_abort))) break;
+            if (!(ok = mbar_wait_warp(v_full + 8 * st, (m / Sh::kStages) & 1, s_abort))) break;
+            if (!(ok = mbar_wait_warp(p_ready, m & 1, s_abort))) break;
             tc_fence_after();
             const uint32_t v = smem_desc(smem_u32(s_v) + st * Sh::kTileBytes, kPanel);
 #pragma unroll
@@ -228,7 +234,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
           if (j < count) {  // S = Q K^T of tile j; over P, which the product before has read
             const int m = n + j, st = m % Sh::kStages;
             const int cols = (keys.extent(j) + 15) / 16 * 16;
-            if (!(ok = mbar_wait(k_full + 8 * st, (m / Sh::kStages) & 1, s_abort))) break;
+            if (!(ok = mbar_wait_warp(k_full + 8 * st, (m / Sh::kStages) & 1, s_abort))) break;
             tc_fence_after();
             const uint32_t k = smem_desc(smem_u32(s_k) + st * Sh::kTileBytes, kPanel);
             const uint32_t qk_desc = mma_desc(kBf16, false, false, cols);
@@ -245,10 +251,10 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
         n += count;
         ++nq;
       }
-      if (*s_abort) {  // products in flight end before TMEM is freed
+      if (__any_sync(kFull, *s_abort)) {  // products in flight end before TMEM is freed
         volatile int none = 0;
         mma_commit(drain);
-        mbar_wait(drain, 0, &none);
+        mbar_wait_warp(drain, 0, &none);
       }
     }
   } else {

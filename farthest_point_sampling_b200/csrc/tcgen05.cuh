@@ -11,6 +11,16 @@ namespace fpstok {
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
+// The loading and the issuing warp run as whole warps with the same values in
+// every lane, and single-thread instructions elect one lane themselves: TMA
+// and tcgen05 operands live in uniform registers, which the compiler can only
+// use where it sees that a warp agrees.  Issued from inside a one-lane branch
+// a product took 80 cycles of its warp.
+#define FPS_ELECT ".reg .pred elected;\n\telect.sync _|elected, 0xffffffff;\n\t"
+
+// A value that every lane of the warp holds alike.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 // ---------------------------------------------------------------- mbarriers
 
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
@@ -19,8 +29,14 @@ __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// By a whole warp: one arrival.
+__device__ __forceinline__ void mbar_arrive_one(uint32_t bar) {
+  asm volatile("{\n\t" FPS_ELECT "@elected mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar) : "memory");
+}
 __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+  asm volatile("{\n\t" FPS_ELECT "@elected mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar),
+               "r"(bytes)
+               : "memory");
 }
 // A poll sleeps in hardware for up to kWaitNs; polled without that, the waits
 // took half of the softmax warps' issue slots.
@@ -50,25 +66,20 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   return true;
 }
 
-// Registers of a warp group (all its warps execute this).  The shares of a
-// block add up to at most what it was launched with.
-template <int kRegs>
-__device__ __forceinline__ void regs_up() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
-template <int kRegs>
-__device__ __forceinline__ void regs_down() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+// By a whole warp, with the same answer for every lane.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
 }
 
 // ---------------------------------------------------------------- TMA
 
+// By a whole warp: one box.
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
-          dst),
-      "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
-      : "memory");
+  asm volatile("{\n\t" FPS_ELECT
+               "@elected cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
+               "%4, %5}], [%2];\n\t}" ::"r"(dst),
+               "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
+               : "memory");
 }
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
@@ -182,27 +193,29 @@ __host__ __device__ constexpr uint32_t mma_desc(bool bf16, bool a_mn, bool b_mn,
          ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
-// D[tmem] (+)= A[smem] B[smem], by one thread; a and b are low descriptor words.
+// D[tmem] (+)= A[smem] B[smem], by a whole warp; a and b are low descriptor words.
 __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "{\n\t" FPS_ELECT ".reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.u32 p, %4, 0;\n\t"
       "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+      "@elected tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
       "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(kDescHigh)
       : "memory");
 }
 // D[tmem] (+)= A[tmem] B[smem].
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "{\n\t" FPS_ELECT ".reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.u32 p, %4, 0;\n\t"
       "mov.b64 y, {%2, %5};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+      "@elected tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
       "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(kDescHigh)
       : "memory");
 }
-// Arrives on `bar` once every tcgen05 operation this thread issued before is done.
+// Arrives on `bar` once every tcgen05 operation this warp issued before is done.
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+  asm volatile("{\n\t" FPS_ELECT
+               "@elected tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+               : "memory");
 }
 
 }  // namespace fpstok
