@@ -280,8 +280,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     // ------------------------------------------------ products
     {
       int m = 0, nk = 0;  // tiles and items with tiles so far
-      const int d_steps = (a.D + 15) / 16;
-      const uint32_t out_desc = mma_desc(kBf16, false, true, d_steps * 16);
+      const uint32_t out_desc = mma_desc(kBf16, false, true, (a.D + 15) / 16 * 16);
       bool ok = true;
       // The scores of a tile are issued before the gradients from the tile
       // before it, which may be the last of the item before.
@@ -298,15 +297,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         tc_fence_after();
         const uint32_t from = smem_desc(smem_u32(s_ring) + 2 * st * Sh::kStreamBytes, kStreamPanel);
         const uint32_t to = tmem + Sh::kColAcc + acc * Sh::kAccColumns, scores = tmem + g * 128;
-        if constexpr (kKeys) {  // dV += P^T dO
-#pragma unroll
-          for (int k = 0; k < kStream / 16; ++k)
-            if (k < p.steps)
-              mma_ts(to + DP, scores + k * 8, from + (Sh::kStreamBytes >> 4) + k * 128, out_desc, k > 0 || !p.first);
-        }
-#pragma unroll
-        for (int k = 0; k < kStream / 16; ++k)  // dK += dS^T Q, or dQ += dS K
-          if (k < p.steps) mma_ts(to, scores + 64 + k * 8, from + k * 128, out_desc, k > 0 || !p.first);
+        if constexpr (kKeys)  // dV += P^T dO
+          mma_ts_steps(to + DP, scores, from + (Sh::kStreamBytes >> 4), p.steps, out_desc, !p.first);
+        mma_ts_steps(to, scores + 64, from, p.steps, out_desc, !p.first);  // dK += dS^T Q, or dQ += dS K
         mma_commit(ring_empty + 8 * st);
         if (p.last) {
           mma_commit(kept_empty + 8 * p.kept);
@@ -345,14 +338,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             const int steps = (tiles.extent(j) + 15) / 16;
             const uint32_t desc = mma_desc(kBf16, false, false, steps * 16);
             const uint32_t from = smem_desc(smem_u32(s_ring) + 2 * st * Sh::kStreamBytes, kStreamPanel);
-            // over the P and dS of two tiles before, which their products have read
+            // over the P and dS of two tiles before, which their products have
+            // read; whole panels: values past D are zeros
 #pragma unroll
             for (int x = 0; x < 2; ++x)
 #pragma unroll
-              for (int k = 0; k < DP / 16; ++k)
-                if (k < d_steps)
-                  mma_ss(tmem + g * 128 + x * 64, kept + ((x * Sh::kKeptBytes + (k >> 2) * kPanel + (k & 3) * 32) >> 4),
-                         from + ((x * Sh::kStreamBytes + (k >> 2) * kStreamPanel + (k & 3) * 32) >> 4), desc, k > 0);
+              for (int q = 0; q < Sh::kPanels; ++q)
+                mma_ss4(tmem + g * 128 + x * 64, kept + ((x * Sh::kKeptBytes + q * kPanel) >> 4),
+                        from + ((x * Sh::kStreamBytes + q * kStreamPanel) >> 4), desc, q > 0);
             mma_commit(score_full + 8 * g);
             if (p.held && !(ok = gradients())) break;
             p.tile = m;

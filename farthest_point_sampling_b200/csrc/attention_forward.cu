@@ -199,8 +199,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     // ------------------------------------------------ products
     {
       int n = 0, nq = 0;
-      const int d_steps = (a.D + 15) / 16;
-      const uint32_t pv_desc = mma_desc(kBf16, false, true, d_steps * 16);
+      const uint32_t pv_desc = mma_desc(kBf16, false, true, (a.D + 15) / 16 * 16);
       bool ok = true;
       for (int i = 0; ok; ++i) {
         const int slot = i % kItemRing;
@@ -225,9 +224,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
             if (!(ok = mbar_wait_warp(p_ready, m & 1, s_abort))) break;
             tc_fence_after();
             const uint32_t v = smem_desc(smem_u32(s_v) + st * Sh::kTileBytes, kPanel);
-#pragma unroll
-            for (int ks = 0; ks < kTile / 16; ++ks)
-              if (ks < steps) mma_ts(tmem + kColO, tmem + ks * 8, v + ks * 128, pv_desc, ks > 0 || j > 1);
+            mma_ts_steps(tmem + kColO, tmem, v, steps, pv_desc, j > 1);
             mma_commit(v_empty + 8 * st);
             if (j == count) mma_commit(o_full);
           }
@@ -238,11 +235,9 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
             tc_fence_after();
             const uint32_t k = smem_desc(smem_u32(s_k) + st * Sh::kTileBytes, kPanel);
             const uint32_t qk_desc = mma_desc(kBf16, false, false, cols);
+            // whole panels: values past D are zeros
 #pragma unroll
-            for (int ks = 0; ks < DP / 16; ++ks) {
-              const uint32_t at = ((ks >> 2) * kPanel + (ks & 3) * 32) >> 4;
-              if (ks < d_steps) mma_ss(tmem, q + at, k + at, qk_desc, ks > 0);
-            }
+            for (int p = 0; p < Sh::kPanels; ++p) mma_ss4(tmem, q + p * (kPanel >> 4), k + p * (kPanel >> 4), qk_desc, p > 0);
             mma_commit(k_empty + 8 * st);
             mma_commit(s_full);
             if (j == count - 1) mma_commit(q_empty + 8 * qs);

@@ -193,15 +193,7 @@ __host__ __device__ constexpr uint32_t mma_desc(bool bf16, bool a_mn, bool b_mn,
          ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
-// D[tmem] (+)= A[smem] B[smem], by a whole warp; a and b are low descriptor words.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
-  asm volatile(
-      "{\n\t" FPS_ELECT ".reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
-      "@elected tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(kDescHigh)
-      : "memory");
-}
+// By a whole warp; a and b are low descriptor words.
 // D[tmem] (+)= A[tmem] B[smem].
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
   asm volatile(
@@ -211,6 +203,44 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint3
       "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(kDescHigh)
       : "memory");
 }
+// Four steps of 16 values at once, one election for all: 64 values along the
+// rows of both operands, or 64 rows of B against 32 columns of A in TMEM.
+__device__ __forceinline__ void mma_ss4(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t" FPS_ELECT ".reg .pred p, t;\n\t.reg .b64 x, y;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.eq.u32 t, 0, 0;\n\t"
+      "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+      "@elected tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t"
+      "add.s64 x, x, 2;\n\tadd.s64 y, y, 2;\n\t"
+      "@elected tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
+      "add.s64 x, x, 2;\n\tadd.s64 y, y, 2;\n\t"
+      "@elected tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
+      "add.s64 x, x, 2;\n\tadd.s64 y, y, 2;\n\t"
+      "@elected tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(kDescHigh)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts4(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t" FPS_ELECT ".reg .pred p, t;\n\t.reg .b64 y;\n\t.reg .b32 x;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "setp.eq.u32 t, 0, 0;\n\tmov.b64 y, {%2, %5};\n\tmov.b32 x, %1;\n\t"
+      "@elected tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, p;\n\t"
+      "add.s64 y, y, 128;\n\tadd.u32 x, x, 8;\n\t"
+      "@elected tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, t;\n\t"
+      "add.s64 y, y, 128;\n\tadd.u32 x, x, 8;\n\t"
+      "@elected tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, t;\n\t"
+      "add.s64 y, y, 128;\n\tadd.u32 x, x, 8;\n\t"
+      "@elected tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, t;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(kDescHigh)
+      : "memory");
+}
+// `steps` steps of 16 rows of B.
+__device__ __forceinline__ void mma_ts_steps(uint32_t d, uint32_t a, uint32_t b, int steps, uint32_t idesc, bool accumulate) {
+#pragma unroll 1
+  for (; steps >= 4; steps -= 4, a += 32, b += 512, accumulate = true) mma_ts4(d, a, b, idesc, accumulate);
+#pragma unroll 1
+  for (; steps > 0; --steps, a += 8, b += 128, accumulate = true) mma_ts(d, a, b, idesc, accumulate);
+}
+
 // Arrives on `bar` once every tcgen05 operation this warp issued before is done.
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
   asm volatile("{\n\t" FPS_ELECT
