@@ -5,7 +5,7 @@
 // the K and V gradients summed over the query heads that share them.
 //
 // Two kernels, one template.  A work item keeps a 128-row tile of one pair of
-// tensors and streams 64-row tiles of the other past it:
+// tensors and streams 128-row tiles of the other past it:
 //   queries: keeps Q, dO of one query tile and head, streams K, V:
 //            scores S = Q K^T and dP = dO V^T, then dQ += dS K;
 //   keys:    keeps K, V of one key tile and key head, streams Q, dO of every
@@ -15,14 +15,15 @@
 // one block in a fixed order, so the result does not depend on scheduling;
 // the price is that the scores are formed twice.
 //
-// Roles as in the forward kernel: a loading warp, an issuing thread, and two
-// groups of four softmax warps with one kept row per thread that take the
-// streamed tiles in turn, so that one group's softmax runs under the other's
-// products; P and dS go back to TMEM as 16-bit operand A.  TMEM holds two
-// stages of scores (128 columns each) and the accumulators, two sets of them
-// where they fit, so that a block goes on with the next item while it stores
-// one.  One block takes an SM; the products bound it, at 64 streamed rows by
-// the shared-memory reads of their two operands.
+// Roles as in the forward kernel: a loading warp, an issuing warp, and eight
+// softmax warps with two threads per kept row, each for half of a tile's
+// streamed rows.  P and dS go back to TMEM as 16-bit operand A, each over the
+// scores its thread read.  The products of a tile are spread under the softmax
+// of it and the next: S of tile m + 1 runs while dS of tile m is formed, then
+// dK of m and dP of m + 1 run while the weights of m + 1 are.  One block takes
+// an SM with all of its TMEM: 128 columns each of S and dP, and the
+// accumulators, two sets of them where they fit, so that a block goes on with
+// the next item while it stores one.
 //
 // Rounding: P and dS are rounded to the input type for their products.  D
 // comes from the rounded output, as the forward left it.
@@ -38,12 +39,13 @@ namespace fpstok {
 
 namespace {
 
-constexpr int kStream = 64;                   // rows of a streamed tile
-constexpr int kStreamPanel = kStream * 128;   // bytes of one of its 64-value panels
-constexpr int kPanel = kTile * 128;
-constexpr int kGroups = 2;                    // softmax groups, and stages of scores
-constexpr int kBwdThreads = 32 * (4 * kGroups + 2);
+constexpr int kStream = 128;                  // rows of a streamed tile
+constexpr int kHalf = kStream / 2;            // of which a thread takes half
+constexpr int kPanel = kTile * 128;           // bytes of a tile's 64-value panel
+constexpr int kSoftmaxThreads = 256;
+constexpr int kBwdThreads = kSoftmaxThreads + 64;
 constexpr int kItemRing = 2;
+constexpr uint32_t kColS = 0, kColDP = 128, kColAcc = 256;
 
 struct BwdArgs {
   int64_t n_q, n_kv;
@@ -101,16 +103,14 @@ __device__ __forceinline__ BwdItem bwd_item(const BwdArgs& a, int h, const TileI
 template <int DP, bool kKeys>
 struct BwdShape {
   static constexpr int kPanels = DP / 64;
-  static constexpr uint32_t kKeptBytes = kPanels * kPanel;          // one kept tensor's tile
-  static constexpr uint32_t kStreamBytes = kPanels * kStreamPanel;  // one streamed tensor's tile
-  // 64 KB of kept tiles, 96 or 128 KB of streamed ones
+  static constexpr uint32_t kTileBytes = kPanels * kPanel;  // one tensor's tile
+  // 192 KB: kept and streamed pairs of tiles
   static constexpr int kKept = DP == 64 ? 2 : 1;
-  static constexpr int kRing = DP == 64 ? 6 : 4;
-  static constexpr uint32_t kColAcc = 128 * kGroups;
+  static constexpr int kRing = DP == 64 ? 4 : 2;
   static constexpr uint32_t kAccColumns = (kKeys ? 2 : 1) * DP;
   static constexpr int kAcc = kColAcc + 2 * kAccColumns <= 512 ? 2 : 1;
   static constexpr uint32_t kColumns = 512;
-  static constexpr size_t kSmem = 1024 + 2 * (kKept * kKeptBytes + kRing * kStreamBytes) + kRing * 512 +
+  static constexpr size_t kSmem = 1024 + 2 * (kKept + kRing) * kTileBytes + kRing * 2 * kStream * sizeof(float) +
                                   kItemRing * sizeof(BwdItem) + 512;
 };
 
@@ -152,36 +152,40 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     const __grid_constant__ CUtensorMap map_s1, const __grid_constant__ CUtensorMap map_s2) {
   using Sh = BwdShape<DP, kKeys>;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
-  constexpr int kLoadWarp = 4 * kGroups, kMmaWarp = kLoadWarp + 1;
+  constexpr int kLoadWarp = kSoftmaxThreads / 32, kMmaWarp = kLoadWarp + 1;
   extern __shared__ uint8_t s_raw[];
   uint8_t* s_base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~(uintptr_t)1023);
   // kept tiles (tensor 1 and 2 of a stage side by side), then the streamed
-  // ring, then the ring's -lse and -D of 64 queries (keys kernel)
+  // ring, then the ring's -lse log2(e) and -D of 128 queries (keys kernel)
   uint8_t* s_kept = s_base;
-  uint8_t* s_ring = s_kept + 2 * Sh::kKept * Sh::kKeptBytes;
-  float* s_col = reinterpret_cast<float*>(s_ring + 2 * Sh::kRing * Sh::kStreamBytes);
-  BwdItem* s_item = reinterpret_cast<BwdItem*>(s_col + Sh::kRing * 128);
+  uint8_t* s_ring = s_kept + 2 * Sh::kKept * Sh::kTileBytes;
+  float* s_col = reinterpret_cast<float*>(s_ring + 2 * Sh::kRing * Sh::kTileBytes);
+  BwdItem* s_item = reinterpret_cast<BwdItem*>(s_col + Sh::kRing * 2 * kStream);
   uint64_t* s_bar = reinterpret_cast<uint64_t*>(s_item + kItemRing);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_bar + 32);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   const uint32_t bars = smem_u32(s_bar);
-  const uint32_t kept_full = bars, kept_empty = bars + 16, score_full = bars + 32, acc_full = bars + 48,
-                 item_full = bars + 64, drain = bars + 80, item_empty = bars + 88, ready = bars + 104,
-                 acc_empty = bars + 120, ring_full = bars + 136, ring_empty = bars + 184;
+  const uint32_t kept_full = bars, kept_empty = bars + 16, acc_full = bars + 32, acc_empty = bars + 48,
+                 item_full = bars + 64, item_empty = bars + 80, s_full = bars + 96, dp_full = bars + 104,
+                 p_ready = bars + 112, ds_ready = bars + 120, drain = bars + 128, ring_full = bars + 136,
+                 ring_empty = bars + 168;
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (const uint32_t b : {kept_full, score_full, acc_full, item_full, drain}) {
-      mbar_init(b, 1);
-      if (b != drain) mbar_init(b + 8, 1);
-    }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(item_empty + 8 * i, 128 * kGroups + 1);
+      mbar_init(kept_full + 8 * i, 1);
       // in the queries kernel the softmax threads read the kept dO themselves
-      mbar_init(kept_empty + 8 * i, kKeys ? 1 : 1 + 128 * kGroups);
-      mbar_init(ready + 8 * i, 128);
-      mbar_init(acc_empty + 8 * i, 128 * kGroups);
+      mbar_init(kept_empty + 8 * i, kKeys ? 1 : 1 + kSoftmaxThreads);
+      mbar_init(acc_full + 8 * i, 1);
+      mbar_init(acc_empty + 8 * i, kSoftmaxThreads);
+      mbar_init(item_full + 8 * i, 1);
+      mbar_init(item_empty + 8 * i, kSoftmaxThreads + 1);
     }
+    mbar_init(s_full, 1);
+    mbar_init(dp_full, 1);
+    mbar_init(p_ready, kSoftmaxThreads);
+    mbar_init(ds_ready, kSoftmaxThreads);
+    mbar_init(drain, 1);
     for (int i = 0; i < Sh::kRing; ++i) {
       mbar_init(ring_full + 8 * i, kKeys ? 33 : 1);  // the tiles, and in the keys kernel each lane's -lse and -D
       mbar_init(ring_empty + 8 * i, 1);
@@ -224,18 +228,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       if (w.count == 0) continue;
       const int ks = nk % Sh::kKept;
       if (nk >= Sh::kKept && !mbar_wait_warp(kept_empty + 8 * ks, ((nk / Sh::kKept) - 1) & 1, s_abort)) break;
-      {
-        const int boxes = (w.rows + 63) / 64;
-        mbar_expect(kept_full + 8 * ks, 2 * boxes * 8192 * Sh::kPanels);
+      const int boxes = (w.rows + 63) / 64;
+      mbar_expect(kept_full + 8 * ks, 2 * boxes * 8192 * Sh::kPanels);
 #pragma unroll 1
-        for (int b = 0; b < boxes; ++b)
+      for (int b = 0; b < boxes; ++b)
 #pragma unroll
-          for (int p = 0; p < Sh::kPanels; ++p) {
-            const uint32_t to = smem_u32(s_kept) + 2 * ks * Sh::kKeptBytes + p * kPanel + b * 8192;
-            tma_load(to, &map_k1, kept_full + 8 * ks, p * 64, w.h, w.kept_row + b * 64);
-            tma_load(to + Sh::kKeptBytes, &map_k2, kept_full + 8 * ks, p * 64, w.h, w.kept_row + b * 64);
-          }
-      }
+        for (int p = 0; p < Sh::kPanels; ++p) {
+          const uint32_t to = smem_u32(s_kept) + 2 * ks * Sh::kTileBytes + p * kPanel + b * 8192;
+          tma_load(to, &map_k1, kept_full + 8 * ks, p * 64, w.h, w.kept_row + b * 64);
+          tma_load(to + Sh::kTileBytes, &map_k2, kept_full + 8 * ks, p * 64, w.h, w.kept_row + b * 64);
+        }
       ++nk;
       const int head0 = kKeys ? w.h * a.group : w.h / a.group;
 #pragma unroll 1
@@ -244,20 +246,20 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         for (int j = 0; j < w.count; ++j, ++n) {
           const int st = n % Sh::kRing;
           if (n >= Sh::kRing && !(ok = mbar_wait_warp(ring_empty + 8 * st, ((n / Sh::kRing) - 1) & 1, s_abort))) break;
-          const int row = w.stream_row + w.tiles.start(j);
-          {
-            mbar_expect(ring_full + 8 * st, 2 * Sh::kStreamBytes);
+          const int row = w.stream_row + w.tiles.start(j), extent = w.tiles.extent(j);
+          const int sboxes = (extent + 63) / 64;
+          mbar_expect(ring_full + 8 * st, 2 * sboxes * 8192 * Sh::kPanels);
+#pragma unroll 1
+          for (int b = 0; b < sboxes; ++b)
 #pragma unroll
             for (int p = 0; p < Sh::kPanels; ++p) {
-              const uint32_t to = smem_u32(s_ring) + 2 * st * Sh::kStreamBytes + p * kStreamPanel;
-              tma_load(to, &map_s1, ring_full + 8 * st, p * 64, head0 + hd, row);
-              tma_load(to + Sh::kStreamBytes, &map_s2, ring_full + 8 * st, p * 64, head0 + hd, row);
+              const uint32_t to = smem_u32(s_ring) + 2 * st * Sh::kTileBytes + p * kPanel + b * 8192;
+              tma_load(to, &map_s1, ring_full + 8 * st, p * 64, head0 + hd, row + b * 64);
+              tma_load(to + Sh::kTileBytes, &map_s2, ring_full + 8 * st, p * 64, head0 + hd, row + b * 64);
             }
-          }
           if constexpr (kKeys) {
-            const int extent = w.tiles.extent(j);
             const float* from = a.rows + (int64_t)(head0 + hd) * a.n_q + row;
-            const uint32_t to = smem_u32(s_col + st * 128);
+            const uint32_t to = smem_u32(s_col + st * 2 * kStream);
 #pragma unroll
             for (int x = 0; x < 2; ++x)
 #pragma unroll
@@ -278,99 +280,108 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------ products
-    {
-      int m = 0, nk = 0;  // tiles and items with tiles so far
-      const uint32_t out_desc = mma_desc(kBf16, false, true, (a.D + 15) / 16 * 16);
-      bool ok = true;
-      // The scores of a tile are issued before the gradients from the tile
-      // before it, which may be the last of the item before.
-      struct {
-        int tile, steps, item, kept;
-        bool first, last, held;
-      } p = {};
-      const auto gradients = [&]() {
-        const int st = p.tile % Sh::kRing, g = p.tile % kGroups, acc = p.item % Sh::kAcc;
-        if (p.first && p.item >= Sh::kAcc &&
-            !mbar_wait_warp(acc_empty + 8 * acc, ((p.item / Sh::kAcc) - 1) & 1, s_abort))
-          return false;
-        if (!mbar_wait_warp(ready + 8 * g, (p.tile / kGroups) & 1, s_abort)) return false;
-        tc_fence_after();
-        const uint32_t from = smem_desc(smem_u32(s_ring) + 2 * st * Sh::kStreamBytes, kStreamPanel);
-        const uint32_t to = tmem + Sh::kColAcc + acc * Sh::kAccColumns, scores = tmem + g * 128;
-        if constexpr (kKeys)  // dV += P^T dO
-          mma_ts_steps(to + DP, scores, from + (Sh::kStreamBytes >> 4), p.steps, out_desc, !p.first);
-        mma_ts_steps(to, scores + 64, from, p.steps, out_desc, !p.first);  // dK += dS^T Q, or dQ += dS K
-        mma_commit(ring_empty + 8 * st);
-        if (p.last) {
-          mma_commit(kept_empty + 8 * p.kept);
-          mma_commit(acc_full + 8 * acc);
-        }
-        return true;
-      };
-      for (int i = 0; ok; ++i) {
+    const uint32_t out_desc = mma_desc(kBf16, false, true, (a.D + 15) / 16 * 16);
+    const int heads = kKeys ? a.group : 1;
+    // The next tile in the order of the work, across items: its item's kept
+    // stage and accumulators, and whether it is the item's first and last.
+    struct Tile {
+      int steps, kept, item;
+      bool first, last;
+    };
+    int i = 0, hd = 0, j = 0, count = 0, items = 0, fetched = 0;  // items read, place in the item, items with tiles
+    KeyTiles<kStream> tiles = {};
+    bool ok = true;
+    const auto fetch = [&](Tile* t) {  // false when the work is done, or a wait gave up (ok)
+      while (hd == heads || count == 0) {
         const int slot = i % kItemRing;
-        if (!(ok = mbar_wait_warp(item_full + 8 * slot, (i / kItemRing) & 1, s_abort))) break;
-        const int count = uniform(s_item[slot].count);
-        KeyTiles<kStream> tiles;
+        if (!(ok = mbar_wait_warp(item_full + 8 * slot, (i / kItemRing) & 1, s_abort))) return false;
+        count = uniform(s_item[slot].count);
         tiles.before = uniform(s_item[slot].tiles.before);
         tiles.first = uniform(s_item[slot].tiles.first);
         tiles.end = uniform(s_item[slot].tiles.end);
         tiles.s = uniform(s_item[slot].tiles.s);
         mbar_arrive_one(item_empty + 8 * slot);
-        if (count < 0) break;
+        if (count < 0) return false;
+        ++i;
+        hd = j = 0;
         if (count == 0) continue;
-        const int ks = nk % Sh::kKept;
-        const uint32_t kept = smem_desc(smem_u32(s_kept) + 2 * ks * Sh::kKeptBytes, kPanel);
-        // With one stage of kept tiles their load waits for the last item's gradients.
-        if (Sh::kKept == 1 && p.held) {
-          if (!(ok = gradients())) break;
-          p.held = false;
-        }
-        if (!(ok = mbar_wait_warp(kept_full + 8 * ks, (nk / Sh::kKept) & 1, s_abort))) break;
-        const int heads = kKeys ? a.group : 1;
-#pragma unroll 1
-        for (int hd = 0; hd < heads && ok; ++hd)
-#pragma unroll 1
-          for (int j = 0; j < count; ++j, ++m) {
-            const int st = m % Sh::kRing, g = m % kGroups;
-            if (!(ok = mbar_wait_warp(ring_full + 8 * st, (m / Sh::kRing) & 1, s_abort))) break;
-            tc_fence_after();
-            const int steps = (tiles.extent(j) + 15) / 16;
-            const uint32_t desc = mma_desc(kBf16, false, false, steps * 16);
-            const uint32_t from = smem_desc(smem_u32(s_ring) + 2 * st * Sh::kStreamBytes, kStreamPanel);
-            // over the P and dS of two tiles before, which their products have
-            // read; whole panels: values past D are zeros
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-#pragma unroll
-              for (int q = 0; q < Sh::kPanels; ++q)
-                mma_ss4(tmem + g * 128 + x * 64, kept + ((x * Sh::kKeptBytes + q * kPanel) >> 4),
-                        from + ((x * Sh::kStreamBytes + q * kStreamPanel) >> 4), desc, q > 0);
-            mma_commit(score_full + 8 * g);
-            if (p.held && !(ok = gradients())) break;
-            p.tile = m;
-            p.steps = steps;
-            p.item = nk;
-            p.kept = ks;
-            p.first = hd == 0 && j == 0;
-            p.last = hd == heads - 1 && j == count - 1;
-            p.held = true;
-          }
-        ++nk;
+        const int ks = items % Sh::kKept;
+        if (!(ok = mbar_wait_warp(kept_full + 8 * ks, (items / Sh::kKept) & 1, s_abort))) return false;
+        ++items;
       }
-      if (ok && p.held) gradients();
-      if (__any_sync(kFull, *s_abort)) {  // products in flight end before TMEM is freed
-        volatile int none = 0;
-        mma_commit(drain);
-        mbar_wait_warp(drain, 0, &none);
+      const int st = fetched % Sh::kRing;
+      if (!(ok = mbar_wait_warp(ring_full + 8 * st, (fetched / Sh::kRing) & 1, s_abort))) return false;
+      ++fetched;
+      t->steps = (tiles.extent(j) + 15) / 16;
+      t->item = items - 1;
+      t->kept = t->item % Sh::kKept;
+      t->first = hd == 0 && j == 0;
+      t->last = hd == heads - 1 && j == count - 1;
+      if (++j == count) {
+        j = 0;
+        ++hd;
       }
+      tc_fence_after();
+      return true;
+    };
+    // S (x = 0) or dP (x = 1) of tile m: a kept and a streamed tensor; whole
+    // panels, as values past D are zeros
+    const auto scores = [&](const Tile& t, int m, int x) {
+      const uint32_t kept = smem_desc(smem_u32(s_kept) + (2 * t.kept + x) * Sh::kTileBytes, kPanel);
+      const uint32_t from = smem_desc(smem_u32(s_ring) + (2 * (m % Sh::kRing) + x) * Sh::kTileBytes, kPanel);
+      const uint32_t desc = mma_desc(kBf16, false, false, t.steps * 16);
+#pragma unroll
+      for (int p = 0; p < Sh::kPanels; ++p)
+        mma_ss4(tmem + (x ? kColDP : kColS), kept + p * (kPanel >> 4), from + p * (kPanel >> 4), desc, p > 0);
+      mma_commit(x ? dp_full : s_full);
+    };
+    // an accumulator += the 16-bit rows over S or dP, times a streamed tensor;
+    // each half of the rows lies over its half of the scores
+    const auto gradient = [&](const Tile& t, int m, uint32_t from, uint32_t to, int x) {
+      const uint32_t rows = smem_desc(smem_u32(s_ring) + (2 * (m % Sh::kRing) + x) * Sh::kTileBytes, kPanel);
+      mma_ts_steps(to, from, rows, min(t.steps, 4), out_desc, !t.first);
+      if (t.steps > 4) mma_ts_steps(to, from + kHalf, rows + 512, t.steps - 4, out_desc, true);
+    };
+    Tile cur, nxt;
+    bool more = fetch(&cur);
+    if (more) {
+      scores(cur, 0, 0);
+      scores(cur, 0, 1);
+      if (cur.last) mma_commit(kept_empty + 8 * cur.kept);
+    }
+    for (int m = 0; more; ++m) {
+      const uint32_t to = tmem + kColAcc + (cur.item % Sh::kAcc) * Sh::kAccColumns;
+      if (cur.first && cur.item >= Sh::kAcc &&
+          !mbar_wait_warp(acc_empty + 8 * (cur.item % Sh::kAcc), ((cur.item / Sh::kAcc) - 1) & 1, s_abort))
+        break;
+      if (!mbar_wait_warp(p_ready, m & 1, s_abort)) break;
+      tc_fence_after();
+      if constexpr (kKeys) gradient(cur, m, tmem + kColS, to + DP, 1);  // dV += P^T dO
+      more = fetch(&nxt);
+      if (!ok) break;
+      if (more) scores(nxt, m + 1, 0);
+      if (!mbar_wait_warp(ds_ready, m & 1, s_abort)) break;
+      tc_fence_after();
+      gradient(cur, m, tmem + kColDP, to, 0);  // dK += dS^T Q, or dQ += dS K
+      mma_commit(ring_empty + 8 * (m % Sh::kRing));
+      if (cur.last) mma_commit(acc_full + 8 * (cur.item % Sh::kAcc));
+      if (more) {
+        scores(nxt, m + 1, 1);
+        if (nxt.last) mma_commit(kept_empty + 8 * nxt.kept);  // only the scores read the kept tiles
+        cur = nxt;
+      }
+    }
+    if (__any_sync(kFull, *s_abort)) {  // products in flight end before TMEM is freed
+      volatile int none = 0;
+      mma_commit(drain);
+      mbar_wait_warp(drain, 0, &none);
     }
   } else {
     // ------------------------------------------------ softmax and its gradient
-    const int g = warp >> 2, quarter = warp & 3;  // warp group: takes the tiles of its score stage
-    const int row = threadIdx.x & 127;
+    const int half = warp >> 2, quarter = warp & 3;
+    const int row = threadIdx.x & 127, h0 = half * kHalf;
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
-    const uint32_t scores = lanes + g * 128;
+    const float2 scale2 = make_float2(a.scale_log2, a.scale_log2);
     int m = 0, nk = 0;
     bool ok = true;
     for (int i = 0; ok; ++i) {
@@ -387,7 +398,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           if (row < w.rows) {
             const int64_t q = (int64_t)w.kept_row + row, at = (int64_t)w.h * a.n_q + q;
             const T* o = static_cast<const T*>(a.out) + (q * a.heads + w.h) * a.D;
-            const uint8_t* d = s_kept + (2 * ks + 1) * Sh::kKeptBytes + row * 128;
+            const uint8_t* d = s_kept + (2 * ks + 1) * Sh::kTileBytes + row * 128;
+#pragma unroll 4
             for (int c = 0; c < a.D / 8; ++c) {
               const uint4 vo = *reinterpret_cast<const uint4*>(o + c * 8);
               const uint4 vd = *reinterpret_cast<const uint4*>(d + (c >> 3) * kPanel + (((c & 7) ^ (row & 7)) << 4));
@@ -401,7 +413,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             }
             lse2 = -a.lse[at] * kLog2e;
             delta = -delta;
-            if (g == 0) {
+            if (half == 0) {
               a.rows[at] = lse2;
               a.rows[(int64_t)a.heads * a.n_q + at] = delta;
             }
@@ -409,93 +421,125 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           mbar_arrive(kept_empty + 8 * ks);
         }
       }
-      const int heads = kKeys ? a.group : 1;
+      const int tiles = count * (kKeys ? a.group : 1);
 #pragma unroll 1
-      for (int hd = 0; hd < heads && ok; ++hd)
-#pragma unroll 1
-        for (int j = 0; j < count; ++j, ++m) {
-          if (m % kGroups != g) continue;
-          const int visit = m / kGroups, st = m % Sh::kRing;
-          const int extent = w.tiles.extent(j), odd = extent & 15;
-          if (kKeys || odd) {
-            // also where -lse and -D are read from
-            if (!(ok = mbar_wait(ring_full + 8 * st, (m / Sh::kRing) & 1, s_abort))) break;
-          }
-          if (odd) {
-            // Streamed rows past the tile's last inside a product's step of 16:
-            // their P and dS are 0, and the rows must be finite for 0 to stay 0.
-            uint8_t* tile = s_ring + 2 * st * Sh::kStreamBytes;
-            constexpr int kTensors = kKeys ? 2 : 1;
-#pragma unroll 1
-            for (int e = row; e < (16 - odd) * 8 * Sh::kPanels * kTensors; e += 128) {
-              const int c = e % (8 * Sh::kPanels * kTensors), r = extent + e / (8 * Sh::kPanels * kTensors);
-              *reinterpret_cast<uint4*>(tile + (c >> 3) * kStreamPanel + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-            }
-            fence_async_smem();
-          }
-          if (!(ok = mbar_wait(score_full + 8 * g, visit & 1, s_abort))) break;
-          tc_fence_after();
-#pragma unroll 1
-          for (int c = 0; c < kStream; c += 32) {
-            if (c >= extent) break;
-            // which pairs of the warp's kept rows and these 32 streamed rows see one another
-            const int r0 = w.at + quarter * 32, c0 = w.tiles.start(j) + c;
-            const int pa = (kKeys ? c0 : r0) + w.shift, key = kKeys ? r0 : c0;
-            uint32_t p16[16], d16[16];
-            if (some_seen(a.mask, pa, pa + 31, key)) {
-              float x[32], y[32];
-              tmem_ld32(scores + c, reinterpret_cast<uint32_t*>(x));
-              tmem_ld32(scores + 64 + c, reinterpret_cast<uint32_t*>(y));
-              tmem_wait_ld32(reinterpret_cast<uint32_t*>(x));
-              tmem_wait_ld32(reinterpret_cast<uint32_t*>(y));
-#pragma unroll
-              for (int k = 0; k < 32; k += 4) {
-                float4 le = make_float4(lse2, lse2, lse2, lse2), de = make_float4(delta, delta, delta, delta);
-                if constexpr (kKeys) {
-                  le = *reinterpret_cast<const float4*>(s_col + st * 128 + c + k);
-                  de = *reinterpret_cast<const float4*>(s_col + st * 128 + kStream + c + k);
-                }
-                const float2 e0 = fma2(make_float2(x[k], x[k + 1]), make_float2(a.scale_log2, a.scale_log2), make_float2(le.x, le.y));
-                const float2 e1 = fma2(make_float2(x[k + 2], x[k + 3]), make_float2(a.scale_log2, a.scale_log2), make_float2(le.z, le.w));
-                x[k] = exp2_approx(e0.x);
-                x[k + 1] = exp2_approx(e0.y);
-                x[k + 2] = exp2_approx(e1.x);
-                x[k + 3] = exp2_approx(e1.y);
-                const uint64_t y0 = mul2(add2(pack2(y[k], y[k + 1]), pack2(de.x, de.y)), pack2(x[k], x[k + 1]));
-                const uint64_t y1 = mul2(add2(pack2(y[k + 2], y[k + 3]), pack2(de.z, de.w)), pack2(x[k + 2], x[k + 3]));
-                y[k] = lo2(y0);
-                y[k + 1] = hi2(y0);
-                y[k + 2] = lo2(y1);
-                y[k + 3] = hi2(y1);
-              }
-              if (c + 32 > extent || !all_seen(a.mask, pa, pa + 31, key)) {
-                uint32_t see = bits(0, extent - c);
-                if constexpr (kKeys) {
-                  const ColumnSpan s = column_span(a.mask, key + lane);
-                  see &= bits(s.lo - pa, s.hi + 1 - pa);
-                } else {
-                  see &= seen_keys(a.mask, pa + lane, key);
-                }
-#pragma unroll
-                for (int k = 0; k < 32; ++k)
-                  if (!(see >> k & 1)) x[k] = y[k] = 0.f;
-              }
-#pragma unroll
-              for (int k = 0; k < 16; ++k) {
-                p16[k] = pack16<T>(x[2 * k], x[2 * k + 1]);
-                d16[k] = pack16<T>(y[2 * k], y[2 * k + 1]);
-              }
-            } else {
-#pragma unroll
-              for (int k = 0; k < 16; ++k) p16[k] = d16[k] = 0;
-            }
-            if constexpr (kKeys) tmem_st16(scores + c / 2, p16);
-            tmem_st16(scores + 64 + c / 2, d16);
-          }
-          tmem_wait_st();
-          tc_fence_before();
-          mbar_arrive(ready + 8 * g);
+      for (int t = 0, j = 0; t < tiles; ++t, ++m) {
+        const int st = m % Sh::kRing;
+        const int extent = w.tiles.extent(j), odd = extent & 15, stream0 = w.tiles.start(j);
+        j = j + 1 == count ? 0 : j + 1;
+        if (kKeys || odd) {
+          // also where -lse and -D are read from
+          if (!(ok = mbar_wait(ring_full + 8 * st, (m / Sh::kRing) & 1, s_abort))) break;
         }
+        if (odd) {
+          // Streamed rows past the tile's last inside a product's step of 16:
+          // their P and dS are 0, and the rows must be finite for 0 to stay 0.
+          uint8_t* tile = s_ring + 2 * st * Sh::kTileBytes;
+          constexpr int kTensors = kKeys ? 2 : 1;
+#pragma unroll 1
+          for (int e = threadIdx.x; e < (16 - odd) * 8 * Sh::kPanels * kTensors; e += kSoftmaxThreads) {
+            const int x = e % (8 * Sh::kPanels * kTensors), r = extent + e / (8 * Sh::kPanels * kTensors);
+            *reinterpret_cast<uint4*>(tile + (x >> 3) * kPanel + r * 128 + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_async_smem();
+        }
+        // which pairs of the warp's kept rows and each 32 of this thread's
+        // streamed rows see one another
+        bool act[2], whole[2];
+        uint32_t see[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int at = h0 + 32 * c, r0 = w.at + quarter * 32, c0 = stream0 + at;
+          const int pa = (kKeys ? c0 : r0) + w.shift, key = kKeys ? r0 : c0;
+          act[c] = at < extent && some_seen(a.mask, pa, pa + 31, key);
+          whole[c] = at + 32 <= extent && all_seen(a.mask, pa, pa + 31, key);
+          see[c] = bits(0, extent - at);
+          if (!whole[c]) {
+            if constexpr (kKeys) {
+              const ColumnSpan span = column_span(a.mask, key + lane);
+              see[c] &= bits(span.lo - pa, span.hi + 1 - pa);
+            } else {
+              see[c] &= seen_keys(a.mask, pa + lane, key);
+            }
+          }
+        }
+        const float* col = s_col + st * 2 * kStream + h0;
+        if (!(ok = mbar_wait(s_full, m & 1, s_abort))) break;
+        tc_fence_after();
+        float x[kHalf];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) tmem_ld32(lanes + kColS + h0 + 32 * c, reinterpret_cast<uint32_t*>(x + 32 * c));
+        tmem_wait_ld32(reinterpret_cast<uint32_t*>(x));
+        tmem_wait_ld32(reinterpret_cast<uint32_t*>(x + 32));
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          if (act[c]) {
+#pragma unroll
+            for (int k = 32 * c; k < 32 * c + 32; k += 4) {
+              float4 le = make_float4(lse2, lse2, lse2, lse2);
+              if constexpr (kKeys) le = *reinterpret_cast<const float4*>(col + k);
+              const float2 e0 = fma2(make_float2(x[k], x[k + 1]), scale2, make_float2(le.x, le.y));
+              const float2 e1 = fma2(make_float2(x[k + 2], x[k + 3]), scale2, make_float2(le.z, le.w));
+              x[k] = exp2_approx(e0.x);
+              x[k + 1] = exp2_approx(e0.y);
+              x[k + 2] = exp2_approx(e1.x);
+              x[k + 3] = exp2_approx(e1.y);
+            }
+            if (!whole[c]) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (!(see[c] >> k & 1)) x[32 * c + k] = 0.f;
+            }
+          }
+          if constexpr (kKeys) {
+            uint32_t p16[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) p16[k] = act[c] ? pack16<T>(x[32 * c + 2 * k], x[32 * c + 2 * k + 1]) : 0u;
+            if (h0 + 32 * c < extent) tmem_st16(lanes + kColS + h0 + 16 * c, p16);
+          }
+        }
+        if constexpr (kKeys) tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(p_ready);
+        if (!(ok = mbar_wait(dp_full, m & 1, s_abort))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t d16[16];
+          if (act[c]) {
+            float y[32];
+            tmem_ld32(lanes + kColDP + h0 + 32 * c, reinterpret_cast<uint32_t*>(y));
+            tmem_wait_ld32(reinterpret_cast<uint32_t*>(y));
+#pragma unroll
+            for (int k = 0; k < 32; k += 4) {
+              float4 de = make_float4(delta, delta, delta, delta);
+              if constexpr (kKeys) de = *reinterpret_cast<const float4*>(col + kStream + 32 * c + k);
+              const uint64_t y0 = mul2(add2(pack2(y[k], y[k + 1]), pack2(de.x, de.y)),
+                                       pack2(x[32 * c + k], x[32 * c + k + 1]));
+              const uint64_t y1 = mul2(add2(pack2(y[k + 2], y[k + 3]), pack2(de.z, de.w)),
+                                       pack2(x[32 * c + k + 2], x[32 * c + k + 3]));
+              y[k] = lo2(y0);
+              y[k + 1] = hi2(y0);
+              y[k + 2] = lo2(y1);
+              y[k + 3] = hi2(y1);
+            }
+            if (!whole[c]) {  // 0 times what a hidden pair's dP holds need not be 0
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (!(see[c] >> k & 1)) y[k] = 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < 16; ++k) d16[k] = pack16<T>(y[2 * k], y[2 * k + 1]);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) d16[k] = 0;
+          }
+          if (h0 + 32 * c < extent) tmem_st16(lanes + kColDP + h0 + 16 * c, d16);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(ds_ready);
+      }
       if (!ok) break;
       const bool live = row < w.rows;
       const int64_t at = (((int64_t)w.kept_row + row) * (kKeys ? a.kv_heads : a.heads) + w.h) * a.D;
@@ -505,14 +549,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (!(ok = mbar_wait(acc_full + 8 * acc, (nk / Sh::kAcc) & 1, s_abort))) break;
         tc_fence_after();
       }
-      // the groups share the stores: dK and dV, or half of dQ each
-      const uint32_t from = lanes + Sh::kColAcc + acc * Sh::kAccColumns;
+      // the halves share the stores: dK and dV, or half of dQ each
+      const uint32_t from = lanes + kColAcc + acc * Sh::kAccColumns;
       if constexpr (kKeys)
-        gradient_row<T, DP>(from + g * DP, count > 0, live, g == 0 ? a.scale : 1.f,
-                            static_cast<T*>(g == 0 ? a.d1 : a.d2) + at, a.D, a.sectors);
+        gradient_row<T, DP>(from + half * DP, count > 0, live, half == 0 ? a.scale : 1.f,
+                            static_cast<T*>(half == 0 ? a.d1 : a.d2) + at, a.D, a.sectors);
       else
-        gradient_row<T, DP / 2>(from + g * (DP / 2), count > 0, live, a.scale, static_cast<T*>(a.d1) + at + g * (DP / 2),
-                                a.D - g * (DP / 2), a.sectors);
+        gradient_row<T, DP / 2>(from + half * (DP / 2), count > 0, live, a.scale,
+                                static_cast<T*>(a.d1) + at + half * (DP / 2), a.D - half * (DP / 2), a.sectors);
       if (count) {
         tc_fence_before();
         mbar_arrive(acc_empty + 8 * acc);
