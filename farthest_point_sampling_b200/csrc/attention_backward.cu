@@ -206,22 +206,22 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 
   if (warp == kLoadWarp) {
     // ------------------------------------------------ items and loads
-    ItemWalk walk(kKeys ? a.kv_heads : a.heads, a.hdr->n_items[kKeys ? kKeyTiles : kQueryTiles]);
-    TileItem next = a.items[walk.more() ? walk.tile : 0];
+    constexpr int kList = kKeys ? kKeyTiles : kQueryTiles;
+    ItemClaims claims(&a.hdr->next_item[kList], a.items, kKeys ? a.kv_heads : a.heads, a.hdr->n_items[kList]);
     int i = 0, n = 0, nk = 0;  // items handed out, streamed and kept tiles loaded so far
     bool ok = true;
     for (; ok; ++i) {
       const int slot = i % kItemRing;
       if (i >= kItemRing && !mbar_wait_warp(item_empty + 8 * slot, ((i / kItemRing) - 1) & 1, s_abort)) break;
-      if (!walk.more()) {
+      TileItem entry;
+      int h;
+      if (!claims.take(&entry, &h)) {
         if (lane == 0) s_item[slot].count = -1;
         __syncwarp();
         mbar_arrive_one(item_full + 8 * slot);
         break;
       }
-      const BwdItem w = bwd_item<kKeys>(a, walk.h, next);
-      walk.advance();
-      if (walk.more()) next = a.items[walk.tile];
+      const BwdItem w = bwd_item<kKeys>(a, h, entry);
       if (lane == 0) s_item[slot] = w;
       __syncwarp();
       mbar_arrive_one(item_full + 8 * slot);

@@ -129,22 +129,21 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
   if (warp == kSoftmaxWarps) {
     // ------------------------------------------------ items and loads
     {
-      ItemWalk walk(a.heads, a.hdr->n_items[kQueryTiles]);
-      TileItem next = a.items[walk.more() ? walk.tile : 0];
+      ItemClaims claims(&a.hdr->next_item[kQueryTiles], a.items, a.heads, a.hdr->n_items[kQueryTiles]);
       int i = 0, n = 0, nq = 0;  // items handed out, key tiles and query tiles loaded so far
       for (bool more = true; more; ++i) {
         const int slot = i % kItemRing;
         if (i >= kItemRing && !mbar_wait_warp(item_empty + 8 * slot, ((i / kItemRing) - 1) & 1, s_abort)) break;
-        more = walk.more();
+        TileItem entry;
+        int h;
+        more = claims.take(&entry, &h);
         if (!more) {
           if (lane == 0) s_item[slot].count = -1;
           __syncwarp();
           mbar_arrive_one(item_full + 8 * slot);
           break;
         }
-        const FwdItem w = fwd_item<kMasked>(a, walk.h, next);
-        walk.advance();
-        if (walk.more()) next = a.items[walk.tile];
+        const FwdItem w = fwd_item<kMasked>(a, h, entry);
         if (lane == 0) s_item[slot] = w;
         __syncwarp();
         mbar_arrive_one(item_full + 8 * slot);

@@ -39,6 +39,24 @@ __device__ __forceinline__ int block_scan(int v, int* s_warp, int* total) {
   return x - v + (warp ? s_warp[warp - 1] : 0);  // exclusive
 }
 
+// Sorts 1024 keys in shared memory, largest first (bitonic).
+__device__ __forceinline__ void block_sort(uint64_t* s) {
+  const int i = threadIdx.x;
+  for (int k = 2; k <= kPlanThreads; k <<= 1)
+    for (int j = k >> 1; j > 0; j >>= 1) {
+      const int x = i ^ j;
+      __syncthreads();
+      if (x > i) {
+        const uint64_t a = s[i], b = s[x];
+        if ((a < b) == ((i & k) == 0)) {
+          s[i] = b;
+          s[x] = a;
+        }
+      }
+    }
+  __syncthreads();
+}
+
 enum PlanList { kPlanQueries, kPlanKeys, kPlanUnits };
 
 // One block per list.  A pass takes 1024 events, one per thread: their items
@@ -53,6 +71,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const int64_t* __res
   __shared__ int s_warp[32];
   __shared__ int s_start[kPlanThreads];
   __shared__ TileItem s_event[kPlanThreads];
+  __shared__ uint64_t s_sort[kPlanThreads];
   const int tid = threadIdx.x;
   // blocks in the order queries, keys, units, without the lists that are not asked for
   const int kind = blockIdx.x == 0 ? kPlanQueries : lists.keys && blockIdx.x == 1 ? kPlanKeys : kPlanUnits;
@@ -88,6 +107,16 @@ __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const int64_t* __res
     // A pass with bad offsets makes no items and ends the list: up to there
     // offsets rise, which is what bounds the items of a list by its buffer.
     if (__syncthreads_or(error == kDevBadOffsets)) break;
+    // Long events first, so that the blocks that claim items in turn end
+    // together; where no event has more than four tiles order matters little.
+    if (kind != kPlanUnits && __syncthreads_or(n > 4)) {
+      s_event[tid] = e;
+      s_sort[tid] = ((uint64_t)n << 32) | (uint32_t)(kPlanThreads - 1 - tid);
+      block_sort(s_sort);
+      n = (int)(s_sort[tid] >> 32);
+      e = s_event[kPlanThreads - 1 - (uint32_t)s_sort[tid]];
+      __syncthreads();
+    }
     int total;
     s_start[tid] = block_scan(n, s_warp, &total);
     if (kind == kPlanUnits) {
@@ -110,6 +139,8 @@ __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const int64_t* __res
       }
       TileItem it = s_event[lo];
       it.t = i - s_start[lo];
+      // causal: the last queries of an event see most
+      if (kind == kPlanQueries && mask.causal) it.t = (it.nq + kTile - 1) / kTile - 1 - it.t;
       items[base + i] = it;
     }
     base += total;
@@ -117,6 +148,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const int64_t* __res
   }
   error = __syncthreads_or(error == kDevBadOffsets) ? kDevBadOffsets : __syncthreads_or(error) ? kDevTooLarge : 0;
   if (tid == 0) {
+    hdr->next_item[kind == kPlanQueries ? kQueryTiles : kind == kPlanKeys ? kKeyTiles : kFewUnits] = 0;
     hdr->n_items[kind == kPlanQueries ? kQueryTiles : kind == kPlanKeys ? kKeyTiles : kFewUnits] = base;
     if (kind == kPlanUnits) hdr->n_items[kFewJoins] = joins;
     if (kind == kPlanQueries) {  // every block sees the same errors; one writes the status word

@@ -22,7 +22,7 @@ struct TileItem {
   int pad[3];
 };
 
-// A block's walk over (tile, head) items, heads first: `step` items at a time
+// A block's walk over (tile, head) items, heads first, `step` items at a time
 // without a division.
 struct ItemWalk {
   int tile, h, step_tiles, step_heads, heads, n_tiles;
@@ -40,6 +40,32 @@ struct ItemWalk {
       h -= heads;
       ++tile;
     }
+  }
+};
+
+// The same items taken in turn by whichever block is free, by a whole warp:
+// the first by block index, the others from a counter that starts at 0.  The
+// next claim and its list entry are on their way while one is worked on.
+struct ItemClaims {
+  int* counter;
+  const TileItem* items;
+  int heads, total, claimed;
+  TileItem entry;
+  __device__ __forceinline__ ItemClaims(int* counter_, const TileItem* items_, int heads_, int n_tiles)
+      : counter(counter_), items(items_), heads(heads_), total(n_tiles * heads_), claimed(blockIdx.x) {
+    fetch();
+  }
+  __device__ __forceinline__ void fetch() { entry = items[claimed < total ? claimed / heads : 0]; }
+  // The next item and its head; false when none is left.
+  __device__ __forceinline__ bool take(TileItem* e, int* h) {
+    if (claimed >= total) return false;
+    *e = entry;
+    *h = claimed % heads;
+    int c = 0;
+    if ((threadIdx.x & 31) == 0) c = atomicAdd(counter, 1);
+    claimed = __shfl_sync(0xffffffffu, c, 0) + gridDim.x;
+    fetch();
+    return true;
   }
 };
 
