@@ -30,6 +30,7 @@
 #include <type_traits>
 
 #include "attention_plan.h"
+#include "attention_short.h"
 #include "attention_tiles.cuh"
 #include "common.cuh"
 #include "internal.h"
@@ -57,8 +58,6 @@ struct BwdArgs {
   float* rows;   // [2][heads, n_q]: -lse log2(e) and -D, written by the queries kernel for the keys kernel
   void* d1;      // dQ, or dK
   void* d2;      // dV
-  const int64_t* offsets;  // of the kept rows
-  int B;
   bool sectors;  // every gradient row starts on a 32-byte sector, and ends on one
   const TileItem* items;
   WsHeader* hdr;
@@ -122,28 +121,6 @@ __device__ __forceinline__ void copy4(uint32_t dst, const float* src, bool real)
 // One arrival on `bar` when this thread's copies so far have landed.
 __device__ __forceinline__ void copy_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
-
-template <typename T>
-__device__ __forceinline__ float2 unpack16(uint32_t v);
-template <>
-__device__ __forceinline__ float2 unpack16<__nv_bfloat16>(uint32_t v) {
-  return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&v));
-}
-template <>
-__device__ __forceinline__ float2 unpack16<__half>(uint32_t v) {
-  return __half22float2(*reinterpret_cast<__half2*>(&v));
-}
-
-// One gradient row from its accumulator, or zeros where no tile was seen.
-template <typename T, int DP>
-__device__ __forceinline__ void gradient_row(uint32_t acc, bool filled, bool live, float f, T* to, int D, bool sectors) {
-  if (filled) {
-    store_row<T, DP>(acc, live, f, to, D, sectors);
-  } else if (live) {
-#pragma unroll 1
-    for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4*>(to + c) = make_uint4(0, 0, 0, 0);
-  }
 }
 
 template <typename T, int DP, bool kKeys>
@@ -211,21 +188,31 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     int i = 0, n = 0, nk = 0;  // items handed out, streamed and kept tiles loaded so far
     bool ok = true;
     for (; ok; ++i) {
+      // The issuing warp looks one item ahead, so the ring holds none without
+      // tiles: this warp clears their gradient rows itself.
+      TileItem entry;
+      BwdItem w;
+      int h;
+      bool more;
+      while ((more = claims.take(&entry, &h))) {
+        w = bwd_item<kKeys>(a, h, entry);
+        if (w.count) break;
+        const int heads = kKeys ? a.kv_heads : a.heads;
+        const int64_t at = ((int64_t)w.kept_row * heads + h) * a.D, stride = (int64_t)heads * a.D;
+        clear_strided(static_cast<T*>(a.d1) + at, w.rows, stride, a.D);
+        if (kKeys) clear_strided(static_cast<T*>(a.d2) + at, w.rows, stride, a.D);
+      }
       const int slot = i % kItemRing;
       if (i >= kItemRing && !mbar_wait_warp(item_empty + 8 * slot, ((i / kItemRing) - 1) & 1, s_abort)) break;
-      TileItem entry;
-      int h;
-      if (!claims.take(&entry, &h)) {
+      if (!more) {
         if (lane == 0) s_item[slot].count = -1;
         __syncwarp();
         mbar_arrive_one(item_full + 8 * slot);
         break;
       }
-      const BwdItem w = bwd_item<kKeys>(a, h, entry);
       if (lane == 0) s_item[slot] = w;
       __syncwarp();
       mbar_arrive_one(item_full + 8 * slot);
-      if (w.count == 0) continue;
       const int ks = nk % Sh::kKept;
       if (nk >= Sh::kKept && !mbar_wait_warp(kept_empty + 8 * ks, ((nk / Sh::kKept) - 1) & 1, s_abort)) break;
       const int boxes = (w.rows + 63) / 64;
@@ -288,11 +275,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       int steps, kept, item;
       bool first, last;
     };
-    int i = 0, hd = 0, j = 0, count = 0, items = 0, fetched = 0;  // items read, place in the item, items with tiles
+    int i = 0, hd = heads, j = 0, count = 0, items = 0, fetched = 0;  // items and tiles read, place in the item
     KeyTiles<kStream> tiles = {};
     bool ok = true;
     const auto fetch = [&](Tile* t) {  // false when the work is done, or a wait gave up (ok)
-      while (hd == heads || count == 0) {
+      if (hd == heads) {
         const int slot = i % kItemRing;
         if (!(ok = mbar_wait_warp(item_full + 8 * slot, (i / kItemRing) & 1, s_abort))) return false;
         count = uniform(s_item[slot].count);
@@ -304,7 +291,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (count < 0) return false;
         ++i;
         hd = j = 0;
-        if (count == 0) continue;
         const int ks = items % Sh::kKept;
         if (!(ok = mbar_wait_warp(kept_full + 8 * ks, (items / Sh::kKept) & 1, s_abort))) return false;
         ++items;
@@ -332,7 +318,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const uint32_t desc = mma_desc(kBf16, false, false, t.steps * 16);
 #pragma unroll
       for (int p = 0; p < Sh::kPanels; ++p)
-        mma_ss4(tmem + (x ? kColDP : kColS), kept + p * (kPanel >> 4), from + p * (kPanel >> 4), desc, p > 0);
+        mma_ss_steps<2, 2>(tmem + (x ? kColDP : kColS), kept + p * (kPanel >> 4), from + p * (kPanel >> 4), 4, desc, p > 0);
       mma_commit(x ? dp_full : s_full);
     };
     // an accumulator += the 16-bit rows over S or dP, times a streamed tensor;
@@ -392,9 +378,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       if (count < 0) break;
       float lse2 = 0.f, delta = 0.f;  // -lse log2(e) and -D of this thread's query
       if constexpr (!kKeys) {
-        if (count) {  // D: dO from its tile, O from memory
-          const int ks = nk % Sh::kKept;
-          if (!(ok = mbar_wait(kept_full + 8 * ks, (nk / Sh::kKept) & 1, s_abort))) break;
+        // D: dO from its tile, O from memory
+        const int ks = nk % Sh::kKept;
+        if (!(ok = mbar_wait(kept_full + 8 * ks, (nk / Sh::kKept) & 1, s_abort))) break;
+        {
           if (row < w.rows) {
             const int64_t q = (int64_t)w.kept_row + row, at = (int64_t)w.h * a.n_q + q;
             const T* o = static_cast<const T*>(a.out) + (q * a.heads + w.h) * a.D;
@@ -545,29 +532,21 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const int64_t at = (((int64_t)w.kept_row + row) * (kKeys ? a.kv_heads : a.heads) + w.h) * a.D;
       mbar_arrive(item_empty + 8 * slot);
       const int acc = nk % Sh::kAcc;
-      if (count) {
-        if (!(ok = mbar_wait(acc_full + 8 * acc, (nk / Sh::kAcc) & 1, s_abort))) break;
-        tc_fence_after();
-      }
+      if (!(ok = mbar_wait(acc_full + 8 * acc, (nk / Sh::kAcc) & 1, s_abort))) break;
+      tc_fence_after();
       // the halves share the stores: dK and dV, or half of dQ each
       const uint32_t from = lanes + kColAcc + acc * Sh::kAccColumns;
       if constexpr (kKeys)
-        gradient_row<T, DP>(from + half * DP, count > 0, live, half == 0 ? a.scale : 1.f,
-                            static_cast<T*>(half == 0 ? a.d1 : a.d2) + at, a.D, a.sectors);
+        store_row<T, DP>(from + half * DP, live, half == 0 ? a.scale : 1.f,
+                         static_cast<T*>(half == 0 ? a.d1 : a.d2) + at, a.D, a.sectors);
       else
-        gradient_row<T, DP / 2>(from + half * (DP / 2), count > 0, live, a.scale,
-                                static_cast<T*>(a.d1) + at + half * (DP / 2), a.D - half * (DP / 2), a.sectors);
-      if (count) {
-        tc_fence_before();
-        mbar_arrive(acc_empty + 8 * acc);
-        ++nk;
-      }
+        store_row<T, DP / 2>(from + half * (DP / 2), live, a.scale, static_cast<T*>(a.d1) + at + half * (DP / 2),
+                             a.D - half * (DP / 2), a.sectors);
+      tc_fence_before();
+      mbar_arrive(acc_empty + 8 * acc);
+      ++nk;
     }
   }
-  const int64_t first = a.B > 0 ? a.offsets[a.B] : 0;
-  const int64_t values = (int64_t)(kKeys ? a.kv_heads : a.heads) * a.D;
-  zero_rows(a.d1, first, kKeys ? a.n_kv : a.n_q, values);
-  if (kKeys) zero_rows(a.d2, first, a.n_kv, values);
   tc_fence_before();
   __syncthreads();
   if (warp == kMmaWarp) {
@@ -580,7 +559,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 
 struct BwdWorkspace {
   WsHeader* hdr;
-  TileItem *queries, *keys;
+  TileItem *queries, *keys, *shorts;
   float* rows;
   size_t bytes;
 };
@@ -596,6 +575,7 @@ BwdWorkspace carve_backward(void* base, int64_t n_q, int64_t n_kv, int B, int he
   w.hdr = reinterpret_cast<WsHeader*>(p);
   w.queries = reinterpret_cast<TileItem*>(take((max_tiles(n_q, B) + 1) * sizeof(TileItem)));
   w.keys = reinterpret_cast<TileItem*>(take((max_tiles(n_kv, B) + 1) * sizeof(TileItem)));
+  w.shorts = reinterpret_cast<TileItem*>(take((size_t)(B + 1) * sizeof(TileItem)));
   w.rows = reinterpret_cast<float*>(take((size_t)n_q * heads * 2 * sizeof(float)));
   w.bytes = off;
   return w;
@@ -624,23 +604,7 @@ cudaError_t run(const BwdArgs& a, int64_t items, const CUtensorMap& k1, const CU
 }
 
 template <typename T, int DP>
-cudaError_t run_backward(const AttnCall& c, const BwdWorkspace& ws, cudaStream_t s) {
-  PlanLists lists = {};
-  lists.queries = ws.queries;
-  lists.keys = ws.keys;
-  cudaError_t e = launch_attention_plan(c, ws.hdr, lists, s);
-  if (e != cudaSuccess) return e;
-  const bool bf16 = std::is_same<T, __nv_bfloat16>::value;
-  // without queries (or keys) no item has a tile of the other: their maps are not used
-  CUtensorMap q = {}, k = {}, v = {}, d = {};
-  if (c.n_q > 0 && (!attention_map(&q, c.q, bf16, c.n_q, c.heads, c.D, c.q_token, c.q_head) ||
-                    !attention_map(&d, c.dout, bf16, c.n_q, c.heads, c.D, c.do_token, c.do_head)))
-    return cudaErrorInvalidValue;
-  if (c.n_kv > 0 && (!attention_map(&k, c.k, bf16, c.n_kv, c.kv_heads, c.D, c.k_token, c.k_head) ||
-                     !attention_map(&v, c.v, bf16, c.n_kv, c.kv_heads, c.D, c.v_token, c.v_head)))
-    return cudaErrorInvalidValue;
-  if (c.n_q == 0) q = k, d = v;
-  if (c.n_kv == 0) k = q, v = d;
+cudaError_t run_tiles(const AttnCall& c, const BwdWorkspace& ws, const BwdMaps& m, cudaStream_t s) {
   BwdArgs a;
   a.n_q = c.n_q;
   a.n_kv = c.n_kv;
@@ -654,24 +618,20 @@ cudaError_t run_backward(const AttnCall& c, const BwdWorkspace& ws, cudaStream_t
   a.out = c.out;
   a.lse = c.lse;
   a.rows = ws.rows;
-  a.B = c.B;
   a.hdr = ws.hdr;
-  a.sectors = ((reinterpret_cast<uintptr_t>(c.dq) | reinterpret_cast<uintptr_t>(c.dk) | reinterpret_cast<uintptr_t>(c.dv)) &
-               31) == 0 && c.D % 16 == 0;
+  a.sectors = m.sectors;
+  cudaError_t e;
   if (c.n_q > 0) {
     a.d1 = c.dq;
     a.d2 = nullptr;
-    a.offsets = c.q_offsets;
     a.items = ws.queries;
-    if ((e = run<T, DP, false>(a, max_tiles(c.n_q, c.B) * c.heads, q, d, k, v, s)) != cudaSuccess) return e;
+    if ((e = run<T, DP, false>(a, max_tiles(c.n_q, c.B) * c.heads, m.q, m.d, m.k, m.v, s)) != cudaSuccess) return e;
   }
   if (c.n_kv > 0) {
     a.d1 = c.dk;
     a.d2 = c.dv;
-    a.offsets = c.kv_offsets;
     a.items = ws.keys;
-    if ((e = run<T, DP, true>(a, max_tiles(c.n_kv, c.B) * c.kv_heads, k, v, q, d, s)) != cudaSuccess)
-      return e;
+    if ((e = run<T, DP, true>(a, max_tiles(c.n_kv, c.B) * c.kv_heads, m.k, m.v, m.q, m.d, s)) != cudaSuccess) return e;
   }
   return cudaSuccess;
 }
@@ -684,9 +644,30 @@ size_t attention_backward_bytes(const AttnCall& c) {
 
 cudaError_t launch_attention_backward(const AttnCall& c, void* workspace, cudaStream_t s) {
   const BwdWorkspace ws = carve_backward(workspace, c.n_q, c.n_kv, c.B, c.heads);
-  if (c.dtype == FPS_DTYPE_BF16)
-    return c.D <= 64 ? run_backward<__nv_bfloat16, 64>(c, ws, s) : run_backward<__nv_bfloat16, 128>(c, ws, s);
-  return c.D <= 64 ? run_backward<__half, 64>(c, ws, s) : run_backward<__half, 128>(c, ws, s);
+  PlanLists lists = {};
+  lists.queries = ws.queries;
+  lists.keys = ws.keys;
+  lists.shorts = ws.shorts;
+  cudaError_t e = launch_attention_plan(c, ws.hdr, lists, s);
+  if (e != cudaSuccess || (c.n_q == 0 && c.n_kv == 0)) return e;
+  const bool bf16 = c.dtype == FPS_DTYPE_BF16;
+  // without queries (or keys) no item has a tile of the other: their maps are not used
+  BwdMaps m = {};
+  if (c.n_q > 0 && (!attention_map(&m.q, c.q, bf16, c.n_q, c.heads, c.D, c.q_token, c.q_head) ||
+                    !attention_map(&m.d, c.dout, bf16, c.n_q, c.heads, c.D, c.do_token, c.do_head)))
+    return cudaErrorInvalidValue;
+  if (c.n_kv > 0 && (!attention_map(&m.k, c.k, bf16, c.n_kv, c.kv_heads, c.D, c.k_token, c.k_head) ||
+                     !attention_map(&m.v, c.v, bf16, c.n_kv, c.kv_heads, c.D, c.v_token, c.v_head)))
+    return cudaErrorInvalidValue;
+  if (c.n_q == 0) m.q = m.k, m.d = m.v;
+  if (c.n_kv == 0) m.k = m.q, m.v = m.d;
+  m.sectors = ((reinterpret_cast<uintptr_t>(c.dq) | reinterpret_cast<uintptr_t>(c.dk) | reinterpret_cast<uintptr_t>(c.dv)) &
+               31) == 0 &&
+              c.D % 16 == 0;
+  if ((e = launch_attention_backward_short(c, m, ws.shorts, ws.hdr, s)) != cudaSuccess) return e;
+  if (c.max_tokens > 0 && c.max_tokens <= kTile) return cudaSuccess;  // every event is short
+  if (bf16) return c.D <= 64 ? run_tiles<__nv_bfloat16, 64>(c, ws, m, s) : run_tiles<__nv_bfloat16, 128>(c, ws, m, s);
+  return c.D <= 64 ? run_tiles<__half, 64>(c, ws, m, s) : run_tiles<__half, 128>(c, ws, m, s);
 }
 
 }  // namespace fpstok

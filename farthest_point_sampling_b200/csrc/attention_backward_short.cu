@@ -1,0 +1,528 @@
+// Attention of packed events, backward, for events of at most 128 queries and
+// 128 keys (the tokenizer's usual K): all three gradients in one kernel.
+//
+// Such an event is one tile, so S and dP are formed once,
+//   S^T = K Q^T,  dP^T = V dO^T,  P = exp2(c S - lse),  dS = P (dP - D),
+//   dV = P^T dO,  dK = scale dS^T Q,  dQ = scale dS K,
+// and q, k, v, out and dout are read once and the gradients written once: with
+// 64-wide heads and 128 tokens that traffic, 8 tensors of it, bounds the
+// kernel, not the products.
+//
+// A work item is an event and a key head, with a unit for each query head of
+// its group; dK and dV are summed over the units in TMEM.  Warps: a loading
+// and an issuing warp; four that form D and the scaled lse of a unit's queries
+// ahead of the others; eight for the softmax with two threads per key row,
+// each for half of the queries.  P goes back over S in TMEM as 16-bit operand
+// A; dS goes to shared memory, where it is read along its rows for dK and
+// across them for dQ.
+//
+// Rounding: as in attention_backward.cu.
+#include <type_traits>
+
+#include "attention_plan.h"
+#include "attention_short.h"
+#include "attention_tiles.cuh"
+#include "common.cuh"
+#include "internal.h"
+#include "tcgen05.cuh"
+
+namespace fpstok {
+
+namespace {
+
+constexpr int kHalf = kTile / 2;
+constexpr int kPanel = kTile * 128;
+constexpr int kSoftmaxThreads = 256;
+constexpr int kRowThreads = 128;
+constexpr int kShortThreads = kSoftmaxThreads + kRowThreads + 64;
+constexpr int kItemRing = 2;
+constexpr uint32_t kColS = 0, kColDP = 128, kColDV = 256;
+
+struct ShortArgs {
+  int64_t n_q, n_kv;
+  int heads, kv_heads, group, D;
+  AttnMask mask;
+  float scale, scale_log2;
+  const void* out;
+  const float* lse;
+  void *dq, *dk, *dv;
+  const int64_t *q_offsets, *kv_offsets;
+  int B;
+  bool sectors;  // every gradient row starts on a 32-byte sector, and ends on one
+  const TileItem* items;
+  WsHeader* hdr;
+};
+
+// One work item as the loading warp hands it to the others; nq = -1 ends the work.
+struct ShortItem {
+  int h, q_row, nq, k_row, nk;  // key head; the event's first query and key rows, queries, keys
+};
+
+template <int DP>
+struct ShortShape {
+  static constexpr int kPanels = DP / 64;
+  static constexpr uint32_t kTileBytes = kPanels * kPanel;
+  static constexpr int kStages = DP == 64 ? 2 : 1;  // of (K, V), and of (Q, dO)
+  static constexpr uint32_t kColDK = kColDV + DP;
+  // 64-wide heads leave TMEM for dQ; with 128-wide ones it takes the place of dP
+  static constexpr uint32_t kColDQ = DP == 64 ? kColDK + DP : kColDP;
+  static constexpr size_t kSmem = 1024 + 4 * kStages * kTileBytes + 2 * kPanel + kStages * 2 * kTile * sizeof(float) +
+                                  kItemRing * sizeof(ShortItem) + 512;
+};
+
+// The rows [n, up to the next 16) of a tile to 0.
+template <int kPanels>
+__device__ __forceinline__ void clear_rows(uint8_t* tile, int n, int thread, int threads) {
+#pragma unroll 1
+  for (int e = thread; e < (-n & 15) * 8 * kPanels; e += threads) {
+    const int r = n + e / (8 * kPanels), c = e % (8 * kPanels);
+    *reinterpret_cast<uint4*>(tile + (c >> 3) * kPanel + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+  }
+}
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(kShortThreads, 1)
+    k_attn_backward_short(const ShortArgs a, const __grid_constant__ CUtensorMap map_q,
+                          const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                          const __grid_constant__ CUtensorMap map_do) {
+  using Sh = ShortShape<DP>;
+  constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+  constexpr int kStages = Sh::kStages;
+  constexpr int kRowWarp = kSoftmaxThreads / 32, kLoadWarp = kRowWarp + kRowThreads / 32, kMmaWarp = kLoadWarp + 1;
+  extern __shared__ uint8_t s_raw[];
+  uint8_t* s_base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t* s_kv = s_base;                                      // [stage][K, V]
+  uint8_t* s_qd = s_kv + 2 * kStages * Sh::kTileBytes;         // [stage][Q, dO]
+  uint8_t* s_ds = s_qd + 2 * kStages * Sh::kTileBytes;         // dS: key rows, a panel for each half of the queries
+  float* s_col = reinterpret_cast<float*>(s_ds + 2 * kPanel);  // [stage][-lse log2(e), -D][128]
+  ShortItem* s_item = reinterpret_cast<ShortItem*>(s_col + kStages * 2 * kTile);
+  uint64_t* s_bar = reinterpret_cast<uint64_t*>((reinterpret_cast<uintptr_t>(s_item + kItemRing) + 7) & ~(uintptr_t)7);
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_bar + 32);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
+  const uint32_t bars = smem_u32(s_bar);
+  const uint32_t kv_full = bars, kv_empty = bars + 16, qd_full = bars + 32, qd_empty = bars + 48, item_full = bars + 64,
+                 item_empty = bars + 80, col_full = bars + 96, s_full = bars + 112, dp_full = bars + 120,
+                 p_ready = bars + 128, ds_ready = bars + 136, done = bars + 144, drain = bars + 152;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(kv_full + 8 * i, 1);
+      mbar_init(kv_empty + 8 * i, 1);
+      mbar_init(qd_full + 8 * i, 1);
+      mbar_init(qd_empty + 8 * i, 1);
+      mbar_init(item_full + 8 * i, 1);
+      mbar_init(item_empty + 8 * i, kSoftmaxThreads + kRowThreads + 1);
+      mbar_init(col_full + 8 * i, kRowThreads);
+    }
+    mbar_init(s_full, 1);
+    mbar_init(dp_full, 1);
+    mbar_init(p_ready, kSoftmaxThreads);
+    mbar_init(ds_ready, kSoftmaxThreads);
+    mbar_init(done, 1);
+    mbar_init(drain, 1);
+    *s_abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    tma_prefetch_map(&map_q);
+    tma_prefetch_map(&map_k);
+    tma_prefetch_map(&map_v);
+    tma_prefetch_map(&map_do);
+  }
+  if (warp == kMmaWarp) tmem_alloc(smem_u32(s_tmem), 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = uniform(*s_tmem);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  if (warp == kLoadWarp) {
+    // ------------------------------------------------ items and loads
+    ItemClaims claims(&a.hdr->next_item[kShortEvents], a.items, a.kv_heads, a.hdr->n_items[kShortEvents]);
+    int n = 0, u = 0;  // items and units with tiles so far
+    bool ok = true;
+    for (int i = 0; ok; ++i) {
+      // The issuing warp looks one item ahead, so the ring holds none without
+      // a pair: this warp clears their gradient rows itself.
+      TileItem e;
+      int h;
+      bool more;
+      while ((more = claims.take(&e, &h)) && (e.nq == 0 || e.nk == 0)) {
+        clear_strided(static_cast<T*>(a.dq) + ((int64_t)e.q0 * a.heads + h * a.group) * a.D, e.nq,
+                      (int64_t)a.heads * a.D, a.group * a.D);
+        const int64_t at = ((int64_t)e.k0 * a.kv_heads + h) * a.D, stride = (int64_t)a.kv_heads * a.D;
+        clear_strided(static_cast<T*>(a.dk) + at, e.nk, stride, a.D);
+        clear_strided(static_cast<T*>(a.dv) + at, e.nk, stride, a.D);
+      }
+      const int slot = i % kItemRing;
+      if (i >= kItemRing && !mbar_wait_warp(item_empty + 8 * slot, ((i / kItemRing) - 1) & 1, s_abort)) break;
+      if (lane == 0) s_item[slot] = more ? ShortItem{h, e.q0, e.nq, e.k0, e.nk} : ShortItem{0, 0, -1, 0, 0};
+      __syncwarp();
+      mbar_arrive_one(item_full + 8 * slot);
+      if (!more) break;
+      const int ks = n % kStages;
+      if (n >= kStages && !mbar_wait_warp(kv_empty + 8 * ks, ((n / kStages) - 1) & 1, s_abort)) break;
+      ++n;
+      const auto load = [&](uint8_t* to, const CUtensorMap* m1, const CUtensorMap* m2, uint32_t bar, int rows, int row, int hd) {
+        const int boxes = (rows + 63) / 64;
+        mbar_expect(bar, 2 * boxes * 8192 * Sh::kPanels);
+#pragma unroll 1
+        for (int b = 0; b < boxes; ++b)
+#pragma unroll
+          for (int p = 0; p < Sh::kPanels; ++p) {
+            const uint32_t at = smem_u32(to) + p * kPanel + b * 8192;
+            tma_load(at, m1, bar, p * 64, hd, row + b * 64);
+            tma_load(at + Sh::kTileBytes, m2, bar, p * 64, hd, row + b * 64);
+          }
+      };
+      load(s_kv + 2 * ks * Sh::kTileBytes, &map_k, &map_v, kv_full + 8 * ks, e.nk, e.k0, h);
+#pragma unroll 1
+      for (int m = 0; m < a.group; ++m, ++u) {
+        const int st = u % kStages;
+        if (u >= kStages && !(ok = mbar_wait_warp(qd_empty + 8 * st, ((u / kStages) - 1) & 1, s_abort))) break;
+        load(s_qd + 2 * st * Sh::kTileBytes, &map_q, &map_do, qd_full + 8 * st, e.nq, e.q0, h * a.group + m);
+      }
+    }
+    // after a wait that gave up: the copies still in flight land first
+    if (__any_sync(kFull, *s_abort)) {
+      volatile int none = 0;
+      for (int b = 0; b < kStages; ++b) {
+        const int lk = n - 1 - b, lu = u - 1 - b;
+        if (lk >= 0) mbar_wait_warp(kv_full + 8 * (lk % kStages), (lk / kStages) & 1, &none);
+        if (lu >= 0) mbar_wait_warp(qd_full + 8 * (lu % kStages), (lu / kStages) & 1, &none);
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------ products
+    const int cols = (a.D + 15) / 16 * 16;
+    const uint32_t ts_desc = mma_desc(kBf16, false, true, cols);  // dV: A in TMEM; dK: dS along its rows
+    const uint32_t dq_desc = mma_desc(kBf16, true, true, cols);   // dQ: dS across its rows
+    struct Unit {
+      int q_steps, k_steps, kv, qd;
+      bool first, last;  // of its item
+    };
+    int i = 0, m = a.group, n = 0, fetched = 0, nq = 0, nk = 0;
+    bool ok = true;
+    const auto fetch = [&](Unit* t) {  // the next unit; false when the work is done, or a wait gave up (ok)
+      if (m == a.group) {
+        const int slot = i % kItemRing;
+        if (!(ok = mbar_wait_warp(item_full + 8 * slot, (i / kItemRing) & 1, s_abort))) return false;
+        nq = uniform(s_item[slot].nq);
+        nk = uniform(s_item[slot].nk);
+        mbar_arrive_one(item_empty + 8 * slot);
+        if (nq < 0) return false;
+        ++i;
+        m = 0;
+        if (!(ok = mbar_wait_warp(kv_full + 8 * (n % kStages), (n / kStages) & 1, s_abort))) return false;
+        ++n;
+      }
+      t->qd = fetched % kStages;
+      if (!(ok = mbar_wait_warp(qd_full + 8 * t->qd, (fetched / kStages) & 1, s_abort))) return false;
+      ++fetched;
+      t->kv = (n - 1) % kStages;
+      t->q_steps = (nq + 15) / 16;
+      t->k_steps = (nk + 15) / 16;
+      t->first = m == 0;
+      t->last = ++m == a.group;
+      tc_fence_after();
+      return true;
+    };
+    // S (x = 0) or dP (x = 1): whole panels, as values past D are zeros
+    const auto scores = [&](const Unit& t, int x) {
+      const uint32_t kept = smem_desc(smem_u32(s_kv) + (2 * t.kv + x) * Sh::kTileBytes, kPanel);
+      const uint32_t from = smem_desc(smem_u32(s_qd) + (2 * t.qd + x) * Sh::kTileBytes, kPanel);
+      const uint32_t desc = mma_desc(kBf16, false, false, t.q_steps * 16);
+#pragma unroll
+      for (int p = 0; p < Sh::kPanels; ++p)
+        mma_ss_steps<2, 2>(tmem + (x ? kColDP : kColS), kept + p * (kPanel >> 4), from + p * (kPanel >> 4), 4, desc, p > 0);
+      mma_commit(x ? dp_full : s_full);
+    };
+    // With one stage the next unit's tiles load only after this one's products;
+    // with 128-wide heads dP also waits for dQ in its place to be stored.
+    constexpr bool kAhead = kStages > 1;
+    Unit cur, nxt;
+    bool more = fetch(&cur);
+    if (more) {
+      scores(cur, 0);
+      if (kAhead) scores(cur, 1);
+    }
+    const uint32_t ds = smem_desc(smem_u32(s_ds), kPanel);
+    for (int u = 0; more; ++u) {
+      if (!mbar_wait_warp(p_ready, u & 1, s_abort)) break;
+      tc_fence_after();
+      if (!kAhead) scores(cur, 1);
+      const uint32_t q_rows = smem_desc(smem_u32(s_qd) + 2 * cur.qd * Sh::kTileBytes, kPanel);
+      const uint32_t do_rows = q_rows + (Sh::kTileBytes >> 4);
+      mma_ts_steps(tmem + kColDV, tmem + kColS, do_rows, min(cur.q_steps, 4), ts_desc, !cur.first);  // dV += P^T dO
+      if (cur.q_steps > 4) mma_ts_steps(tmem + kColDV, tmem + kColS + kHalf, do_rows + 512, cur.q_steps - 4, ts_desc, true);
+      if (kAhead) {
+        more = fetch(&nxt);
+        if (!ok) break;
+        if (more) scores(nxt, 0);
+      }
+      if (!mbar_wait_warp(ds_ready, u & 1, s_abort)) break;
+      tc_fence_after();
+      mma_ss_steps<2, 128>(tmem + Sh::kColDK, ds, q_rows, min(cur.q_steps, 4), ts_desc, !cur.first);  // dK += dS^T Q
+      if (cur.q_steps > 4)
+        mma_ss_steps<2, 128>(tmem + Sh::kColDK, ds + (kPanel >> 4), q_rows + 512, cur.q_steps - 4, ts_desc, true);
+      mma_ss_steps<128, 128>(tmem + Sh::kColDQ, ds, smem_desc(smem_u32(s_kv) + 2 * cur.kv * Sh::kTileBytes, kPanel),
+                             cur.k_steps, dq_desc, false);  // dQ = dS K
+      mma_commit(qd_empty + 8 * cur.qd);
+      if (cur.last) mma_commit(kv_empty + 8 * cur.kv);
+      mma_commit(done);
+      if (!kAhead) {
+        more = fetch(&nxt);
+        if (!ok) break;
+        if (more) scores(nxt, 0);
+      } else if (more) {
+        scores(nxt, 1);
+      }
+      cur = nxt;
+    }
+    if (__any_sync(kFull, *s_abort)) {  // products in flight end before TMEM is freed
+      volatile int none = 0;
+      mma_commit(drain);
+      mbar_wait_warp(drain, 0, &none);
+    }
+  } else if (warp >= kRowWarp) {
+    // ------------------------------------------------ D and lse of a unit's queries, ahead of the softmax
+    const int row = threadIdx.x - kSoftmaxThreads;
+    int u = 0;
+    bool ok = true;
+    for (int i = 0; ok; ++i) {
+      const int slot = i % kItemRing;
+      if (!(ok = mbar_wait(item_full + 8 * slot, (i / kItemRing) & 1, s_abort))) break;
+      const ShortItem w = s_item[slot];
+      if (w.nq < 0) break;
+      mbar_arrive(item_empty + 8 * slot);
+      const int64_t q = (int64_t)w.q_row + row;
+#pragma unroll 1
+      for (int m = 0; m < a.group; ++m, ++u) {
+        const int st = u % kStages, h = w.h * a.group + m;
+        uint4 o[DP / 8];
+        float lse = 0.f, delta = 0.f;
+        if (row < w.nq) {  // O is on its way while dO's tile is waited for
+          const T* from = static_cast<const T*>(a.out) + (q * a.heads + h) * a.D;
+#pragma unroll
+          for (int c = 0; c < DP / 8; ++c) o[c] = c * 8 < a.D ? *reinterpret_cast<const uint4*>(from + c * 8) : make_uint4(0, 0, 0, 0);
+          lse = a.lse[(int64_t)h * a.n_q + q];
+        }
+        if (!(ok = mbar_wait(qd_full + 8 * st, (u / kStages) & 1, s_abort))) break;
+        if (row < w.nq) {
+          const uint8_t* d = s_qd + (2 * st + 1) * Sh::kTileBytes + row * 128;
+#pragma unroll
+          for (int c = 0; c < DP / 8; ++c) {
+            const uint4 vd = *reinterpret_cast<const uint4*>(d + (c >> 3) * kPanel + (((c & 7) ^ (row & 7)) << 4));
+            const uint32_t* po = reinterpret_cast<const uint32_t*>(&o[c]);
+            const uint32_t* pd = reinterpret_cast<const uint32_t*>(&vd);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 x = unpack16<T>(po[k]), y = unpack16<T>(pd[k]);
+              delta = fmaf(x.x, y.x, fmaf(x.y, y.y, delta));
+            }
+          }
+        }
+        s_col[st * 2 * kTile + row] = -lse * kLog2e;
+        s_col[st * 2 * kTile + kTile + row] = -delta;
+        mbar_arrive(col_full + 8 * st);
+      }
+    }
+  } else {
+    // ------------------------------------------------ softmax and its gradient
+    const int half = warp >> 2, quarter = warp & 3;
+    const int row = threadIdx.x & 127, h0 = half * kHalf;
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+    const float2 scale2 = make_float2(a.scale_log2, a.scale_log2);
+    uint8_t* ds_row = s_ds + half * kPanel + row * 128;
+    int n = 0, u = 0;
+    bool ok = true;
+    for (int i = 0; ok; ++i) {
+      const int slot = i % kItemRing;
+      if (!(ok = mbar_wait(item_full + 8 * slot, (i / kItemRing) & 1, s_abort))) break;
+      const ShortItem w = s_item[slot];
+      if (w.nq < 0) break;
+      mbar_arrive(item_empty + 8 * slot);
+      T* dq = static_cast<T*>(a.dq) + (((int64_t)w.q_row + row) * a.heads + w.h * a.group) * a.D;
+      const int64_t key_at = (((int64_t)w.k_row + row) * a.kv_heads + w.h) * a.D;
+      const int shift = w.nk - w.nq, ks = n % kStages;
+      // which pairs of the warp's key rows and each 32 of this thread's queries see one another
+      bool act[2], whole[2];
+      uint32_t see[2];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int at = h0 + 32 * c, key = quarter * 32, pa = at + shift;
+        act[c] = at < w.nq && key < w.nk && some_seen(a.mask, pa, pa + 31, key);
+        whole[c] = at + 32 <= w.nq && key + 32 <= w.nk && all_seen(a.mask, pa, pa + 31, key);
+        const ColumnSpan span = column_span(a.mask, row);
+        see[c] = row < w.nk ? bits(0, w.nq - at) & bits(span.lo - pa, span.hi + 1 - pa) : 0u;
+      }
+#pragma unroll 1
+      for (int m = 0; m < a.group; ++m, ++u) {
+        const int st = u % kStages;
+        // Rows past the event's last inside a product's step of 16: their P and
+        // dS are 0, and the rows must be finite for 0 to stay 0.
+        if (w.nq & 15) {
+          if (!(ok = mbar_wait(qd_full + 8 * st, (u / kStages) & 1, s_abort))) break;
+          uint8_t* tile = s_qd + 2 * st * Sh::kTileBytes;
+          clear_rows<Sh::kPanels>(tile, w.nq, threadIdx.x, kSoftmaxThreads);
+          clear_rows<Sh::kPanels>(tile + Sh::kTileBytes, w.nq, threadIdx.x, kSoftmaxThreads);
+        }
+        if (m == 0 && (w.nk & 15)) {
+          if (!(ok = mbar_wait(kv_full + 8 * ks, (n / kStages) & 1, s_abort))) break;
+          clear_rows<Sh::kPanels>(s_kv + 2 * ks * Sh::kTileBytes, w.nk, threadIdx.x, kSoftmaxThreads);
+        }
+        if (!(ok = mbar_wait(col_full + 8 * st, (u / kStages) & 1, s_abort))) break;
+        const float* col = s_col + st * 2 * kTile + h0;
+        if (!(ok = mbar_wait(s_full, u & 1, s_abort))) break;
+        tc_fence_after();
+        float x[kHalf];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) tmem_ld32(lanes + kColS + h0 + 32 * c, reinterpret_cast<uint32_t*>(x + 32 * c));
+        tmem_wait_ld32(reinterpret_cast<uint32_t*>(x));
+        tmem_wait_ld32(reinterpret_cast<uint32_t*>(x + 32));
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          if (act[c]) {
+#pragma unroll
+            for (int k = 32 * c; k < 32 * c + 32; k += 4) {
+              const float4 le = *reinterpret_cast<const float4*>(col + k);
+              const float2 e0 = fma2(make_float2(x[k], x[k + 1]), scale2, make_float2(le.x, le.y));
+              const float2 e1 = fma2(make_float2(x[k + 2], x[k + 3]), scale2, make_float2(le.z, le.w));
+              x[k] = exp2_approx(e0.x);
+              x[k + 1] = exp2_approx(e0.y);
+              x[k + 2] = exp2_approx(e1.x);
+              x[k + 3] = exp2_approx(e1.y);
+            }
+            if (!whole[c]) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (!(see[c] >> k & 1)) x[32 * c + k] = 0.f;
+            }
+          }
+          uint32_t p16[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) p16[k] = act[c] ? pack16<T>(x[32 * c + 2 * k], x[32 * c + 2 * k + 1]) : 0u;
+          if (h0 + 32 * c < w.nq) tmem_st16(lanes + kColS + h0 + 16 * c, p16);
+        }
+        tmem_wait_st();
+        fence_async_smem();  // the cleared rows
+        tc_fence_before();
+        mbar_arrive(p_ready);
+        if (!(ok = mbar_wait(dp_full, u & 1, s_abort))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          if (h0 + 32 * c >= w.nq) continue;
+          uint32_t d16[16];
+          if (act[c]) {
+            float y[32];
+            tmem_ld32(lanes + kColDP + h0 + 32 * c, reinterpret_cast<uint32_t*>(y));
+            tmem_wait_ld32(reinterpret_cast<uint32_t*>(y));
+#pragma unroll
+            for (int k = 0; k < 32; k += 4) {
+              const float4 de = *reinterpret_cast<const float4*>(col + kTile + 32 * c + k);
+              const uint64_t y0 = mul2(add2(pack2(y[k], y[k + 1]), pack2(de.x, de.y)),
+                                       pack2(x[32 * c + k], x[32 * c + k + 1]));
+              const uint64_t y1 = mul2(add2(pack2(y[k + 2], y[k + 3]), pack2(de.z, de.w)),
+                                       pack2(x[32 * c + k + 2], x[32 * c + k + 3]));
+              y[k] = lo2(y0);
+              y[k + 1] = hi2(y0);
+              y[k + 2] = lo2(y1);
+              y[k + 3] = hi2(y1);
+            }
+            if (!whole[c]) {  // 0 times what a hidden pair's dP holds need not be 0
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (!(see[c] >> k & 1)) y[k] = 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < 16; ++k) d16[k] = pack16<T>(y[2 * k], y[2 * k + 1]);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) d16[k] = 0;
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            *reinterpret_cast<uint4*>(ds_row + (((c * 4 + k) ^ (row & 7)) << 4)) =
+                make_uint4(d16[4 * k], d16[4 * k + 1], d16[4 * k + 2], d16[4 * k + 3]);
+        }
+        fence_async_smem();
+        tc_fence_before();
+        mbar_arrive(ds_ready);
+        // stores: dQ of this head, half of the columns each; after the last
+        // head dK and dV
+        if (!(ok = mbar_wait(done, u & 1, s_abort))) break;
+        tc_fence_after();
+        store_row<T, DP / 2>(lanes + Sh::kColDQ + half * (DP / 2), row < w.nq, a.scale, dq + m * a.D + half * (DP / 2),
+                             a.D - half * (DP / 2), a.sectors);
+        if (m == a.group - 1)
+          store_row<T, DP>(lanes + (half == 0 ? Sh::kColDK : kColDV), row < w.nk, half == 0 ? a.scale : 1.f,
+                           static_cast<T*>(half == 0 ? a.dk : a.dv) + key_at, a.D, a.sectors);
+        tc_fence_before();
+      }
+      ++n;
+    }
+  }
+  zero_rows(a.dq, a.B > 0 ? a.q_offsets[a.B] : 0, a.n_q, (int64_t)a.heads * a.D);
+  zero_rows(a.dk, a.B > 0 ? a.kv_offsets[a.B] : 0, a.n_kv, (int64_t)a.kv_heads * a.D);
+  zero_rows(a.dv, a.B > 0 ? a.kv_offsets[a.B] : 0, a.n_kv, (int64_t)a.kv_heads * a.D);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_free(tmem, 512);
+  }
+  if (threadIdx.x == 0 && *s_abort) record_error(a.hdr, kDevWaitTimeout);
+}
+
+template <typename T, int DP>
+cudaError_t run(const ShortArgs& a, const BwdMaps& m, cudaStream_t s) {
+  const auto kernel = k_attn_backward_short<T, DP>;
+  constexpr int smem = (int)ShortShape<DP>::kSmem;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int64_t items = (int64_t)a.B * a.kv_heads, slots = device_info().sm_count;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(items < 1 ? 1 : items < slots ? items : slots));
+  cfg.blockDim = dim3(kShortThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  count_launch();
+  return cudaLaunchKernelEx(&cfg, kernel, a, m.q, m.k, m.v, m.d);
+}
+
+}  // namespace
+
+cudaError_t launch_attention_backward_short(const AttnCall& c, const BwdMaps& maps, const TileItem* items, WsHeader* hdr,
+                                            cudaStream_t s) {
+  ShortArgs a;
+  a.n_q = c.n_q;
+  a.n_kv = c.n_kv;
+  a.heads = c.heads;
+  a.kv_heads = c.kv_heads;
+  a.group = c.group;
+  a.D = c.D;
+  a.mask = c.mask;
+  a.scale = c.scale;
+  a.scale_log2 = c.scale * kLog2e;
+  a.out = c.out;
+  a.lse = c.lse;
+  a.dq = c.dq;
+  a.dk = c.dk;
+  a.dv = c.dv;
+  a.q_offsets = c.q_offsets;
+  a.kv_offsets = c.kv_offsets;
+  a.B = c.B;
+  a.sectors = maps.sectors;
+  a.items = items;
+  a.hdr = hdr;
+  if (c.dtype == FPS_DTYPE_BF16) return c.D <= 64 ? run<__nv_bfloat16, 64>(a, maps, s) : run<__nv_bfloat16, 128>(a, maps, s);
+  return c.D <= 64 ? run<__half, 64>(a, maps, s) : run<__half, 128>(a, maps, s);
+}
+
+}  // namespace fpstok

@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
             const uint32_t qk_desc = mma_desc(kBf16, false, false, cols);
             // whole panels: values past D are zeros
 #pragma unroll
-            for (int p = 0; p < Sh::kPanels; ++p) mma_ss4(tmem, q + p * (kPanel >> 4), k + p * (kPanel >> 4), qk_desc, p > 0);
+            for (int p = 0; p < Sh::kPanels; ++p) mma_ss_steps<2, 2>(tmem, q + p * (kPanel >> 4), k + p * (kPanel >> 4), 4, qk_desc, p > 0);
             mma_commit(k_empty + 8 * st);
             mma_commit(s_full);
             if (j == count - 1) mma_commit(q_empty + 8 * qs);

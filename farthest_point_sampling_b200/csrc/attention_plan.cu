@@ -57,7 +57,7 @@ __device__ __forceinline__ void block_sort(uint64_t* s) {
   __syncthreads();
 }
 
-enum PlanList { kPlanQueries, kPlanKeys, kPlanUnits };
+enum PlanList { kPlanQueries, kPlanKeys, kPlanUnits, kPlanShorts };
 
 // One block per list.  A pass takes 1024 events, one per thread: their items
 // are counted and scanned, then all threads write the pass's items, each
@@ -73,9 +73,12 @@ __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const int64_t* __res
   __shared__ TileItem s_event[kPlanThreads];
   __shared__ uint64_t s_sort[kPlanThreads];
   const int tid = threadIdx.x;
-  // blocks in the order queries, keys, units, without the lists that are not asked for
-  const int kind = blockIdx.x == 0 ? kPlanQueries : lists.keys && blockIdx.x == 1 ? kPlanKeys : kPlanUnits;
-  TileItem* items = kind == kPlanQueries ? lists.queries : kind == kPlanKeys ? lists.keys : lists.units;
+  // forward: queries, units; backward: queries, keys, shorts
+  const int kind = blockIdx.x == 0 ? kPlanQueries : lists.units ? kPlanUnits : blockIdx.x == 1 ? kPlanKeys : kPlanShorts;
+  TileItem* items = kind == kPlanQueries ? lists.queries
+                    : kind == kPlanKeys  ? lists.keys
+                    : kind == kPlanUnits ? lists.units
+                                         : lists.shorts;
   int base = 0, slots = 0, joins = 0, error = 0;
   if (tid == 0 && B > 0 && (q_off[0] != 0 || k_off[0] != 0)) error = kDevBadOffsets;
   for (int b0 = 0; b0 < B; b0 += kPlanThreads) {
@@ -94,10 +97,13 @@ __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const int64_t* __res
         e.k0 = (int)k0;
         e.nk = (int)(k1 - k0);
         const bool few = lists.units && (int64_t)e.nq * group <= kFewRows;
+        const bool brief = lists.shorts && e.nq <= kTile && e.nk <= kTile;
         if (kind == kPlanQueries) {
-          n = few ? 0 : (e.nq + kTile - 1) / kTile;
+          n = few || brief ? 0 : (e.nq + kTile - 1) / kTile;
         } else if (kind == kPlanKeys) {
-          n = (e.nk + kTile - 1) / kTile;
+          n = brief ? 0 : (e.nk + kTile - 1) / kTile;
+        } else if (kind == kPlanShorts) {
+          n = brief;
         } else if (few && e.nq > 0) {
           n = max((few_span(mask, e.nq, e.nk).count() + lists.chunk - 1) / lists.chunk, 1);
           parts = n > 1 ? n : 0;
@@ -109,7 +115,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const int64_t* __res
     if (__syncthreads_or(error == kDevBadOffsets)) break;
     // Long events first, so that the blocks that claim items in turn end
     // together; where no event has more than four tiles order matters little.
-    if (kind != kPlanUnits && __syncthreads_or(n > 4)) {
+    if (kind <= kPlanKeys && __syncthreads_or(n > 4)) {
       s_event[tid] = e;
       s_sort[tid] = ((uint64_t)n << 32) | (uint32_t)(kPlanThreads - 1 - tid);
       block_sort(s_sort);
@@ -148,8 +154,12 @@ __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const int64_t* __res
   }
   error = __syncthreads_or(error == kDevBadOffsets) ? kDevBadOffsets : __syncthreads_or(error) ? kDevTooLarge : 0;
   if (tid == 0) {
-    hdr->next_item[kind == kPlanQueries ? kQueryTiles : kind == kPlanKeys ? kKeyTiles : kFewUnits] = 0;
-    hdr->n_items[kind == kPlanQueries ? kQueryTiles : kind == kPlanKeys ? kKeyTiles : kFewUnits] = base;
+    const int list = kind == kPlanQueries ? kQueryTiles
+                     : kind == kPlanKeys  ? kKeyTiles
+                     : kind == kPlanUnits ? kFewUnits
+                                          : kShortEvents;
+    hdr->next_item[list] = 0;
+    hdr->n_items[list] = base;
     if (kind == kPlanUnits) hdr->n_items[kFewJoins] = joins;
     if (kind == kPlanQueries) {  // every block sees the same errors; one writes the status word
       hdr->status = error;
@@ -178,7 +188,7 @@ EncodeTiled encode_tiled() {
 
 cudaError_t launch_attention_plan(const AttnCall& c, WsHeader* hdr, const PlanLists& lists, cudaStream_t s) {
   count_launch();
-  k_attn_plan<<<1 + (lists.keys != nullptr) + (lists.units != nullptr), kPlanThreads, 0, s>>>(
+  k_attn_plan<<<lists.shorts ? 3 : lists.units ? 2 : 1, kPlanThreads, 0, s>>>(
       c.q_offsets, c.kv_offsets, c.B, c.n_q, c.n_kv, c.max_tokens, c.group, c.mask, hdr, lists);
   return cudaGetLastError();
 }

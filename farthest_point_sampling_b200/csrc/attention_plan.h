@@ -16,6 +16,7 @@ constexpr int kQueryTiles = 0;
 constexpr int kKeyTiles = 1;
 constexpr int kFewUnits = 2;
 constexpr int kFewJoins = 3;
+constexpr int kShortEvents = 4;
 
 // The lists of one call; those that are NULL are not made.
 struct PlanLists {
@@ -24,6 +25,7 @@ struct PlanLists {
   TileItem* units;    // chunks of the events with at most kFewRows query rows, which then have no query tiles
   JoinItem* joins;    // those of them with several chunks
   int chunk;
+  TileItem* shorts;   // the events of at most 128 queries and 128 keys, which then have no tiles of either kind
 };
 
 // Fills the lists in event order, their counts in hdr->n_items, and resets the

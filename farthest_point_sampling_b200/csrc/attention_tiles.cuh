@@ -235,6 +235,25 @@ __device__ __forceinline__ void store_row(uint32_t acc, bool live, float f, T* t
   }
 }
 
+template <typename T>
+__device__ __forceinline__ float2 unpack16(uint32_t v);
+template <>
+__device__ __forceinline__ float2 unpack16<__nv_bfloat16>(uint32_t v) {
+  return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&v));
+}
+template <>
+__device__ __forceinline__ float2 unpack16<__half>(uint32_t v) {
+  return __half22float2(*reinterpret_cast<__half2*>(&v));
+}
+
+// `values` 16-bit values (a multiple of 8) of `rows` rows to 0, by one warp.
+template <typename T>
+__device__ __forceinline__ void clear_strided(T* base, int rows, int64_t stride, int values) {
+  for (int r = 0; r < rows; ++r)
+    for (int c = (threadIdx.x & 31) * 8; c < values; c += 256)
+      *reinterpret_cast<uint4*>(base + r * stride + c) = make_uint4(0, 0, 0, 0);
+}
+
 // Rows [first, n) of a [n, row_values] 16-bit tensor to 0, over the whole grid.
 __device__ __forceinline__ void zero_rows(void* base, int64_t first, int64_t n, int64_t row_values) {
   if (first < 0 || first >= n) return;

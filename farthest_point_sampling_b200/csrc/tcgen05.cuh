@@ -203,22 +203,34 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint3
       "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(kDescHigh)
       : "memory");
 }
-// Four steps of 16 values at once, one election for all: 64 values along the
-// rows of both operands, or 64 rows of B against 32 columns of A in TMEM.
-__device__ __forceinline__ void mma_ss4(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
-  asm volatile(
-      "{\n\t" FPS_ELECT ".reg .pred p, t;\n\t.reg .b64 x, y;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.eq.u32 t, 0, 0;\n\t"
-      "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
-      "@elected tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t"
-      "add.s64 x, x, 2;\n\tadd.s64 y, y, 2;\n\t"
-      "@elected tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
-      "add.s64 x, x, 2;\n\tadd.s64 y, y, 2;\n\t"
-      "@elected tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
-      "add.s64 x, x, 2;\n\tadd.s64 y, y, 2;\n\t"
-      "@elected tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t}" ::"r"(d),
-      "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(kDescHigh)
-      : "memory");
+// `steps` steps of 16 with both operands in shared memory, each along its rows
+// (2 per step) or across them (128 per step); one election for four.
+template <int kA, int kB>
+__device__ __forceinline__ void mma_ss_steps(uint32_t d, uint32_t a, uint32_t b, int steps, uint32_t idesc, bool accumulate) {
+#pragma unroll 1
+  for (; steps >= 4; steps -= 4, a += 4 * kA, b += 4 * kB, accumulate = true)
+    asm volatile(
+        "{\n\t" FPS_ELECT ".reg .pred p, t;\n\t.reg .b64 x, y;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.eq.u32 t, 0, 0;\n\t"
+        "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+        "@elected tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t"
+        "add.s64 x, x, %6;\n\tadd.s64 y, y, %7;\n\t"
+        "@elected tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
+        "add.s64 x, x, %6;\n\tadd.s64 y, y, %7;\n\t"
+        "@elected tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
+        "add.s64 x, x, %6;\n\tadd.s64 y, y, %7;\n\t"
+        "@elected tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(kDescHigh), "n"(kA), "n"(kB)
+        : "memory");
+#pragma unroll 1
+  for (; steps > 0; --steps, a += kA, b += kB, accumulate = true)
+    asm volatile(
+        "{\n\t" FPS_ELECT ".reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+        "@elected tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(kDescHigh)
+        : "memory");
 }
+// Four steps of 16 rows of B against 32 columns of A in TMEM, one election for all.
 __device__ __forceinline__ void mma_ts4(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
   asm volatile(
       "{\n\t" FPS_ELECT ".reg .pred p, t;\n\t.reg .b64 y;\n\t.reg .b32 x;\n\tsetp.ne.u32 p, %4, 0;\n\t"

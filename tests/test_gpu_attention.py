@@ -312,6 +312,30 @@ def test_no_rows():
     assert bool((dk == 0).all()) and bool((dv == 0).all())
 
 
+@pytest.mark.parametrize("H,G", [(2, 2), (6, 2)])
+def test_runs_of_events_without_pairs(H, G):
+    """Several events in a row without queries, or without keys, between others, short and long: their gradients are 0."""
+    g = torch.Generator().manual_seed(2)
+    nq, nk = [], []
+    for _ in range(60):
+        for _ in range(int(torch.randint(0, 7, (1,), generator=g))):
+            n = int(torch.randint(1, 400, (1,), generator=g))
+            a, b = [(0, n), (n, 0), (0, 0)][int(torch.randint(0, 3, (1,), generator=g))]
+            nq.append(a)
+            nk.append(b)
+        n = int(torch.randint(1, 260, (1,), generator=g))
+        nq.append(n)
+        nk.append(n)
+    ws = torch.zeros(1 << 26, dtype=torch.uint8, device="cuda")
+    for D in (64, 128):
+        q, k, v, dout, qo, ko = _inputs(nq, nk, H, G, D, BF16, 210)
+        _check(q, k, v, dout, qo, ko)
+        out, lse = fps.attention_forward(q, k, v, qo, ko, workspace=ws)
+        fps.device_status(ws)
+        fps.attention_backward(dout, q, k, v, out, lse, qo, ko, workspace=ws)
+        fps.device_status(ws)  # no wait ran out
+
+
 def test_tokens_to_attention():
     """The run a model makes: tokenize, pack, project, turn by the centroids, attend, gradients, summary query."""
     import workloads
