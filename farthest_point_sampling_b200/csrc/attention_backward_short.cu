@@ -10,11 +10,16 @@
 //
 // A work item is an event and a key head, with a unit for each query head of
 // its group; dK and dV are summed over the units in TMEM.  Warps: a loading
-// and an issuing warp; four that form D and the scaled lse of a unit's queries
-// ahead of the others; eight for the softmax with two threads per key row,
+// and an issuing warp, and eight for the rest with two threads per key row,
 // each for half of the queries.  P goes back over S in TMEM as 16-bit operand
 // A; dS goes to shared memory, where it is read along its rows for dK and
 // across them for dQ.
+//
+// The phases of a unit follow one another, so what fills an SM is a second
+// block.  With 64-wide heads of their own keys (kTwo) a block makes do with 256
+// columns of TMEM: dK and dQ take the place of dP, and dV that of the scores
+// that P does not cover.  Otherwise one block takes the SM, with dV and dK kept
+// over the heads of a group.
 //
 // Rounding: as in attention_backward.cu.
 #include <type_traits>
@@ -33,10 +38,9 @@ namespace {
 constexpr int kHalf = kTile / 2;
 constexpr int kPanel = kTile * 128;
 constexpr int kSoftmaxThreads = 256;
-constexpr int kRowThreads = 128;
-constexpr int kShortThreads = kSoftmaxThreads + kRowThreads + 64;
+constexpr int kShortThreads = kSoftmaxThreads + 64;
 constexpr int kItemRing = 2;
-constexpr uint32_t kColS = 0, kColDP = 128, kColDV = 256;
+constexpr uint32_t kColS = 0, kColDP = 128;
 
 struct ShortArgs {
   int64_t n_q, n_kv;
@@ -58,15 +62,16 @@ struct ShortItem {
   int h, q_row, nq, k_row, nk;  // key head; the event's first query and key rows, queries, keys
 };
 
-template <int DP>
+template <int DP, bool kTwo>
 struct ShortShape {
   static constexpr int kPanels = DP / 64;
   static constexpr uint32_t kTileBytes = kPanels * kPanel;
-  static constexpr int kStages = DP == 64 ? 2 : 1;  // of (K, V), and of (Q, dO)
-  static constexpr uint32_t kColDK = kColDV + DP;
-  // 64-wide heads leave TMEM for dQ; with 128-wide ones it takes the place of dP
-  static constexpr uint32_t kColDQ = DP == 64 ? kColDK + DP : kColDP;
-  static constexpr size_t kSmem = 1024 + 4 * kStages * kTileBytes + 2 * kPanel + kStages * 2 * kTile * sizeof(float) +
+  static constexpr int kStages = DP == 64 && !kTwo ? 2 : 1;  // of (K, V), and of (Q, dO)
+  static constexpr uint32_t kColumns = kTwo ? 256 : 512;
+  // 64-wide heads leave room for dQ beside dV and dK; with 128-wide ones it takes the place of dP
+  static constexpr uint32_t kColDV = 256, kColDK = kTwo ? kColDP : 256 + DP;
+  static constexpr uint32_t kColDQ = kTwo ? kColDP + 64 : DP == 64 ? kColDK + DP : kColDP;
+  static constexpr size_t kSmem = 1024 + 4 * kStages * kTileBytes + 2 * kPanel + 2 * kTile * sizeof(float) +
                                   kItemRing * sizeof(ShortItem) + 512;
 };
 
@@ -80,29 +85,30 @@ __device__ __forceinline__ void clear_rows(uint8_t* tile, int n, int thread, int
   }
 }
 
-template <typename T, int DP>
-__global__ void __launch_bounds__(kShortThreads, 1)
+template <typename T, int DP, bool kTwo>
+__global__ void __launch_bounds__(kShortThreads, kTwo ? 2 : 1)
     k_attn_backward_short(const ShortArgs a, const __grid_constant__ CUtensorMap map_q,
                           const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                           const __grid_constant__ CUtensorMap map_do) {
-  using Sh = ShortShape<DP>;
+  using Sh = ShortShape<DP, kTwo>;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   constexpr int kStages = Sh::kStages;
-  constexpr int kRowWarp = kSoftmaxThreads / 32, kLoadWarp = kRowWarp + kRowThreads / 32, kMmaWarp = kLoadWarp + 1;
+  constexpr int kLoadWarp = kSoftmaxThreads / 32, kMmaWarp = kLoadWarp + 1;
   extern __shared__ uint8_t s_raw[];
   uint8_t* s_base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t* s_kv = s_base;                                      // [stage][K, V]
   uint8_t* s_qd = s_kv + 2 * kStages * Sh::kTileBytes;         // [stage][Q, dO]
   uint8_t* s_ds = s_qd + 2 * kStages * Sh::kTileBytes;         // dS: key rows, a panel for each half of the queries
-  float* s_col = reinterpret_cast<float*>(s_ds + 2 * kPanel);  // [stage][-lse log2(e), -D][128]
-  ShortItem* s_item = reinterpret_cast<ShortItem*>(s_col + kStages * 2 * kTile);
+  float* s_col = reinterpret_cast<float*>(s_ds + 2 * kPanel);  // [-lse log2(e), -D][128 queries]
+  ShortItem* s_item = reinterpret_cast<ShortItem*>(s_col + 2 * kTile);
   uint64_t* s_bar = reinterpret_cast<uint64_t*>((reinterpret_cast<uintptr_t>(s_item + kItemRing) + 7) & ~(uintptr_t)7);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_bar + 32);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   const uint32_t bars = smem_u32(s_bar);
   const uint32_t kv_full = bars, kv_empty = bars + 16, qd_full = bars + 32, qd_empty = bars + 48, item_full = bars + 64,
-                 item_empty = bars + 80, col_full = bars + 96, s_full = bars + 112, dp_full = bars + 120,
-                 p_ready = bars + 128, ds_ready = bars + 136, done = bars + 144, drain = bars + 152;
+                 item_empty = bars + 80, col_full = bars + 96, stored = bars + 104, s_full = bars + 112,
+                 dp_full = bars + 120, p_ready = bars + 128, ds_ready = bars + 136, done = bars + 144,
+                 drain = bars + 152;
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -112,9 +118,10 @@ __global__ void __launch_bounds__(kShortThreads, 1)
       mbar_init(qd_full + 8 * i, 1);
       mbar_init(qd_empty + 8 * i, 1);
       mbar_init(item_full + 8 * i, 1);
-      mbar_init(item_empty + 8 * i, kSoftmaxThreads + kRowThreads + 1);
-      mbar_init(col_full + 8 * i, kRowThreads);
+      mbar_init(item_empty + 8 * i, kSoftmaxThreads + 1);
     }
+    mbar_init(col_full, kSoftmaxThreads);
+    mbar_init(stored, kSoftmaxThreads);
     mbar_init(s_full, 1);
     mbar_init(dp_full, 1);
     mbar_init(p_ready, kSoftmaxThreads);
@@ -128,7 +135,7 @@ __global__ void __launch_bounds__(kShortThreads, 1)
     tma_prefetch_map(&map_v);
     tma_prefetch_map(&map_do);
   }
-  if (warp == kMmaWarp) tmem_alloc(smem_u32(s_tmem), 512);
+  if (warp == kMmaWarp) tmem_alloc(smem_u32(s_tmem), Sh::kColumns);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -196,6 +203,7 @@ __global__ void __launch_bounds__(kShortThreads, 1)
     const int cols = (a.D + 15) / 16 * 16;
     const uint32_t ts_desc = mma_desc(kBf16, false, true, cols);  // dV: A in TMEM; dK: dS along its rows
     const uint32_t dq_desc = mma_desc(kBf16, true, true, cols);   // dQ: dS across its rows
+    const uint32_t dv_low = mma_desc(kBf16, false, true, min(cols, 32)), dv_high = mma_desc(kBf16, false, true, cols - 32);
     struct Unit {
       int q_steps, k_steps, kv, qd;
       bool first, last;  // of its item
@@ -236,24 +244,35 @@ __global__ void __launch_bounds__(kShortThreads, 1)
         mma_ss_steps<2, 2>(tmem + (x ? kColDP : kColS), kept + p * (kPanel >> 4), from + p * (kPanel >> 4), 4, desc, p > 0);
       mma_commit(x ? dp_full : s_full);
     };
-    // With one stage the next unit's tiles load only after this one's products;
-    // with 128-wide heads dP also waits for dQ in its place to be stored.
+    // With one stage the next unit's tiles load only after this one's
+    // products.  Where dQ takes the place of dP, dP waits for its stores, which
+    // come before the next P; where dV takes that of S (kTwo) so does S, which
+    // needs a signal of its own.
     constexpr bool kAhead = kStages > 1;
     Unit cur, nxt;
     bool more = fetch(&cur);
     if (more) {
       scores(cur, 0);
-      if (kAhead) scores(cur, 1);
+      if (kAhead || kTwo) scores(cur, 1);
     }
     const uint32_t ds = smem_desc(smem_u32(s_ds), kPanel);
     for (int u = 0; more; ++u) {
       if (!mbar_wait_warp(p_ready, u & 1, s_abort)) break;
       tc_fence_after();
-      if (!kAhead) scores(cur, 1);
+      if (!kAhead && !kTwo) scores(cur, 1);
       const uint32_t q_rows = smem_desc(smem_u32(s_qd) + 2 * cur.qd * Sh::kTileBytes, kPanel);
       const uint32_t do_rows = q_rows + (Sh::kTileBytes >> 4);
-      mma_ts_steps(tmem + kColDV, tmem + kColS, do_rows, min(cur.q_steps, 4), ts_desc, !cur.first);  // dV += P^T dO
-      if (cur.q_steps > 4) mma_ts_steps(tmem + kColDV, tmem + kColS + kHalf, do_rows + 512, cur.q_steps - 4, ts_desc, true);
+      // dV += P^T dO: 64 queries of P lie over the first half of their scores
+      const auto dv = [&](uint32_t to, uint32_t from, uint32_t desc) {
+        mma_ts_steps(to, tmem + kColS, from, min(cur.q_steps, 4), desc, !cur.first);
+        if (cur.q_steps > 4) mma_ts_steps(to, tmem + kColS + kHalf, from + 512, cur.q_steps - 4, desc, true);
+      };
+      if constexpr (kTwo) {
+        dv(tmem + kColS + 32, do_rows, dv_low);
+        if (cols > 32) dv(tmem + kColS + 96, do_rows + 4, dv_high);  // 32 values, 64 bytes on
+      } else {
+        dv(tmem + Sh::kColDV, do_rows, ts_desc);
+      }
       if (kAhead) {
         more = fetch(&nxt);
         if (!ok) break;
@@ -272,7 +291,12 @@ __global__ void __launch_bounds__(kShortThreads, 1)
       if (!kAhead) {
         more = fetch(&nxt);
         if (!ok) break;
+        if (kTwo && more) {
+          if (!mbar_wait_warp(stored, u & 1, s_abort)) break;
+          tc_fence_after();
+        }
         if (more) scores(nxt, 0);
+        if (kTwo && more) scores(nxt, 1);
       } else if (more) {
         scores(nxt, 1);
       }
@@ -282,49 +306,6 @@ __global__ void __launch_bounds__(kShortThreads, 1)
       volatile int none = 0;
       mma_commit(drain);
       mbar_wait_warp(drain, 0, &none);
-    }
-  } else if (warp >= kRowWarp) {
-    // ------------------------------------------------ D and lse of a unit's queries, ahead of the softmax
-    const int row = threadIdx.x - kSoftmaxThreads;
-    int u = 0;
-    bool ok = true;
-    for (int i = 0; ok; ++i) {
-      const int slot = i % kItemRing;
-      if (!(ok = mbar_wait(item_full + 8 * slot, (i / kItemRing) & 1, s_abort))) break;
-      const ShortItem w = s_item[slot];
-      if (w.nq < 0) break;
-      mbar_arrive(item_empty + 8 * slot);
-      const int64_t q = (int64_t)w.q_row + row;
-#pragma unroll 1
-      for (int m = 0; m < a.group; ++m, ++u) {
-        const int st = u % kStages, h = w.h * a.group + m;
-        uint4 o[DP / 8];
-        float lse = 0.f, delta = 0.f;
-        if (row < w.nq) {  // O is on its way while dO's tile is waited for
-          const T* from = static_cast<const T*>(a.out) + (q * a.heads + h) * a.D;
-#pragma unroll
-          for (int c = 0; c < DP / 8; ++c) o[c] = c * 8 < a.D ? *reinterpret_cast<const uint4*>(from + c * 8) : make_uint4(0, 0, 0, 0);
-          lse = a.lse[(int64_t)h * a.n_q + q];
-        }
-        if (!(ok = mbar_wait(qd_full + 8 * st, (u / kStages) & 1, s_abort))) break;
-        if (row < w.nq) {
-          const uint8_t* d = s_qd + (2 * st + 1) * Sh::kTileBytes + row * 128;
-#pragma unroll
-          for (int c = 0; c < DP / 8; ++c) {
-            const uint4 vd = *reinterpret_cast<const uint4*>(d + (c >> 3) * kPanel + (((c & 7) ^ (row & 7)) << 4));
-            const uint32_t* po = reinterpret_cast<const uint32_t*>(&o[c]);
-            const uint32_t* pd = reinterpret_cast<const uint32_t*>(&vd);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float2 x = unpack16<T>(po[k]), y = unpack16<T>(pd[k]);
-              delta = fmaf(x.x, y.x, fmaf(x.y, y.y, delta));
-            }
-          }
-        }
-        s_col[st * 2 * kTile + row] = -lse * kLog2e;
-        s_col[st * 2 * kTile + kTile + row] = -delta;
-        mbar_arrive(col_full + 8 * st);
-      }
     }
   } else {
     // ------------------------------------------------ softmax and its gradient
@@ -344,6 +325,7 @@ __global__ void __launch_bounds__(kShortThreads, 1)
       T* dq = static_cast<T*>(a.dq) + (((int64_t)w.q_row + row) * a.heads + w.h * a.group) * a.D;
       const int64_t key_at = (((int64_t)w.k_row + row) * a.kv_heads + w.h) * a.D;
       const int shift = w.nk - w.nq, ks = n % kStages;
+      const int q = warp * 16 + (lane >> 1);  // the query whose D this thread and the next form
       // which pairs of the warp's key rows and each 32 of this thread's queries see one another
       bool act[2], whole[2];
       uint32_t see[2];
@@ -357,12 +339,24 @@ __global__ void __launch_bounds__(kShortThreads, 1)
       }
 #pragma unroll 1
       for (int m = 0; m < a.group; ++m, ++u) {
-        const int st = u % kStages;
+        const int st = u % kStages, h = w.h * a.group + m;
+        // D and lse of the unit's queries, two threads for each; O is on its
+        // way while dO's tile is waited for
+        uint4 o[DP / 16];
+        float lse = 0.f, delta = 0.f;
+        const int d0 = (lane & 1) * (DP / 16);
+        if (q < w.nq) {
+          const T* from = static_cast<const T*>(a.out) + (((int64_t)w.q_row + q) * a.heads + h) * a.D;
+#pragma unroll
+          for (int c = 0; c < DP / 16; ++c)
+            o[c] = (d0 + c) * 8 < a.D ? *reinterpret_cast<const uint4*>(from + (d0 + c) * 8) : make_uint4(0, 0, 0, 0);
+          lse = a.lse[(int64_t)h * a.n_q + w.q_row + q];
+        }
+        if (!(ok = mbar_wait(qd_full + 8 * st, (u / kStages) & 1, s_abort))) break;
+        uint8_t* tile = s_qd + 2 * st * Sh::kTileBytes;
         // Rows past the event's last inside a product's step of 16: their P and
         // dS are 0, and the rows must be finite for 0 to stay 0.
         if (w.nq & 15) {
-          if (!(ok = mbar_wait(qd_full + 8 * st, (u / kStages) & 1, s_abort))) break;
-          uint8_t* tile = s_qd + 2 * st * Sh::kTileBytes;
           clear_rows<Sh::kPanels>(tile, w.nq, threadIdx.x, kSoftmaxThreads);
           clear_rows<Sh::kPanels>(tile + Sh::kTileBytes, w.nq, threadIdx.x, kSoftmaxThreads);
         }
@@ -370,8 +364,25 @@ __global__ void __launch_bounds__(kShortThreads, 1)
           if (!(ok = mbar_wait(kv_full + 8 * ks, (n / kStages) & 1, s_abort))) break;
           clear_rows<Sh::kPanels>(s_kv + 2 * ks * Sh::kTileBytes, w.nk, threadIdx.x, kSoftmaxThreads);
         }
-        if (!(ok = mbar_wait(col_full + 8 * st, (u / kStages) & 1, s_abort))) break;
-        const float* col = s_col + st * 2 * kTile + h0;
+        if (q < w.nq) {
+          const uint8_t* d = tile + Sh::kTileBytes + q * 128;
+#pragma unroll
+          for (int c = 0; c < DP / 16; ++c) {
+            const int at = d0 + c;
+            const uint4 vd = *reinterpret_cast<const uint4*>(d + (at >> 3) * kPanel + (((at & 7) ^ (q & 7)) << 4));
+            const uint32_t* po = reinterpret_cast<const uint32_t*>(&o[c]);
+            const uint32_t* pd = reinterpret_cast<const uint32_t*>(&vd);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 x = unpack16<T>(po[k]), y = unpack16<T>(pd[k]);
+              delta = fmaf(x.x, y.x, fmaf(x.y, y.y, delta));
+            }
+          }
+        }
+        delta += __shfl_xor_sync(kFull, delta, 1);
+        s_col[(lane & 1) * kTile + q] = lane & 1 ? -delta : -lse * kLog2e;
+        mbar_arrive(col_full);
+        const float* col = s_col + h0;
         if (!(ok = mbar_wait(s_full, u & 1, s_abort))) break;
         tc_fence_after();
         float x[kHalf];
@@ -379,6 +390,7 @@ __global__ void __launch_bounds__(kShortThreads, 1)
         for (int c = 0; c < 2; ++c) tmem_ld32(lanes + kColS + h0 + 32 * c, reinterpret_cast<uint32_t*>(x + 32 * c));
         tmem_wait_ld32(reinterpret_cast<uint32_t*>(x));
         tmem_wait_ld32(reinterpret_cast<uint32_t*>(x + 32));
+        if (!(ok = mbar_wait(col_full, u & 1, s_abort))) break;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           if (act[c]) {
@@ -454,9 +466,17 @@ __global__ void __launch_bounds__(kShortThreads, 1)
         tc_fence_after();
         store_row<T, DP / 2>(lanes + Sh::kColDQ + half * (DP / 2), row < w.nq, a.scale, dq + m * a.D + half * (DP / 2),
                              a.D - half * (DP / 2), a.sectors);
-        if (m == a.group - 1)
-          store_row<T, DP>(lanes + (half == 0 ? Sh::kColDK : kColDV), row < w.nk, half == 0 ? a.scale : 1.f,
+        if (kTwo) {  // half of dV's columns are in each half of the scores
+          store_row<T, 32>(lanes + Sh::kColDK + half * 32, row < w.nk, a.scale, static_cast<T*>(a.dk) + key_at + half * 32,
+                           a.D - half * 32, a.sectors);
+          store_row<T, 32>(lanes + kColS + 32 + half * 64, row < w.nk, 1.f, static_cast<T*>(a.dv) + key_at + half * 32,
+                           a.D - half * 32, a.sectors);
+          tc_fence_before();
+          mbar_arrive(stored);
+        } else if (m == a.group - 1) {
+          store_row<T, DP>(lanes + (half == 0 ? Sh::kColDK : Sh::kColDV), row < w.nk, half == 0 ? a.scale : 1.f,
                            static_cast<T*>(half == 0 ? a.dk : a.dv) + key_at, a.D, a.sectors);
+        }
         tc_fence_before();
       }
       ++n;
@@ -470,18 +490,18 @@ __global__ void __launch_bounds__(kShortThreads, 1)
   if (warp == kMmaWarp) {
     __syncwarp();
     tc_fence_after();
-    tmem_free(tmem, 512);
+    tmem_free(tmem, Sh::kColumns);
   }
   if (threadIdx.x == 0 && *s_abort) record_error(a.hdr, kDevWaitTimeout);
 }
 
-template <typename T, int DP>
+template <typename T, int DP, bool kTwo>
 cudaError_t run(const ShortArgs& a, const BwdMaps& m, cudaStream_t s) {
-  const auto kernel = k_attn_backward_short<T, DP>;
-  constexpr int smem = (int)ShortShape<DP>::kSmem;
+  const auto kernel = k_attn_backward_short<T, DP, kTwo>;
+  constexpr int smem = (int)ShortShape<DP, kTwo>::kSmem;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const int64_t items = (int64_t)a.B * a.kv_heads, slots = device_info().sm_count;
+  const int64_t items = (int64_t)a.B * a.kv_heads, slots = (int64_t)device_info().sm_count * (kTwo ? 2 : 1);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(items < 1 ? 1 : items < slots ? items : slots));
   cfg.blockDim = dim3(kShortThreads);
@@ -494,6 +514,12 @@ cudaError_t run(const ShortArgs& a, const BwdMaps& m, cudaStream_t s) {
   cfg.numAttrs = 1;
   count_launch();
   return cudaLaunchKernelEx(&cfg, kernel, a, m.q, m.k, m.v, m.d);
+}
+
+template <typename T>
+cudaError_t run_type(const ShortArgs& a, const BwdMaps& m, cudaStream_t s) {
+  if (a.D > 64) return run<T, 128, false>(a, m, s);
+  return a.group == 1 ? run<T, 64, true>(a, m, s) : run<T, 64, false>(a, m, s);
 }
 
 }  // namespace
@@ -521,8 +547,7 @@ cudaError_t launch_attention_backward_short(const AttnCall& c, const BwdMaps& ma
   a.sectors = maps.sectors;
   a.items = items;
   a.hdr = hdr;
-  if (c.dtype == FPS_DTYPE_BF16) return c.D <= 64 ? run<__nv_bfloat16, 64>(a, maps, s) : run<__nv_bfloat16, 128>(a, maps, s);
-  return c.D <= 64 ? run<__half, 64>(a, maps, s) : run<__half, 128>(a, maps, s);
+  return c.dtype == FPS_DTYPE_BF16 ? run_type<__nv_bfloat16>(a, maps, s) : run_type<__half>(a, maps, s);
 }
 
 }  // namespace fpstok
