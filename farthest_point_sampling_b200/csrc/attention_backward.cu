@@ -318,15 +318,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const uint32_t desc = mma_desc(kBf16, false, false, t.steps * 16);
 #pragma unroll
       for (int p = 0; p < Sh::kPanels; ++p)
-        mma_ss_steps<2, 2>(tmem + (x ? kColDP : kColS), kept + p * (kPanel >> 4), from + p * (kPanel >> 4), 4, desc, p > 0);
+        mma_ss<2, 2>(tmem + (x ? kColDP : kColS), kept + p * (kPanel >> 4), from + p * (kPanel >> 4), desc, p > 0);
       mma_commit(x ? dp_full : s_full);
     };
     // an accumulator += the 16-bit rows over S or dP, times a streamed tensor;
     // each half of the rows lies over its half of the scores
     const auto gradient = [&](const Tile& t, int m, uint32_t from, uint32_t to, int x) {
       const uint32_t rows = smem_desc(smem_u32(s_ring) + (2 * (m % Sh::kRing) + x) * Sh::kTileBytes, kPanel);
-      mma_ts_steps(to, from, rows, min(t.steps, 4), out_desc, !t.first);
-      if (t.steps > 4) mma_ts_steps(to, from + kHalf, rows + 512, t.steps - 4, out_desc, true);
+      mma_ts(to, from, rows, out_desc, !t.first);
+      if (t.steps > 4) mma_ts(to, from + kHalf, rows + kRun, out_desc, true);
     };
     Tile cur, nxt;
     bool more = fetch(&cur);
@@ -412,22 +412,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll 1
       for (int t = 0, j = 0; t < tiles; ++t, ++m) {
         const int st = m % Sh::kRing;
-        const int extent = w.tiles.extent(j), odd = extent & 15, stream0 = w.tiles.start(j);
+        const int extent = w.tiles.extent(j), stream0 = w.tiles.start(j);
         j = j + 1 == count ? 0 : j + 1;
-        if (kKeys || odd) {
+        if (kKeys || (extent & 63)) {
           // also where -lse and -D are read from
           if (!(ok = mbar_wait(ring_full + 8 * st, (m / Sh::kRing) & 1, s_abort))) break;
         }
-        if (odd) {
-          // Streamed rows past the tile's last inside a product's step of 16:
-          // their P and dS are 0, and the rows must be finite for 0 to stay 0.
+        if (extent & 63) {
           uint8_t* tile = s_ring + 2 * st * Sh::kTileBytes;
-          constexpr int kTensors = kKeys ? 2 : 1;
-#pragma unroll 1
-          for (int e = threadIdx.x; e < (16 - odd) * 8 * Sh::kPanels * kTensors; e += kSoftmaxThreads) {
-            const int x = e % (8 * Sh::kPanels * kTensors), r = extent + e / (8 * Sh::kPanels * kTensors);
-            *reinterpret_cast<uint4*>(tile + (x >> 3) * kPanel + r * 128 + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
-          }
+          clear_rows<Sh::kPanels>(tile, extent, threadIdx.x, kSoftmaxThreads);
+          if (kKeys) clear_rows<Sh::kPanels>(tile + Sh::kTileBytes, extent, threadIdx.x, kSoftmaxThreads);
           fence_async_smem();
         }
         // which pairs of the warp's kept rows and each 32 of this thread's
@@ -482,7 +476,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             uint32_t p16[16];
 #pragma unroll
             for (int k = 0; k < 16; ++k) p16[k] = act[c] ? pack16<T>(x[32 * c + 2 * k], x[32 * c + 2 * k + 1]) : 0u;
-            if (h0 + 32 * c < extent) tmem_st16(lanes + kColS + h0 + 16 * c, p16);
+            if (h0 < extent) tmem_st16(lanes + kColS + h0 + 16 * c, p16);  // zeros too, to the end of 64 rows
           }
         }
         if constexpr (kKeys) tmem_wait_st();
@@ -521,7 +515,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
             for (int k = 0; k < 16; ++k) d16[k] = 0;
           }
-          if (h0 + 32 * c < extent) tmem_st16(lanes + kColDP + h0 + 16 * c, d16);
+          if (h0 < extent) tmem_st16(lanes + kColDP + h0 + 16 * c, d16);
         }
         tmem_wait_st();
         tc_fence_before();

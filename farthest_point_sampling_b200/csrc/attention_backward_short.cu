@@ -15,11 +15,13 @@
 // A; dS goes to shared memory, where it is read along its rows for dK and
 // across them for dQ.
 //
-// The phases of a unit follow one another, so what fills an SM is a second
-// block.  With 64-wide heads of their own keys (kTwo) a block makes do with 256
-// columns of TMEM: dK and dQ take the place of dP, and dV that of the scores
-// that P does not cover.  Otherwise one block takes the SM, with dV and dK kept
-// over the heads of a group.
+// The phases of a unit (scores, weights, gradients, stores) follow one another,
+// so what fills an SM is a second block: with 64-wide heads of their own keys
+// (kTwo) a block makes do with 256 columns of TMEM, dK and dQ in the place of dP
+// and dV in that of the scores that P does not cover.  Otherwise one block takes
+// the SM, with dV and dK kept over the heads of a group.  The two 32-query
+// chunks of a thread go through one loop body, which keeps the kernel in
+// the instruction cache and a thread at 96 registers.
 //
 // Rounding: as in attention_backward.cu.
 #include <type_traits>
@@ -75,16 +77,6 @@ struct ShortShape {
                                   kItemRing * sizeof(ShortItem) + 512;
 };
 
-// The rows [n, up to the next 16) of a tile to 0.
-template <int kPanels>
-__device__ __forceinline__ void clear_rows(uint8_t* tile, int n, int thread, int threads) {
-#pragma unroll 1
-  for (int e = thread; e < (-n & 15) * 8 * kPanels; e += threads) {
-    const int r = n + e / (8 * kPanels), c = e % (8 * kPanels);
-    *reinterpret_cast<uint4*>(tile + (c >> 3) * kPanel + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-  }
-}
-
 template <typename T, int DP, bool kTwo>
 __global__ void __launch_bounds__(kShortThreads, kTwo ? 2 : 1)
     k_attn_backward_short(const ShortArgs a, const __grid_constant__ CUtensorMap map_q,
@@ -106,9 +98,8 @@ __global__ void __launch_bounds__(kShortThreads, kTwo ? 2 : 1)
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   const uint32_t bars = smem_u32(s_bar);
   const uint32_t kv_full = bars, kv_empty = bars + 16, qd_full = bars + 32, qd_empty = bars + 48, item_full = bars + 64,
-                 item_empty = bars + 80, col_full = bars + 96, stored = bars + 104, s_full = bars + 112,
-                 dp_full = bars + 120, p_ready = bars + 128, ds_ready = bars + 136, done = bars + 144,
-                 drain = bars + 152;
+                 item_empty = bars + 80, col_full = bars + 96, stored = bars + 104,
+                 scores_full = bars + 112, ready = bars + 120, done = bars + 128, drain = bars + 136;
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -122,10 +113,8 @@ __global__ void __launch_bounds__(kShortThreads, kTwo ? 2 : 1)
     }
     mbar_init(col_full, kSoftmaxThreads);
     mbar_init(stored, kSoftmaxThreads);
-    mbar_init(s_full, 1);
-    mbar_init(dp_full, 1);
-    mbar_init(p_ready, kSoftmaxThreads);
-    mbar_init(ds_ready, kSoftmaxThreads);
+    mbar_init(scores_full, 1);
+    mbar_init(ready, kSoftmaxThreads);
     mbar_init(done, 1);
     mbar_init(drain, 1);
     *s_abort = 0;
@@ -204,103 +193,56 @@ __global__ void __launch_bounds__(kShortThreads, kTwo ? 2 : 1)
     const uint32_t ts_desc = mma_desc(kBf16, false, true, cols);  // dV: A in TMEM; dK: dS along its rows
     const uint32_t dq_desc = mma_desc(kBf16, true, true, cols);   // dQ: dS across its rows
     const uint32_t dv_low = mma_desc(kBf16, false, true, min(cols, 32)), dv_high = mma_desc(kBf16, false, true, cols - 32);
-    struct Unit {
-      int q_steps, k_steps, kv, qd;
-      bool first, last;  // of its item
-    };
-    int i = 0, m = a.group, n = 0, fetched = 0, nq = 0, nk = 0;
-    bool ok = true;
-    const auto fetch = [&](Unit* t) {  // the next unit; false when the work is done, or a wait gave up (ok)
-      if (m == a.group) {
-        const int slot = i % kItemRing;
-        if (!(ok = mbar_wait_warp(item_full + 8 * slot, (i / kItemRing) & 1, s_abort))) return false;
-        nq = uniform(s_item[slot].nq);
-        nk = uniform(s_item[slot].nk);
-        mbar_arrive_one(item_empty + 8 * slot);
-        if (nq < 0) return false;
-        ++i;
-        m = 0;
-        if (!(ok = mbar_wait_warp(kv_full + 8 * (n % kStages), (n / kStages) & 1, s_abort))) return false;
-        ++n;
-      }
-      t->qd = fetched % kStages;
-      if (!(ok = mbar_wait_warp(qd_full + 8 * t->qd, (fetched / kStages) & 1, s_abort))) return false;
-      ++fetched;
-      t->kv = (n - 1) % kStages;
-      t->q_steps = (nq + 15) / 16;
-      t->k_steps = (nk + 15) / 16;
-      t->first = m == 0;
-      t->last = ++m == a.group;
-      tc_fence_after();
-      return true;
-    };
-    // S (x = 0) or dP (x = 1): whole panels, as values past D are zeros
-    const auto scores = [&](const Unit& t, int x) {
-      const uint32_t kept = smem_desc(smem_u32(s_kv) + (2 * t.kv + x) * Sh::kTileBytes, kPanel);
-      const uint32_t from = smem_desc(smem_u32(s_qd) + (2 * t.qd + x) * Sh::kTileBytes, kPanel);
-      const uint32_t desc = mma_desc(kBf16, false, false, t.q_steps * 16);
-#pragma unroll
-      for (int p = 0; p < Sh::kPanels; ++p)
-        mma_ss_steps<2, 2>(tmem + (x ? kColDP : kColS), kept + p * (kPanel >> 4), from + p * (kPanel >> 4), 4, desc, p > 0);
-      mma_commit(x ? dp_full : s_full);
-    };
-    // With one stage the next unit's tiles load only after this one's
-    // products.  Where dQ takes the place of dP, dP waits for its stores, which
-    // come before the next P; where dV takes that of S (kTwo) so does S, which
-    // needs a signal of its own.
-    constexpr bool kAhead = kStages > 1;
-    Unit cur, nxt;
-    bool more = fetch(&cur);
-    if (more) {
-      scores(cur, 0);
-      if (kAhead || kTwo) scores(cur, 1);
-    }
     const uint32_t ds = smem_desc(smem_u32(s_ds), kPanel);
-    for (int u = 0; more; ++u) {
-      if (!mbar_wait_warp(p_ready, u & 1, s_abort)) break;
-      tc_fence_after();
-      if (!kAhead && !kTwo) scores(cur, 1);
-      const uint32_t q_rows = smem_desc(smem_u32(s_qd) + 2 * cur.qd * Sh::kTileBytes, kPanel);
-      const uint32_t do_rows = q_rows + (Sh::kTileBytes >> 4);
-      // dV += P^T dO: 64 queries of P lie over the first half of their scores
-      const auto dv = [&](uint32_t to, uint32_t from, uint32_t desc) {
-        mma_ts_steps(to, tmem + kColS, from, min(cur.q_steps, 4), desc, !cur.first);
-        if (cur.q_steps > 4) mma_ts_steps(to, tmem + kColS + kHalf, from + 512, cur.q_steps - 4, desc, true);
-      };
-      if constexpr (kTwo) {
-        dv(tmem + kColS + 32, do_rows, dv_low);
-        if (cols > 32) dv(tmem + kColS + 96, do_rows + 4, dv_high);  // 32 values, 64 bytes on
-      } else {
-        dv(tmem + Sh::kColDV, do_rows, ts_desc);
-      }
-      if (kAhead) {
-        more = fetch(&nxt);
-        if (!ok) break;
-        if (more) scores(nxt, 0);
-      }
-      if (!mbar_wait_warp(ds_ready, u & 1, s_abort)) break;
-      tc_fence_after();
-      mma_ss_steps<2, 128>(tmem + Sh::kColDK, ds, q_rows, min(cur.q_steps, 4), ts_desc, !cur.first);  // dK += dS^T Q
-      if (cur.q_steps > 4)
-        mma_ss_steps<2, 128>(tmem + Sh::kColDK, ds + (kPanel >> 4), q_rows + 512, cur.q_steps - 4, ts_desc, true);
-      mma_ss_steps<128, 128>(tmem + Sh::kColDQ, ds, smem_desc(smem_u32(s_kv) + 2 * cur.kv * Sh::kTileBytes, kPanel),
-                             cur.k_steps, dq_desc, false);  // dQ = dS K
-      mma_commit(qd_empty + 8 * cur.qd);
-      if (cur.last) mma_commit(kv_empty + 8 * cur.kv);
-      mma_commit(done);
-      if (!kAhead) {
-        more = fetch(&nxt);
-        if (!ok) break;
-        if (kTwo && more) {
-          if (!mbar_wait_warp(stored, u & 1, s_abort)) break;
-          tc_fence_after();
+    int n = 0, u = 0;  // items and units so far
+    bool ok = true;
+    for (int i = 0; ok; ++i, ++n) {
+      const int slot = i % kItemRing;
+      if (!(ok = mbar_wait_warp(item_full + 8 * slot, (i / kItemRing) & 1, s_abort))) break;
+      const int nq = uniform(s_item[slot].nq), nk = uniform(s_item[slot].nk);
+      mbar_arrive_one(item_empty + 8 * slot);
+      if (nq < 0) break;
+      const int ks = n % kStages;
+      const uint32_t kv = smem_desc(smem_u32(s_kv) + 2 * ks * Sh::kTileBytes, kPanel);
+      if (!(ok = mbar_wait_warp(kv_full + 8 * ks, (n / kStages) & 1, s_abort))) break;
+      const uint32_t s_desc = mma_desc(kBf16, false, false, (nq + 15) / 16 * 16);
+#pragma unroll 1
+      for (int m = 0; m < a.group; ++m, ++u) {
+        const int st = u % kStages;
+        const uint32_t qd = smem_desc(smem_u32(s_qd) + 2 * st * Sh::kTileBytes, kPanel);
+        if (!(ok = mbar_wait_warp(qd_full + 8 * st, (u / kStages) & 1, s_abort))) break;
+        // the last unit's gradients lie where these scores go
+        if (u > 0 && !(ok = mbar_wait_warp(stored, (u - 1) & 1, s_abort))) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int x = 0; x < 2; ++x)  // S, then dP: whole panels, as values past D are zeros
+#pragma unroll
+          for (int p = 0; p < Sh::kPanels; ++p)
+            mma_ss<2, 2>(tmem + (x ? kColDP : kColS), kv + ((x * Sh::kTileBytes + p * kPanel) >> 4),
+                         qd + ((x * Sh::kTileBytes + p * kPanel) >> 4), s_desc, p > 0);
+        mma_commit(scores_full);
+        if (!(ok = mbar_wait_warp(ready, u & 1, s_abort))) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int half = 0; half * 64 < nq; ++half) {  // 64 queries at a time
+          const bool more = m > 0 || half > 0;
+          const uint32_t q_rows = qd + half * kRun, do_rows = q_rows + (Sh::kTileBytes >> 4);
+          const uint32_t p16 = tmem + kColS + half * 64;  // P lies over the first half of its scores
+          if constexpr (kTwo) {  // dV += P^T dO
+            mma_ts(tmem + kColS + 32, p16, do_rows, dv_low, more);
+            if (cols > 32) mma_ts(tmem + kColS + 96, p16, do_rows + 4, dv_high, more);  // 32 values, 64 bytes on
+          } else {
+            mma_ts(tmem + Sh::kColDV, p16, do_rows, ts_desc, more);
+          }
+          mma_ss<2, 128>(tmem + Sh::kColDK, ds + half * (kPanel >> 4), q_rows, ts_desc, more);  // dK += dS^T Q
         }
-        if (more) scores(nxt, 0);
-        if (kTwo && more) scores(nxt, 1);
-      } else if (more) {
-        scores(nxt, 1);
+#pragma unroll 1
+        for (int half = 0; half * 64 < nk; ++half)  // dQ = dS K, 64 keys at a time
+          mma_ss<128, 128>(tmem + Sh::kColDQ, ds + half * kRun, kv + half * kRun, dq_desc, half > 0);
+        mma_commit(qd_empty + 8 * st);
+        if (m == a.group - 1) mma_commit(kv_empty + 8 * ks);
+        mma_commit(done);
       }
-      cur = nxt;
     }
     if (__any_sync(kFull, *s_abort)) {  // products in flight end before TMEM is freed
       volatile int none = 0;
@@ -326,17 +268,7 @@ __global__ void __launch_bounds__(kShortThreads, kTwo ? 2 : 1)
       const int64_t key_at = (((int64_t)w.k_row + row) * a.kv_heads + w.h) * a.D;
       const int shift = w.nk - w.nq, ks = n % kStages;
       const int q = warp * 16 + (lane >> 1);  // the query whose D this thread and the next form
-      // which pairs of the warp's key rows and each 32 of this thread's queries see one another
-      bool act[2], whole[2];
-      uint32_t see[2];
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int at = h0 + 32 * c, key = quarter * 32, pa = at + shift;
-        act[c] = at < w.nq && key < w.nk && some_seen(a.mask, pa, pa + 31, key);
-        whole[c] = at + 32 <= w.nq && key + 32 <= w.nk && all_seen(a.mask, pa, pa + 31, key);
-        const ColumnSpan span = column_span(a.mask, row);
-        see[c] = row < w.nk ? bits(0, w.nq - at) & bits(span.lo - pa, span.hi + 1 - pa) : 0u;
-      }
+      const ColumnSpan span = column_span(a.mask, row);
 #pragma unroll 1
       for (int m = 0; m < a.group; ++m, ++u) {
         const int st = u % kStages, h = w.h * a.group + m;
@@ -354,13 +286,11 @@ __global__ void __launch_bounds__(kShortThreads, kTwo ? 2 : 1)
         }
         if (!(ok = mbar_wait(qd_full + 8 * st, (u / kStages) & 1, s_abort))) break;
         uint8_t* tile = s_qd + 2 * st * Sh::kTileBytes;
-        // Rows past the event's last inside a product's step of 16: their P and
-        // dS are 0, and the rows must be finite for 0 to stay 0.
-        if (w.nq & 15) {
+        if (w.nq & 63) {
           clear_rows<Sh::kPanels>(tile, w.nq, threadIdx.x, kSoftmaxThreads);
           clear_rows<Sh::kPanels>(tile + Sh::kTileBytes, w.nq, threadIdx.x, kSoftmaxThreads);
         }
-        if (m == 0 && (w.nk & 15)) {
+        if (m == 0 && (w.nk & 63)) {
           if (!(ok = mbar_wait(kv_full + 8 * ks, (n / kStages) & 1, s_abort))) break;
           clear_rows<Sh::kPanels>(s_kv + 2 * ks * Sh::kTileBytes, w.nk, threadIdx.x, kSoftmaxThreads);
         }
@@ -382,84 +312,65 @@ __global__ void __launch_bounds__(kShortThreads, kTwo ? 2 : 1)
         delta += __shfl_xor_sync(kFull, delta, 1);
         s_col[(lane & 1) * kTile + q] = lane & 1 ? -delta : -lse * kLog2e;
         mbar_arrive(col_full);
-        const float* col = s_col + h0;
-        if (!(ok = mbar_wait(s_full, u & 1, s_abort))) break;
-        tc_fence_after();
-        float x[kHalf];
-#pragma unroll
-        for (int c = 0; c < 2; ++c) tmem_ld32(lanes + kColS + h0 + 32 * c, reinterpret_cast<uint32_t*>(x + 32 * c));
-        tmem_wait_ld32(reinterpret_cast<uint32_t*>(x));
-        tmem_wait_ld32(reinterpret_cast<uint32_t*>(x + 32));
+        if (!(ok = mbar_wait(scores_full, u & 1, s_abort))) break;
         if (!(ok = mbar_wait(col_full, u & 1, s_abort))) break;
+        tc_fence_after();
+        // 32 queries at a time, to the end of this thread's 64 if there are any:
+        // the products take P and dS of all of them
+#pragma unroll 1
+        for (int at = h0; at < h0 + kHalf && h0 < w.nq; at += 32) {
+          uint32_t p16[16], d16[16];
+          // which pairs of the warp's key rows and these queries see one another
+          const int key = quarter * 32, pa = at + shift;
+          if (at < w.nq && key < w.nk && some_seen(a.mask, pa, pa + 31, key)) {
+            float x[32], y[32];
+            tmem_ld32(lanes + kColS + at, reinterpret_cast<uint32_t*>(x));
+            tmem_ld32(lanes + kColDP + at, reinterpret_cast<uint32_t*>(y));
+            tmem_wait_ld32(reinterpret_cast<uint32_t*>(x));
+            tmem_wait_ld32(reinterpret_cast<uint32_t*>(y));
+            const float* col = s_col + at;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          if (act[c]) {
-#pragma unroll
-            for (int k = 32 * c; k < 32 * c + 32; k += 4) {
+            for (int k = 0; k < 32; k += 4) {
               const float4 le = *reinterpret_cast<const float4*>(col + k);
+              const float4 de = *reinterpret_cast<const float4*>(col + kTile + k);
               const float2 e0 = fma2(make_float2(x[k], x[k + 1]), scale2, make_float2(le.x, le.y));
               const float2 e1 = fma2(make_float2(x[k + 2], x[k + 3]), scale2, make_float2(le.z, le.w));
               x[k] = exp2_approx(e0.x);
               x[k + 1] = exp2_approx(e0.y);
               x[k + 2] = exp2_approx(e1.x);
               x[k + 3] = exp2_approx(e1.y);
-            }
-            if (!whole[c]) {
-#pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (!(see[c] >> k & 1)) x[32 * c + k] = 0.f;
-            }
-          }
-          uint32_t p16[16];
-#pragma unroll
-          for (int k = 0; k < 16; ++k) p16[k] = act[c] ? pack16<T>(x[32 * c + 2 * k], x[32 * c + 2 * k + 1]) : 0u;
-          if (h0 + 32 * c < w.nq) tmem_st16(lanes + kColS + h0 + 16 * c, p16);
-        }
-        tmem_wait_st();
-        fence_async_smem();  // the cleared rows
-        tc_fence_before();
-        mbar_arrive(p_ready);
-        if (!(ok = mbar_wait(dp_full, u & 1, s_abort))) break;
-        tc_fence_after();
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          if (h0 + 32 * c >= w.nq) continue;
-          uint32_t d16[16];
-          if (act[c]) {
-            float y[32];
-            tmem_ld32(lanes + kColDP + h0 + 32 * c, reinterpret_cast<uint32_t*>(y));
-            tmem_wait_ld32(reinterpret_cast<uint32_t*>(y));
-#pragma unroll
-            for (int k = 0; k < 32; k += 4) {
-              const float4 de = *reinterpret_cast<const float4*>(col + kTile + 32 * c + k);
-              const uint64_t y0 = mul2(add2(pack2(y[k], y[k + 1]), pack2(de.x, de.y)),
-                                       pack2(x[32 * c + k], x[32 * c + k + 1]));
-              const uint64_t y1 = mul2(add2(pack2(y[k + 2], y[k + 3]), pack2(de.z, de.w)),
-                                       pack2(x[32 * c + k + 2], x[32 * c + k + 3]));
+              const uint64_t y0 = mul2(add2(pack2(y[k], y[k + 1]), pack2(de.x, de.y)), pack2(x[k], x[k + 1]));
+              const uint64_t y1 = mul2(add2(pack2(y[k + 2], y[k + 3]), pack2(de.z, de.w)), pack2(x[k + 2], x[k + 3]));
               y[k] = lo2(y0);
               y[k + 1] = hi2(y0);
               y[k + 2] = lo2(y1);
               y[k + 3] = hi2(y1);
             }
-            if (!whole[c]) {  // 0 times what a hidden pair's dP holds need not be 0
+            if (at + 32 > w.nq || key + 32 > w.nk || !all_seen(a.mask, pa, pa + 31, key)) {
+              const uint32_t see = row < w.nk ? bits(0, w.nq - at) & bits(span.lo - pa, span.hi + 1 - pa) : 0u;
 #pragma unroll
               for (int k = 0; k < 32; ++k)
-                if (!(see[c] >> k & 1)) y[k] = 0.f;
+                if (!(see >> k & 1)) x[k] = y[k] = 0.f;
             }
 #pragma unroll
-            for (int k = 0; k < 16; ++k) d16[k] = pack16<T>(y[2 * k], y[2 * k + 1]);
+            for (int k = 0; k < 16; ++k) {
+              p16[k] = pack16<T>(x[2 * k], x[2 * k + 1]);
+              d16[k] = pack16<T>(y[2 * k], y[2 * k + 1]);
+            }
           } else {
 #pragma unroll
-            for (int k = 0; k < 16; ++k) d16[k] = 0;
+            for (int k = 0; k < 16; ++k) p16[k] = d16[k] = 0;
           }
+          tmem_st16(lanes + kColS + h0 + (at - h0) / 2, p16);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            *reinterpret_cast<uint4*>(ds_row + (((c * 4 + k) ^ (row & 7)) << 4)) =
+            *reinterpret_cast<uint4*>(ds_row + ((((at - h0) / 8 + k) ^ (row & 7)) << 4)) =
                 make_uint4(d16[4 * k], d16[4 * k + 1], d16[4 * k + 2], d16[4 * k + 3]);
         }
-        fence_async_smem();
+        tmem_wait_st();
+        fence_async_smem();  // dS, and the cleared rows
         tc_fence_before();
-        mbar_arrive(ds_ready);
+        mbar_arrive(ready);
         // stores: dQ of this head, half of the columns each; after the last
         // head dK and dV
         if (!(ok = mbar_wait(done, u & 1, s_abort))) break;
@@ -471,13 +382,12 @@ __global__ void __launch_bounds__(kShortThreads, kTwo ? 2 : 1)
                            a.D - half * 32, a.sectors);
           store_row<T, 32>(lanes + kColS + 32 + half * 64, row < w.nk, 1.f, static_cast<T*>(a.dv) + key_at + half * 32,
                            a.D - half * 32, a.sectors);
-          tc_fence_before();
-          mbar_arrive(stored);
         } else if (m == a.group - 1) {
           store_row<T, DP>(lanes + (half == 0 ? Sh::kColDK : Sh::kColDV), row < w.nk, half == 0 ? a.scale : 1.f,
                            static_cast<T*>(half == 0 ? a.dk : a.dv) + key_at, a.D, a.sectors);
         }
         tc_fence_before();
+        mbar_arrive(stored);
       }
       ++n;
     }

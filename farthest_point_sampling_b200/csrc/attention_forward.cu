@@ -218,12 +218,13 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
         for (int j = 0; j <= count; ++j) {
           if (j > 0) {  // O += P V of tile j - 1
             const int m = n + j - 1, st = m % Sh::kStages;
-            const int steps = (keys.extent(j - 1) + 15) / 16;
+            const bool both = keys.extent(j - 1) > 64;
             if (!(ok = mbar_wait_warp(v_full + 8 * st, (m / Sh::kStages) & 1, s_abort))) break;
             if (!(ok = mbar_wait_warp(p_ready, m & 1, s_abort))) break;
             tc_fence_after();
             const uint32_t v = smem_desc(smem_u32(s_v) + st * Sh::kTileBytes, kPanel);
-            mma_ts_steps(tmem + kColO, tmem, v, steps, pv_desc, j > 1);
+            mma_ts(tmem + kColO, tmem, v, pv_desc, j > 1);
+            if (both) mma_ts(tmem + kColO, tmem + 32, v + kRun, pv_desc, true);
             mma_commit(v_empty + 8 * st);
             if (j == count) mma_commit(o_full);
           }
@@ -236,7 +237,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
             const uint32_t qk_desc = mma_desc(kBf16, false, false, cols);
             // whole panels: values past D are zeros
 #pragma unroll
-            for (int p = 0; p < Sh::kPanels; ++p) mma_ss_steps<2, 2>(tmem, q + p * (kPanel >> 4), k + p * (kPanel >> 4), 4, qk_desc, p > 0);
+            for (int p = 0; p < Sh::kPanels; ++p) mma_ss<2, 2>(tmem, q + p * (kPanel >> 4), k + p * (kPanel >> 4), qk_desc, p > 0);
             mma_commit(k_empty + 8 * st);
             mma_commit(s_full);
             if (j == count - 1) mma_commit(q_empty + 8 * qs);
@@ -266,18 +267,10 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
       float m_used = -INFINITY, l = 0.f;
       for (int j = 0; j < count; ++j, ++n) {
         const int k0 = w.keys.start(j), extent = w.keys.extent(j);
-        const int odd = extent & 15;
-        if (odd) {
-          // Keys past the tile's last inside the product's step of 16: their
-          // weights are 0, and their values must be finite for 0 to stay 0.
+        if (extent & 63) {
           const int st = n % Sh::kStages;
           if (!(ok = mbar_wait(v_full + 8 * st, (n / Sh::kStages) & 1, s_abort))) break;
-          uint8_t* v_tile = s_v + st * Sh::kTileBytes;
-#pragma unroll 1
-          for (int e = threadIdx.x; e < (16 - odd) * 8 * Sh::kPanels; e += kSoftmaxThreads) {
-            const int r = extent + e / (8 * Sh::kPanels), c = e % (8 * Sh::kPanels);
-            *reinterpret_cast<uint4*>(v_tile + (c >> 3) * kPanel + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-          }
+          clear_rows<Sh::kPanels>(s_v + st * Sh::kTileBytes, extent, threadIdx.x, kSoftmaxThreads);
           fence_async_smem();
         }
         // the tile's 32-key chunks: which of them some row of the warp
@@ -367,7 +360,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
 #pragma unroll
             for (int k = 0; k < 16; ++k) pk[k] = 0;
           }
-          if (32 * c < extent) tmem_st16(lanes + 16 * c, pk);
+          if (32 * (c & ~1) < extent) tmem_st16(lanes + 16 * c, pk);  // zeros too, to the end of 64 keys
         }
         l += sum.x + sum.y;
         tmem_wait_st();

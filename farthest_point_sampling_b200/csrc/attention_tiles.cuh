@@ -246,10 +246,24 @@ __device__ __forceinline__ float2 unpack16<__half>(uint32_t v) {
   return __half22float2(*reinterpret_cast<__half2*>(&v));
 }
 
+// Rows of a 128-row tile from n up to the next multiple of 64 to 0, by
+// `threads` threads.  Products run over 64 rows at a time: past the event's
+// last row the weights are 0, and the rows must be finite for 0 to stay 0.
+template <int kPanels>
+__device__ __forceinline__ void clear_rows(uint8_t* tile, int n, int thread, int threads) {
+#pragma unroll 1
+  for (int e = thread; e < (-n & 63) * 8 * kPanels; e += threads) {
+    const int r = n + e / (8 * kPanels), c = e % (8 * kPanels);
+    *reinterpret_cast<uint4*>(tile + (c >> 3) * (kTile * 128) + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+  }
+}
+
 // `values` 16-bit values (a multiple of 8) of `rows` rows to 0, by one warp.
 template <typename T>
 __device__ __forceinline__ void clear_strided(T* base, int rows, int64_t stride, int values) {
+#pragma unroll 1
   for (int r = 0; r < rows; ++r)
+#pragma unroll 1
     for (int c = (threadIdx.x & 31) * 8; c < values; c += 256)
       *reinterpret_cast<uint4*>(base + r * stride + c) = make_uint4(0, 0, 0, 0);
 }
@@ -259,6 +273,7 @@ __device__ __forceinline__ void zero_rows(void* base, int64_t first, int64_t n, 
   if (first < 0 || first >= n) return;
   uint4* p = reinterpret_cast<uint4*>(static_cast<char*>(base) + first * row_values * 2);
   const int64_t total = (n - first) * row_values / 8;
+#pragma unroll 1
   for (int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; e < total; e += (int64_t)gridDim.x * blockDim.x)
     p[e] = make_uint4(0, 0, 0, 0);
 }

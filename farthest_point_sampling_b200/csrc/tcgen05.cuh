@@ -193,45 +193,26 @@ __host__ __device__ constexpr uint32_t mma_desc(bool bf16, bool a_mn, bool b_mn,
          ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
-// By a whole warp; a and b are low descriptor words.
-// D[tmem] (+)= A[tmem] B[smem].
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
+// D[tmem] (+)= A B over 64 values of the sum, by a whole warp with one
+// election for its four instructions: A and B in shared memory (low descriptor
+// words), each along its rows (2 per step) or across them (128 per step).
+template <int kA, int kB>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
   asm volatile(
-      "{\n\t" FPS_ELECT ".reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "mov.b64 y, {%2, %5};\n\t"
-      "@elected tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(kDescHigh)
+      "{\n\t" FPS_ELECT ".reg .pred p, t;\n\t.reg .b64 x, y;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.eq.u32 t, 0, 0;\n\t"
+      "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+      "@elected tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t"
+      "add.s64 x, x, %6;\n\tadd.s64 y, y, %7;\n\t"
+      "@elected tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
+      "add.s64 x, x, %6;\n\tadd.s64 y, y, %7;\n\t"
+      "@elected tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
+      "add.s64 x, x, %6;\n\tadd.s64 y, y, %7;\n\t"
+      "@elected tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(kDescHigh), "n"(kA), "n"(kB)
       : "memory");
 }
-// `steps` steps of 16 with both operands in shared memory, each along its rows
-// (2 per step) or across them (128 per step); one election for four.
-template <int kA, int kB>
-__device__ __forceinline__ void mma_ss_steps(uint32_t d, uint32_t a, uint32_t b, int steps, uint32_t idesc, bool accumulate) {
-#pragma unroll 1
-  for (; steps >= 4; steps -= 4, a += 4 * kA, b += 4 * kB, accumulate = true)
-    asm volatile(
-        "{\n\t" FPS_ELECT ".reg .pred p, t;\n\t.reg .b64 x, y;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.eq.u32 t, 0, 0;\n\t"
-        "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
-        "@elected tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t"
-        "add.s64 x, x, %6;\n\tadd.s64 y, y, %7;\n\t"
-        "@elected tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
-        "add.s64 x, x, %6;\n\tadd.s64 y, y, %7;\n\t"
-        "@elected tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
-        "add.s64 x, x, %6;\n\tadd.s64 y, y, %7;\n\t"
-        "@elected tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t}" ::"r"(d),
-        "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(kDescHigh), "n"(kA), "n"(kB)
-        : "memory");
-#pragma unroll 1
-  for (; steps > 0; --steps, a += kA, b += kB, accumulate = true)
-    asm volatile(
-        "{\n\t" FPS_ELECT ".reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
-        "@elected tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(kDescHigh)
-        : "memory");
-}
-// Four steps of 16 rows of B against 32 columns of A in TMEM, one election for all.
-__device__ __forceinline__ void mma_ts4(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
+// The same with A as 32 columns of 16-bit pairs in TMEM and B across its rows.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
   asm volatile(
       "{\n\t" FPS_ELECT ".reg .pred p, t;\n\t.reg .b64 y;\n\t.reg .b32 x;\n\tsetp.ne.u32 p, %4, 0;\n\t"
       "setp.eq.u32 t, 0, 0;\n\tmov.b64 y, {%2, %5};\n\tmov.b32 x, %1;\n\t"
@@ -245,13 +226,7 @@ __device__ __forceinline__ void mma_ts4(uint32_t d, uint32_t a, uint32_t b, uint
       "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(kDescHigh)
       : "memory");
 }
-// `steps` steps of 16 rows of B.
-__device__ __forceinline__ void mma_ts_steps(uint32_t d, uint32_t a, uint32_t b, int steps, uint32_t idesc, bool accumulate) {
-#pragma unroll 1
-  for (; steps >= 4; steps -= 4, a += 32, b += 512, accumulate = true) mma_ts4(d, a, b, idesc, accumulate);
-#pragma unroll 1
-  for (; steps > 0; --steps, a += 8, b += 128, accumulate = true) mma_ts(d, a, b, idesc, accumulate);
-}
+constexpr uint32_t kRun = 64 * 128 >> 4;  // 64 rows on, in descriptor units
 
 // Arrives on `bar` once every tcgen05 operation this warp issued before is done.
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
