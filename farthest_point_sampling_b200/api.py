@@ -508,6 +508,7 @@ class RotaryTable:
         st = _lib.load().fps_rotary_table_init(ctypes.byref(self.c), (ctypes.c_int * len(dims))(*dims), len(dims),
                                                float(base), scale, int(bool(interleaved)))
         _lib.check(st, "fps_rotary_table_init")
+        self.ref = ctypes.byref(self.c)
 
     @property
     def axes(self) -> int:
@@ -519,6 +520,20 @@ class RotaryTable:
 
 
 _DTYPES = {torch.float32: _lib.FPS_DTYPE_F32, torch.bfloat16: _lib.FPS_DTYPE_BF16, torch.float16: _lib.FPS_DTYPE_F16}
+_HALF_DTYPES = {torch.bfloat16: _lib.FPS_DTYPE_BF16, torch.float16: _lib.FPS_DTYPE_F16}
+
+
+def _call(fn, where: str, device: torch.device, *args) -> None:
+    """``fn(*args, stream)`` on the current stream of ``device``, which need
+    not be the current device."""
+    index = device.index
+    if index == torch.cuda.current_device():
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if st:
+        _lib.check(st, where)
 
 
 def _need_rows(t: torch.Tensor, name: str, dtypes, device: Optional[torch.device] = None):
@@ -527,11 +542,12 @@ def _need_rows(t: torch.Tensor, name: str, dtypes, device: Optional[torch.device
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be one of {[str(d) for d in dtypes]}, got {t.dtype} (no implicit conversion)")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [rows, heads, D], got shape {tuple(t.shape)}")
+    shape = t.shape
+    if len(shape) != 3:
+        raise ValueError(f"{name} must be [rows, heads, D], got shape {tuple(shape)}")
     if device is not None and t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if t.shape[2] > 1 and t.stride(2) != 1:
+    if shape[2] > 1 and t.stride(2) != 1:
         raise ValueError(f"the values of a head of {name} must be contiguous")
 
 
@@ -573,11 +589,8 @@ def rotary_embed(x: torch.Tensor, positions: torch.Tensor, table: RotaryTable, i
         if out.shape != x.shape:
             raise ValueError("out must have the shape of x")
     (xt, xh), (yt, yh) = _strides(x), _strides(out)
-    with torch.cuda.device(dev):
-        st = _lib.load().fps_rotary(_ptr(x), _ptr(out), _DTYPES[x.dtype], T, H, D, xt, xh, yt, yh, _ptr(positions),
-                                    positions.stride(0) if T > 1 else table.axes, ctypes.byref(table.c),
-                                    int(bool(inverse)), _stream(dev))
-    _lib.check(st, "fps_rotary")
+    _call(_lib.load().fps_rotary, "fps_rotary", dev, x.data_ptr(), out.data_ptr(), _DTYPES[x.dtype], T, H, D, xt, xh, yt, yh,
+          positions.data_ptr(), positions.stride(0) if T > 1 else table.axes, table.ref, 1 if inverse else 0)
     return out
 
 
@@ -614,45 +627,41 @@ def _dense_heads(t: torch.Tensor) -> torch.Tensor:
 
 def _attention_args(q, k, v, tok_offsets, kv_offsets, scale, causal, window, sinks, max_tokens):
     dev = _cuda_device(q)
-    half = (torch.bfloat16, torch.float16)
-    _need_rows(q, "q", half)
+    _need_rows(q, "q", _HALF_DTYPES)
     _need_rows(k, "k", (q.dtype,), dev)
     _need_rows(v, "v", (q.dtype,), dev)
-    if k.shape != v.shape or k.shape[2] != q.shape[2]:
-        raise ValueError(f"k and v must have one shape and the head size of q, got {tuple(q.shape)}, {tuple(k.shape)}, {tuple(v.shape)}")
-    if q.shape[1] < 1 or k.shape[1] < 1 or q.shape[1] % k.shape[1]:
-        raise ValueError(f"the query heads must be a multiple of the key heads, got {q.shape[1]} and {k.shape[1]}")
-    if q.shape[2] % 8 or not 8 <= q.shape[2] <= _lib.FPS_MAX_ATTENTION_DIM:
-        raise ValueError(f"the head size must be a multiple of 8 up to {_lib.FPS_MAX_ATTENTION_DIM}, got {q.shape[2]}")
+    q_shape, k_shape = q.shape, k.shape
+    if k_shape != v.shape or k_shape[2] != q_shape[2]:
+        raise ValueError(f"k and v must have one shape and the head size of q, got {tuple(q_shape)}, {tuple(k_shape)}, {tuple(v.shape)}")
+    if q_shape[1] < 1 or k_shape[1] < 1 or q_shape[1] % k_shape[1]:
+        raise ValueError(f"the query heads must be a multiple of the key heads, got {q_shape[1]} and {k_shape[1]}")
+    if q_shape[2] % 8 or not 8 <= q_shape[2] <= _lib.FPS_MAX_ATTENTION_DIM:
+        raise ValueError(f"the head size must be a multiple of 8 up to {_lib.FPS_MAX_ATTENTION_DIM}, got {q_shape[2]}")
     if kv_offsets is None:
-        if q.shape[0] != k.shape[0]:
+        if q_shape[0] != k_shape[0]:
             raise ValueError("q and k must have the same rows unless kv_offsets is given")
         kv_offsets = tok_offsets
     _need(tok_offsets, "tok_offsets", torch.int64, 1, dev)
-    _need(kv_offsets, "kv_offsets", torch.int64, 1, dev)
+    if kv_offsets is not tok_offsets:
+        _need(kv_offsets, "kv_offsets", torch.int64, 1, dev)
     if tok_offsets.numel() < 1 or tok_offsets.numel() != kv_offsets.numel():
         raise ValueError("tok_offsets and kv_offsets must both be [B + 1]")
     strides = []
     for t, name in ((q, "q"), (k, "k"), (v, "v")):
         st = _strides(t)
-        if t.numel() and (t.data_ptr() % 16 or any(x <= 0 or x % 8 for x in st)):
+        if t.numel() and (t.data_ptr() % 16 or st[0] % 8 or st[1] % 8 or st[0] <= 0 or st[1] <= 0):
             raise ValueError(f"{name} must start on 16 bytes, with row and head strides that are positive multiples of 8")
         strides += st
     window, sinks = int(window), int(sinks)
     if window < -1 or sinks < 0:
         raise ValueError("window must be -1 or more and sinks 0 or more")
-    scale = q.shape[2] ** -0.5 if scale is None else float(scale)
+    scale = q_shape[2] ** -0.5 if scale is None else float(scale)
     if not 0.0 < scale < float("inf"):
         raise ValueError("scale must be positive and finite")
-    a = _lib.AttentionArgs()
-    a.q, a.k, a.v = q.data_ptr(), k.data_ptr(), v.data_ptr()
-    a.dtype, a.heads, a.kv_heads, a.head_dim = _DTYPES[q.dtype], q.shape[1], k.shape[1], q.shape[2]
-    a.n_q, a.n_kv = q.shape[0], k.shape[0]
-    (a.q_token_stride, a.q_head_stride, a.k_token_stride, a.k_head_stride, a.v_token_stride, a.v_head_stride) = strides
-    a.q_offsets, a.kv_offsets, a.events = tok_offsets.data_ptr(), kv_offsets.data_ptr(), tok_offsets.numel() - 1
-    a.scale, a.causal, a.window, a.sinks = scale, int(bool(causal)), min(window, 1 << 40), min(sinks, 1 << 40)
-    a.max_tokens = min(int(max_tokens), 2**31 - 1)
-    return a, dev
+    return _lib.AttentionArgs(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), _HALF_DTYPES[q.dtype], q_shape[1], k_shape[1], q_shape[2], q_shape[0],
+        k_shape[0], *strides, tok_offsets.data_ptr(), kv_offsets.data_ptr(), tok_offsets.numel() - 1, scale,
+        1 if causal else 0, min(window, 1 << 40), min(sinks, 1 << 40), min(int(max_tokens), 2**31 - 1), 0), dev
 
 
 def attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, tok_offsets: torch.Tensor,
@@ -675,10 +684,10 @@ def attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, tok_off
     lse = None
     if need_lse:  # rows of no event read as a query that sees nothing
         lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=dev)
-    ws = _workspace(lib.fps_attention_workspace_bytes(ctypes.byref(a), 0), dev, workspace)
-    with torch.cuda.device(dev):
-        st = lib.fps_attention(ctypes.byref(a), _ptr(out), _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(), _stream(dev))
-    _lib.check(st, "fps_attention")
+    ref = ctypes.byref(a)
+    ws = _workspace(lib.fps_attention_workspace_bytes(ref, 0), dev, workspace)
+    _call(lib.fps_attention, "fps_attention", dev, ref, out.data_ptr(), None if lse is None else lse.data_ptr(), ws.data_ptr(),
+          ws.numel() * ws.element_size())
     return out, lse
 
 
@@ -699,11 +708,10 @@ def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: 
         raise ValueError("dout and out must start on 16 bytes, with dout's strides positive multiples of 8")
     dq, dk, dv = (torch.empty(t.shape, dtype=q.dtype, device=dev) for t in (q, k, v))
     lib = _lib.load()
-    ws = _workspace(lib.fps_attention_workspace_bytes(ctypes.byref(a), 1), dev, workspace)
-    with torch.cuda.device(dev):
-        st = lib.fps_attention_backward(ctypes.byref(a), _ptr(out), _ptr(lse), _ptr(dout), dt, dh, _ptr(dq), _ptr(dk),
-                                        _ptr(dv), _ptr(ws), ws.numel() * ws.element_size(), _stream(dev))
-    _lib.check(st, "fps_attention_backward")
+    ref = ctypes.byref(a)
+    ws = _workspace(lib.fps_attention_workspace_bytes(ref, 1), dev, workspace)
+    _call(lib.fps_attention_backward, "fps_attention_backward", dev, ref, out.data_ptr(), lse.data_ptr(), dout.data_ptr(), dt,
+          dh, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
     return dq, dk, dv
 
 

@@ -89,6 +89,8 @@ struct FewArgs {
   const JoinItem* joins;
   float* part_o;    // [slot][key head][16][DP]
   float2* part_ml;  // [slot][key head][16]
+  const int64_t* q_offsets;
+  int B, zero_tail;
   WsHeader* hdr;
 };
 
@@ -269,6 +271,7 @@ __global__ void __launch_bounds__(kFewThreads, FewShape<DP>::kBlocks) k_attn_few
         reinterpret_cast<uint4*>(w_o)[e] = make_uint4(0, 0, 0, 0);
     __syncthreads();
   }
+  if (a.zero_tail) zero_rows(a.out, a.B > 0 ? a.q_offsets[a.B] : 0, a.n_q, (int64_t)a.heads * a.D);
 }
 
 // Joins the chunks of one event and head: sum_c 2^(m_c - M) (l_c, O_c).  The
@@ -408,6 +411,9 @@ cudaError_t launch_attention_few(const AttnCall& c, const FewPlan& plan, WsHeade
   const int64_t slots = (2 * (c.n_kv / plan.chunk) + 1) * c.kv_heads * kFewRows;
   a.part_ml = reinterpret_cast<float2*>(plan.partial);
   a.part_o = plan.partial + 2 * slots;
+  a.q_offsets = c.q_offsets;
+  a.B = c.B;
+  a.zero_tail = c.zero_tail;
   a.hdr = hdr;
   if (c.dtype == FPS_DTYPE_BF16) return c.D <= 64 ? run<__nv_bfloat16, 64>(c, a, s) : run<__nv_bfloat16, 128>(c, a, s);
   return c.D <= 64 ? run<__half, 64>(c, a, s) : run<__half, 128>(c, a, s);

@@ -472,7 +472,7 @@ cudaError_t run_forward(const AttnCall& c, const FwdWorkspace& ws, cudaStream_t 
   a.lse = c.lse;
   a.q_offsets = c.q_offsets;
   a.B = c.B;
-  a.zero_tail = c.zero_tail;
+  a.zero_tail = c.zero_tail && !few_rows(c);  // the other kernel has done it
   a.sectors = reinterpret_cast<uintptr_t>(c.out) % 32 == 0 && c.D % 16 == 0;
   a.items = ws.items;
   a.hdr = ws.hdr;
@@ -521,6 +521,7 @@ cudaError_t launch_attention_forward(const AttnCall& c, void* workspace, cudaStr
   if (lists.units) {
     const FewPlan plan = {ws.chunk, ws.units, ws.joins, ws.partial};
     if ((e = launch_attention_few(c, plan, ws.hdr, s)) != cudaSuccess) return e;
+    if (c.n_q * c.group <= kFewRows) return cudaSuccess;  // no event can have more rows than the call
   }
   return c.dtype == FPS_DTYPE_BF16 ? run_type<__nv_bfloat16>(c, ws, s) : run_type<__half>(c, ws, s);
 }
