@@ -673,17 +673,19 @@ def attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, tok_off
     ``out`` that belong to no event are left as they were; in a new one they
     are 0."""
     a, dev = _attention_args(q, k, v, tok_offsets, kv_offsets, scale, causal, window, sinks, max_tokens)
+    return _attention_forward(a, dev, q, need_lse, workspace, out)
+
+
+def _attention_forward(a, dev, q, need_lse, workspace, out):
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        out = torch.empty_like(q) if q.is_contiguous() else torch.empty(q.shape, dtype=q.dtype, device=dev)
         a.zero_tail = 1
     else:
         _need(out, "out", q.dtype, 3, dev)
         if out.shape != q.shape or out.data_ptr() % 16:
             raise ValueError("out must have the shape of q and start on 16 bytes")
     lib = _lib.load()
-    lse = None
-    if need_lse:  # rows of no event read as a query that sees nothing
-        lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=dev)
+    lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=dev) if need_lse else None
     ref = ctypes.byref(a)
     ws = _workspace(lib.fps_attention_workspace_bytes(ref, 0), dev, workspace)
     _call(lib.fps_attention, "fps_attention", dev, ref, out.data_ptr(), None if lse is None else lse.data_ptr(), ws.data_ptr(),
@@ -717,8 +719,8 @@ def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: 
 
 class _PackedAttention(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, v, tok_offsets, kv_offsets, opts):
-        out, lse = attention_forward(q, k, v, tok_offsets, kv_offsets, **opts)
+    def forward(ctx, q, k, v, tok_offsets, kv_offsets, args, opts):
+        out, lse = _attention_forward(args, q.device, q, True, None, None)
         ctx.save_for_backward(q, k, v, out, lse, tok_offsets, kv_offsets)
         ctx.opts = opts
         return out
@@ -728,7 +730,7 @@ class _PackedAttention(torch.autograd.Function):
     def backward(ctx, dout):
         q, k, v, out, lse, tok_offsets, kv_offsets = ctx.saved_tensors
         dq, dk, dv = attention_backward(_dense_heads(dout), q, k, v, out, lse, tok_offsets, kv_offsets, **ctx.opts)
-        return dq, dk, dv, None, None, None
+        return dq, dk, dv, None, None, None, None
 
 
 def packed_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, tok_offsets: torch.Tensor,
@@ -747,10 +749,11 @@ def packed_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, tok_offs
     ``D ** -0.5``.  ``max_tokens``: an upper bound on the tokens of an event
     (e.g. the K of the tokenizer), 0 when unknown; it selects kernels.
     Returns ``[n_q, H, D]``; rows behind the last event are 0."""
-    opts = dict(scale=scale, causal=causal, window=window, sinks=sinks, max_tokens=max_tokens)
-    if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in (q, k, v)):
-        return _PackedAttention.apply(q, k, v, tok_offsets, kv_offsets, opts)
-    return attention_forward(q, k, v, tok_offsets, kv_offsets, need_lse=False, **opts)[0]
+    a, dev = _attention_args(q, k, v, tok_offsets, kv_offsets, scale, causal, window, sinks, max_tokens)
+    if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad):
+        opts = dict(scale=scale, causal=causal, window=window, sinks=sinks, max_tokens=max_tokens)
+        return _PackedAttention.apply(q, k, v, tok_offsets, kv_offsets, a, opts)
+    return _attention_forward(a, dev, q, False, None, None)[0]
 
 
 def device_status(workspace: torch.Tensor) -> None:

@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const uint32_t kept_full = bars, kept_empty = bars + 16, acc_full = bars + 32, acc_empty = bars + 48,
                  item_full = bars + 64, item_empty = bars + 80, s_full = bars + 96, dp_full = bars + 104,
                  p_ready = bars + 112, ds_ready = bars + 120, drain = bars + 128, ring_full = bars + 136,
-                 ring_empty = bars + 168;
+                 ring_empty = bars + 168, row_ready = bars + 208;
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -163,6 +163,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     mbar_init(p_ready, kSoftmaxThreads);
     mbar_init(ds_ready, kSoftmaxThreads);
     mbar_init(drain, 1);
+    mbar_init(row_ready, kSoftmaxThreads);
     for (int i = 0; i < Sh::kRing; ++i) {
       mbar_init(ring_full + 8 * i, kKeys ? 33 : 1);  // the tiles, and in the keys kernel each lane's -lse and -D
       mbar_init(ring_empty + 8 * i, 1);
@@ -370,43 +371,62 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const float2 scale2 = make_float2(a.scale_log2, a.scale_log2);
     int m = 0, nk = 0;
     bool ok = true;
+    // Queries kernel: two threads read the row of O that belongs to a query of
+    // the next item, before they store this one's gradients.
+    const int q = warp * 16 + (lane >> 1), d0 = (lane & 1) * (DP / 16);
+    uint4 o[DP / 16];
+    float lse = 0.f;
+    const auto ahead = [&](int i) {
+      if (!mbar_wait(item_full + 8 * (i % kItemRing), (i / kItemRing) & 1, s_abort)) return false;
+      const BwdItem& w = s_item[i % kItemRing];
+      if (w.count > 0 && q < w.rows) {
+        const T* from = static_cast<const T*>(a.out) + (((int64_t)w.kept_row + q) * a.heads + w.h) * a.D;
+#pragma unroll
+        for (int c = 0; c < DP / 16; ++c)
+          o[c] = (d0 + c) * 8 < a.D ? *reinterpret_cast<const uint4*>(from + (d0 + c) * 8) : make_uint4(0, 0, 0, 0);
+        lse = a.lse[(int64_t)w.h * a.n_q + w.kept_row + q];
+      }
+      return true;
+    };
+    if constexpr (!kKeys) ok = ahead(0);
     for (int i = 0; ok; ++i) {
       const int slot = i % kItemRing;
-      if (!(ok = mbar_wait(item_full + 8 * slot, (i / kItemRing) & 1, s_abort))) break;
+      if (kKeys && !(ok = mbar_wait(item_full + 8 * slot, (i / kItemRing) & 1, s_abort))) break;
       const BwdItem& w = s_item[slot];  // read where it is needed: it stays until this thread lets go of the slot
       const int count = w.count;
       if (count < 0) break;
       float lse2 = 0.f, delta = 0.f;  // -lse log2(e) and -D of this thread's query
       if constexpr (!kKeys) {
-        // D: dO from its tile, O from memory
+        // D: O as read ahead, dO from its tile; shared with the keys kernel
+        // through memory and with the threads of each row through the block's
         const int ks = nk % Sh::kKept;
         if (!(ok = mbar_wait(kept_full + 8 * ks, (nk / Sh::kKept) & 1, s_abort))) break;
-        {
-          if (row < w.rows) {
-            const int64_t q = (int64_t)w.kept_row + row, at = (int64_t)w.h * a.n_q + q;
-            const T* o = static_cast<const T*>(a.out) + (q * a.heads + w.h) * a.D;
-            const uint8_t* d = s_kept + (2 * ks + 1) * Sh::kTileBytes + row * 128;
-#pragma unroll 4
-            for (int c = 0; c < a.D / 8; ++c) {
-              const uint4 vo = *reinterpret_cast<const uint4*>(o + c * 8);
-              const uint4 vd = *reinterpret_cast<const uint4*>(d + (c >> 3) * kPanel + (((c & 7) ^ (row & 7)) << 4));
-              const uint32_t* po = reinterpret_cast<const uint32_t*>(&vo);
-              const uint32_t* pd = reinterpret_cast<const uint32_t*>(&vd);
+        float sum = 0.f;
+        if (q < w.rows) {
+          const uint8_t* d = s_kept + (2 * ks + 1) * Sh::kTileBytes + q * 128;
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const float2 x = unpack16<T>(po[k]), y = unpack16<T>(pd[k]);
-                delta = fmaf(x.x, y.x, fmaf(x.y, y.y, delta));
-              }
-            }
-            lse2 = -a.lse[at] * kLog2e;
-            delta = -delta;
-            if (half == 0) {
-              a.rows[at] = lse2;
-              a.rows[(int64_t)a.heads * a.n_q + at] = delta;
+          for (int c = 0; c < DP / 16; ++c) {
+            const int at = d0 + c;
+            const uint4 vd = *reinterpret_cast<const uint4*>(d + (at >> 3) * kPanel + (((at & 7) ^ (q & 7)) << 4));
+            const uint32_t* po = reinterpret_cast<const uint32_t*>(&o[c]);
+            const uint32_t* pd = reinterpret_cast<const uint32_t*>(&vd);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 x = unpack16<T>(po[k]), y = unpack16<T>(pd[k]);
+              sum = fmaf(x.x, y.x, fmaf(x.y, y.y, sum));
             }
           }
-          mbar_arrive(kept_empty + 8 * ks);
         }
+        sum += __shfl_xor_sync(kFull, sum, 1);
+        const float mine = lane & 1 ? -sum : -lse * kLog2e;
+        s_col[(lane & 1) * kTile + q] = mine;
+        mbar_arrive(kept_empty + 8 * ks);
+        mbar_arrive(row_ready);
+        if (q < w.rows)
+          a.rows[((int64_t)(lane & 1) * a.heads + w.h) * a.n_q + w.kept_row + q] = mine;
+        if (!(ok = mbar_wait(row_ready, nk & 1, s_abort))) break;
+        lse2 = s_col[row];
+        delta = s_col[kTile + row];
       }
       const int tiles = count * (kKeys ? a.group : 1);
 #pragma unroll 1
@@ -525,6 +545,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const bool live = row < w.rows;
       const int64_t at = (((int64_t)w.kept_row + row) * (kKeys ? a.kv_heads : a.heads) + w.h) * a.D;
       mbar_arrive(item_empty + 8 * slot);
+      if (!kKeys && !(ok = ahead(i + 1))) break;
       const int acc = nk % Sh::kAcc;
       if (!(ok = mbar_wait(acc_full + 8 * acc, (nk / Sh::kAcc) & 1, s_abort))) break;
       tc_fence_after();
@@ -580,7 +601,7 @@ cudaError_t run(const BwdArgs& a, int64_t items, const CUtensorMap& k1, const CU
                 const CUtensorMap& s2, cudaStream_t s) {
   using Sh = BwdShape<DP, kKeys>;
   const auto kernel = k_attn_backward<T, DP, kKeys>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sh::kSmem);
+  cudaError_t e = allow_shared_memory(reinterpret_cast<const void*>(kernel), (int)Sh::kSmem);
   if (e != cudaSuccess) return e;
   const int64_t slots = device_info().sm_count;
   cudaLaunchConfig_t cfg = {};

@@ -409,7 +409,7 @@ template <typename T, int DP, bool kTwo>
 cudaError_t run(const ShortArgs& a, const BwdMaps& m, cudaStream_t s) {
   const auto kernel = k_attn_backward_short<T, DP, kTwo>;
   constexpr int smem = (int)ShortShape<DP, kTwo>::kSmem;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = allow_shared_memory(reinterpret_cast<const void*>(kernel), smem);
   if (e != cudaSuccess) return e;
   const int64_t items = (int64_t)a.B * a.kv_heads, slots = (int64_t)device_info().sm_count * (kTwo ? 2 : 1);
   cudaLaunchConfig_t cfg = {};

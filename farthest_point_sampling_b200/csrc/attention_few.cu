@@ -357,7 +357,7 @@ template <typename T, int DP>
 cudaError_t run(const AttnCall& c, const FewArgs& a, cudaStream_t s) {
   using Sh = FewShape<DP>;
   static_assert(4 * kFewRows * DP * 4 + 4 * kFewRows * 8 <= Sh::kStages * 2 * Sh::kTileBytes, "results over the tiles");
-  cudaError_t e = cudaFuncSetAttribute(k_attn_few<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sh::kSmem);
+  cudaError_t e = allow_shared_memory(reinterpret_cast<const void*>(k_attn_few<T, DP>), (int)Sh::kSmem);
   if (e != cudaSuccess) return e;
   const int64_t sms = device_info().sm_count;
   const int64_t units = (c.n_kv / a.chunk + c.B) * c.kv_heads, joins = (c.n_kv / a.chunk) * c.heads;

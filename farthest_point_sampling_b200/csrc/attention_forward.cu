@@ -478,7 +478,7 @@ cudaError_t run_forward(const AttnCall& c, const FwdWorkspace& ws, cudaStream_t 
   a.hdr = ws.hdr;
   const auto kernel = k_attn_forward<T, DP, kMasked>;
   constexpr int smem = (int)FwdShape<DP>::kSmem;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  e = allow_shared_memory(reinterpret_cast<const void*>(kernel), smem);
   if (e != cudaSuccess) return e;
   const int64_t items = max_tiles(c.n_q, c.B) * c.heads;
   const int64_t slots = (int64_t)device_info().sm_count * 2;

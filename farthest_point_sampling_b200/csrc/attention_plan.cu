@@ -3,6 +3,8 @@
 // length is bounded by rows / 128 + events.
 #include "attention_plan.h"
 
+#include <atomic>
+
 #include "attention_few.h"
 #include "attention_tiles.cuh"
 #include "common.cuh"
@@ -185,6 +187,32 @@ EncodeTiled encode_tiled() {
 }
 
 }  // namespace
+
+cudaError_t allow_shared_memory(const void* kernel, int bytes) {
+  // a few kernels, each found after as many compares; a lost race sets one twice
+  struct Entry {
+    std::atomic<const void*> kernel;
+    std::atomic<uint64_t> devices;  // bit per device
+  };
+  static Entry entries[64];
+  int device;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (device & 63);
+  Entry* at = nullptr;
+  for (Entry& x : entries) {
+    const void* free_slot = nullptr;
+    if (x.kernel.load(std::memory_order_acquire) == kernel ||
+        (x.kernel.compare_exchange_strong(free_slot, kernel) || free_slot == kernel)) {
+      at = &x;
+      break;
+    }
+  }
+  if (at && device < 64 && (at->devices.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && at) at->devices.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 cudaError_t launch_attention_plan(const AttnCall& c, WsHeader* hdr, const PlanLists& lists, cudaStream_t s) {
   count_launch();
