@@ -69,7 +69,7 @@ struct BwdItem {
   int h;                // head (queries kernel) or key head
   int kept_row, rows;   // first kept row, how many
   int at;               // the first kept row in its event
-  int stream_row;       // the event's first streamed row
+  int stream_row, stream_rows;  // the event's first streamed row, and how many it has
   int shift;            // nk - nq: position of query 0
   KeyTiles<kStream> tiles;
 };
@@ -81,6 +81,7 @@ __device__ __forceinline__ BwdItem bwd_item(const BwdArgs& a, int h, const TileI
   w.kept_row = (kKeys ? e.k0 : e.q0) + w.at;
   w.rows = min(kTile, (kKeys ? e.nk : e.nq) - w.at);
   w.stream_row = kKeys ? e.q0 : e.k0;
+  w.stream_rows = kKeys ? e.nq : e.nk;
   w.shift = e.nk - e.nq;
   if constexpr (kKeys) {
     // queries that see some key of the tile: the first key's lower and the
@@ -434,28 +435,30 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const int st = m % Sh::kRing;
         const int extent = w.tiles.extent(j), stream0 = w.tiles.start(j);
         j = j + 1 == count ? 0 : j + 1;
-        if (kKeys || (extent & 63)) {
+        const int left = w.stream_rows - stream0;
+        const bool clear = rows_to_clear(extent, left);
+        if (kKeys || clear) {
           // also where -lse and -D are read from
           if (!(ok = mbar_wait(ring_full + 8 * st, (m / Sh::kRing) & 1, s_abort))) break;
         }
-        if (extent & 63) {
+        if (clear) {
           uint8_t* tile = s_ring + 2 * st * Sh::kTileBytes;
-          clear_rows<Sh::kPanels>(tile, extent, threadIdx.x, kSoftmaxThreads);
-          if (kKeys) clear_rows<Sh::kPanels>(tile + Sh::kTileBytes, extent, threadIdx.x, kSoftmaxThreads);
+          clear_rows<Sh::kPanels>(tile, extent, left, threadIdx.x, kSoftmaxThreads);
+          if (kKeys) clear_rows<Sh::kPanels>(tile + Sh::kTileBytes, extent, left, threadIdx.x, kSoftmaxThreads);
           fence_async_smem();
         }
         // which pairs of the warp's kept rows and each 32 of this thread's
-        // streamed rows see one another
+        // streamed rows see one another: some, all, and those of this thread's row
         bool act[2], whole[2];
-        uint32_t see[2];
+        uint32_t see[2] = {0, 0};
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const int at = h0 + 32 * c, r0 = w.at + quarter * 32, c0 = stream0 + at;
           const int pa = (kKeys ? c0 : r0) + w.shift, key = kKeys ? r0 : c0;
           act[c] = at < extent && some_seen(a.mask, pa, pa + 31, key);
           whole[c] = at + 32 <= extent && all_seen(a.mask, pa, pa + 31, key);
-          see[c] = bits(0, extent - at);
-          if (!whole[c]) {
+          if (act[c] && !whole[c]) {
+            see[c] = bits(0, extent - at);
             if constexpr (kKeys) {
               const ColumnSpan span = column_span(a.mask, key + lane);
               see[c] &= bits(span.lo - pa, span.hi + 1 - pa);

@@ -287,12 +287,12 @@ __global__ void __launch_bounds__(kShortThreads, kTwo ? 2 : 1)
         if (!(ok = mbar_wait(qd_full + 8 * st, (u / kStages) & 1, s_abort))) break;
         uint8_t* tile = s_qd + 2 * st * Sh::kTileBytes;
         if (w.nq & 63) {
-          clear_rows<Sh::kPanels>(tile, w.nq, threadIdx.x, kSoftmaxThreads);
-          clear_rows<Sh::kPanels>(tile + Sh::kTileBytes, w.nq, threadIdx.x, kSoftmaxThreads);
+          clear_rows<Sh::kPanels>(tile, w.nq, w.nq, threadIdx.x, kSoftmaxThreads);
+          clear_rows<Sh::kPanels>(tile + Sh::kTileBytes, w.nq, w.nq, threadIdx.x, kSoftmaxThreads);
         }
         if (m == 0 && (w.nk & 63)) {
           if (!(ok = mbar_wait(kv_full + 8 * ks, (n / kStages) & 1, s_abort))) break;
-          clear_rows<Sh::kPanels>(s_kv + 2 * ks * Sh::kTileBytes, w.nk, threadIdx.x, kSoftmaxThreads);
+          clear_rows<Sh::kPanels>(s_kv + 2 * ks * Sh::kTileBytes, w.nk, w.nk, threadIdx.x, kSoftmaxThreads);
         }
         if (q < w.nq) {
           const uint8_t* d = tile + Sh::kTileBytes + q * 128;

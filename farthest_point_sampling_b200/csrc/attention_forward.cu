@@ -267,32 +267,24 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
       float m_used = -INFINITY, l = 0.f;
       for (int j = 0; j < count; ++j, ++n) {
         const int k0 = w.keys.start(j), extent = w.keys.extent(j);
-        if (extent & 63) {
+        const int left = w.nk - k0;
+        if (rows_to_clear(extent, left)) {
           const int st = n % Sh::kStages;
           if (!(ok = mbar_wait(v_full + 8 * st, (n / Sh::kStages) & 1, s_abort))) break;
-          clear_rows<Sh::kPanels>(s_v + st * Sh::kTileBytes, extent, threadIdx.x, kSoftmaxThreads);
+          clear_rows<Sh::kPanels>(s_v + st * Sh::kTileBytes, extent, left, threadIdx.x, kSoftmaxThreads);
           fence_async_smem();
         }
-        // the tile's 32-key chunks: which of them some row of the warp
-        // sees, and, unless all its rows see all of one, what this row sees
+        // the tile's 32-key chunks, one lane each: which of them some row of the
+        // warp sees, and of which all its rows see every key
         constexpr int kChunks = kTile / 32;
-        bool act[kChunks], whole[kChunks];
-        uint32_t see[kChunks];
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-          const int at = 32 * c;
-          act[c] = at < extent && warp_rows > 0;
-          whole[c] = at + 32 <= extent;
-          see[c] = bits(0, extent - at);
-          if constexpr (kMasked) {
-            const int pa = w.p0 + warp * 32, pb = pa + warp_rows - 1;
-            act[c] = act[c] && some_seen(a.mask, pa, pb, k0 + at);
-            if (!all_seen(a.mask, pa, pb, k0 + at)) {
-              whole[c] = false;
-              see[c] &= seen_keys(a.mask, pa + lane, k0 + at);
-            }
-          }
+        const int pa = w.p0 + warp * 32;
+        bool some = 32 * lane < extent && warp_rows > 0, all = 32 * lane + 32 <= extent;
+        if constexpr (kMasked) {
+          const int pb = pa + warp_rows - 1, key = k0 + 32 * lane;
+          some = some && some_seen(a.mask, pa, pb, key);
+          all = all && all_seen(a.mask, pa, pb, key);
         }
+        const uint32_t act = __ballot_sync(kFull, some && lane < kChunks), whole = __ballot_sync(kFull, all);
         if (!(ok = mbar_wait(s_full, n & 1, s_abort))) break;
         tc_fence_after();
         float s[kTile];
@@ -301,17 +293,21 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
           tmem_ld32(lanes + 32 * c, reinterpret_cast<uint32_t*>(s + 32 * c));
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) tmem_wait_ld32(reinterpret_cast<uint32_t*>(s + 32 * c));
+        if (act & ~whole) {
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c)
-          if (act[c] && !whole[c]) {
+          for (int c = 0; c < kChunks; ++c)
+            if (act >> c & ~whole >> c & 1) {  // what this row sees of it
+              uint32_t see = bits(0, extent - 32 * c);
+              if constexpr (kMasked) see &= seen_keys(a.mask, pa + lane, k0 + 32 * c);
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (!(see[c] >> k & 1)) s[32 * c + k] = -INFINITY;
-          }
+              for (int k = 0; k < 32; ++k)
+                if (!(see >> k & 1)) s[32 * c + k] = -INFINITY;
+            }
+        }
         float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
 #pragma unroll
         for (int c = 0; c < kChunks; ++c)
-          if (act[c]) {
+          if (act >> c & 1) {
 #pragma unroll
             for (int k = 32 * c; k < 32 * c + 32; k += 8) {
               m0 = max3f(m0, s[k], s[k + 1]);
@@ -347,7 +343,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
           uint32_t pk[16];
-          if (act[c]) {
+          if (act >> c & 1) {
 #pragma unroll
             for (int k = 0; k < 32; k += 2) {
               float2 e = fma2(make_float2(s[32 * c + k], s[32 * c + k + 1]), scale2, base2);
