@@ -5,7 +5,7 @@
 // the K and V gradients summed over the query heads that share them.
 //
 // Two kernels, one template.  A work item keeps a 128-row tile of one pair of
-// tensors and streams 128-row tiles of the other past it:
+// tensors and streams tiles of the other past it:
 //   queries: keeps Q, dO of one query tile and head, streams K, V:
 //            scores S = Q K^T and dP = dO V^T, then dQ += dS K;
 //   keys:    keeps K, V of one key tile and key head, streams Q, dO of every
@@ -15,15 +15,19 @@
 // one block in a fixed order, so the result does not depend on scheduling;
 // the price is that the scores are formed twice.
 //
-// Roles as in the forward kernel: a loading warp, an issuing warp, and eight
-// softmax warps with two threads per kept row, each for half of a tile's
-// streamed rows.  P and dS go back to TMEM as 16-bit operand A, each over the
-// scores its thread read.  The products of a tile are spread under the softmax
-// of it and the next: S of tile m + 1 runs while dS of tile m is formed, then
-// dK of m and dP of m + 1 run while the weights of m + 1 are.  One block takes
-// an SM with all of its TMEM: 128 columns each of S and dP, and the
-// accumulators, two sets of them where they fit, so that a block goes on with
-// the next item while it stores one.
+// Roles as in the forward kernel: a loading warp, an issuing warp, and softmax
+// warps with a thread for each kept row and 64 streamed rows.  P and dS go
+// back to TMEM as 16-bit operand A, each over the scores its thread read.  The
+// products of a tile are spread under the softmax of it and the next: S of
+// tile m + 1 runs while dS of tile m is formed, then dK of m and dP of m + 1
+// run while the weights of m + 1 are.
+//
+// Streamed tiles are 128 rows for 128-wide heads, whose accumulators take half
+// of an SM's TMEM: one block with eight softmax warps has it all.  For 64-wide
+// heads they are 64 rows, and two blocks share an SM, each with four softmax
+// warps and 256 columns: where events are a few tiles long one block's loads
+// and stores then run under the other's products.  Where two sets of
+// accumulators fit, a block goes on with the next item while it stores one.
 //
 // Rounding: P and dS are rounded to the input type for their products.  D
 // comes from the rounded output, as the forward left it.
@@ -40,13 +44,9 @@ namespace fpstok {
 
 namespace {
 
-constexpr int kStream = 128;                  // rows of a streamed tile
-constexpr int kHalf = kStream / 2;            // of which a thread takes half
-constexpr int kPanel = kTile * 128;           // bytes of a tile's 64-value panel
-constexpr int kSoftmaxThreads = 256;
-constexpr int kBwdThreads = kSoftmaxThreads + 64;
+constexpr int kRows = 64;                     // streamed rows that a thread takes
+constexpr int kPanel = kTile * 128;           // bytes of a kept tile's 64-value panel
 constexpr int kItemRing = 2;
-constexpr uint32_t kColS = 0, kColDP = 128, kColAcc = 256;
 
 struct BwdArgs {
   int64_t n_q, n_kv;
@@ -64,6 +64,7 @@ struct BwdArgs {
 };
 
 // One work item as the loading warp hands it to the others.
+template <int kStream>
 struct BwdItem {
   int count;            // streamed tiles of one head; -1 ends the work
   int h;                // head (queries kernel) or key head
@@ -73,9 +74,9 @@ struct BwdItem {
   int shift;            // nk - nq: position of query 0
   KeyTiles<kStream> tiles;
 };
-template <bool kKeys>
-__device__ __forceinline__ BwdItem bwd_item(const BwdArgs& a, int h, const TileItem& e) {
-  BwdItem w;
+template <bool kKeys, int kStream>
+__device__ __forceinline__ BwdItem<kStream> bwd_item(const BwdArgs& a, int h, const TileItem& e) {
+  BwdItem<kStream> w;
   w.h = h;
   w.at = e.t * kTile;
   w.kept_row = (kKeys ? e.k0 : e.q0) + w.at;
@@ -103,15 +104,24 @@ __device__ __forceinline__ BwdItem bwd_item(const BwdArgs& a, int h, const TileI
 template <int DP, bool kKeys>
 struct BwdShape {
   static constexpr int kPanels = DP / 64;
-  static constexpr uint32_t kTileBytes = kPanels * kPanel;  // one tensor's tile
-  // 192 KB: kept and streamed pairs of tiles
+  static constexpr int kBlocks = DP == 64 ? 2 : 1;
+  static constexpr int kStream = DP == 64 ? 64 : 128;  // rows of a streamed tile
+  static constexpr int kParts = kStream / kRows;       // threads of a kept row
+  static constexpr int kSoftmaxThreads = kTile * kParts;
+  static constexpr int kThreads = kSoftmaxThreads + 64;
+  static constexpr uint32_t kKeptBytes = kPanels * kPanel;           // one kept tensor's tile
+  static constexpr uint32_t kStreamPanel = kStream * 128;
+  static constexpr uint32_t kStreamBytes = kPanels * kStreamPanel;   // one streamed tensor's tile
+  // 96 KB for each of two blocks, or 192 KB for one
   static constexpr int kKept = DP == 64 ? 2 : 1;
-  static constexpr int kRing = DP == 64 ? 4 : 2;
+  static constexpr int kRing = 2;
+  static constexpr uint32_t kColS = 0, kColDP = kStream, kColAcc = 2 * kStream;
   static constexpr uint32_t kAccColumns = (kKeys ? 2 : 1) * DP;
-  static constexpr int kAcc = kColAcc + 2 * kAccColumns <= 512 ? 2 : 1;
-  static constexpr uint32_t kColumns = 512;
-  static constexpr size_t kSmem = 1024 + 2 * (kKept + kRing) * kTileBytes + kRing * 2 * kStream * sizeof(float) +
-                                  kItemRing * sizeof(BwdItem) + 512;
+  static constexpr uint32_t kColumns = 512 / kBlocks;
+  static constexpr int kAcc = kColAcc + 2 * kAccColumns <= kColumns ? 2 : 1;
+  static constexpr size_t kColFloats = kRing * 2 * kStream > 2 * kTile ? kRing * 2 * kStream : 2 * kTile;
+  static constexpr size_t kSmem = 1024 + 2 * (kKept * kKeptBytes + kRing * kStreamBytes) + kColFloats * sizeof(float) +
+                                  kItemRing * sizeof(BwdItem<kStream>) + 512;
 };
 
 // 4 bytes from global to shared memory, asynchronously; zero where not real.
@@ -125,20 +135,24 @@ __device__ __forceinline__ void copy_arrive(uint32_t bar) {
 }
 
 template <typename T, int DP, bool kKeys>
-__global__ void __launch_bounds__(kBwdThreads, 1)
+__global__ void __launch_bounds__(BwdShape<DP, kKeys>::kThreads, BwdShape<DP, kKeys>::kBlocks)
     k_attn_backward(const BwdArgs a, const __grid_constant__ CUtensorMap map_k1, const __grid_constant__ CUtensorMap map_k2,
                     const __grid_constant__ CUtensorMap map_s1, const __grid_constant__ CUtensorMap map_s2) {
   using Sh = BwdShape<DP, kKeys>;
+  using Item = BwdItem<Sh::kStream>;
+  constexpr int kStream = Sh::kStream, kSoftmaxThreads = Sh::kSoftmaxThreads;
+  constexpr uint32_t kColS = Sh::kColS, kColDP = Sh::kColDP, kColAcc = Sh::kColAcc;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   constexpr int kLoadWarp = kSoftmaxThreads / 32, kMmaWarp = kLoadWarp + 1;
   extern __shared__ uint8_t s_raw[];
   uint8_t* s_base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~(uintptr_t)1023);
   // kept tiles (tensor 1 and 2 of a stage side by side), then the streamed
-  // ring, then the ring's -lse log2(e) and -D of 128 queries (keys kernel)
+  // ring, then the ring's -lse log2(e) and -D of its queries (keys kernel), or
+  // those of the kept rows (queries kernel)
   uint8_t* s_kept = s_base;
-  uint8_t* s_ring = s_kept + 2 * Sh::kKept * Sh::kTileBytes;
-  float* s_col = reinterpret_cast<float*>(s_ring + 2 * Sh::kRing * Sh::kTileBytes);
-  BwdItem* s_item = reinterpret_cast<BwdItem*>(s_col + Sh::kRing * 2 * kStream);
+  uint8_t* s_ring = s_kept + 2 * Sh::kKept * Sh::kKeptBytes;
+  float* s_col = reinterpret_cast<float*>(s_ring + 2 * Sh::kRing * Sh::kStreamBytes);
+  Item* s_item = reinterpret_cast<Item*>(s_col + Sh::kColFloats);
   uint64_t* s_bar = reinterpret_cast<uint64_t*>(s_item + kItemRing);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_bar + 32);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
@@ -193,11 +207,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       // The issuing warp looks one item ahead, so the ring holds none without
       // tiles: this warp clears their gradient rows itself.
       TileItem entry;
-      BwdItem w;
+      Item w;
       int h;
       bool more;
       while ((more = claims.take(&entry, &h))) {
-        w = bwd_item<kKeys>(a, h, entry);
+        w = bwd_item<kKeys, kStream>(a, h, entry);
         if (w.count) break;
         const int heads = kKeys ? a.kv_heads : a.heads;
         const int64_t at = ((int64_t)w.kept_row * heads + h) * a.D, stride = (int64_t)heads * a.D;
@@ -223,9 +237,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       for (int b = 0; b < boxes; ++b)
 #pragma unroll
         for (int p = 0; p < Sh::kPanels; ++p) {
-          const uint32_t to = smem_u32(s_kept) + 2 * ks * Sh::kTileBytes + p * kPanel + b * 8192;
+          const uint32_t to = smem_u32(s_kept) + 2 * ks * Sh::kKeptBytes + p * kPanel + b * 8192;
           tma_load(to, &map_k1, kept_full + 8 * ks, p * 64, w.h, w.kept_row + b * 64);
-          tma_load(to + Sh::kTileBytes, &map_k2, kept_full + 8 * ks, p * 64, w.h, w.kept_row + b * 64);
+          tma_load(to + Sh::kKeptBytes, &map_k2, kept_full + 8 * ks, p * 64, w.h, w.kept_row + b * 64);
         }
       ++nk;
       const int head0 = kKeys ? w.h * a.group : w.h / a.group;
@@ -242,9 +256,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           for (int b = 0; b < sboxes; ++b)
 #pragma unroll
             for (int p = 0; p < Sh::kPanels; ++p) {
-              const uint32_t to = smem_u32(s_ring) + 2 * st * Sh::kTileBytes + p * kPanel + b * 8192;
+              const uint32_t to = smem_u32(s_ring) + 2 * st * Sh::kStreamBytes + p * Sh::kStreamPanel + b * 8192;
               tma_load(to, &map_s1, ring_full + 8 * st, p * 64, head0 + hd, row + b * 64);
-              tma_load(to + Sh::kTileBytes, &map_s2, ring_full + 8 * st, p * 64, head0 + hd, row + b * 64);
+              tma_load(to + Sh::kStreamBytes, &map_s2, ring_full + 8 * st, p * 64, head0 + hd, row + b * 64);
             }
           if constexpr (kKeys) {
             const float* from = a.rows + (int64_t)(head0 + hd) * a.n_q + row;
@@ -315,20 +329,20 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     // S (x = 0) or dP (x = 1) of tile m: a kept and a streamed tensor; whole
     // panels, as values past D are zeros
     const auto scores = [&](const Tile& t, int m, int x) {
-      const uint32_t kept = smem_desc(smem_u32(s_kept) + (2 * t.kept + x) * Sh::kTileBytes, kPanel);
-      const uint32_t from = smem_desc(smem_u32(s_ring) + (2 * (m % Sh::kRing) + x) * Sh::kTileBytes, kPanel);
+      const uint32_t kept = smem_desc(smem_u32(s_kept) + (2 * t.kept + x) * Sh::kKeptBytes, kPanel);
+      const uint32_t from = smem_desc(smem_u32(s_ring) + (2 * (m % Sh::kRing) + x) * Sh::kStreamBytes, Sh::kStreamPanel);
       const uint32_t desc = mma_desc(kBf16, false, false, t.steps * 16);
 #pragma unroll
       for (int p = 0; p < Sh::kPanels; ++p)
-        mma_ss<2, 2>(tmem + (x ? kColDP : kColS), kept + p * (kPanel >> 4), from + p * (kPanel >> 4), desc, p > 0);
+        mma_ss<2, 2>(tmem + (x ? kColDP : kColS), kept + p * (kPanel >> 4), from + p * (Sh::kStreamPanel >> 4), desc, p > 0);
       mma_commit(x ? dp_full : s_full);
     };
     // an accumulator += the 16-bit rows over S or dP, times a streamed tensor;
-    // each half of the rows lies over its half of the scores
+    // each 64 of the rows lie over the first half of their scores
     const auto gradient = [&](const Tile& t, int m, uint32_t from, uint32_t to, int x) {
-      const uint32_t rows = smem_desc(smem_u32(s_ring) + (2 * (m % Sh::kRing) + x) * Sh::kTileBytes, kPanel);
+      const uint32_t rows = smem_desc(smem_u32(s_ring) + (2 * (m % Sh::kRing) + x) * Sh::kStreamBytes, Sh::kStreamPanel);
       mma_ts(to, from, rows, out_desc, !t.first);
-      if (t.steps > 4) mma_ts(to, from + kHalf, rows + kRun, out_desc, true);
+      if (Sh::kParts > 1 && t.steps > 4) mma_ts(to, from + kRows, rows + kRun, out_desc, true);
     };
     Tile cur, nxt;
     bool more = fetch(&cur);
@@ -366,26 +380,31 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
   } else {
     // ------------------------------------------------ softmax and its gradient
-    const int half = warp >> 2, quarter = warp & 3;
-    const int row = threadIdx.x & 127, h0 = half * kHalf;
+    const int part = warp >> 2, quarter = warp & 3;
+    const int row = threadIdx.x & 127, h0 = part * kRows;
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
     const float2 scale2 = make_float2(a.scale_log2, a.scale_log2);
     int m = 0, nk = 0;
     bool ok = true;
     // Queries kernel: two threads read the row of O that belongs to a query of
     // the next item, before they store this one's gradients.
-    const int q = warp * 16 + (lane >> 1), d0 = (lane & 1) * (DP / 16);
-    uint4 o[DP / 16];
-    float lse = 0.f;
+    constexpr int kOwn = 2 / Sh::kParts;  // queries of a pair of threads, 64 apart
+    const int q0 = warp * 16 + (lane >> 1), d0 = (lane & 1) * (DP / 16);
+    uint4 o[kOwn][DP / 16];
+    float lse[kOwn] = {};
     const auto ahead = [&](int i) {
       if (!mbar_wait(item_full + 8 * (i % kItemRing), (i / kItemRing) & 1, s_abort)) return false;
-      const BwdItem& w = s_item[i % kItemRing];
-      if (w.count > 0 && q < w.rows) {
+      const Item& w = s_item[i % kItemRing];
+      if (w.count <= 0) return true;
+#pragma unroll
+      for (int r = 0; r < kOwn; ++r) {
+        const int q = q0 + 64 * r;
+        if (q >= w.rows) continue;
         const T* from = static_cast<const T*>(a.out) + (((int64_t)w.kept_row + q) * a.heads + w.h) * a.D;
 #pragma unroll
         for (int c = 0; c < DP / 16; ++c)
-          o[c] = (d0 + c) * 8 < a.D ? *reinterpret_cast<const uint4*>(from + (d0 + c) * 8) : make_uint4(0, 0, 0, 0);
-        lse = a.lse[(int64_t)w.h * a.n_q + w.kept_row + q];
+          o[r][c] = (d0 + c) * 8 < a.D ? *reinterpret_cast<const uint4*>(from + (d0 + c) * 8) : make_uint4(0, 0, 0, 0);
+        lse[r] = a.lse[(int64_t)w.h * a.n_q + w.kept_row + q];
       }
       return true;
     };
@@ -393,7 +412,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     for (int i = 0; ok; ++i) {
       const int slot = i % kItemRing;
       if (kKeys && !(ok = mbar_wait(item_full + 8 * slot, (i / kItemRing) & 1, s_abort))) break;
-      const BwdItem& w = s_item[slot];  // read where it is needed: it stays until this thread lets go of the slot
+      const Item& w = s_item[slot];  // read where it is needed: it stays until this thread lets go of the slot
       const int count = w.count;
       if (count < 0) break;
       float lse2 = 0.f, delta = 0.f;  // -lse log2(e) and -D of this thread's query
@@ -402,29 +421,32 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         // through memory and with the threads of each row through the block's
         const int ks = nk % Sh::kKept;
         if (!(ok = mbar_wait(kept_full + 8 * ks, (nk / Sh::kKept) & 1, s_abort))) break;
-        float sum = 0.f;
-        if (q < w.rows) {
-          const uint8_t* d = s_kept + (2 * ks + 1) * Sh::kTileBytes + q * 128;
 #pragma unroll
-          for (int c = 0; c < DP / 16; ++c) {
-            const int at = d0 + c;
-            const uint4 vd = *reinterpret_cast<const uint4*>(d + (at >> 3) * kPanel + (((at & 7) ^ (q & 7)) << 4));
-            const uint32_t* po = reinterpret_cast<const uint32_t*>(&o[c]);
-            const uint32_t* pd = reinterpret_cast<const uint32_t*>(&vd);
+        for (int r = 0; r < kOwn; ++r) {
+          const int q = q0 + 64 * r;
+          float sum = 0.f;
+          if (q < w.rows) {
+            const uint8_t* d = s_kept + (2 * ks + 1) * Sh::kKeptBytes + q * 128;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float2 x = unpack16<T>(po[k]), y = unpack16<T>(pd[k]);
-              sum = fmaf(x.x, y.x, fmaf(x.y, y.y, sum));
+            for (int c = 0; c < DP / 16; ++c) {
+              const int at = d0 + c;
+              const uint4 vd = *reinterpret_cast<const uint4*>(d + (at >> 3) * kPanel + (((at & 7) ^ (q & 7)) << 4));
+              const uint32_t* po = reinterpret_cast<const uint32_t*>(&o[r][c]);
+              const uint32_t* pd = reinterpret_cast<const uint32_t*>(&vd);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float2 x = unpack16<T>(po[k]), y = unpack16<T>(pd[k]);
+                sum = fmaf(x.x, y.x, fmaf(x.y, y.y, sum));
+              }
             }
           }
+          sum += __shfl_xor_sync(kFull, sum, 1);
+          const float mine = lane & 1 ? -sum : -lse[r] * kLog2e;
+          s_col[(lane & 1) * kTile + q] = mine;
+          if (q < w.rows) a.rows[((int64_t)(lane & 1) * a.heads + w.h) * a.n_q + w.kept_row + q] = mine;
         }
-        sum += __shfl_xor_sync(kFull, sum, 1);
-        const float mine = lane & 1 ? -sum : -lse * kLog2e;
-        s_col[(lane & 1) * kTile + q] = mine;
         mbar_arrive(kept_empty + 8 * ks);
         mbar_arrive(row_ready);
-        if (q < w.rows)
-          a.rows[((int64_t)(lane & 1) * a.heads + w.h) * a.n_q + w.kept_row + q] = mine;
         if (!(ok = mbar_wait(row_ready, nk & 1, s_abort))) break;
         lse2 = s_col[row];
         delta = s_col[kTile + row];
@@ -442,9 +464,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           if (!(ok = mbar_wait(ring_full + 8 * st, (m / Sh::kRing) & 1, s_abort))) break;
         }
         if (clear) {
-          uint8_t* tile = s_ring + 2 * st * Sh::kTileBytes;
-          clear_rows<Sh::kPanels>(tile, extent, left, threadIdx.x, kSoftmaxThreads);
-          if (kKeys) clear_rows<Sh::kPanels>(tile + Sh::kTileBytes, extent, left, threadIdx.x, kSoftmaxThreads);
+          uint8_t* tile = s_ring + 2 * st * Sh::kStreamBytes;
+          clear_rows<Sh::kPanels, kStream>(tile, extent, left, threadIdx.x, kSoftmaxThreads);
+          if (kKeys) clear_rows<Sh::kPanels, kStream>(tile + Sh::kStreamBytes, extent, left, threadIdx.x, kSoftmaxThreads);
           fence_async_smem();
         }
         // which pairs of the warp's kept rows and each 32 of this thread's
@@ -470,7 +492,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const float* col = s_col + st * 2 * kStream + h0;
         if (!(ok = mbar_wait(s_full, m & 1, s_abort))) break;
         tc_fence_after();
-        float x[kHalf];
+        float x[kRows];
 #pragma unroll
         for (int c = 0; c < 2; ++c) tmem_ld32(lanes + kColS + h0 + 32 * c, reinterpret_cast<uint32_t*>(x + 32 * c));
         tmem_wait_ld32(reinterpret_cast<uint32_t*>(x));
@@ -552,14 +574,17 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const int acc = nk % Sh::kAcc;
       if (!(ok = mbar_wait(acc_full + 8 * acc, (nk / Sh::kAcc) & 1, s_abort))) break;
       tc_fence_after();
-      // the halves share the stores: dK and dV, or half of dQ each
+      // the parts share the stores: dK and dV, or half of dQ each
       const uint32_t from = lanes + kColAcc + acc * Sh::kAccColumns;
-      if constexpr (kKeys)
-        store_row<T, DP>(from + half * DP, live, half == 0 ? a.scale : 1.f,
-                         static_cast<T*>(half == 0 ? a.d1 : a.d2) + at, a.D, a.sectors);
-      else
-        store_row<T, DP / 2>(from + half * (DP / 2), live, a.scale, static_cast<T*>(a.d1) + at + half * (DP / 2),
-                             a.D - half * (DP / 2), a.sectors);
+#pragma unroll
+      for (int x = part; x < 2; x += Sh::kParts) {
+        if constexpr (kKeys)
+          store_row<T, DP>(from + x * DP, live, x == 0 ? a.scale : 1.f, static_cast<T*>(x == 0 ? a.d1 : a.d2) + at, a.D,
+                           a.sectors);
+        else
+          store_row<T, DP / 2>(from + x * (DP / 2), live, a.scale, static_cast<T*>(a.d1) + at + x * (DP / 2),
+                               a.D - x * (DP / 2), a.sectors);
+      }
       tc_fence_before();
       mbar_arrive(acc_empty + 8 * acc);
       ++nk;
@@ -606,10 +631,10 @@ cudaError_t run(const BwdArgs& a, int64_t items, const CUtensorMap& k1, const CU
   const auto kernel = k_attn_backward<T, DP, kKeys>;
   cudaError_t e = allow_shared_memory(reinterpret_cast<const void*>(kernel), (int)Sh::kSmem);
   if (e != cudaSuccess) return e;
-  const int64_t slots = device_info().sm_count;
+  const int64_t slots = (int64_t)device_info().sm_count * Sh::kBlocks;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(items < 1 ? 1 : items < slots ? items : slots));
-  cfg.blockDim = dim3(kBwdThreads);
+  cfg.blockDim = dim3(Sh::kThreads);
   cfg.dynamicSmemBytes = Sh::kSmem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];

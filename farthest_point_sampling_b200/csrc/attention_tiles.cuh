@@ -246,19 +246,19 @@ __device__ __forceinline__ float2 unpack16<__half>(uint32_t v) {
   return __half22float2(*reinterpret_cast<__half2*>(&v));
 }
 
-// Products run over 64 rows of a 128-row tile at a time.  Past the rows a tile
+// Products run over 64 rows of a tile at a time.  Past the rows a tile
 // takes (`extent`) the weights are 0, and what follows is rows of the same
 // event up to its last (`left` rows from the tile's first), then those of
 // another event or of nothing, which must not reach this one: they are set to
 // 0, by `threads` threads.  Returns whether there are any to set.
 __device__ __forceinline__ bool rows_to_clear(int extent, int left) { return left < ((extent + 63) & ~63); }
-template <int kPanels>
+template <int kPanels, int kTileRows = kTile>
 __device__ __forceinline__ void clear_rows(uint8_t* tile, int extent, int left, int thread, int threads) {
   const int rows = ((extent + 63) & ~63) - left;
 #pragma unroll 1
   for (int e = thread; e < rows * 8 * kPanels; e += threads) {
     const int r = left + e / (8 * kPanels), c = e % (8 * kPanels);
-    *reinterpret_cast<uint4*>(tile + (c >> 3) * (kTile * 128) + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+    *reinterpret_cast<uint4*>(tile + (c >> 3) * (kTileRows * 128) + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
   }
 }
 
