@@ -41,14 +41,15 @@ __device__ __forceinline__ int block_scan(int v, int* s_warp, int* total) {
   return x - v + (warp ? s_warp[warp - 1] : 0);  // exclusive
 }
 
-// Sorts 1024 keys in shared memory, largest first (bitonic).
-__device__ __forceinline__ void block_sort(uint64_t* s) {
+// Sorts the first `count` (a power of two) keys in shared memory, largest
+// first (bitonic).
+__device__ __forceinline__ void block_sort(uint64_t* s, int count) {
   const int i = threadIdx.x;
-  for (int k = 2; k <= kPlanThreads; k <<= 1)
+  for (int k = 2; k <= count; k <<= 1)
     for (int j = k >> 1; j > 0; j >>= 1) {
       const int x = i ^ j;
       __syncthreads();
-      if (x > i) {
+      if (x > i && x < count) {
         const uint64_t a = s[i], b = s[x];
         if ((a < b) == ((i & k) == 0)) {
           s[i] = b;
@@ -120,7 +121,9 @@ __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const int64_t* __res
     if (kind <= kPlanKeys && __syncthreads_or(n > 4)) {
       s_event[tid] = e;
       s_sort[tid] = ((uint64_t)n << 32) | (uint32_t)(kPlanThreads - 1 - tid);
-      block_sort(s_sort);
+      int count = 2;
+      while (count < min(B - b0, kPlanThreads)) count <<= 1;
+      block_sort(s_sort, count);
       n = (int)(s_sort[tid] >> 32);
       e = s_event[kPlanThreads - 1 - (uint32_t)s_sort[tid]];
       __syncthreads();

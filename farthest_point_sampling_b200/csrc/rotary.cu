@@ -28,7 +28,16 @@ namespace fpstok {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTile = 16;  // tokens of one block
+constexpr int kMaxTile = 16;     // tokens of one block
+// (token, head) rows that a thread has on the way, every load before the first
+// store.  Float32 rows, two at once: 256 events (30,691 tokens x 10 heads x 72)
+// 43 -> 41 us.  16-bit rows, one at once in at least six blocks an SM: 446,880
+// tokens x 24 heads x 64 take 495 us; two at once 599, four 933, because a
+// block then reads from as many more places at a time.
+template <typename T>
+constexpr int kRowsOf = sizeof(T) == 4 ? 2 : 1;
+template <typename T>
+constexpr int kBlocksOf = sizeof(T) == 4 ? 1 : 6;
 
 template <typename T>
 __device__ __forceinline__ float to_float(T v);
@@ -69,8 +78,9 @@ struct Shape {
 // vector of V / 2 pairs (interleaved layout; two values for V = 1), or one
 // vector of the part that does not turn.
 template <typename T, int V, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads) k_rotary(const T* x, T* y, const Shape s,
+__global__ void __launch_bounds__(kThreads, kBlocksOf<T>) k_rotary(const T* x, T* y, const Shape s,
                                                      const __grid_constant__ fps_rotary_table table) {
+  constexpr int kRowsAtOnce = kRowsOf<T>;
   extern __shared__ float2 s_cs[];  // [tile][R] (cos, sin)
   const int64_t t0 = (int64_t)blockIdx.x * s.tile;
   const int nt = (int)min((int64_t)s.tile, s.T - t0);
@@ -95,42 +105,58 @@ __global__ void __launch_bounds__(kThreads) k_rotary(const T* x, T* y, const Sha
   const int g = threadIdx.x / units, u = threadIdx.x - g * units;
   if (g >= groups) return;
   int t = g / s.H, h = g - t * s.H;
+  const bool turns = u < turn_units;
+  // vectors of a row that this thread moves: the pair's halves, or one
+  const bool two = turns && !(kInterleaved && V > 1);
+  const int i1 = !turns                    ? 2 * s.R + (u - turn_units) * V
+                 : kInterleaved && V == 1 ? 2 * u
+                                          : u * V;
+  const int i2 = kInterleaved ? i1 + 1 : i1 + s.R;
   while (t < nt) {
-    const T* xr = x + (t0 + t) * s.x_token + h * s.x_head;
-    T* yr = y + (t0 + t) * s.y_token + h * s.y_head;
-    const float2* cs = s_cs + t * s.R;
-    if (u >= turn_units) {
-      const int i = 2 * s.R + (u - turn_units) * V;
-      *reinterpret_cast<Vec<T, V>*>(yr + i) = *reinterpret_cast<const Vec<T, V>*>(xr + i);
-    } else if constexpr (kInterleaved && V > 1) {
-      Vec<T, V> a = *reinterpret_cast<const Vec<T, V>*>(xr + u * V);
+    Vec<T, V> a[kRowsAtOnce], b[kRowsAtOnce];
+    int tt[kRowsAtOnce], hh[kRowsAtOnce];
 #pragma unroll
-      for (int q = 0; q < V / 2; ++q) {
-        const float2 c = cs[u * (V / 2) + q];
-        const float a1 = to_float(a.v[2 * q]), a2 = to_float(a.v[2 * q + 1]);
-        a.v[2 * q] = from_float<T>(fmaf(a1, c.x, -(a2 * c.y)));
-        a.v[2 * q + 1] = from_float<T>(fmaf(a2, c.x, a1 * c.y));
+    for (int k = 0; k < kRowsAtOnce; ++k) {
+      tt[k] = t;
+      hh[k] = h;
+      if (t < nt) {
+        const T* xr = x + (t0 + t) * s.x_token + h * s.x_head;
+        a[k] = *reinterpret_cast<const Vec<T, V>*>(xr + i1);
+        if (two) b[k] = *reinterpret_cast<const Vec<T, V>*>(xr + i2);
       }
-      *reinterpret_cast<Vec<T, V>*>(yr + u * V) = a;
-    } else {
-      const int i1 = kInterleaved ? 2 * u : u * V, i2 = kInterleaved ? 2 * u + 1 : u * V + s.R;
-      Vec<T, V> a = *reinterpret_cast<const Vec<T, V>*>(xr + i1);
-      Vec<T, V> b = *reinterpret_cast<const Vec<T, V>*>(xr + i2);
-#pragma unroll
-      for (int q = 0; q < V; ++q) {
-        const float2 c = cs[u * V + q];
-        const float a1 = to_float(a.v[q]), a2 = to_float(b.v[q]);
-        a.v[q] = from_float<T>(fmaf(a1, c.x, -(a2 * c.y)));
-        b.v[q] = from_float<T>(fmaf(a2, c.x, a1 * c.y));
+      t += step_t;
+      h += step_h;
+      if (h >= s.H) {
+        h -= s.H;
+        ++t;
       }
-      *reinterpret_cast<Vec<T, V>*>(yr + i1) = a;
-      *reinterpret_cast<Vec<T, V>*>(yr + i2) = b;
     }
-    t += step_t;
-    h += step_h;
-    if (h >= s.H) {
-      h -= s.H;
-      ++t;
+#pragma unroll
+    for (int k = 0; k < kRowsAtOnce; ++k) {
+      if (tt[k] >= nt) continue;
+      T* yr = y + (t0 + tt[k]) * s.y_token + hh[k] * s.y_head;
+      const float2* cs = s_cs + tt[k] * s.R;
+      if (turns) {
+        if constexpr (kInterleaved && V > 1) {
+#pragma unroll
+          for (int q = 0; q < V / 2; ++q) {
+            const float2 c = cs[u * (V / 2) + q];
+            const float a1 = to_float(a[k].v[2 * q]), a2 = to_float(a[k].v[2 * q + 1]);
+            a[k].v[2 * q] = from_float<T>(fmaf(a1, c.x, -(a2 * c.y)));
+            a[k].v[2 * q + 1] = from_float<T>(fmaf(a2, c.x, a1 * c.y));
+          }
+        } else {
+#pragma unroll
+          for (int q = 0; q < V; ++q) {
+            const float2 c = cs[u * V + q];
+            const float a1 = to_float(a[k].v[q]), a2 = to_float(b[k].v[q]);
+            a[k].v[q] = from_float<T>(fmaf(a1, c.x, -(a2 * c.y)));
+            b[k].v[q] = from_float<T>(fmaf(a2, c.x, a1 * c.y));
+          }
+          *reinterpret_cast<Vec<T, V>*>(yr + i2) = b[k];
+        }
+      }
+      *reinterpret_cast<Vec<T, V>*>(yr + i1) = a[k];
     }
   }
 }
