@@ -267,13 +267,6 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
       float m_used = -INFINITY, l = 0.f;
       for (int j = 0; j < count; ++j, ++n) {
         const int k0 = w.keys.start(j), extent = w.keys.extent(j);
-        const int left = w.nk - k0;
-        if (rows_to_clear(extent, left)) {
-          const int st = n % Sh::kStages;
-          if (!(ok = mbar_wait(v_full + 8 * st, (n / Sh::kStages) & 1, s_abort))) break;
-          clear_rows<Sh::kPanels>(s_v + st * Sh::kTileBytes, extent, left, threadIdx.x, kSoftmaxThreads);
-          fence_async_smem();
-        }
         // the tile's 32-key chunks, one lane each: which of them some row of the
         // warp sees, and of which all its rows see every key
         constexpr int kChunks = kTile / 32;
@@ -287,6 +280,16 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
         const uint32_t act = __ballot_sync(kFull, some && lane < kChunks), whole = __ballot_sync(kFull, all);
         if (!(ok = mbar_wait(s_full, n & 1, s_abort))) break;
         tc_fence_after();
+        // Only now is the values' barrier waited for: with one stage, before these
+        // scores it may still be in the phase of the tile before, whose end looks
+        // the same as that of the tile before it.
+        const int left = w.nk - k0;
+        if (rows_to_clear(extent, left)) {
+          const int st = n % Sh::kStages;
+          if (!(ok = mbar_wait(v_full + 8 * st, (n / Sh::kStages) & 1, s_abort))) break;
+          clear_rows<Sh::kPanels>(s_v + st * Sh::kTileBytes, extent, left, threadIdx.x, kSoftmaxThreads);
+          fence_async_smem();
+        }
         float s[kTile];
 #pragma unroll
         for (int c = 0; c < kChunks; ++c)

@@ -192,6 +192,25 @@ def test_same_bits_twice_and_streams():
         assert all(torch.equal(a, b) for a, b in zip(g, grads))
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_same_bits_many_times(D):
+    """Events whose last tile holds few rows, over and over: no tile is touched while another still reads it."""
+    g = torch.Generator().manual_seed(3)
+    sizes = [128 * int(a) + int(b) for a, b in zip(torch.randint(1, 8, (48,), generator=g), torch.randint(1, 80, (48,), generator=g))]
+    q, k, v, dout, qo, ko = _inputs(sizes, sizes, 8, 2, D, F16, 115)
+    kw = dict(causal=True, window=300, sinks=4)
+    want = attention(q, k, v, qo, qo, dout=dout, **kw)
+    first = None
+    for _ in range(12):
+        out, lse = fps.attention_forward(q, k, v, qo, **kw)
+        got = (out, lse, *fps.attention_backward(dout, q, k, v, out, lse, qo, **kw))
+        if first is None:
+            first = got
+            for t, name in zip(got, ("out", "lse", "dq", "dk", "dv")):
+                assert_within(t, want[name], name)
+        assert all(torch.equal(a, b) for a, b in zip(got, first))
+
+
 def test_autograd_and_differences():
     sizes = [90, 33]
     q, k, v, dout, qo, ko = _inputs(sizes, sizes, 4, 2, 64, F16, 120)
