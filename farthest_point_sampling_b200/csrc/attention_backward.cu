@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(BwdShape<DP, kKeys>::kThreads, BwdShape<DP, kK
   const uint32_t kept_full = bars, kept_empty = bars + 16, acc_full = bars + 32, acc_empty = bars + 48,
                  item_full = bars + 64, item_empty = bars + 80, s_full = bars + 96, dp_full = bars + 104,
                  p_ready = bars + 112, ds_ready = bars + 120, drain = bars + 128, ring_full = bars + 136,
-                 ring_empty = bars + 168, row_ready = bars + 208;
+                 ring_empty = bars + 168, row_ready = bars + 208, dv_done = bars + 216;
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -179,6 +179,7 @@ __global__ void __launch_bounds__(BwdShape<DP, kKeys>::kThreads, BwdShape<DP, kK
     mbar_init(ds_ready, kSoftmaxThreads);
     mbar_init(drain, 1);
     mbar_init(row_ready, kSoftmaxThreads);
+    mbar_init(dv_done, 1);
     for (int i = 0; i < Sh::kRing; ++i) {
       mbar_init(ring_full + 8 * i, kKeys ? 33 : 1);  // the tiles, and in the keys kernel each lane's -lse and -D
       mbar_init(ring_empty + 8 * i, 1);
@@ -358,9 +359,15 @@ __global__ void __launch_bounds__(BwdShape<DP, kKeys>::kThreads, BwdShape<DP, kK
         break;
       if (!mbar_wait_warp(p_ready, m & 1, s_abort)) break;
       tc_fence_after();
-      if constexpr (kKeys) gradient(cur, m, tmem + kColS, to + DP, 1);  // dV += P^T dO
+      // Products of different shapes are not promised to run in order: scores
+      // wait for the product that reads the 16-bit rows in their place.
+      if constexpr (kKeys) {
+        gradient(cur, m, tmem + kColS, to + DP, 1);  // dV += P^T dO
+        mma_commit(dv_done);
+      }
       more = fetch(&nxt);
       if (!ok) break;
+      if (kKeys && !mbar_wait_warp(dv_done, m & 1, s_abort)) break;
       if (more) scores(nxt, m + 1, 0);
       if (!mbar_wait_warp(ds_ready, m & 1, s_abort)) break;
       tc_fence_after();
@@ -368,6 +375,7 @@ __global__ void __launch_bounds__(BwdShape<DP, kKeys>::kThreads, BwdShape<DP, kK
       mma_commit(ring_empty + 8 * (m % Sh::kRing));
       if (cur.last) mma_commit(acc_full + 8 * (cur.item % Sh::kAcc));
       if (more) {
+        if (!mbar_wait_warp(ring_empty + 8 * (m % Sh::kRing), (m / Sh::kRing) & 1, s_abort)) break;
         scores(nxt, m + 1, 1);
         if (nxt.last) mma_commit(kept_empty + 8 * nxt.kept);  // only the scores read the kept tiles
         cur = nxt;

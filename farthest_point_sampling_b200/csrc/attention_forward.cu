@@ -36,7 +36,6 @@ constexpr int kSoftmaxThreads = 32 * kSoftmaxWarps;
 constexpr int kFwdThreads = kSoftmaxThreads + 64;
 constexpr int kPanel = kTile * 128;  // bytes of a 128-row panel of 64 values
 constexpr uint32_t kTmemColumns = 256;
-constexpr uint32_t kColO = 128;  // S (and P over it) in columns 0 .. 127
 
 struct FwdArgs {
   int64_t n_q;
@@ -82,6 +81,10 @@ struct FwdShape {
   static constexpr int kPanels = DP / 64;
   static constexpr int kStages = DP == 64 ? 2 : 1;  // of Q, K and V each: 96 KB either way, two blocks per SM
   static constexpr uint32_t kTileBytes = kPanels * kPanel;
+  // S in columns 0 .. 127; 64-wide heads leave room for P beside it, with
+  // 128-wide ones P lies over S and the next S waits for the product that reads it
+  static constexpr bool kOver = DP == 128;
+  static constexpr uint32_t kColP = kOver ? 0 : 128, kColO = kOver ? 128 : 192;
   static constexpr size_t kSmem =
       1024 + 3 * kStages * kTileBytes + kItemRing * sizeof(FwdItem) + 256;
 };
@@ -223,12 +226,14 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
             if (!(ok = mbar_wait_warp(p_ready, m & 1, s_abort))) break;
             tc_fence_after();
             const uint32_t v = smem_desc(smem_u32(s_v) + st * Sh::kTileBytes, kPanel);
-            mma_ts(tmem + kColO, tmem, v, pv_desc, j > 1);
-            if (both) mma_ts(tmem + kColO, tmem + 32, v + kRun, pv_desc, true);
+            mma_ts(tmem + Sh::kColO, tmem + Sh::kColP, v, pv_desc, j > 1);
+            if (both) mma_ts(tmem + Sh::kColO, tmem + Sh::kColP + 32, v + kRun, pv_desc, true);
             mma_commit(v_empty + 8 * st);
             if (j == count) mma_commit(o_full);
+            // products of different shapes are not promised to run in order
+            if (Sh::kOver && !(ok = mbar_wait_warp(v_empty + 8 * st, (m / Sh::kStages) & 1, s_abort))) break;
           }
-          if (j < count) {  // S = Q K^T of tile j; over P, which the product before has read
+          if (j < count) {  // S = Q K^T of tile j
             const int m = n + j, st = m % Sh::kStages;
             const int cols = (keys.extent(j) + 15) / 16 * 16;
             if (!(ok = mbar_wait_warp(k_full + 8 * st, (m / Sh::kStages) & 1, s_abort))) break;
@@ -332,11 +337,11 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
 #pragma unroll 1
             for (int c = 0; c < DP; c += 8) {
               uint32_t o[8];
-              tmem_ld8(lanes + kColO + c, o);
+              tmem_ld8(lanes + Sh::kColO + c, o);
               tmem_wait_ld8(o);
 #pragma unroll
               for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-              tmem_st8(lanes + kColO + c, o);
+              tmem_st8(lanes + Sh::kColO + c, o);
             }
           }
         }
@@ -359,7 +364,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
 #pragma unroll
             for (int k = 0; k < 16; ++k) pk[k] = 0;
           }
-          if (32 * (c & ~1) < extent) tmem_st16(lanes + 16 * c, pk);  // zeros too, to the end of 64 keys
+          if (32 * (c & ~1) < extent) tmem_st16(lanes + Sh::kColP + 16 * c, pk);  // zeros too, to the end of 64 keys
         }
         l += sum.x + sum.y;
         tmem_wait_st();
@@ -391,15 +396,15 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
 #pragma unroll 1
         for (int c = 0; c < DP; c += 8) {
           uint32_t o[8];
-          tmem_ld8(lanes + kColO + c, o);
+          tmem_ld8(lanes + Sh::kColO + c, o);
           tmem_wait_ld8(o);
 #pragma unroll
           for (int k = 0; k < 8; ++k) o[k] = l == 0.f ? 0u : o[k];
-          tmem_st8(lanes + kColO + c, o);
+          tmem_st8(lanes + Sh::kColO + c, o);
         }
         tmem_wait_st();
       }
-      store_row<T, DP>(lanes + kColO, live, l == 0.f ? 0.f : rcp_approx(l), out + lane * row_values, a.D, a.sectors);
+      store_row<T, DP>(lanes + Sh::kColO, live, l == 0.f ? 0.f : rcp_approx(l), out + lane * row_values, a.D, a.sectors);
       tc_fence_before();
       if (lse && live) lse[lane] = l == 0.f ? -INFINITY : fmaf(m_used, a.scale, log2_approx(l) * kLn2);
     }
