@@ -15,6 +15,13 @@
 // one block in a fixed order, so the result does not depend on scheduling;
 // the price is that the scores are formed twice.
 //
+// A key tile that every query of a long event sees - the first keys under
+// `sinks`, or all without a window - is as much work as its event is long, and
+// one block would end last with it.  Such tiles are cut into pieces of their
+// (head, query tile) range; each piece leaves float32 sums, and a second kernel
+// adds a tile's pieces in order.  64 track events of up to 20000 tokens (causal
+// window of 511, 4 sinks, 8 query and 2 key heads of 128): 322 us, whole 385.
+//
 // Roles as in the forward kernel: a loading warp, an issuing warp, and softmax
 // warps with a thread for each kept row and 64 streamed rows.  P and dS go
 // back to TMEM as 16-bit operand A, each over the scores its thread read.  The
@@ -30,9 +37,11 @@
 // accumulators fit, a block goes on with the next item while it stores one.
 //
 // Rounding: P and dS are rounded to the input type for their products.  D
-// comes from the rounded output, as the forward left it.
+// comes from the rounded output, as the forward left it, but for queries that
+// see few keys, where that would show (attention_backward_rows.cu).
 #include <type_traits>
 
+#include "attention_few.h"
 #include "attention_plan.h"
 #include "attention_short.h"
 #include "attention_tiles.cuh"
@@ -55,7 +64,10 @@ struct BwdArgs {
   float scale, scale_log2;
   const void* out;
   const float* lse;
-  float* rows;   // [2][heads, n_q]: -lse log2(e) and -D, written by the queries kernel for the keys kernel
+  // [2][heads, n_q]: -lse log2(e) and -D, written by the queries kernel for the
+  // keys kernel; of queries that see few keys -D is there before
+  float* rows;
+  float* partial;  // [slot][key head][128][2 DP]: dK and dV of the pieces of a key tile
   void* d1;      // dQ, or dK
   void* d2;      // dV
   bool sectors;  // every gradient row starts on a 32-byte sector, and ends on one
@@ -67,6 +79,9 @@ struct BwdArgs {
 template <int kStream>
 struct BwdItem {
   int count;            // streamed tiles of one head; -1 ends the work
+  int f0, f1;           // which of those of all heads in turn this item takes
+  int hd, j;            // the first one's head in the group, and its place among the head's
+  int slot;             // where its sums go: -1 for the gradients
   int h;                // head (queries kernel) or key head
   int kept_row, rows;   // first kept row, how many
   int at;               // the first kept row in its event
@@ -85,11 +100,8 @@ __device__ __forceinline__ BwdItem<kStream> bwd_item(const BwdArgs& a, int h, co
   w.stream_rows = kKeys ? e.nq : e.nk;
   w.shift = e.nk - e.nq;
   if constexpr (kKeys) {
-    // queries that see some key of the tile: the first key's lower and the
-    // last key's upper bound; a tile with a sink in it is seen to the end
-    const ColumnSpan first = column_span(a.mask, w.at), last = column_span(a.mask, w.at + w.rows - 1);
-    const int lo = min(max(first.lo - w.shift, 0), e.nq);
-    const int hi = min(max(max(first.hi, last.hi) - w.shift + 1, 0), e.nq);
+    int lo, hi;
+    queries_of(a.mask, w.at, w.rows, w.shift, e.nq, &lo, &hi);
     w.tiles.before = w.tiles.s = 0;
     w.tiles.first = lo & ~15;
     w.tiles.end = hi;
@@ -98,6 +110,19 @@ __device__ __forceinline__ BwdItem<kStream> bwd_item(const BwdArgs& a, int h, co
     w.tiles = key_tiles<kStream>(a.mask, w.at + w.shift, w.at + w.rows - 1 + w.shift, e.nk);
   }
   w.count = w.tiles.count;
+  w.f0 = 0;
+  w.f1 = w.count * (kKeys ? a.group : 1);
+  w.slot = -1;
+  w.hd = w.j = 0;
+  if (kKeys && e.pad[2] != -1) {  // a piece
+    w.f0 = e.pad[0];
+    w.f1 = e.pad[1];
+    w.slot = e.pad[2];
+    if (w.f1 > w.f0) {
+      w.hd = w.f0 / w.count;
+      w.j = w.f0 - w.hd * w.count;
+    }
+  }
   return w;
 }
 
@@ -213,7 +238,8 @@ __global__ void __launch_bounds__(BwdShape<DP, kKeys>::kThreads, BwdShape<DP, kK
       bool more;
       while ((more = claims.take(&entry, &h))) {
         w = bwd_item<kKeys, kStream>(a, h, entry);
-        if (w.count) break;
+        if (w.slot == -2) continue;
+        if (w.f1 > w.f0) break;
         const int heads = kKeys ? a.kv_heads : a.heads;
         const int64_t at = ((int64_t)w.kept_row * heads + h) * a.D, stride = (int64_t)heads * a.D;
         clear_strided(static_cast<T*>(a.d1) + at, w.rows, stride, a.D);
@@ -244,34 +270,37 @@ __global__ void __launch_bounds__(BwdShape<DP, kKeys>::kThreads, BwdShape<DP, kK
         }
       ++nk;
       const int head0 = kKeys ? w.h * a.group : w.h / a.group;
+      int hd = w.hd, j = w.j;
 #pragma unroll 1
-      for (int hd = 0; hd < (kKeys ? a.group : 1) && ok; ++hd)
+      for (int f = w.f0; f < w.f1; ++f, ++n) {
+        const int st = n % Sh::kRing;
+        if (n >= Sh::kRing && !(ok = mbar_wait_warp(ring_empty + 8 * st, ((n / Sh::kRing) - 1) & 1, s_abort))) break;
+        const int row = w.stream_row + w.tiles.start(j), extent = w.tiles.extent(j);
+        const int sboxes = (extent + 63) / 64;
+        mbar_expect(ring_full + 8 * st, 2 * sboxes * 8192 * Sh::kPanels);
 #pragma unroll 1
-        for (int j = 0; j < w.count; ++j, ++n) {
-          const int st = n % Sh::kRing;
-          if (n >= Sh::kRing && !(ok = mbar_wait_warp(ring_empty + 8 * st, ((n / Sh::kRing) - 1) & 1, s_abort))) break;
-          const int row = w.stream_row + w.tiles.start(j), extent = w.tiles.extent(j);
-          const int sboxes = (extent + 63) / 64;
-          mbar_expect(ring_full + 8 * st, 2 * sboxes * 8192 * Sh::kPanels);
-#pragma unroll 1
-          for (int b = 0; b < sboxes; ++b)
+        for (int b = 0; b < sboxes; ++b)
 #pragma unroll
-            for (int p = 0; p < Sh::kPanels; ++p) {
-              const uint32_t to = smem_u32(s_ring) + 2 * st * Sh::kStreamBytes + p * Sh::kStreamPanel + b * 8192;
-              tma_load(to, &map_s1, ring_full + 8 * st, p * 64, head0 + hd, row + b * 64);
-              tma_load(to + Sh::kStreamBytes, &map_s2, ring_full + 8 * st, p * 64, head0 + hd, row + b * 64);
-            }
-          if constexpr (kKeys) {
-            const float* from = a.rows + (int64_t)(head0 + hd) * a.n_q + row;
-            const uint32_t to = smem_u32(s_col + st * 2 * kStream);
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-#pragma unroll
-              for (int c = lane; c < kStream; c += 32)
-                copy4(to + (x * kStream + c) * 4, from + (c < extent ? (int64_t)x * a.heads * a.n_q + c : 0), c < extent);
-            copy_arrive(ring_full + 8 * st);
+          for (int p = 0; p < Sh::kPanels; ++p) {
+            const uint32_t to = smem_u32(s_ring) + 2 * st * Sh::kStreamBytes + p * Sh::kStreamPanel + b * 8192;
+            tma_load(to, &map_s1, ring_full + 8 * st, p * 64, head0 + hd, row + b * 64);
+            tma_load(to + Sh::kStreamBytes, &map_s2, ring_full + 8 * st, p * 64, head0 + hd, row + b * 64);
           }
+        if constexpr (kKeys) {
+          const float* from = a.rows + (int64_t)(head0 + hd) * a.n_q + row;
+          const uint32_t to = smem_u32(s_col + st * 2 * kStream);
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int c = lane; c < kStream; c += 32)
+              copy4(to + (x * kStream + c) * 4, from + (c < extent ? (int64_t)x * a.heads * a.n_q + c : 0), c < extent);
+          copy_arrive(ring_full + 8 * st);
         }
+        if (++j == w.count) {
+          j = 0;
+          ++hd;
+        }
+      }
     }
     // after a wait that gave up: the copies still in flight land first
     if (__any_sync(kFull, *s_abort)) {
@@ -285,21 +314,23 @@ __global__ void __launch_bounds__(BwdShape<DP, kKeys>::kThreads, BwdShape<DP, kK
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------ products
     const uint32_t out_desc = mma_desc(kBf16, false, true, (a.D + 15) / 16 * 16);
-    const int heads = kKeys ? a.group : 1;
     // The next tile in the order of the work, across items: its item's kept
     // stage and accumulators, and whether it is the item's first and last.
     struct Tile {
       int steps, kept, item;
       bool first, last;
     };
-    int i = 0, hd = heads, j = 0, count = 0, items = 0, fetched = 0;  // items and tiles read, place in the item
+    int i = 0, f = 0, f0 = 0, f1 = 0, j = 0, count = 0, items = 0, fetched = 0;  // items and tiles read, place in the item
     KeyTiles<kStream> tiles = {};
     bool ok = true;
     const auto fetch = [&](Tile* t) {  // false when the work is done, or a wait gave up (ok)
-      if (hd == heads) {
+      if (f == f1) {
         const int slot = i % kItemRing;
         if (!(ok = mbar_wait_warp(item_full + 8 * slot, (i / kItemRing) & 1, s_abort))) return false;
         count = uniform(s_item[slot].count);
+        f0 = f = uniform(s_item[slot].f0);
+        f1 = uniform(s_item[slot].f1);
+        j = uniform(s_item[slot].j);
         tiles.before = uniform(s_item[slot].tiles.before);
         tiles.first = uniform(s_item[slot].tiles.first);
         tiles.end = uniform(s_item[slot].tiles.end);
@@ -307,7 +338,6 @@ __global__ void __launch_bounds__(BwdShape<DP, kKeys>::kThreads, BwdShape<DP, kK
         mbar_arrive_one(item_empty + 8 * slot);
         if (count < 0) return false;
         ++i;
-        hd = j = 0;
         const int ks = items % Sh::kKept;
         if (!(ok = mbar_wait_warp(kept_full + 8 * ks, (items / Sh::kKept) & 1, s_abort))) return false;
         ++items;
@@ -318,12 +348,9 @@ __global__ void __launch_bounds__(BwdShape<DP, kKeys>::kThreads, BwdShape<DP, kK
       t->steps = (tiles.extent(j) + 15) / 16;
       t->item = items - 1;
       t->kept = t->item % Sh::kKept;
-      t->first = hd == 0 && j == 0;
-      t->last = hd == heads - 1 && j == count - 1;
-      if (++j == count) {
-        j = 0;
-        ++hd;
-      }
+      t->first = f == f0;
+      t->last = ++f == f1;
+      if (++j == count) j = 0;
       tc_fence_after();
       return true;
     };
@@ -400,6 +427,7 @@ __global__ void __launch_bounds__(BwdShape<DP, kKeys>::kThreads, BwdShape<DP, kK
     const int q0 = warp * 16 + (lane >> 1), d0 = (lane & 1) * (DP / 16);
     uint4 o[kOwn][DP / 16];
     float lse[kOwn] = {};
+    bool given[kOwn] = {};
     const auto ahead = [&](int i) {
       if (!mbar_wait(item_full + 8 * (i % kItemRing), (i / kItemRing) & 1, s_abort)) return false;
       const Item& w = s_item[i % kItemRing];
@@ -408,11 +436,13 @@ __global__ void __launch_bounds__(BwdShape<DP, kKeys>::kThreads, BwdShape<DP, kK
       for (int r = 0; r < kOwn; ++r) {
         const int q = q0 + 64 * r;
         if (q >= w.rows) continue;
+        // the second of the two has no need of lse: where -D is there, it reads that
+        given[r] = (lane & 1) && few_keys(a.mask, w.at + q + w.shift, w.stream_rows);
+        lse[r] = (given[r] ? a.rows + (int64_t)a.heads * a.n_q : a.lse)[(int64_t)w.h * a.n_q + w.kept_row + q];
         const T* from = static_cast<const T*>(a.out) + (((int64_t)w.kept_row + q) * a.heads + w.h) * a.D;
 #pragma unroll
         for (int c = 0; c < DP / 16; ++c)
           o[r][c] = (d0 + c) * 8 < a.D ? *reinterpret_cast<const uint4*>(from + (d0 + c) * 8) : make_uint4(0, 0, 0, 0);
-        lse[r] = a.lse[(int64_t)w.h * a.n_q + w.kept_row + q];
       }
       return true;
     };
@@ -449,7 +479,7 @@ __global__ void __launch_bounds__(BwdShape<DP, kKeys>::kThreads, BwdShape<DP, kK
             }
           }
           sum += __shfl_xor_sync(kFull, sum, 1);
-          const float mine = lane & 1 ? -sum : -lse[r] * kLog2e;
+          const float mine = given[r] ? lse[r] : lane & 1 ? -sum : -lse[r] * kLog2e;
           s_col[(lane & 1) * kTile + q] = mine;
           if (q < w.rows) a.rows[((int64_t)(lane & 1) * a.heads + w.h) * a.n_q + w.kept_row + q] = mine;
         }
@@ -459,9 +489,9 @@ __global__ void __launch_bounds__(BwdShape<DP, kKeys>::kThreads, BwdShape<DP, kK
         lse2 = s_col[row];
         delta = s_col[kTile + row];
       }
-      const int tiles = count * (kKeys ? a.group : 1);
+      const int f1 = w.f1;
 #pragma unroll 1
-      for (int t = 0, j = 0; t < tiles; ++t, ++m) {
+      for (int f = w.f0, j = w.j; f < f1; ++f, ++m) {
         const int st = m % Sh::kRing;
         const int extent = w.tiles.extent(j), stream0 = w.tiles.start(j);
         j = j + 1 == count ? 0 : j + 1;
@@ -577,6 +607,9 @@ __global__ void __launch_bounds__(BwdShape<DP, kKeys>::kThreads, BwdShape<DP, kK
       if (!ok) break;
       const bool live = row < w.rows;
       const int64_t at = (((int64_t)w.kept_row + row) * (kKeys ? a.kv_heads : a.heads) + w.h) * a.D;
+      float* sums = kKeys && w.slot >= 0
+                        ? a.partial + (((int64_t)w.slot * a.kv_heads + w.h) * kTile + row) * (2 * DP)
+                        : nullptr;
       mbar_arrive(item_empty + 8 * slot);
       if (!kKeys && !(ok = ahead(i + 1))) break;
       const int acc = nk % Sh::kAcc;
@@ -586,7 +619,17 @@ __global__ void __launch_bounds__(BwdShape<DP, kKeys>::kThreads, BwdShape<DP, kK
       const uint32_t from = lanes + kColAcc + acc * Sh::kAccColumns;
 #pragma unroll
       for (int x = part; x < 2; x += Sh::kParts) {
-        if constexpr (kKeys)
+        if (kKeys && sums) {  // a piece of a tile: its float32 sums, to be joined
+#pragma unroll 1
+          for (int c = 0; c < DP; c += 32) {
+            uint32_t v[32];
+            tmem_ld32(from + x * DP + c, v);
+            tmem_wait_ld32(v);
+#pragma unroll
+            for (int k = 0; k < 32; k += 4)
+              if (live) *reinterpret_cast<uint4*>(sums + x * DP + c + k) = make_uint4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+          }
+        } else if constexpr (kKeys)
           store_row<T, DP>(from + x * DP, live, x == 0 ? a.scale : 1.f, static_cast<T*>(x == 0 ? a.d1 : a.d2) + at, a.D,
                            a.sectors);
         else
@@ -608,14 +651,75 @@ __global__ void __launch_bounds__(BwdShape<DP, kKeys>::kThreads, BwdShape<DP, kK
   if (threadIdx.x == 0 && *s_abort) record_error(a.hdr, kDevWaitTimeout);
 }
 
+// dK and dV of the key tiles that were cut into pieces: their sums in order.
+template <typename T, int DP>
+__global__ void __launch_bounds__(256) k_attn_join_keys(const BwdArgs a, const JoinItem* joins) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int slots = a.hdr->n_items[kKeySlots];
+  for (int i = blockIdx.x; i < slots * a.kv_heads; i += gridDim.x) {
+    const JoinItem j = joins[i / a.kv_heads];
+    const int h = i % a.kv_heads;
+    if (j.chunks == 0) continue;  // not a tile's first slot
+    for (int e = threadIdx.x; e < j.nq * (2 * DP / 4); e += 256) {
+      const int row = e / (2 * DP / 4), c = (e - row * (2 * DP / 4)) * 4, d = c % DP;
+      if (d >= a.D) continue;
+      const float* from = a.partial + (((int64_t)j.slot * a.kv_heads + h) * kTile + row) * (2 * DP) + c;
+      const int64_t step = (int64_t)a.kv_heads * kTile * 2 * DP;
+      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int p = 0; p < j.chunks; ++p) {
+        const float4 x = *reinterpret_cast<const float4*>(from + p * step);
+        s.x += x.x;
+        s.y += x.y;
+        s.z += x.z;
+        s.w += x.w;
+      }
+      const float f = c < DP ? a.scale : 1.f;
+      T* to = static_cast<T*>(c < DP ? a.d1 : a.d2) + ((int64_t)(j.q0 + row) * a.kv_heads + h) * a.D + d;
+      *reinterpret_cast<uint2*>(to) = make_uint2(pack16<T>(s.x * f, s.y * f), pack16<T>(s.z * f, s.w * f));
+    }
+  }
+}
+
+// How a call cuts the key tiles that every query sees: into pieces of so many
+// streamed tiles, with so many slots for their sums; 0 where none is long
+// enough.  A piece is no shorter than a tile within a window, and than half a
+// block's share of the work if it were even.
+struct Pieces {
+  int piece, slots;
+};
+Pieces pieces_of(const AttnCall& c) {
+  const int64_t stream = c.D <= 64 ? 64 : 128, blocks = 148 * (c.D <= 64 ? 2 : 1);
+  const int64_t longest = c.max_tokens > 0 && c.max_tokens < c.n_q ? c.max_tokens : c.n_q;
+  const int64_t full = (longest / stream + 2) * c.group, tiles = c.n_kv / kTile + c.B;
+  const bool window = c.mask.left < kFar;
+  const int64_t sink_tiles = ((int64_t)c.mask.sinks + kTile - 1) / kTile;
+  const int64_t in_window = ((int64_t)kTile + c.mask.left + c.mask.right) / stream + 3;
+  const int64_t other = window && in_window * c.group < full ? in_window * c.group : full;
+  const int64_t long_work = window ? (sink_tiles < tiles ? sink_tiles : tiles) * (c.n_q / stream + 2 * (int64_t)c.B) * c.group
+                                   : tiles * full;
+  const int64_t work = (window ? tiles * other : 0) + long_work;
+  int64_t piece = work * c.kv_heads / (2 * blocks);
+  if (piece < 16) piece = 16;
+  if (window && piece < other) piece = other;
+  if (full <= piece || long_work == 0) return {0, 0};
+  return {(int)piece, (int)(2 * long_work / piece + 1)};
+}
+
 struct BwdWorkspace {
   WsHeader* hdr;
   TileItem *queries, *keys, *shorts;
+  JoinItem* joins;
+  float* partial;
+  Pieces pieces;
   float* rows;
   size_t bytes;
 };
-BwdWorkspace carve_backward(void* base, int64_t n_q, int64_t n_kv, int B, int heads) {
-  BwdWorkspace w;
+BwdWorkspace carve_backward(void* base, const AttnCall& c) {
+  BwdWorkspace w = {};
+  const int64_t n_q = c.n_q, n_kv = c.n_kv;
+  const int B = c.B, heads = c.heads;
+  w.pieces = pieces_of(c);
   char* p = static_cast<char*>(base);
   size_t off = 256;
   const auto take = [&](size_t bytes) {
@@ -625,7 +729,10 @@ BwdWorkspace carve_backward(void* base, int64_t n_q, int64_t n_kv, int B, int he
   };
   w.hdr = reinterpret_cast<WsHeader*>(p);
   w.queries = reinterpret_cast<TileItem*>(take((max_tiles(n_q, B) + 1) * sizeof(TileItem)));
-  w.keys = reinterpret_cast<TileItem*>(take((max_tiles(n_kv, B) + 1) * sizeof(TileItem)));
+  w.keys = reinterpret_cast<TileItem*>(take((max_tiles(n_kv, B) + w.pieces.slots + 1) * sizeof(TileItem)));
+  w.joins = reinterpret_cast<JoinItem*>(take((size_t)w.pieces.slots * sizeof(JoinItem)));
+  w.partial = reinterpret_cast<float*>(
+      take((size_t)w.pieces.slots * c.kv_heads * kTile * 2 * (c.D <= 64 ? 64 : 128) * sizeof(float)));
   w.shorts = reinterpret_cast<TileItem*>(take((size_t)(B + 1) * sizeof(TileItem)));
   w.rows = reinterpret_cast<float*>(take((size_t)n_q * heads * 2 * sizeof(float)));
   w.bytes = off;
@@ -682,7 +789,24 @@ cudaError_t run_tiles(const AttnCall& c, const BwdWorkspace& ws, const BwdMaps& 
     a.d1 = c.dk;
     a.d2 = c.dv;
     a.items = ws.keys;
-    if ((e = run<T, DP, true>(a, max_tiles(c.n_kv, c.B) * c.kv_heads, m.k, m.v, m.q, m.d, s)) != cudaSuccess) return e;
+    a.partial = ws.partial;
+    if ((e = run<T, DP, true>(a, (max_tiles(c.n_kv, c.B) + ws.pieces.slots) * c.kv_heads, m.k, m.v, m.q, m.d, s)) !=
+        cudaSuccess)
+      return e;
+    if (ws.pieces.slots > 0) {
+      const int64_t items = (int64_t)ws.pieces.slots * c.kv_heads, most = (int64_t)device_info().sm_count * 8;
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3((unsigned)(items < most ? items : most));
+      cfg.blockDim = dim3(256);
+      cfg.stream = s;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      attr[0].val.programmaticStreamSerializationAllowed = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      count_launch();
+      if ((e = cudaLaunchKernelEx(&cfg, k_attn_join_keys<T, DP>, a, (const JoinItem*)ws.joins)) != cudaSuccess) return e;
+    }
   }
   return cudaSuccess;
 }
@@ -690,15 +814,19 @@ cudaError_t run_tiles(const AttnCall& c, const BwdWorkspace& ws, const BwdMaps& 
 }  // namespace
 
 size_t attention_backward_bytes(const AttnCall& c) {
-  return carve_backward(nullptr, c.n_q, c.n_kv, c.B, c.heads).bytes;
+  return carve_backward(nullptr, c).bytes;
 }
 
 cudaError_t launch_attention_backward(const AttnCall& c, void* workspace, cudaStream_t s) {
-  const BwdWorkspace ws = carve_backward(workspace, c.n_q, c.n_kv, c.B, c.heads);
+  const BwdWorkspace ws = carve_backward(workspace, c);
   PlanLists lists = {};
   lists.queries = ws.queries;
   lists.keys = ws.keys;
   lists.shorts = ws.shorts;
+  lists.piece = ws.pieces.piece;
+  lists.slots = ws.pieces.slots;
+  lists.stream = c.D <= 64 ? 64 : 128;
+  lists.key_joins = ws.joins;
   cudaError_t e = launch_attention_plan(c, ws.hdr, lists, s);
   if (e != cudaSuccess || (c.n_q == 0 && c.n_kv == 0)) return e;
   const bool bf16 = c.dtype == FPS_DTYPE_BF16;
@@ -715,7 +843,8 @@ cudaError_t launch_attention_backward(const AttnCall& c, void* workspace, cudaSt
   m.sectors = ((reinterpret_cast<uintptr_t>(c.dq) | reinterpret_cast<uintptr_t>(c.dk) | reinterpret_cast<uintptr_t>(c.dv)) &
                31) == 0 &&
               c.D % 16 == 0;
-  if ((e = launch_attention_backward_short(c, m, ws.shorts, ws.hdr, s)) != cudaSuccess) return e;
+  if (c.n_q > 0 && (e = launch_attention_backward_rows(c, ws.rows, s)) != cudaSuccess) return e;
+  if ((e = launch_attention_backward_short(c, m, ws.rows, ws.shorts, ws.hdr, s)) != cudaSuccess) return e;
   if (c.max_tokens > 0 && c.max_tokens <= kTile) return cudaSuccess;  // every event is short
   if (bf16) return c.D <= 64 ? run_tiles<__nv_bfloat16, 64>(c, ws, m, s) : run_tiles<__nv_bfloat16, 128>(c, ws, m, s);
   return c.D <= 64 ? run_tiles<__half, 64>(c, ws, m, s) : run_tiles<__half, 128>(c, ws, m, s);

@@ -51,6 +51,7 @@ struct ShortArgs {
   float scale, scale_log2;
   const void* out;
   const float* lse;
+  const float* rows;  // [2][heads, n_q]: the second half holds -D of queries that see few keys
   void *dq, *dk, *dv;
   const int64_t *q_offsets, *kv_offsets;
   int B;
@@ -268,6 +269,9 @@ __global__ void __launch_bounds__(kShortThreads, kTwo ? 2 : 1)
       const int64_t key_at = (((int64_t)w.k_row + row) * a.kv_heads + w.h) * a.D;
       const int shift = w.nk - w.nq, ks = n % kStages;
       const int q = warp * 16 + (lane >> 1);  // the query whose D this thread and the next form
+      // the second of a pair of threads has no need of lse: where -D is there, it reads that
+      const bool some_few = may_see_few(a.mask, w.nq, w.nk);
+      const auto given = [&] { return some_few && (lane & 1) && few_keys(a.mask, q + shift, w.nk); };
       const ColumnSpan span = column_span(a.mask, row);
 #pragma unroll 1
       for (int m = 0; m < a.group; ++m, ++u) {
@@ -282,7 +286,7 @@ __global__ void __launch_bounds__(kShortThreads, kTwo ? 2 : 1)
 #pragma unroll
           for (int c = 0; c < DP / 16; ++c)
             o[c] = (d0 + c) * 8 < a.D ? *reinterpret_cast<const uint4*>(from + (d0 + c) * 8) : make_uint4(0, 0, 0, 0);
-          lse = a.lse[(int64_t)h * a.n_q + w.q_row + q];
+          lse = (given() ? a.rows + (int64_t)a.heads * a.n_q : a.lse)[(int64_t)h * a.n_q + w.q_row + q];
         }
         if (!(ok = mbar_wait(qd_full + 8 * st, (u / kStages) & 1, s_abort))) break;
         uint8_t* tile = s_qd + 2 * st * Sh::kTileBytes;
@@ -310,7 +314,7 @@ __global__ void __launch_bounds__(kShortThreads, kTwo ? 2 : 1)
           }
         }
         delta += __shfl_xor_sync(kFull, delta, 1);
-        s_col[(lane & 1) * kTile + q] = lane & 1 ? -delta : -lse * kLog2e;
+        s_col[(lane & 1) * kTile + q] = given() ? lse : lane & 1 ? -delta : -lse * kLog2e;
         mbar_arrive(col_full);
         if (!(ok = mbar_wait(scores_full, u & 1, s_abort))) break;
         if (!(ok = mbar_wait(col_full, u & 1, s_abort))) break;
@@ -434,8 +438,8 @@ cudaError_t run_type(const ShortArgs& a, const BwdMaps& m, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_attention_backward_short(const AttnCall& c, const BwdMaps& maps, const TileItem* items, WsHeader* hdr,
-                                            cudaStream_t s) {
+cudaError_t launch_attention_backward_short(const AttnCall& c, const BwdMaps& maps, const float* rows, const TileItem* items,
+                                            WsHeader* hdr, cudaStream_t s) {
   ShortArgs a;
   a.n_q = c.n_q;
   a.n_kv = c.n_kv;
@@ -448,6 +452,7 @@ cudaError_t launch_attention_backward_short(const AttnCall& c, const BwdMaps& ma
   a.scale_log2 = c.scale * kLog2e;
   a.out = c.out;
   a.lse = c.lse;
+  a.rows = rows;
   a.dq = c.dq;
   a.dk = c.dk;
   a.dv = c.dv;

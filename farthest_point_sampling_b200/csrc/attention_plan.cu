@@ -128,6 +128,26 @@ __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const int64_t* __res
       e = s_event[kPlanThreads - 1 - (uint32_t)s_sort[tid]];
       __syncthreads();
     }
+    if (kind == kPlanKeys && lists.slots > 0) {
+      // tiles that hold a sink, or all without a window, are seen by every query
+      int cuts = 1, whole = 0;
+      if (n > 0) {
+        whole = mask.left < kFar ? min((mask.sinks + kTile - 1) / kTile, n) : n;
+        cuts = ((e.nq / lists.stream + 2) * group + lists.piece - 1) / lists.piece;
+      }
+      int total_parts;
+      const int want = cuts > 1 ? (int)min((int64_t)whole * cuts, (int64_t)lists.slots + 1) : 0;
+      const int slot = slots + block_scan(want, s_warp, &total_parts);
+      if (cuts > 1 && slot + want > lists.slots) {  // no room, which the host's count rules out
+        cuts = 1;
+        for (int i = slot; i < lists.slots; ++i) lists.key_joins[i] = JoinItem{0, 0, 0, 0};
+      }
+      e.pad[0] = cuts;
+      e.pad[1] = whole;
+      e.pad[2] = slot;
+      if (cuts > 1) n += whole * (cuts - 1);
+      slots = min(slots + total_parts, lists.slots);
+    }
     int total;
     s_start[tid] = block_scan(n, s_warp, &total);
     if (kind == kPlanUnits) {
@@ -151,6 +171,32 @@ __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const int64_t* __res
       TileItem it = s_event[lo];
       it.t = i - s_start[lo];
       // causal: the last queries of an event see most
+      if (kind == kPlanKeys) {
+        const int cuts = lists.slots > 0 ? it.pad[0] : 1, whole = it.pad[1], slot = it.pad[2], at = it.t;
+        it.pad[0] = 0;
+        it.pad[1] = -1;
+        it.pad[2] = -1;
+        if (cuts > 1 && at < whole * cuts) {
+          it.t = at / cuts;
+          const int piece = at - it.t * cuts, rows = min(kTile, it.nk - it.t * kTile);
+          int lo, hi;
+          queries_of(mask, it.t * kTile, rows, it.nk - it.nq, it.nq, &lo, &hi);
+          const int all = hi > lo ? (hi - (lo & ~15) + lists.stream - 1) / lists.stream * group : 0;
+          const int each = all > 0 ? (all + cuts - 1) / cuts : 1, pieces = max((all + each - 1) / each, 1);
+          JoinItem j = {0, 0, 0, 0};
+          if (pieces > 1 && piece < pieces) {
+            it.pad[0] = piece * each;
+            it.pad[1] = min(it.pad[0] + each, all);
+            it.pad[2] = slot + at;
+            if (piece == 0) j = JoinItem{it.k0 + it.t * kTile, rows, slot + at, pieces};
+          } else if (piece > 0) {
+            it.pad[2] = -2;
+          }
+          lists.key_joins[slot + at] = j;
+        } else if (cuts > 1) {
+          it.t = whole + at - whole * cuts;
+        }
+      }
       if (kind == kPlanQueries && mask.causal) it.t = (it.nq + kTile - 1) / kTile - 1 - it.t;
       items[base + i] = it;
     }
@@ -166,6 +212,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const int64_t* __res
     hdr->next_item[list] = 0;
     hdr->n_items[list] = base;
     if (kind == kPlanUnits) hdr->n_items[kFewJoins] = joins;
+    if (kind == kPlanKeys) hdr->n_items[kKeySlots] = slots;
     if (kind == kPlanQueries) {  // every block sees the same errors; one writes the status word
       hdr->status = error;
       hdr->detail = 0;

@@ -17,6 +17,7 @@ constexpr int kKeyTiles = 1;
 constexpr int kFewUnits = 2;
 constexpr int kFewJoins = 3;
 constexpr int kShortEvents = 4;
+constexpr int kKeySlots = 5;
 
 // The lists of one call; those that are NULL are not made.
 struct PlanLists {
@@ -25,6 +26,12 @@ struct PlanLists {
   TileItem* units;    // chunks of the events with at most kFewRows query rows, which then have no query tiles
   JoinItem* joins;    // those of them with several chunks
   int chunk;
+  // Key tiles that every query sees take the work of a whole event: those of
+  // more than `piece` (0: none) streamed tiles of `stream` rows are cut into
+  // pieces, pad[0] .. pad[1] - 1 of the tiles of all heads in turn, whose sums
+  // go to slot pad[2] (-1: to the gradients; -2: a piece that is not needed).
+  int piece, stream, slots;
+  JoinItem* key_joins;  // per slot: at a tile's first one its rows and how many, else none
   TileItem* shorts;   // the events of at most 128 queries and 128 keys, which then have no tiles of either kind
 };
 

@@ -17,9 +17,12 @@ struct BwdMaps {
   bool sectors;
 };
 
+// -D of the queries that see few keys, into rows[heads + head, query].
+cudaError_t launch_attention_backward_rows(const AttnCall& c, float* rows, cudaStream_t s);
+
 // Gradients of the events in `items` (at most 128 queries and 128 keys each),
 // and zeros in the gradient rows behind the last event.
-cudaError_t launch_attention_backward_short(const AttnCall& c, const BwdMaps& maps, const TileItem* items, WsHeader* hdr,
-                                            cudaStream_t s);
+cudaError_t launch_attention_backward_short(const AttnCall& c, const BwdMaps& maps, const float* rows,
+                                            const TileItem* items, WsHeader* hdr, cudaStream_t s);
 
 }  // namespace fpstok

@@ -120,6 +120,25 @@ __device__ __forceinline__ FewSpan few_span(const AttnMask& m, int nq, int nk) {
   return f;
 }
 
+// The same for one query, at position p.
+__device__ __forceinline__ FewSpan row_span(const AttnMask& m, int p, int nk) {
+  FewSpan f;
+  f.s = max(min(sinks_of(m, p), nk), 0);
+  f.lo = max(max(0, p - m.left), f.s);
+  f.hi = min(nk, p + m.right + 1);
+  return f;
+}
+// Queries that see so few keys take their D from attention_backward_rows.cu.
+constexpr int kFewKeys = 16;
+__device__ __forceinline__ bool few_keys(const AttnMask& m, int p, int nk) {
+  return row_span(m, p, nk).count() <= kFewKeys;
+}
+// Whether an event may have such queries: but for few keys or a narrow window
+// they stand before the first key, or are the first ones under a causal mask.
+__device__ __forceinline__ bool may_see_few(const AttnMask& m, int nq, int nk) {
+  return m.causal || nk <= kFewKeys || m.left < kFewKeys || nq > nk;
+}
+
 // Positions of the queries that see key j, as [lo, hi].
 struct ColumnSpan {
   int lo, hi;
@@ -133,6 +152,15 @@ __device__ __forceinline__ ColumnSpan column_span(const AttnMask& m, int j) {
     if (!m.causal) c.lo = -kFar;
   }
   return c;
+}
+
+// Queries [lo, hi) of the nq that see some key of the `rows` keys from `at` on:
+// the first key's lower and the last key's upper bound; a tile with a sink in
+// it is seen to the end.
+__device__ __forceinline__ void queries_of(const AttnMask& m, int at, int rows, int shift, int nq, int* lo, int* hi) {
+  const ColumnSpan first = column_span(m, at), last = column_span(m, at + rows - 1);
+  *lo = min(max(first.lo - shift, 0), nq);
+  *hi = min(max(max(first.hi, last.hi) - shift + 1, 0), nq);
 }
 
 // Bits lo .. hi - 1 of a word, bounds clipped to 0 .. 32.

@@ -27,7 +27,7 @@ int check_attention_sizes(const fps_attention_args* a) {
     return FPS_ERR_TOO_LARGE;
   // work items (tiles of at least 64 rows, times heads) are counted in 32 bits
   const int64_t rows = a->n_q > a->n_kv ? a->n_q : a->n_kv;
-  if ((rows / 64 + a->events) * a->heads >= ((int64_t)1 << 31)) return FPS_ERR_TOO_LARGE;
+  if ((rows / 32 + 2 * (int64_t)a->events) * a->heads >= ((int64_t)1 << 31)) return FPS_ERR_TOO_LARGE;
   return FPS_OK;
 }
 
@@ -47,6 +47,12 @@ int make_sizes(const fps_attention_args* a, AttnCall* c) {
   c->group = a->heads / a->kv_heads;
   c->D = a->head_dim;
   c->B = a->events;
+  // positions stay below kMaxRows = kFar: a wider window sees everything
+  c->mask.causal = a->causal;
+  c->mask.left = a->window < 0 || a->window >= kMaxRows ? kFar : (int)a->window;
+  c->mask.right = a->causal ? 0 : c->mask.left;
+  c->mask.sinks = c->mask.left == kFar ? 0 : (int)(a->sinks >= kMaxRows ? kMaxRows : a->sinks);
+  c->max_tokens = a->max_tokens;
   return FPS_OK;
 }
 
@@ -74,12 +80,6 @@ int make_call(const fps_attention_args* a, AttnCall* c) {
   c->q_offsets = a->q_offsets;
   c->kv_offsets = a->kv_offsets;
   c->scale = a->scale;
-  // positions stay below kMaxRows = kFar: a wider window sees everything
-  c->mask.causal = a->causal;
-  c->mask.left = a->window < 0 || a->window >= kMaxRows ? kFar : (int)a->window;
-  c->mask.right = a->causal ? 0 : c->mask.left;
-  c->mask.sinks = c->mask.left == kFar ? 0 : (int)(a->sinks >= kMaxRows ? kMaxRows : a->sinks);
-  c->max_tokens = a->max_tokens;
   c->zero_tail = a->zero_tail;
   return FPS_OK;
 }

@@ -379,3 +379,85 @@ def test_tokens_to_attention():
     s = fps.packed_attention(summary, qk[:, H:].detach(), qkv[:, 2 * H:].detach(), one, kv_offsets=tok_off)
     want = attention(summary, qk[:, H:].detach(), qkv[:, 2 * H:].detach(), one, tok_off)
     assert_within(s, want["out"], "summary")
+
+
+@pytest.mark.parametrize("causal,window,sinks", [(False, -1, 0), (True, -1, 0), (True, 50, 4), (False, 300, 130), (False, 0, 1), (True, 20, 5000)])
+@pytest.mark.parametrize("D,dtype", [(64, BF16), (128, F16), (40, F16), (88, BF16)])
+def test_key_tiles_in_pieces(causal, window, sinks, D, dtype):
+    """Key tiles that so many queries of so many heads see that their work is
+    cut into pieces; beside them events whose tiles are whole, and none."""
+    nq, nk = [1500, 3, 0, 200, 1000], [1500, 40, 0, 200, 130]
+    q, k, v, dout, qo, ko = _inputs(nq, nk, 8, 2, D, dtype, 110)
+    _check(q, k, v, dout, qo, ko, causal=causal, window=window, sinks=sinks)
+    _check(q, k, v, dout, qo, ko, causal=causal, window=window, sinks=sinks, max_tokens=1500)
+
+
+@pytest.mark.parametrize("D,dtype", [(8, BF16), (24, F16), (56, BF16), (72, F16), (104, BF16), (128, F16)])
+@pytest.mark.parametrize("causal,window,sinks", [(False, -1, 0), (True, 700, 3), (False, 90, 600), (True, 0, 0)])
+def test_few_queries_of_long_events(D, dtype, causal, window, sinks):
+    """One to three queries of an event whose keys take several parts."""
+    nq, nk = [1, 2, 3, 1, 1, 0, 1], [3000, 1300, 511, 0, 64, 7, 1]
+    q, k, v, dout, qo, ko = _inputs(nq, nk, 8, 2, D, dtype, 120)
+    _check(q, k, v, dout, qo, ko, causal=causal, window=window, sinks=sinks)
+
+
+def test_few_queries_leave_other_rows():
+    """Output rows behind the last event stay, also where no tile kernel runs."""
+    q, k, v, dout, qo, ko = _inputs([1] * 5, [40, 0, 2000, 1, 300], 4, 4, 64, BF16, 130, tail=3)
+    want = attention(q, k, v, qo, ko)
+    out = torch.full_like(q, 7.0)
+    fps.attention_forward(q, k, v, qo, ko, out=out)
+    assert_within(out[:5], tuple(x[:5] for x in want["out"]), "out")
+    assert bool((out[5:] == 7.0).all())
+
+
+def test_gradient_of_a_broadcast():
+    """An output gradient without memory of its own, as sum() makes it."""
+    sizes = [150, 20]
+    q, k, v, _, qo, _ = _inputs(sizes, sizes, 4, 2, 64, BF16, 140)
+    leaves = [t.clone().requires_grad_() for t in (q, k, v)]
+    fps.packed_attention(*leaves, qo).sum().backward()
+    want = attention(q, k, v, qo, qo, dout=torch.ones_like(q))
+    for t, name in zip(leaves, ("dq", "dk", "dv")):
+        assert_within(t.grad, want[name], name)
+
+
+@pytest.mark.parametrize("D,dtype", [(64, BF16), (64, F16), (128, BF16), (40, F16)])
+@pytest.mark.parametrize("sizes", [[1] * 9, [200, 1, 300], [128] * 3])
+def test_queries_that_see_one_key(sizes, D, dtype):
+    """A query that sees one key moves nothing: its weight is 1 whatever the score.
+
+    dS = P (dP - D) is then what two float32 sums of D <= 128 products differ
+    by, and the weight's distance from 1: below 2^-16 of sum |dO V| (256
+    roundings of 2^-24) each.  dQ = scale dS K, and dK sums the group's; 2^-25
+    is half of fp16's smallest step.
+    """
+    q, k, v, dout, qo, _ = _inputs(sizes, sizes, 4, 2, D, dtype, 150)
+    out, lse = fps.attention_forward(q, k, v, qo, causal=True, window=0)
+    assert_within(out, attention(q, k, v, qo, qo, causal=True, window=0)["out"], "out")
+    dq, dk, dv = fps.attention_backward(dout, q, k, v, out, lse, qo, causal=True, window=0)
+    K, V = (t.repeat_interleave(2, 1).double() for t in (k, v))
+    dS = 2 * 2.0 ** -16 * (dout.double() * V).abs().sum(2, keepdim=True) * D ** -0.5
+    assert bool((dq.double().abs() <= dS * K.abs() + 2.0 ** -25).all())
+    limit = (dS * q.double().abs()).unflatten(1, (2, 2)).sum(2)
+    assert bool((dk.double().abs() <= limit + 2.0 ** -25).all())
+
+
+@pytest.mark.parametrize("causal,window,sinks", [(True, -1, 0), (True, 1, 0), (False, 1, 1), (True, 6, 3), (False, -1, 0)])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_gradient_error_of_short_rows(causal, window, sinks, D, dtype):
+    """Error of a whole gradient, in norms: that of rounding dS (or P) and then
+    the gradient, and little more.  Rounding normal values costs 0.432 half
+    steps, sqrt(E ulp(x)^2 / 12) / (eps / 2); two add in squares to 0.61, and
+    D from the rounded output at 17 keys or more adds 2 / 16 of one's square:
+    0.432 sqrt(2 + 1 / 8) = 0.63.  Above 0.65 something else is rounded.
+    """
+    sizes = [5, 2, 9, 300, 1, 40, 3] * 6 if window >= 0 or causal else [2, 3, 4, 5, 6] * 20
+    q, k, v, dout, qo, _ = _inputs(sizes, sizes, 4, 2, D, dtype, 160)
+    mask = dict(causal=causal, window=window, sinks=sinks)
+    got = fps.attention_backward(dout, q, k, v, *fps.attention_forward(q, k, v, qo, **mask), qo, **mask)
+    want = attention(q, k, v, qo, qo, dout=dout, **mask)
+    for g, name in zip(got, ("dq", "dk", "dv")):
+        w = want[name][0]
+        assert float((g.double() - w).norm() / w.norm()) <= torch.finfo(dtype).eps / 2 * 0.65, name
