@@ -33,8 +33,16 @@
 // of an SM's TMEM: one block with eight softmax warps has it all.  For 64-wide
 // heads they are 64 rows, and two blocks share an SM, each with four softmax
 // warps and 256 columns: where events are a few tiles long one block's loads
-// and stores then run under the other's products.  Where two sets of
+// and stores then run under the other's products (2048 events of up to 256
+// tokens, 8 heads of 64: 1741 us, with tiles and blocks as for 128: 2084).  Where two sets of
 // accumulators fit, a block goes on with the next item while it stores one.
+//
+// What bounds it: the softmax side.  4 causal events of 4000 to 9000 tokens, 16
+// query and 4 key heads of 128: 2.4 ms, 680 TFLOP/s of five products (seven are
+// done), where the products would take 1.0 ms; the two kernels form each weight
+// twice and each holds a thread's 64 scores in registers between TMEM reads and
+// writes.  Short items add the latency of filling the pipeline: 2048 events of up
+// to 256 tokens, 8 heads of 64: 1.79 ms, 2.0 TB/s.
 //
 // Rounding: P and dS are rounded to the input type for their products.  D
 // comes from the rounded output, as the forward left it, but for queries that

@@ -9,10 +9,22 @@
 // A block is six warps: one thread loads Q, K and V tiles with TMA, one issues
 // the tcgen05 products, and four warps do the softmax with one query row (a
 // TMEM lane) per thread, its scores in registers, so that no row crosses
-// threads.  S goes to TMEM, P comes back over it as 16-bit operand A of the
-// second product, O stays in TMEM until the item ends.  Two blocks share an
-// SM: while one's softmax runs, the other's products do.  Blocks are
-// persistent; the loader runs ahead into the next items.
+// threads.  S goes to TMEM, P comes back as 16-bit operand A of the second
+// product (64-wide heads: beside S, so that the next scores need not wait for
+// it; 128-wide: over S, the columns being taken), O stays in TMEM until the
+// item ends.  Two blocks share an SM: while one's softmax runs, the other's
+// products do.  Blocks are persistent; the loader runs ahead into the next
+// items.  Only the 32-key chunks that some of a warp's rows do not see whole
+// pay for masks, so one kernel serves every mask (a second one for calls
+// without any took 514 us where this takes 496).
+//
+// What bounds it: events of a tile or two, memory - 4096 events of up to 128
+// tokens, 12 heads of 64: 496 us, 5.5 TB/s; long events, the softmax - 4 causal
+// events of 4000 to 9000 tokens, 16 query and 4 key heads of 128: 681 us, 958
+// TFLOP/s, where the products alone would take 392 us at the rate of a library's
+// large product and the exponentials 280 us; 8 events of 50000 to 200000 tokens
+// under a window of 128 on both sides: 1750 us, of whose scores (three key tiles
+// for each query tile) a third is masked.
 //
 // Rounding: P is rounded to the input type for P V; l sums the unrounded
 // values.  O is rescaled only when m grows by more than 8 / log2 units, which
@@ -61,7 +73,6 @@ struct FwdItem {
   KeyTiles<kTile> keys;
 };
 constexpr int kItemRing = 2;
-template <bool kMasked>
 __device__ __forceinline__ FwdItem fwd_item(const FwdArgs& a, int h, const TileItem& e) {
   FwdItem w;
   w.h = h;
@@ -70,8 +81,7 @@ __device__ __forceinline__ FwdItem fwd_item(const FwdArgs& a, int h, const TileI
   w.p0 = e.t * kTile + e.nk - e.nq;
   w.k_row = e.k0;
   w.nk = e.nk;
-  w.keys = kMasked ? key_tiles<kTile>(a.mask, w.p0, w.p0 + w.rows - 1, e.nk)
-                   : KeyTiles<kTile>{0, 0, e.nk, 0, (e.nk + kTile - 1) / kTile};
+  w.keys = key_tiles<kTile>(a.mask, w.p0, w.p0 + w.rows - 1, e.nk);
   w.count = w.keys.count;
   return w;
 }
@@ -89,8 +99,7 @@ struct FwdShape {
       1024 + 3 * kStages * kTileBytes + kItemRing * sizeof(FwdItem) + 256;
 };
 
-// kMasked: a causal or windowed call; without, every query sees its whole event.
-template <typename T, int DP, bool kMasked>
+template <typename T, int DP>
 __global__ void __launch_bounds__(kFwdThreads, 2)
     k_attn_forward(const FwdArgs a, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                    const __grid_constant__ CUtensorMap map_v) {
@@ -146,7 +155,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
           mbar_arrive_one(item_full + 8 * slot);
           break;
         }
-        const FwdItem w = fwd_item<kMasked>(a, h, entry);
+        const FwdItem w = fwd_item(a, h, entry);
         if (lane == 0) s_item[slot] = w;
         __syncwarp();
         mbar_arrive_one(item_full + 8 * slot);
@@ -276,12 +285,9 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
         // warp sees, and of which all its rows see every key
         constexpr int kChunks = kTile / 32;
         const int pa = w.p0 + warp * 32;
-        bool some = 32 * lane < extent && warp_rows > 0, all = 32 * lane + 32 <= extent;
-        if constexpr (kMasked) {
-          const int pb = pa + warp_rows - 1, key = k0 + 32 * lane;
-          some = some && some_seen(a.mask, pa, pb, key);
-          all = all && all_seen(a.mask, pa, pb, key);
-        }
+        const int pb = pa + warp_rows - 1, key = k0 + 32 * lane;
+        const bool some = 32 * lane < extent && warp_rows > 0 && some_seen(a.mask, pa, pb, key);
+        const bool all = 32 * lane + 32 <= extent && all_seen(a.mask, pa, pb, key);
         const uint32_t act = __ballot_sync(kFull, some && lane < kChunks), whole = __ballot_sync(kFull, all);
         if (!(ok = mbar_wait(s_full, n & 1, s_abort))) break;
         tc_fence_after();
@@ -305,8 +311,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
 #pragma unroll
           for (int c = 0; c < kChunks; ++c)
             if (act >> c & ~whole >> c & 1) {  // what this row sees of it
-              uint32_t see = bits(0, extent - 32 * c);
-              if constexpr (kMasked) see &= seen_keys(a.mask, pa + lane, k0 + 32 * c);
+              const uint32_t see = bits(0, extent - 32 * c) & seen_keys(a.mask, pa + lane, k0 + 32 * c);
 #pragma unroll
               for (int k = 0; k < 32; ++k)
                 if (!(see >> k & 1)) s[32 * c + k] = -INFINITY;
@@ -389,10 +394,10 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
       if (!(ok = mbar_wait(o_full, nq & 1, s_abort))) break;
       ++nq;
       tc_fence_after();
-      // O / l.  Where no row saw a key O may hold
-      // what masked infinities left, so those rows are cleared, not scaled.
+      // O / l.  Where a row saw no key O may hold what masked infinities left, so
+      // such rows are cleared, not scaled.
       const bool live = lane < warp_rows;
-      if (__any_sync(kFull, l == 0.f) && kMasked) {
+      if (__any_sync(kFull, l == 0.f)) {
 #pragma unroll 1
         for (int c = 0; c < DP; c += 8) {
           uint32_t o[8];
@@ -421,7 +426,9 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
 }
 
 // Whether a call looks for events with at most kFewRows query rows: when its
-// events have no more than that on average.
+// events have no more than that on average.  One query for each of 8 events of
+// 50000 to 200000 tokens, 12 and 4 heads of 64: 206 us, and 2503 us in tiles of
+// 128 queries by this kernel; one event of 128 tokens takes 14 us either way.
 bool few_rows(const AttnCall& c) { return c.B > 0 && c.n_q * c.group <= (int64_t)kFewRows * c.B; }
 
 struct FwdWorkspace {
@@ -454,7 +461,7 @@ FwdWorkspace carve_forward(void* base, const AttnCall& c) {
   return w;
 }
 
-template <typename T, int DP, bool kMasked>
+template <typename T, int DP>
 cudaError_t run_forward(const AttnCall& c, const FwdWorkspace& ws, cudaStream_t s) {
   cudaError_t e;
   const bool bf16 = std::is_same<T, __nv_bfloat16>::value;
@@ -480,7 +487,7 @@ cudaError_t run_forward(const AttnCall& c, const FwdWorkspace& ws, cudaStream_t 
   a.sectors = reinterpret_cast<uintptr_t>(c.out) % 32 == 0 && c.D % 16 == 0;
   a.items = ws.items;
   a.hdr = ws.hdr;
-  const auto kernel = k_attn_forward<T, DP, kMasked>;
+  const auto kernel = k_attn_forward<T, DP>;
   constexpr int smem = (int)FwdShape<DP>::kSmem;
   e = allow_shared_memory(reinterpret_cast<const void*>(kernel), smem);
   if (e != cudaSuccess) return e;
@@ -502,9 +509,7 @@ cudaError_t run_forward(const AttnCall& c, const FwdWorkspace& ws, cudaStream_t 
 
 template <typename T>
 cudaError_t run_type(const AttnCall& c, const FwdWorkspace& ws, cudaStream_t s) {
-  if (c.mask.causal || c.mask.left < kFar)
-    return c.D <= 64 ? run_forward<T, 64, true>(c, ws, s) : run_forward<T, 128, true>(c, ws, s);
-  return c.D <= 64 ? run_forward<T, 64, false>(c, ws, s) : run_forward<T, 128, false>(c, ws, s);
+  return c.D <= 64 ? run_forward<T, 64>(c, ws, s) : run_forward<T, 128>(c, ws, s);
 }
 
 }  // namespace

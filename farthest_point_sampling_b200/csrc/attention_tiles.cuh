@@ -231,7 +231,8 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 // One row's kCols float32 accumulator columns from TMEM to memory, times f,
 // rounded: whole 32-byte sectors per thread where rows start on them, else 16
-// bytes.  Rows past the tile's read TMEM like the others (a warp reads as
+// bytes (sectors took the forward over 4096 events of up to 128 tokens, 12 heads
+// of 64, from 682 to 642 us, the backward over 2048 from 1281 to 1100).  Rows past the tile's read TMEM like the others (a warp reads as
 // one) and store nothing; columns from D on are not part of the row.
 template <typename T, int kCols>
 __device__ __forceinline__ void store_row(uint32_t acc, bool live, float f, T* to, int cols, bool sectors) {
