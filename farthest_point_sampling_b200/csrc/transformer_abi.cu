@@ -22,6 +22,7 @@ int check_attention_sizes(const fps_attention_args* a) {
   if (a->dtype != FPS_DTYPE_BF16 && a->dtype != FPS_DTYPE_F16) return FPS_ERR_ARG;
   if (a->heads < 1 || a->kv_heads < 1 || a->heads % a->kv_heads || a->head_dim < 8 || a->head_dim % 8)
     return FPS_ERR_ARG;
+  if ((a->causal != 0 && a->causal != 1) || a->window < -1 || a->sinks < 0) return FPS_ERR_ARG;
   if (a->n_q < 0 || a->n_kv < 0 || a->events < 0 || a->max_tokens < 0) return FPS_ERR_ARG;
   if (a->head_dim > FPS_MAX_ATTENTION_DIM || a->heads > 65535 || a->n_q >= kMaxRows || a->n_kv >= kMaxRows)
     return FPS_ERR_TOO_LARGE;
@@ -60,7 +61,6 @@ int make_call(const fps_attention_args* a, AttnCall* c) {
   const int rc = make_sizes(a, c);
   if (rc) return rc;
   if (!(a->scale > 0.f) || !std::isfinite(a->scale)) return FPS_ERR_ARG;
-  if ((a->causal != 0 && a->causal != 1) || a->window < -1 || a->sinks < 0) return FPS_ERR_ARG;
   if (a->events > 0 && (!a->q_offsets || !a->kv_offsets)) return FPS_ERR_ARG;
   if (a->n_q > 0 && (!a->q || !aligned(a->q, 16) || !row_strides_ok(a->q_token_stride, a->q_head_stride)))
     return FPS_ERR_ARG;

@@ -404,8 +404,8 @@ int fps_rotary(const void *x, void *y, int dtype, int64_t T, int H, int D, int64
  * values of a head contiguous, the other strides in elements.  D is a multiple
  * of 8, at most FPS_MAX_ATTENTION_DIM; pointers are 16-byte aligned and
  * strides positive multiples of 8 elements.  out [n_q, heads, D] and the
- * gradients (like q, k, v) are contiguous and 16-byte aligned.  lse float32
- * [heads, n_q]: log of the softmax sum, natural logarithm.
+ * gradients (like q, k, v) are contiguous and 16-byte aligned, and overlap no
+ * input.  lse float32 [heads, n_q]: log of the softmax sum, natural logarithm.
  *
  * Scores, the running maximum and sum, outputs and gradients accumulate in
  * float32; softmax weights and score gradients are rounded to `dtype` for
@@ -436,7 +436,8 @@ typedef struct fps_attention_args {
     int zero_tail;
 } fps_attention_args;
 
-/* Workspace bytes of the two calls below for these sizes (pointers are not read). */
+/* Workspace bytes of the two calls below for these sizes and this mask
+ * (pointers and scale are not read); 0 where they would be refused. */
 size_t fps_attention_workspace_bytes(const fps_attention_args *args, int backward);
 /* lse may be NULL when no gradient follows. */
 int fps_attention(const fps_attention_args *args, void *out, float *lse, void *workspace, size_t workspace_bytes,

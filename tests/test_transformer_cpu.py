@@ -117,3 +117,22 @@ def test_binding_refusals():
                  lambda: fps.attention_backward(h, h, h, h, h, torch.zeros((2, 3)), off)):
         with pytest.raises(ValueError, match="CUDA"):
             call()
+
+
+def test_workspace_of_long_and_refused_calls():
+    """Long events keep float32 sums of key-tile pieces; their room stays bounded."""
+    lib = fps.load_library()
+
+    def size(**kw):
+        return lib.fps_attention_workspace_bytes(ctypes.byref(_args(**kw)), 1)
+
+    for kw in (dict(causal=2), dict(window=-2), dict(sinks=-1), dict(window=5, sinks=-(1 << 40))):
+        assert size(**kw) == 0 and lib.fps_attention_workspace_bytes(ctypes.byref(_args(**kw)), 0) == 0
+    big = dict(heads=8, kv_heads=2, head_dim=128, n_q=1 << 20, n_kv=1 << 20)
+    for events in (1, 64, 1 << 20):
+        # -lse and -D; lists of n / 128 + events tiles of queries and as many of keys, and of the events
+        lists = 8 * (1 << 20) * 2 * 4 + 32 * (2 * (1 << 13) + 3 * events)
+        for mask in (dict(), dict(causal=1), dict(window=0, sinks=1), dict(window=511, sinks=1 << 30, causal=1), dict(window=1 << 40)):
+            # at most 4 pieces for each of 148 blocks and a few more, 128 x 256 floats each
+            got = size(events=events, **big, **mask)
+            assert lists <= got <= lists + (4 * 148 + 8) * (128 * 256 * 4 + 64) + (1 << 16), (events, mask)
