@@ -7,7 +7,7 @@
 // and q, k, v, out and dout are read once and the gradients written once: with
 // 64-wide heads and 128 tokens that traffic, 8 tensors of it, bounds the
 // kernel, not the products.  2048 events of up to 128 tokens, 12 heads of 64:
-// 767 us, 3.5 TB/s; the same events through the kernels of attention_backward.cu
+// 759 us, 3.6 TB/s; the same events through the kernels of attention_backward.cu
 // 982 us.  What is left is latency: a unit's phases wait for one another.
 //
 // A work item is an event and a key head, with a unit for each query head of
