@@ -21,6 +21,8 @@ struct AttnMask {
 };
 constexpr int kFar = 1 << 29;
 
+constexpr int kDevWaitTimeout = FPS_DEV_WAIT_TIMEOUT;
+
 struct AttnCall {
   const void* q;
   const void* k;

@@ -45,4 +45,8 @@ cudaError_t launch_attention_plan(const AttnCall& c, WsHeader* hdr, const PlanLi
 bool attention_map(CUtensorMap* map, const void* base, bool bf16, int64_t rows, int heads, int D, int64_t token_stride,
                    int64_t head_stride);
 
+// Dynamic shared memory of a kernel above the default limit: set on its first
+// launch on each device.
+cudaError_t allow_shared_memory(const void* kernel, int bytes);
+
 }  // namespace fpstok

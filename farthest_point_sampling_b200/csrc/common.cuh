@@ -32,7 +32,6 @@ constexpr int kDevBadStart = 2;
 constexpr int kDevBadToken = 3;
 constexpr int kDevTooLarge = 4;
 constexpr int kDevExchangeTimeout = 5;
-constexpr int kDevWaitTimeout = 6;
 
 // Workspace header: status word, detail word, work-list sizes and the
 // cursors the persistent kernels take items from (all reset by the binning

@@ -154,10 +154,6 @@ struct DeviceInfo {
 const DeviceInfo& device_info();  // prepares the current device on first use
 cudaError_t prepare_aux_kernels();   // shared-memory attributes of the auxiliary kernels
 
-// Dynamic shared memory of a kernel above the default limit: set on its first
-// launch on each device.
-cudaError_t allow_shared_memory(const void* kernel, int bytes);
-
 void count_launch(int n = 1);
 
 // Chunk pipeline of the host-buffer entry point: offsets[i] -= base, and

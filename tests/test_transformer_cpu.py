@@ -136,3 +136,18 @@ def test_workspace_of_long_and_refused_calls():
             # at most 4 pieces for each of 148 blocks and a few more, 128 x 256 floats each
             got = size(events=events, **big, **mask)
             assert lists <= got <= lists + (4 * 148 + 8) * (128 * 256 * 4 + 64) + (1 << 16), (events, mask)
+
+
+def test_recorded_traffic_is_of_these_sources():
+    """The measured DRAM bytes of the sampling kernels stay those of the sources that are here."""
+    import os
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    sys.path.insert(0, root)
+    try:
+        import bench
+    finally:
+        sys.path.remove(root)
+    with open(os.path.join(root, "profiles", "traffic.md")) as fh:
+        assert bench.kernel_source_hash() in fh.read()
