@@ -225,7 +225,9 @@ __global__ void __launch_bounds__(kFewThreads, FewShape<DP>::kBlocks) k_attn_few
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
         const float2 ml = w_ml[w * kFewRows + r];
-        if (ml.x == -INFINITY) continue;  // nothing seen: what its output holds is not a number to add
+        // nothing seen: what its output holds is not a number to add.  Scores that
+        // are all NaN leave the maximum at -inf too, and a sum of NaN, which goes on.
+        if (ml.x == -INFINITY && ml.y == 0.f) continue;
         const float f = exp2_approx((ml.x - top) * a.scale_log2);
         const float4 x = *reinterpret_cast<const float4*>(w_o + (w * kFewRows + r) * DP + c);
         sum = fmaf(ml.y, f, sum);
@@ -259,9 +261,10 @@ __global__ void __launch_bounds__(kFewThreads, FewShape<DP>::kBlocks) k_attn_few
   if (a.zero_tail) zero_rows(a.out, a.B > 0 ? a.q_offsets[a.B] : 0, a.n_q, (int64_t)a.heads * a.D);
 }
 
-// Joins the chunks of one event and head: sum_c 2^(m_c - M) (l_c, O_c).  The
-// threads of a column take every eighth (or fourth) chunk, and their sums are
-// added in order.
+// Joins the chunks of one event and head: sum_c 2^(m_c - M) (l_c, O_c); a
+// chunk that saw nothing has l = 0 and O = 0, one that saw only NaN has a l of
+// NaN, which 0 times it stays.  The threads of a column take every eighth (or
+// fourth) chunk, and their sums are added in order.
 template <typename T, int DP>
 __global__ void __launch_bounds__(kFewThreads) k_attn_join(const FewArgs a) {
   constexpr int kColumns = DP / 4, kParts = kFewThreads / kColumns;
