@@ -747,7 +747,9 @@ def packed_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, tok_offs
     j when ``(|p - j| <= window, or window is -1, or j < sinks) and (j <= p if
     causal)``; a query that sees none returns 0.  ``scale`` defaults to
     ``D ** -0.5``.  ``max_tokens``: an upper bound on the tokens of an event
-    (e.g. the K of the tokenizer), 0 when unknown; it selects kernels.
+    (e.g. the K of the tokenizer), 0 when unknown; it selects kernels, and an
+    event above it gets rows of NaN, in the gradients too, as do all events
+    from the thousand on in which the offsets go wrong.
     Returns ``[n_q, H, D]``; rows behind the last event are 0."""
     a, dev = _attention_args(q, k, v, tok_offsets, kv_offsets, scale, causal, window, sinks, max_tokens)
     if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad):

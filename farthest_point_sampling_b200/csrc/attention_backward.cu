@@ -831,6 +831,8 @@ cudaError_t launch_attention_backward(const AttnCall& c, void* workspace, cudaSt
   lists.queries = ws.queries;
   lists.keys = ws.keys;
   lists.shorts = ws.shorts;
+  lists.of_queries = {{c.dq, nullptr}, (int64_t)c.heads * c.D, nullptr, 0};
+  lists.of_keys = {{c.dk, c.dv}, (int64_t)c.kv_heads * c.D, nullptr, 0};
   lists.piece = ws.pieces.piece;
   lists.slots = ws.pieces.slots;
   lists.stream = c.D <= 64 ? 64 : 128;

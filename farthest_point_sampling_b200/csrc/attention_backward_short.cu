@@ -399,9 +399,11 @@ __global__ void __launch_bounds__(kShortThreads, kTwo ? 2 : 1)
       ++n;
     }
   }
-  zero_rows(a.dq, a.B > 0 ? a.q_offsets[a.B] : 0, a.n_q, (int64_t)a.heads * a.D);
-  zero_rows(a.dk, a.B > 0 ? a.kv_offsets[a.B] : 0, a.n_kv, (int64_t)a.kv_heads * a.D);
-  zero_rows(a.dv, a.B > 0 ? a.kv_offsets[a.B] : 0, a.n_kv, (int64_t)a.kv_heads * a.D);
+  if (rows_known(a.hdr)) {
+    zero_rows(a.dq, a.B > 0 ? a.q_offsets[a.B] : 0, a.n_q, (int64_t)a.heads * a.D);
+    zero_rows(a.dk, a.B > 0 ? a.kv_offsets[a.B] : 0, a.n_kv, (int64_t)a.kv_heads * a.D);
+    zero_rows(a.dv, a.B > 0 ? a.kv_offsets[a.B] : 0, a.n_kv, (int64_t)a.kv_heads * a.D);
+  }
   tc_fence_before();
   __syncthreads();
   if (warp == kMmaWarp) {

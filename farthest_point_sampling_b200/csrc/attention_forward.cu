@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
       if (lse && live) lse[lane] = l == 0.f ? -INFINITY : fmaf(m_used, a.scale, log2_approx(l) * kLn2);
     }
   }
-  if (a.zero_tail) zero_rows(a.out, a.B > 0 ? a.q_offsets[a.B] : 0, a.n_q, (int64_t)a.heads * a.D);
+  if (a.zero_tail && rows_known(a.hdr)) zero_rows(a.out, a.B > 0 ? a.q_offsets[a.B] : 0, a.n_q, (int64_t)a.heads * a.D);
   tc_fence_before();
   __syncthreads();
   if (warp == kSoftmaxWarps + 1) {
@@ -520,6 +520,7 @@ cudaError_t launch_attention_forward(const AttnCall& c, void* workspace, cudaStr
   const FwdWorkspace ws = carve_forward(workspace, c);
   PlanLists lists = {};
   lists.queries = ws.items;
+  lists.of_queries = {{c.out, nullptr}, (int64_t)c.heads * c.D, c.lse, c.heads};
   if (few_rows(c)) {
     lists.units = ws.units;
     lists.joins = ws.joins;

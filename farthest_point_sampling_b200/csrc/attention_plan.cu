@@ -60,6 +60,43 @@ __device__ __forceinline__ void block_sort(uint64_t* s, int count) {
   __syncthreads();
 }
 
+// NaN in `count` rows from `first` on, by threads `thread` of `threads`.
+__device__ __forceinline__ void void_rows(const PlanRows& w, int64_t n, int64_t first, int64_t count, int thread,
+                                          int threads) {
+  const uint32_t nan2 = 0x7fff7fffu;  // two 16-bit NaN, of either type
+  for (int x = 0; x < 2; ++x) {
+    if (!w.rows[x]) continue;
+    uint4* p = reinterpret_cast<uint4*>(static_cast<char*>(w.rows[x]) + first * w.values * 2);
+    for (int64_t e = thread; e < count * w.values / 8; e += threads) p[e] = make_uint4(nan2, nan2, nan2, nan2);
+  }
+  if (w.lse)
+    for (int h = 0; h < w.heads; ++h)
+      for (int64_t e = thread; e < count; e += threads) w.lse[(int64_t)h * n + first + e] = __uint_as_float(0x7fffffffu);
+}
+
+// The rows (of `off`, n in all) of the events above max_tokens among the first
+// `taken`, a warp each, and of all events from there on.  By the whole block,
+// and only where there are such: a call that is wrong need not be fast.
+__device__ __forceinline__ void void_events(const PlanRows& w, const int64_t* off, const int64_t* q_off, const int64_t* k_off,
+                                         int taken, int B, int64_t n, int max_tokens) {
+  const int lane = threadIdx.x & 31;
+  for (int b0 = 0; b0 < taken; b0 += kPlanThreads) {
+    const int b = b0 + threadIdx.x;
+    const bool above = b < taken && max_tokens > 0 &&
+                       (q_off[b + 1] - q_off[b] > max_tokens || k_off[b + 1] - k_off[b] > max_tokens);
+    uint32_t left = __ballot_sync(kFull, above);
+    while (left) {
+      const int64_t first = off[b - lane + __ffs(left) - 1], end = off[b - lane + __ffs(left)];
+      void_rows(w, n, first, end - first, lane, 32);
+      left &= left - 1;
+    }
+  }
+  if (taken < B) {
+    const int64_t first = taken > 0 ? off[taken] : 0;  // the end of an event that was taken
+    void_rows(w, n, first, n - first, threadIdx.x, kPlanThreads);
+  }
+}
+
 enum PlanList { kPlanQueries, kPlanKeys, kPlanUnits, kPlanShorts };
 
 // One block per list.  A pass takes 1024 events, one per thread: their items
@@ -82,7 +119,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const int64_t* __res
                     : kind == kPlanKeys  ? lists.keys
                     : kind == kPlanUnits ? lists.units
                                          : lists.shorts;
-  int base = 0, slots = 0, joins = 0, error = 0;
+  int base = 0, slots = 0, joins = 0, error = 0, taken = B;
   if (tid == 0 && B > 0 && (q_off[0] != 0 || k_off[0] != 0)) error = kDevBadOffsets;
   for (int b0 = 0; b0 < B; b0 += kPlanThreads) {
     const int b = b0 + tid;
@@ -115,7 +152,10 @@ __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const int64_t* __res
     }
     // A pass with bad offsets makes no items and ends the list: up to there
     // offsets rise, which is what bounds the items of a list by its buffer.
-    if (__syncthreads_or(error == kDevBadOffsets)) break;
+    if (__syncthreads_or(error == kDevBadOffsets)) {
+      taken = b0;
+      break;
+    }
     // Long events first, so that the blocks that claim items in turn end
     // together; where no event has more than four tiles order matters little.
     if (kind <= kPlanKeys && __syncthreads_or(n > 4)) {
@@ -204,6 +244,8 @@ __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const int64_t* __res
     __syncthreads();
   }
   error = __syncthreads_or(error == kDevBadOffsets) ? kDevBadOffsets : __syncthreads_or(error) ? kDevTooLarge : 0;
+  if (error && kind == kPlanQueries) void_events(lists.of_queries, q_off, q_off, k_off, taken, B, n_q, max_tokens);
+  if (error && kind == kPlanKeys) void_events(lists.of_keys, k_off, q_off, k_off, taken, B, n_kv, max_tokens);
   if (tid == 0) {
     const int list = kind == kPlanQueries ? kQueryTiles
                      : kind == kPlanKeys  ? kKeyTiles

@@ -19,6 +19,15 @@ constexpr int kFewJoins = 3;
 constexpr int kShortEvents = 4;
 constexpr int kKeySlots = 5;
 
+// 16-bit rows that a call writes for its queries or its keys: up to two
+// tensors of `values` a row (a multiple of 8), and a float for each of `heads`.
+struct PlanRows {
+  void* rows[2];
+  int64_t values;
+  float* lse;
+  int heads;
+};
+
 // The lists of one call; those that are NULL are not made.
 struct PlanLists {
   TileItem* queries;  // tiles of 128 queries
@@ -33,11 +42,14 @@ struct PlanLists {
   int piece, stream, slots;
   JoinItem* key_joins;  // per slot: at a tile's first one its rows and how many, else none
   TileItem* shorts;   // the events of at most 128 queries and 128 keys, which then have no tiles of either kind
+  PlanRows of_queries, of_keys;  // what the call writes
 };
 
-// Fills the lists in event order, their counts in hdr->n_items, and resets the
-// call's status words.  An event longer than max_tokens is recorded and is in
-// no list; inconsistent offsets are recorded and end the lists.
+// Fills the lists, 1024 events at a time and long ones of these first, their
+// counts in hdr->n_items, and resets the call's status words.  An event longer
+// than max_tokens is recorded and is in no list; inconsistent offsets are
+// recorded and end the lists before the 1024 events they are among.  What the
+// call would have written for the events in no list is set to NaN.
 cudaError_t launch_attention_plan(const AttnCall& c, WsHeader* hdr, const PlanLists& lists, cudaStream_t s);
 
 // Map of a [rows, heads, D] 16-bit tensor for boxes of 64 rows x one head x

@@ -318,6 +318,9 @@ __device__ __forceinline__ void clear_strided(T* base, int rows, int64_t stride,
       *reinterpret_cast<uint4*>(base + r * stride + c) = make_uint4(0, 0, 0, 0);
 }
 
+// Whether the offsets tell which rows lie behind the last event.
+__device__ __forceinline__ bool rows_known(const WsHeader* hdr) { return hdr->status != kDevBadOffsets; }
+
 // Rows [first, n) of a [n, row_values] 16-bit tensor to 0, over the whole grid.
 __device__ __forceinline__ void zero_rows(void* base, int64_t first, int64_t n, int64_t row_values) {
   if (first < 0 || first >= n) return;

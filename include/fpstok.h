@@ -416,6 +416,11 @@ int fps_rotary(const void *x, void *y, int dtype, int64_t T, int H, int D, int64
  * rows that belong to no event are set to 0.  Non-finite values of one event
  * do not reach another; within an event they may reach rows that do not see
  * them.
+ *
+ * Checked on the device (fps_device_status()): an event above max_tokens, whose
+ * rows of out, lse and the gradients become NaN, and offsets that do not start
+ * at 0, do not rise or pass the rows given.  Offsets are taken 1024 events at a
+ * time; from the first 1024 with a bad one on, every row to the end is NaN.
  */
 typedef struct fps_attention_args {
     const void *q, *k, *v;
@@ -432,7 +437,7 @@ typedef struct fps_attention_args {
     int64_t window; /* keys on each side, -1 = unlimited */
     int64_t sinks;  /* first keys of an event that every query may see, >= 0 */
     int max_tokens; /* upper bound on the queries and keys of any event, 0 = unknown; an event above it
-                       is reported by fps_device_status() and its rows are not valid */
+                       is reported by fps_device_status() and its rows become NaN */
     int zero_tail;
 } fps_attention_args;
 

@@ -1,0 +1,86 @@
+"""What a call gives that the device finds wrong: a status, and NaN in the rows
+it could not compute."""
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # pragma: no cover - the gpu marker is deselected on CPU hosts
+    pytest.skip("needs a CUDA device", allow_module_level=True)
+
+import farthest_point_sampling_b200 as fps  # noqa: E402
+
+BF16 = torch.bfloat16
+
+
+def _rand(shape, seed, dtype=BF16):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(shape, generator=g, device="cuda").to(dtype)
+
+
+def _off(sizes):
+    return torch.tensor([0] + torch.tensor(sizes, dtype=torch.int64).cumsum(0).tolist(), dtype=torch.int64, device="cuda")
+
+
+def _stale(*shapes):
+    """Memory of the outputs' sizes that holds numbers, given back to the allocator."""
+    for s in shapes:
+        t = torch.full(s, 3.0, dtype=BF16, device="cuda")
+        del t
+
+
+@pytest.mark.parametrize("dtype", [BF16, torch.float16])
+@pytest.mark.parametrize("nq,nk,hint", [([100, 300, 0, 20], [100, 300, 0, 20], 128), ([200, 90, 257, 3], [200, 90, 257, 3], 256),
+                                        ([1, 1, 1, 1], [64, 900, 128, 2], 128)])
+def test_rows_of_an_event_above_the_stated_longest_are_nan(nq, nk, hint, dtype):
+    """The other events' rows, and those behind the last event, are as without the hint."""
+    tail = 5
+    qo, ko = _off(nq), _off(nk)
+    q, dout = _rand((sum(nq) + tail, 4, 64), 1, dtype), _rand((sum(nq) + tail, 4, 64), 2, dtype)
+    k, v = _rand((sum(nk) + tail, 2, 64), 3, dtype), _rand((sum(nk) + tail, 2, 64), 4, dtype)
+    out0, lse0 = fps.attention_forward(q, k, v, qo, ko)
+    grads0 = fps.attention_backward(dout, q, k, v, out0, lse0, qo, ko)
+    _stale(q.shape, k.shape, k.shape, q.shape)
+    out, lse = fps.attention_forward(q, k, v, qo, ko, max_tokens=hint)
+    grads = fps.attention_backward(dout, q, k, v, out0, lse0, qo, ko, max_tokens=hint)
+    bad = [max(a, b) > hint for a, b in zip(nq, nk)]
+    q_bad = torch.tensor([x for x, n in zip(bad, nq) for _ in range(n)] + [False] * tail, device="cuda")
+    k_bad = torch.tensor([x for x, n in zip(bad, nk) for _ in range(n)] + [False] * tail, device="cuda")
+    for got, want, rows in ((out, out0, q_bad), (grads[0], grads0[0], q_bad), (grads[1], grads0[1], k_bad), (grads[2], grads0[2], k_bad)):
+        assert bool(got[rows].isnan().all())
+        assert torch.allclose(got[~rows].float(), want[~rows].float(), rtol=2 * torch.finfo(dtype).eps, atol=1e-5)
+    assert bool(lse[:, q_bad].isnan().all())
+    given = torch.full_like(q, 7.0)
+    fps.attention_forward(q, k, v, qo, ko, max_tokens=hint, out=given)
+    assert bool(given[q_bad].isnan().all()) and bool((given[-tail:] == 7.0).all())
+
+
+@pytest.mark.parametrize("queries", [0, 1])
+def test_rows_after_offsets_that_do_not_rise_are_nan(queries):
+    """Offsets are taken 1024 events at a time; those of an earlier thousand count."""
+    B = 2100
+    ko = _off([3] * B)
+    ko[1500] = 0
+    ko[B] = 0
+    qo = _off([queries] * B) if queries else ko
+    n = 3 * B
+    n_q = queries * B or n
+    q, k, v = _rand((n_q, 2, 64), 5), _rand((n, 2, 64), 6), _rand((n, 2, 64), 7)
+    good_k = _off([3] * B)
+    good_q = _off([queries] * B) if queries else good_k
+    want, _ = fps.attention_forward(q, k, v, good_q, good_k)
+    ws = torch.zeros(1 << 24, dtype=torch.uint8, device="cuda")
+    _stale(q.shape)
+    out, lse = fps.attention_forward(q, k, v, qo, ko, workspace=ws)
+    with pytest.raises(fps.FpsError) as err:
+        fps.device_status(ws)
+    assert err.value.detail == 1
+    done = 1024 * (queries or 3)
+    assert torch.equal(out[:done], want[:done])
+    assert bool(out[done:].isnan().all()) and bool(lse[:, done:].isnan().all())
+    dout = _rand(q.shape, 8)
+    good = fps.attention_backward(dout, q, k, v, want, torch.zeros_like(lse), good_q, good_k)
+    _stale(q.shape, k.shape, k.shape)
+    got = fps.attention_backward(dout, q, k, v, want, torch.zeros_like(lse), qo, ko, workspace=ws)
+    for g, w, at in zip(got, good, (done, 3 * 1024, 3 * 1024)):
+        assert torch.equal(g[:at], w[:at]) and bool(g[at:].isnan().all())
