@@ -676,6 +676,12 @@ def attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, tok_off
     return _attention_forward(a, dev, q, need_lse, workspace, out)
 
 
+def _attention_workspace(nbytes: int, dev: torch.device, workspace: Optional[torch.Tensor]) -> torch.Tensor:
+    if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
+        raise ValueError(f"workspace must be contiguous and on {dev}")
+    return _workspace(nbytes, dev, workspace)
+
+
 def _attention_forward(a, dev, q, need_lse, workspace, out):
     if out is None:
         out = torch.empty_like(q) if q.is_contiguous() else torch.empty(q.shape, dtype=q.dtype, device=dev)
@@ -687,7 +693,7 @@ def _attention_forward(a, dev, q, need_lse, workspace, out):
     lib = _lib.load()
     lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=dev) if need_lse else None
     ref = ctypes.byref(a)
-    ws = _workspace(lib.fps_attention_workspace_bytes(ref, 0), dev, workspace)
+    ws = _attention_workspace(lib.fps_attention_workspace_bytes(ref, 0), dev, workspace)
     _call(lib.fps_attention, "fps_attention", dev, ref, out.data_ptr(), None if lse is None else lse.data_ptr(), ws.data_ptr(),
           ws.numel() * ws.element_size())
     return out, lse
@@ -711,7 +717,7 @@ def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: 
     dq, dk, dv = (torch.empty(t.shape, dtype=q.dtype, device=dev) for t in (q, k, v))
     lib = _lib.load()
     ref = ctypes.byref(a)
-    ws = _workspace(lib.fps_attention_workspace_bytes(ref, 1), dev, workspace)
+    ws = _attention_workspace(lib.fps_attention_workspace_bytes(ref, 1), dev, workspace)
     _call(lib.fps_attention_backward, "fps_attention_backward", dev, ref, out.data_ptr(), lse.data_ptr(), dout.data_ptr(), dt,
           dh, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
     return dq, dk, dv

@@ -1,0 +1,38 @@
+"""The binding of the packed-token operators, with the launch stood in for on
+the host: what it checks, and what it hands to the library and to autograd."""
+import pytest
+
+import farthest_point_sampling_b200 as fps
+from farthest_point_sampling_b200 import api
+
+torch = pytest.importorskip("torch")
+BF16 = torch.bfloat16
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """Host tensors pass for the device's; a call to the library is noted by name and goes no further."""
+    made = []
+    monkeypatch.setattr(api, "_cuda_device", lambda t: t.device)
+    monkeypatch.setattr(api, "_call", lambda fn, where, device, *args: made.append((where, args)))
+    return made
+
+
+def _qkv(n=6, H=2, G=1, D=16, **kw):
+    return [torch.zeros((n, h, D), dtype=BF16, **kw) for h in (H, G, G)], torch.tensor([0, 2, n])
+
+
+def test_workspace_of_another_device_or_without_memory(calls):
+    (q, k, v), off = _qkv()
+    need = 1 << 20
+    good = torch.empty(need, dtype=torch.uint8)
+    out, lse = fps.attention_forward(q, k, v, off, workspace=good)
+    fps.attention_backward(q, q, k, v, out, lse, off, workspace=good)
+    assert [c[0] for c in calls] == ["fps_attention", "fps_attention_backward"]
+    for bad in (torch.empty(need, dtype=torch.uint8, device="meta"), torch.empty(1, dtype=torch.uint8).expand(need),
+                torch.empty(2 * need, dtype=torch.uint8)[::2], torch.empty(16, dtype=torch.uint8)):
+        with pytest.raises(ValueError, match="workspace"):
+            fps.attention_forward(q, k, v, off, workspace=bad)
+        with pytest.raises(ValueError, match="workspace"):
+            fps.attention_backward(q, q, k, v, out, lse, off, workspace=bad)
+    assert len(calls) == 2
