@@ -667,13 +667,14 @@ def _attention_args(q, k, v, tok_offsets, kv_offsets, scale, causal, window, sin
 def attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, tok_offsets: torch.Tensor,
                       kv_offsets: Optional[torch.Tensor] = None, scale: Optional[float] = None, causal: bool = False,
                       window: int = -1, sinks: int = 0, max_tokens: int = 0, need_lse: bool = True,
-                      workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None):
+                      workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                      check_device: bool = False):
     """C ``fps_attention``: returns ``(out [n_q, H, D], lse [H, n_q])`` (lse
     None without ``need_lse``); see :func:`packed_attention`.  Rows of a given
     ``out`` that belong to no event are left as they were; in a new one they
     are 0."""
     a, dev = _attention_args(q, k, v, tok_offsets, kv_offsets, scale, causal, window, sinks, max_tokens)
-    return _attention_forward(a, dev, q, need_lse, workspace, out)
+    return _attention_forward(a, dev, q, need_lse, workspace, out, check_device)
 
 
 def _attention_workspace(nbytes: int, dev: torch.device, workspace: Optional[torch.Tensor]) -> torch.Tensor:
@@ -682,7 +683,7 @@ def _attention_workspace(nbytes: int, dev: torch.device, workspace: Optional[tor
     return _workspace(nbytes, dev, workspace)
 
 
-def _attention_forward(a, dev, q, need_lse, workspace, out):
+def _attention_forward(a, dev, q, need_lse, workspace, out, check_device):
     if out is None:
         out = torch.empty_like(q) if q.is_contiguous() else torch.empty(q.shape, dtype=q.dtype, device=dev)
         a.zero_tail = 1
@@ -696,13 +697,15 @@ def _attention_forward(a, dev, q, need_lse, workspace, out):
     ws = _attention_workspace(lib.fps_attention_workspace_bytes(ref, 0), dev, workspace)
     _call(lib.fps_attention, "fps_attention", dev, ref, out.data_ptr(), None if lse is None else lse.data_ptr(), ws.data_ptr(),
           ws.numel() * ws.element_size())
+    if check_device:
+        device_status(ws)
     return out, lse
 
 
 def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
                        lse: torch.Tensor, tok_offsets: torch.Tensor, kv_offsets: Optional[torch.Tensor] = None,
                        scale: Optional[float] = None, causal: bool = False, window: int = -1, sinks: int = 0,
-                       max_tokens: int = 0, workspace: Optional[torch.Tensor] = None):
+                       max_tokens: int = 0, workspace: Optional[torch.Tensor] = None, check_device: bool = False):
     """C ``fps_attention_backward``: ``(dq, dk, dv)`` given the forward's
     ``out`` and ``lse``.  Gradient rows that belong to no event are 0."""
     a, dev = _attention_args(q, k, v, tok_offsets, kv_offsets, scale, causal, window, sinks, max_tokens)
@@ -720,13 +723,15 @@ def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: 
     ws = _attention_workspace(lib.fps_attention_workspace_bytes(ref, 1), dev, workspace)
     _call(lib.fps_attention_backward, "fps_attention_backward", dev, ref, out.data_ptr(), lse.data_ptr(), dout.data_ptr(), dt,
           dh, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
+    if check_device:
+        device_status(ws)
     return dq, dk, dv
 
 
 class _PackedAttention(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, v, tok_offsets, kv_offsets, args, opts):
-        out, lse = _attention_forward(args, q.device, q, True, None, None)
+    def forward(ctx, q, k, v, tok_offsets, kv_offsets, args, opts, workspace):
+        out, lse = _attention_forward(args, q.device, q, True, workspace, None, opts["check_device"])
         ctx.save_for_backward(q, k, v, out, lse, tok_offsets, kv_offsets)
         ctx.opts = opts
         return out
@@ -736,12 +741,13 @@ class _PackedAttention(torch.autograd.Function):
     def backward(ctx, dout):
         q, k, v, out, lse, tok_offsets, kv_offsets = ctx.saved_tensors
         dq, dk, dv = attention_backward(_dense_heads(dout), q, k, v, out, lse, tok_offsets, kv_offsets, **ctx.opts)
-        return dq, dk, dv, None, None, None, None
+        return dq, dk, dv, None, None, None, None, None
 
 
 def packed_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, tok_offsets: torch.Tensor,
                      kv_offsets: Optional[torch.Tensor] = None, scale: Optional[float] = None, causal: bool = False,
-                     window: int = -1, sinks: int = 0, max_tokens: int = 0) -> torch.Tensor:
+                     window: int = -1, sinks: int = 0, max_tokens: int = 0, workspace: Optional[torch.Tensor] = None,
+                     check_device: bool = False) -> torch.Tensor:
     """Attention within each packed event (the layout of :func:`pack_tokens`),
     differentiable with respect to ``q``, ``k`` and ``v``.
 
@@ -755,13 +761,17 @@ def packed_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, tok_offs
     ``D ** -0.5``.  ``max_tokens``: an upper bound on the tokens of an event
     (e.g. the K of the tokenizer), 0 when unknown; it selects kernels, and an
     event above it gets rows of NaN, in the gradients too, as do all events
-    from the thousand on in which the offsets go wrong.
+    from the thousand on in which the offsets go wrong.  ``check_device=True``
+    synchronises and raises on either, and on a kernel that gave up waiting,
+    after the call and after its backward pass; without it,
+    :func:`device_status` of a ``workspace`` given here tells of the call (the
+    backward pass has one of its own).
     Returns ``[n_q, H, D]``; rows behind the last event are 0."""
     a, dev = _attention_args(q, k, v, tok_offsets, kv_offsets, scale, causal, window, sinks, max_tokens)
     if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad):
-        opts = dict(scale=scale, causal=causal, window=window, sinks=sinks, max_tokens=max_tokens)
-        return _PackedAttention.apply(q, k, v, tok_offsets, kv_offsets, a, opts)
-    return _attention_forward(a, dev, q, False, None, None)[0]
+        opts = dict(scale=scale, causal=causal, window=window, sinks=sinks, max_tokens=max_tokens, check_device=check_device)
+        return _PackedAttention.apply(q, k, v, tok_offsets, kv_offsets, a, opts, workspace)
+    return _attention_forward(a, dev, q, False, workspace, None, check_device)[0]
 
 
 def device_status(workspace: torch.Tensor) -> None:

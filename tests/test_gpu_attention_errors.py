@@ -84,3 +84,40 @@ def test_rows_after_offsets_that_do_not_rise_are_nan(queries):
     got = fps.attention_backward(dout, q, k, v, want, torch.zeros_like(lse), qo, ko, workspace=ws)
     for g, w, at in zip(got, good, (done, 3 * 1024, 3 * 1024)):
         assert torch.equal(g[:at], w[:at]) and bool(g[at:].isnan().all())
+
+
+@pytest.mark.parametrize("grad", [False, True])
+def test_the_public_call_reports(grad):
+    """With check_device the call raises what the device found; without it the status is in the given workspace."""
+    qo = _off([100, 129])
+    q, k, v = (_rand((229, 2, 64), 9 + i).requires_grad_(grad) for i in range(3))
+    assert bool(fps.packed_attention(q, k, v, qo, max_tokens=129, check_device=True).isfinite().all())
+    bad = _off([100, 129])
+    bad[1] = 300
+    for offsets, hint, reason in ((qo, 128, 4), (bad, 0, 1)):
+        with pytest.raises(fps.FpsError) as err:
+            fps.packed_attention(q, k, v, offsets, max_tokens=hint, check_device=True)
+        assert err.value.detail == reason
+        ws = torch.zeros(1 << 22, dtype=torch.uint8, device="cuda")
+        out = fps.packed_attention(q, k, v, offsets, max_tokens=hint, workspace=ws)
+        with pytest.raises(fps.FpsError) as err:
+            fps.device_status(ws)
+        assert err.value.detail == reason
+        assert bool(out[100:].isnan().all()) and bool(out[:100].isfinite().all()) == (reason == 4)
+
+
+def test_the_backward_pass_reports():
+    """Its own plan finds what has gone wrong with the offsets since."""
+    qo = _off([100, 129])
+    q, k, v = (_rand((229, 2, 64), 19 + i).requires_grad_() for i in range(3))
+    for check in (True, False):
+        off = qo.clone()
+        out = fps.packed_attention(q, k, v, off, check_device=check)
+        off.data[1] = 300  # behind autograd's back
+        if check:
+            with pytest.raises(fps.FpsError) as err:
+                out.sum().backward()
+            assert err.value.detail == 1
+        else:
+            out.sum().backward()
+            assert all(bool(t.grad.isnan().all()) for t in (q, k, v))

@@ -36,3 +36,18 @@ def test_workspace_of_another_device_or_without_memory(calls):
         with pytest.raises(ValueError, match="workspace"):
             fps.attention_backward(q, q, k, v, out, lse, off, workspace=bad)
     assert len(calls) == 2
+
+
+def test_check_device_reads_the_status_after_each_pass(calls, monkeypatch):
+    (q, k, v), off = _qkv(requires_grad=True)
+    monkeypatch.setattr(api, "device_status", lambda ws: calls.append(("status", ws)))
+    mine = torch.empty(1 << 20, dtype=torch.uint8)
+    out = fps.packed_attention(q, k, v, off, workspace=mine, check_device=True)
+    out.backward(torch.zeros_like(out))
+    assert [c[0] for c in calls] == ["fps_attention", "status", "fps_attention_backward", "status"]
+    assert calls[1][1] is mine and calls[3][1] is not mine
+    del calls[:]
+    with torch.no_grad():
+        fps.packed_attention(q, k, v, off, workspace=mine, check_device=True)
+        fps.packed_attention(q, k, v, off)
+    assert [c[0] for c in calls] == ["fps_attention", "status", "fps_attention"] and calls[1][1] is mine
