@@ -18,6 +18,7 @@ import ctypes
 from typing import Dict, Optional, Union
 
 import torch
+from torch.autograd.forward_ad import unpack_dual
 
 from . import _lib
 
@@ -672,7 +673,7 @@ def attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, tok_off
     """C ``fps_attention``: returns ``(out [n_q, H, D], lse [H, n_q])`` (lse
     None without ``need_lse``); see :func:`packed_attention`.  Rows of a given
     ``out`` that belong to no event are left as they were; in a new one they
-    are 0."""
+    are 0.  Not recorded by autograd."""
     a, dev = _attention_args(q, k, v, tok_offsets, kv_offsets, scale, causal, window, sinks, max_tokens)
     return _attention_forward(a, dev, q, need_lse, workspace, out, check_device)
 
@@ -768,7 +769,9 @@ def packed_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, tok_offs
     backward pass has one of its own).
     Returns ``[n_q, H, D]``; rows behind the last event are 0."""
     a, dev = _attention_args(q, k, v, tok_offsets, kv_offsets, scale, causal, window, sinks, max_tokens)
-    if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad):
+    # a forward-mode tangent, which the call would drop, is refused by apply()
+    tangent = unpack_dual(q).tangent is not None or unpack_dual(k).tangent is not None or unpack_dual(v).tangent is not None
+    if tangent or torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad):
         opts = dict(scale=scale, causal=causal, window=window, sinks=sinks, max_tokens=max_tokens, check_device=check_device)
         return _PackedAttention.apply(q, k, v, tok_offsets, kv_offsets, a, opts, workspace)
     return _attention_forward(a, dev, q, False, workspace, None, check_device)[0]

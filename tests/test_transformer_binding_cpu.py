@@ -51,3 +51,32 @@ def test_check_device_reads_the_status_after_each_pass(calls, monkeypatch):
         fps.packed_attention(q, k, v, off, workspace=mine, check_device=True)
         fps.packed_attention(q, k, v, off)
     assert [c[0] for c in calls] == ["fps_attention", "status", "fps_attention"] and calls[1][1] is mine
+
+
+@pytest.mark.parametrize("which", [0, 1, 2])
+def test_forward_mode_tangents_are_refused(calls, which):
+    """A dual tensor whose tangent the call would drop raises, with and without a gradient to come."""
+    import torch.autograd.forward_ad as fwad
+
+    for grad in (False, True):
+        t, off = _qkv(requires_grad=grad)
+        with fwad.dual_level():
+            t[which] = fwad.make_dual(t[which], torch.ones_like(t[which]))
+            with pytest.raises(NotImplementedError):
+                fps.packed_attention(*t, off)
+            with torch.no_grad(), pytest.raises(NotImplementedError):
+                fps.packed_attention(*t, off)
+            plain, off = _qkv()
+            assert fps.packed_attention(*plain, off).shape == plain[0].shape
+
+
+def test_forward_mode_tangents_of_rotary_are_refused(calls):
+    import torch.autograd.forward_ad as fwad
+
+    table = fps.RotaryTable((4, 4))
+    x, pos = torch.zeros((3, 2, 16)), torch.zeros((3, 2))
+    with fwad.dual_level():
+        with pytest.raises(NotImplementedError):
+            fps.apply_rotary(fwad.make_dual(x, torch.ones_like(x)), pos, table)
+        with pytest.raises(NotImplementedError):
+            fps.apply_rotary(x, fwad.make_dual(pos, torch.ones_like(pos)), table)
