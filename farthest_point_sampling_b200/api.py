@@ -623,7 +623,8 @@ def _dense_heads(t: torch.Tensor) -> torch.Tensor:
     """A gradient as autograd hands it over (any strides) with rows the kernels read."""
     ok = t.stride(2) == 1 and t.stride(1) >= t.shape[2] and t.stride(0) >= t.shape[2] and t.stride(1) % 8 == 0 and \
         t.stride(0) % 8 == 0 and t.data_ptr() % 16 == 0
-    return t if ok else t.contiguous()
+    # contiguous() would hand back a contiguous one that only starts off 16 bytes
+    return t if ok else t.clone(memory_format=torch.contiguous_format)
 
 
 def _attention_args(q, k, v, tok_offsets, kv_offsets, scale, causal, window, sinks, max_tokens):

@@ -80,3 +80,13 @@ def test_forward_mode_tangents_of_rotary_are_refused(calls):
             fps.apply_rotary(fwad.make_dual(x, torch.ones_like(x)), pos, table)
         with pytest.raises(NotImplementedError):
             fps.apply_rotary(x, fwad.make_dual(pos, torch.ones_like(pos)), table)
+
+
+def test_incoming_gradients_are_made_readable():
+    base = torch.arange(1 + 4 * 2 * 16, dtype=torch.float32).to(BF16)
+    aligned = base[:-1].view(4, 2, 16)
+    assert aligned.data_ptr() % 16 == 0 and api._dense_heads(aligned) is aligned
+    for t in (base[1:].view(4, 2, 16), torch.ones((), dtype=BF16).expand(4, 2, 16), aligned.transpose(1, 2).contiguous().transpose(1, 2),
+              base[1:33].view(1, 2, 16)):
+        got = api._dense_heads(t)
+        assert got.data_ptr() % 16 == 0 and got.is_contiguous() and torch.equal(got, t)
