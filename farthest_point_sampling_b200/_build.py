@@ -7,6 +7,7 @@ no fast-math.
 from __future__ import annotations
 
 import concurrent.futures
+import fcntl
 import glob
 import hashlib
 import os
@@ -53,10 +54,19 @@ def stale() -> bool:
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     """Compile every ``csrc/*.cu`` into ``libfpstok.so`` (in-tree) when stale:
     one object per file, several at a time, an object again only when its
-    source, a header or the command line changed."""
+    source, a header or the command line changed.  Of several processes that
+    find it stale one builds, and the others wait for it."""
     if not force and not stale():
         return LIB
     os.makedirs(OBJ, exist_ok=True)
+    with open(os.path.join(OBJ, "lock"), "w") as lock:
+        fcntl.flock(lock, fcntl.LOCK_EX)  # until the file is closed
+        if force or stale():
+            _compile_and_link(force, verbose, extra)
+    return LIB
+
+
+def _compile_and_link(force: bool, verbose: bool, extra) -> None:
     headers = [p for p in deps() if not p.endswith(".cu")]
     common = hashlib.sha256()
     for p in headers:
@@ -72,8 +82,6 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
             if verbose:
                 print(" ".join(cmd))
             subprocess.check_call([*cmd, "-o", tmp])
-            for old in glob.glob(os.path.join(OBJ, os.path.basename(src)[:-3] + ".*.o")):
-                os.remove(old)
             os.replace(tmp, obj)
         return obj
 
@@ -82,7 +90,8 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     tmp = LIB + f".tmp{os.getpid()}"
     subprocess.check_call([nvcc(), *NVCC_FLAGS, *objects, "-o", tmp])
     os.replace(tmp, LIB)
-    return LIB
+    for old in set(glob.glob(os.path.join(OBJ, "*.o"))) - set(objects):
+        os.remove(old)
 
 
 def build_microbench(force: bool = False) -> str:
