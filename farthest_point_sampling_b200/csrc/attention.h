@@ -23,6 +23,13 @@ constexpr int kFar = 1 << 29;
 
 constexpr int kDevWaitTimeout = FPS_DEV_WAIT_TIMEOUT;
 
+// How long a wait for a tile polls, and (tests alone) of which kernels the
+// first block leaves its first load out, so that the waits for it run out:
+// bits of FPS_SKIP_*.
+struct WaitTest {
+  int polls, skip;
+};
+
 struct AttnCall {
   const void* q;
   const void* k;
@@ -38,6 +45,7 @@ struct AttnCall {
   AttnMask mask;
   int max_tokens;
   int zero_tail;
+  WaitTest test;
   void* out;   // [n_q, heads, D]
   float* lse;  // [heads, n_q]
   // backward

@@ -78,6 +78,7 @@ struct BwdArgs {
   float* partial;  // [slot][key head][128][2 DP]: dK and dV of the pieces of a key tile
   void* d1;      // dQ, or dK
   void* d2;      // dV
+  WaitTest test;
   bool sectors;  // every gradient row starts on a 32-byte sector, and ends on one
   const TileItem* items;
   WsHeader* hdr;
@@ -188,7 +189,7 @@ __global__ void __launch_bounds__(BwdShape<DP, kKeys>::kThreads, BwdShape<DP, kK
   Item* s_item = reinterpret_cast<Item*>(s_col + Sh::kColFloats);
   uint64_t* s_bar = reinterpret_cast<uint64_t*>(s_item + kItemRing);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_bar + 32);
-  volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
+  volatile WaitState* s_wait = reinterpret_cast<volatile WaitState*>(s_tmem + 1);
   const uint32_t bars = smem_u32(s_bar);
   const uint32_t kept_full = bars, kept_empty = bars + 16, acc_full = bars + 32, acc_empty = bars + 48,
                  item_full = bars + 64, item_empty = bars + 80, s_full = bars + 96, dp_full = bars + 104,
@@ -217,7 +218,8 @@ __global__ void __launch_bounds__(BwdShape<DP, kKeys>::kThreads, BwdShape<DP, kK
       mbar_init(ring_full + 8 * i, kKeys ? 33 : 1);  // the tiles, and in the keys kernel each lane's -lse and -D
       mbar_init(ring_empty + 8 * i, 1);
     }
-    *s_abort = 0;
+    s_wait->gave_up = 0;
+    s_wait->polls = a.test.polls;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     tma_prefetch_map(&map_k1);
     tma_prefetch_map(&map_k2);
@@ -254,7 +256,7 @@ __global__ void __launch_bounds__(BwdShape<DP, kKeys>::kThreads, BwdShape<DP, kK
         if (kKeys) clear_strided(static_cast<T*>(a.d2) + at, w.rows, stride, a.D);
       }
       const int slot = i % kItemRing;
-      if (i >= kItemRing && !mbar_wait_warp(item_empty + 8 * slot, ((i / kItemRing) - 1) & 1, s_abort)) break;
+      if (i >= kItemRing && !mbar_wait_warp(item_empty + 8 * slot, ((i / kItemRing) - 1) & 1, s_wait)) break;
       if (!more) {
         if (lane == 0) s_item[slot].count = -1;
         __syncwarp();
@@ -265,11 +267,12 @@ __global__ void __launch_bounds__(BwdShape<DP, kKeys>::kThreads, BwdShape<DP, kK
       __syncwarp();
       mbar_arrive_one(item_full + 8 * slot);
       const int ks = nk % Sh::kKept;
-      if (nk >= Sh::kKept && !mbar_wait_warp(kept_empty + 8 * ks, ((nk / Sh::kKept) - 1) & 1, s_abort)) break;
+      if (nk >= Sh::kKept && !mbar_wait_warp(kept_empty + 8 * ks, ((nk / Sh::kKept) - 1) & 1, s_wait)) break;
       const int boxes = (w.rows + 63) / 64;
-      mbar_expect(kept_full + 8 * ks, 2 * boxes * 8192 * Sh::kPanels);
+      const bool skip = (a.test.skip & (kKeys ? FPS_SKIP_KEYS : FPS_SKIP_QUERIES)) && blockIdx.x == 0 && nk == 0;
+      if (!skip) mbar_expect(kept_full + 8 * ks, 2 * boxes * 8192 * Sh::kPanels);
 #pragma unroll 1
-      for (int b = 0; b < boxes; ++b)
+      for (int b = 0; b < (skip ? 0 : boxes); ++b)
 #pragma unroll
         for (int p = 0; p < Sh::kPanels; ++p) {
           const uint32_t to = smem_u32(s_kept) + 2 * ks * Sh::kKeptBytes + p * kPanel + b * 8192;
@@ -282,7 +285,7 @@ __global__ void __launch_bounds__(BwdShape<DP, kKeys>::kThreads, BwdShape<DP, kK
 #pragma unroll 1
       for (int f = w.f0; f < w.f1; ++f, ++n) {
         const int st = n % Sh::kRing;
-        if (n >= Sh::kRing && !(ok = mbar_wait_warp(ring_empty + 8 * st, ((n / Sh::kRing) - 1) & 1, s_abort))) break;
+        if (n >= Sh::kRing && !(ok = mbar_wait_warp(ring_empty + 8 * st, ((n / Sh::kRing) - 1) & 1, s_wait))) break;
         const int row = w.stream_row + w.tiles.start(j), extent = w.tiles.extent(j);
         const int sboxes = (extent + 63) / 64;
         mbar_expect(ring_full + 8 * st, 2 * sboxes * 8192 * Sh::kPanels);
@@ -311,12 +314,11 @@ __global__ void __launch_bounds__(BwdShape<DP, kKeys>::kThreads, BwdShape<DP, kK
       }
     }
     // after a wait that gave up: the copies still in flight land first
-    if (__any_sync(kFull, *s_abort)) {
-      volatile int none = 0;
+    if (__any_sync(kFull, s_wait->gave_up)) {
       for (int b = 0; b < Sh::kRing; ++b) {
         const int lk = nk - 1 - b, ls = n - 1 - b;
-        if (lk >= 0 && b < Sh::kKept) mbar_wait_warp(kept_full + 8 * (lk % Sh::kKept), (lk / Sh::kKept) & 1, &none);
-        if (ls >= 0) mbar_wait_warp(ring_full + 8 * (ls % Sh::kRing), (ls / Sh::kRing) & 1, &none);
+        if (lk >= 0 && b < Sh::kKept) mbar_land_warp(kept_full + 8 * (lk % Sh::kKept), (lk / Sh::kKept) & 1, s_wait);
+        if (ls >= 0) mbar_land_warp(ring_full + 8 * (ls % Sh::kRing), (ls / Sh::kRing) & 1, s_wait);
       }
     }
   } else if (warp == kMmaWarp) {
@@ -334,7 +336,7 @@ __global__ void __launch_bounds__(BwdShape<DP, kKeys>::kThreads, BwdShape<DP, kK
     const auto fetch = [&](Tile* t) {  // false when the work is done, or a wait gave up (ok)
       if (f == f1) {
         const int slot = i % kItemRing;
-        if (!(ok = mbar_wait_warp(item_full + 8 * slot, (i / kItemRing) & 1, s_abort))) return false;
+        if (!(ok = mbar_wait_warp(item_full + 8 * slot, (i / kItemRing) & 1, s_wait))) return false;
         count = uniform(s_item[slot].count);
         f0 = f = uniform(s_item[slot].f0);
         f1 = uniform(s_item[slot].f1);
@@ -347,11 +349,11 @@ __global__ void __launch_bounds__(BwdShape<DP, kKeys>::kThreads, BwdShape<DP, kK
         if (count < 0) return false;
         ++i;
         const int ks = items % Sh::kKept;
-        if (!(ok = mbar_wait_warp(kept_full + 8 * ks, (items / Sh::kKept) & 1, s_abort))) return false;
+        if (!(ok = mbar_wait_warp(kept_full + 8 * ks, (items / Sh::kKept) & 1, s_wait))) return false;
         ++items;
       }
       const int st = fetched % Sh::kRing;
-      if (!(ok = mbar_wait_warp(ring_full + 8 * st, (fetched / Sh::kRing) & 1, s_abort))) return false;
+      if (!(ok = mbar_wait_warp(ring_full + 8 * st, (fetched / Sh::kRing) & 1, s_wait))) return false;
       ++fetched;
       t->steps = (tiles.extent(j) + 15) / 16;
       t->item = items - 1;
@@ -390,9 +392,9 @@ __global__ void __launch_bounds__(BwdShape<DP, kKeys>::kThreads, BwdShape<DP, kK
     for (int m = 0; more; ++m) {
       const uint32_t to = tmem + kColAcc + (cur.item % Sh::kAcc) * Sh::kAccColumns;
       if (cur.first && cur.item >= Sh::kAcc &&
-          !mbar_wait_warp(acc_empty + 8 * (cur.item % Sh::kAcc), ((cur.item / Sh::kAcc) - 1) & 1, s_abort))
+          !mbar_wait_warp(acc_empty + 8 * (cur.item % Sh::kAcc), ((cur.item / Sh::kAcc) - 1) & 1, s_wait))
         break;
-      if (!mbar_wait_warp(p_ready, m & 1, s_abort)) break;
+      if (!mbar_wait_warp(p_ready, m & 1, s_wait)) break;
       tc_fence_after();
       // Products of different shapes are not promised to run in order: scores
       // wait for the product that reads the 16-bit rows in their place.
@@ -402,24 +404,23 @@ __global__ void __launch_bounds__(BwdShape<DP, kKeys>::kThreads, BwdShape<DP, kK
       }
       more = fetch(&nxt);
       if (!ok) break;
-      if (kKeys && !mbar_wait_warp(dv_done, m & 1, s_abort)) break;
+      if (kKeys && !mbar_wait_warp(dv_done, m & 1, s_wait)) break;
       if (more) scores(nxt, m + 1, 0);
-      if (!mbar_wait_warp(ds_ready, m & 1, s_abort)) break;
+      if (!mbar_wait_warp(ds_ready, m & 1, s_wait)) break;
       tc_fence_after();
       gradient(cur, m, tmem + kColDP, to, 0);  // dK += dS^T Q, or dQ += dS K
       mma_commit(ring_empty + 8 * (m % Sh::kRing));
       if (cur.last) mma_commit(acc_full + 8 * (cur.item % Sh::kAcc));
       if (more) {
-        if (!mbar_wait_warp(ring_empty + 8 * (m % Sh::kRing), (m / Sh::kRing) & 1, s_abort)) break;
+        if (!mbar_wait_warp(ring_empty + 8 * (m % Sh::kRing), (m / Sh::kRing) & 1, s_wait)) break;
         scores(nxt, m + 1, 1);
         if (nxt.last) mma_commit(kept_empty + 8 * nxt.kept);  // only the scores read the kept tiles
         cur = nxt;
       }
     }
-    if (__any_sync(kFull, *s_abort)) {  // products in flight end before TMEM is freed
-      volatile int none = 0;
+    if (__any_sync(kFull, s_wait->gave_up)) {  // products in flight end before TMEM is freed
       mma_commit(drain);
-      mbar_wait_warp(drain, 0, &none);
+      mbar_land_warp(drain, 0, s_wait);
     }
   } else {
     // ------------------------------------------------ softmax and its gradient
@@ -437,7 +438,7 @@ __global__ void __launch_bounds__(BwdShape<DP, kKeys>::kThreads, BwdShape<DP, kK
     float lse[kOwn] = {};
     bool given[kOwn] = {};
     const auto ahead = [&](int i) {
-      if (!mbar_wait(item_full + 8 * (i % kItemRing), (i / kItemRing) & 1, s_abort)) return false;
+      if (!mbar_wait_warp(item_full + 8 * (i % kItemRing), (i / kItemRing) & 1, s_wait)) return false;
       const Item& w = s_item[i % kItemRing];
       if (w.count <= 0) return true;
 #pragma unroll
@@ -457,7 +458,7 @@ __global__ void __launch_bounds__(BwdShape<DP, kKeys>::kThreads, BwdShape<DP, kK
     if constexpr (!kKeys) ok = ahead(0);
     for (int i = 0; ok; ++i) {
       const int slot = i % kItemRing;
-      if (kKeys && !(ok = mbar_wait(item_full + 8 * slot, (i / kItemRing) & 1, s_abort))) break;
+      if (kKeys && !(ok = mbar_wait_warp(item_full + 8 * slot, (i / kItemRing) & 1, s_wait))) break;
       const Item& w = s_item[slot];  // read where it is needed: it stays until this thread lets go of the slot
       const int count = w.count;
       if (count < 0) break;
@@ -466,7 +467,7 @@ __global__ void __launch_bounds__(BwdShape<DP, kKeys>::kThreads, BwdShape<DP, kK
         // D: O as read ahead, dO from its tile; shared with the keys kernel
         // through memory and with the threads of each row through the block's
         const int ks = nk % Sh::kKept;
-        if (!(ok = mbar_wait(kept_full + 8 * ks, (nk / Sh::kKept) & 1, s_abort))) break;
+        if (!(ok = mbar_wait_warp(kept_full + 8 * ks, (nk / Sh::kKept) & 1, s_wait))) break;
 #pragma unroll
         for (int r = 0; r < kOwn; ++r) {
           const int q = q0 + 64 * r;
@@ -493,7 +494,7 @@ __global__ void __launch_bounds__(BwdShape<DP, kKeys>::kThreads, BwdShape<DP, kK
         }
         mbar_arrive(kept_empty + 8 * ks);
         mbar_arrive(row_ready);
-        if (!(ok = mbar_wait(row_ready, nk & 1, s_abort))) break;
+        if (!(ok = mbar_wait_warp(row_ready, nk & 1, s_wait))) break;
         lse2 = s_col[row];
         delta = s_col[kTile + row];
       }
@@ -507,7 +508,7 @@ __global__ void __launch_bounds__(BwdShape<DP, kKeys>::kThreads, BwdShape<DP, kK
         const bool clear = rows_to_clear(extent, left);
         if (kKeys || clear) {
           // also where -lse and -D are read from
-          if (!(ok = mbar_wait(ring_full + 8 * st, (m / Sh::kRing) & 1, s_abort))) break;
+          if (!(ok = mbar_wait_warp(ring_full + 8 * st, (m / Sh::kRing) & 1, s_wait))) break;
         }
         if (clear) {
           uint8_t* tile = s_ring + 2 * st * Sh::kStreamBytes;
@@ -536,7 +537,7 @@ __global__ void __launch_bounds__(BwdShape<DP, kKeys>::kThreads, BwdShape<DP, kK
           }
         }
         const float* col = s_col + st * 2 * kStream + h0;
-        if (!(ok = mbar_wait(s_full, m & 1, s_abort))) break;
+        if (!(ok = mbar_wait_warp(s_full, m & 1, s_wait))) break;
         tc_fence_after();
         float x[kRows];
 #pragma unroll
@@ -573,7 +574,7 @@ __global__ void __launch_bounds__(BwdShape<DP, kKeys>::kThreads, BwdShape<DP, kK
         if constexpr (kKeys) tmem_wait_st();
         tc_fence_before();
         mbar_arrive(p_ready);
-        if (!(ok = mbar_wait(dp_full, m & 1, s_abort))) break;
+        if (!(ok = mbar_wait_warp(dp_full, m & 1, s_wait))) break;
         tc_fence_after();
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
@@ -621,7 +622,7 @@ __global__ void __launch_bounds__(BwdShape<DP, kKeys>::kThreads, BwdShape<DP, kK
       mbar_arrive(item_empty + 8 * slot);
       if (!kKeys && !(ok = ahead(i + 1))) break;
       const int acc = nk % Sh::kAcc;
-      if (!(ok = mbar_wait(acc_full + 8 * acc, (nk / Sh::kAcc) & 1, s_abort))) break;
+      if (!(ok = mbar_wait_warp(acc_full + 8 * acc, (nk / Sh::kAcc) & 1, s_wait))) break;
       tc_fence_after();
       // the parts share the stores: dK and dV, or half of dQ each
       const uint32_t from = lanes + kColAcc + acc * Sh::kAccColumns;
@@ -656,7 +657,7 @@ __global__ void __launch_bounds__(BwdShape<DP, kKeys>::kThreads, BwdShape<DP, kK
     tc_fence_after();
     tmem_free(tmem, Sh::kColumns);
   }
-  if (threadIdx.x == 0 && *s_abort) record_error(a.hdr, kDevWaitTimeout);
+  if (threadIdx.x == 0 && s_wait->gave_up) record_error(a.hdr, kDevWaitTimeout);
 }
 
 // dK and dV of the key tiles that were cut into pieces: their sums in order.
@@ -785,6 +786,7 @@ cudaError_t run_tiles(const AttnCall& c, const BwdWorkspace& ws, const BwdMaps& 
   a.lse = c.lse;
   a.rows = ws.rows;
   a.hdr = ws.hdr;
+  a.test = c.test;
   a.sectors = m.sectors;
   cudaError_t e;
   if (c.n_q > 0) {

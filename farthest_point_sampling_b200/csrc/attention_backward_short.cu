@@ -58,6 +58,7 @@ struct ShortArgs {
   void *dq, *dk, *dv;
   const int64_t *q_offsets, *kv_offsets;
   int B;
+  WaitTest test;
   bool sectors;  // every gradient row starts on a 32-byte sector, and ends on one
   const TileItem* items;
   WsHeader* hdr;
@@ -99,7 +100,7 @@ __global__ void __launch_bounds__(kShortThreads, kTwo ? 2 : 1)
   ShortItem* s_item = reinterpret_cast<ShortItem*>(s_col + 2 * kTile);
   uint64_t* s_bar = reinterpret_cast<uint64_t*>((reinterpret_cast<uintptr_t>(s_item + kItemRing) + 7) & ~(uintptr_t)7);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_bar + 32);
-  volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
+  volatile WaitState* s_wait = reinterpret_cast<volatile WaitState*>(s_tmem + 1);
   const uint32_t bars = smem_u32(s_bar);
   const uint32_t kv_full = bars, kv_empty = bars + 16, qd_full = bars + 32, qd_empty = bars + 48, item_full = bars + 64,
                  item_empty = bars + 80, col_full = bars + 96, stored = bars + 104,
@@ -121,7 +122,8 @@ __global__ void __launch_bounds__(kShortThreads, kTwo ? 2 : 1)
     mbar_init(ready, kSoftmaxThreads);
     mbar_init(done, 1);
     mbar_init(drain, 1);
-    *s_abort = 0;
+    s_wait->gave_up = 0;
+    s_wait->polls = a.test.polls;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     tma_prefetch_map(&map_q);
     tma_prefetch_map(&map_k);
@@ -154,13 +156,13 @@ __global__ void __launch_bounds__(kShortThreads, kTwo ? 2 : 1)
         clear_strided(static_cast<T*>(a.dv) + at, e.nk, stride, a.D);
       }
       const int slot = i % kItemRing;
-      if (i >= kItemRing && !mbar_wait_warp(item_empty + 8 * slot, ((i / kItemRing) - 1) & 1, s_abort)) break;
+      if (i >= kItemRing && !mbar_wait_warp(item_empty + 8 * slot, ((i / kItemRing) - 1) & 1, s_wait)) break;
       if (lane == 0) s_item[slot] = more ? ShortItem{h, e.q0, e.nq, e.k0, e.nk} : ShortItem{0, 0, -1, 0, 0};
       __syncwarp();
       mbar_arrive_one(item_full + 8 * slot);
       if (!more) break;
       const int ks = n % kStages;
-      if (n >= kStages && !mbar_wait_warp(kv_empty + 8 * ks, ((n / kStages) - 1) & 1, s_abort)) break;
+      if (n >= kStages && !mbar_wait_warp(kv_empty + 8 * ks, ((n / kStages) - 1) & 1, s_wait)) break;
       ++n;
       const auto load = [&](uint8_t* to, const CUtensorMap* m1, const CUtensorMap* m2, uint32_t bar, int rows, int row, int hd) {
         const int boxes = (rows + 63) / 64;
@@ -178,17 +180,17 @@ __global__ void __launch_bounds__(kShortThreads, kTwo ? 2 : 1)
 #pragma unroll 1
       for (int m = 0; m < a.group; ++m, ++u) {
         const int st = u % kStages;
-        if (u >= kStages && !(ok = mbar_wait_warp(qd_empty + 8 * st, ((u / kStages) - 1) & 1, s_abort))) break;
+        if (u >= kStages && !(ok = mbar_wait_warp(qd_empty + 8 * st, ((u / kStages) - 1) & 1, s_wait))) break;
+        if ((a.test.skip & FPS_SKIP_SHORT) && blockIdx.x == 0 && u == 0) continue;
         load(s_qd + 2 * st * Sh::kTileBytes, &map_q, &map_do, qd_full + 8 * st, e.nq, e.q0, h * a.group + m);
       }
     }
     // after a wait that gave up: the copies still in flight land first
-    if (__any_sync(kFull, *s_abort)) {
-      volatile int none = 0;
+    if (__any_sync(kFull, s_wait->gave_up)) {
       for (int b = 0; b < kStages; ++b) {
         const int lk = n - 1 - b, lu = u - 1 - b;
-        if (lk >= 0) mbar_wait_warp(kv_full + 8 * (lk % kStages), (lk / kStages) & 1, &none);
-        if (lu >= 0) mbar_wait_warp(qd_full + 8 * (lu % kStages), (lu / kStages) & 1, &none);
+        if (lk >= 0) mbar_land_warp(kv_full + 8 * (lk % kStages), (lk / kStages) & 1, s_wait);
+        if (lu >= 0) mbar_land_warp(qd_full + 8 * (lu % kStages), (lu / kStages) & 1, s_wait);
       }
     }
   } else if (warp == kMmaWarp) {
@@ -202,21 +204,21 @@ __global__ void __launch_bounds__(kShortThreads, kTwo ? 2 : 1)
     bool ok = true;
     for (int i = 0; ok; ++i, ++n) {
       const int slot = i % kItemRing;
-      if (!(ok = mbar_wait_warp(item_full + 8 * slot, (i / kItemRing) & 1, s_abort))) break;
+      if (!(ok = mbar_wait_warp(item_full + 8 * slot, (i / kItemRing) & 1, s_wait))) break;
       const int nq = uniform(s_item[slot].nq), nk = uniform(s_item[slot].nk);
       mbar_arrive_one(item_empty + 8 * slot);
       if (nq < 0) break;
       const int ks = n % kStages;
       const uint32_t kv = smem_desc(smem_u32(s_kv) + 2 * ks * Sh::kTileBytes, kPanel);
-      if (!(ok = mbar_wait_warp(kv_full + 8 * ks, (n / kStages) & 1, s_abort))) break;
+      if (!(ok = mbar_wait_warp(kv_full + 8 * ks, (n / kStages) & 1, s_wait))) break;
       const uint32_t s_desc = mma_desc(kBf16, false, false, (nq + 15) / 16 * 16);
 #pragma unroll 1
       for (int m = 0; m < a.group; ++m, ++u) {
         const int st = u % kStages;
         const uint32_t qd = smem_desc(smem_u32(s_qd) + 2 * st * Sh::kTileBytes, kPanel);
-        if (!(ok = mbar_wait_warp(qd_full + 8 * st, (u / kStages) & 1, s_abort))) break;
+        if (!(ok = mbar_wait_warp(qd_full + 8 * st, (u / kStages) & 1, s_wait))) break;
         // the last unit's gradients lie where these scores go
-        if (u > 0 && !(ok = mbar_wait_warp(stored, (u - 1) & 1, s_abort))) break;
+        if (u > 0 && !(ok = mbar_wait_warp(stored, (u - 1) & 1, s_wait))) break;
         tc_fence_after();
 #pragma unroll 1
         for (int x = 0; x < 2; ++x)  // S, then dP: whole panels, as values past D are zeros
@@ -225,7 +227,7 @@ __global__ void __launch_bounds__(kShortThreads, kTwo ? 2 : 1)
             mma_ss<2, 2>(tmem + (x ? kColDP : kColS), kv + ((x * Sh::kTileBytes + p * kPanel) >> 4),
                          qd + ((x * Sh::kTileBytes + p * kPanel) >> 4), s_desc, p > 0);
         mma_commit(scores_full);
-        if (!(ok = mbar_wait_warp(ready, u & 1, s_abort))) break;
+        if (!(ok = mbar_wait_warp(ready, u & 1, s_wait))) break;
         tc_fence_after();
 #pragma unroll 1
         for (int half = 0; half * 64 < nq; ++half) {  // 64 queries at a time
@@ -248,10 +250,9 @@ __global__ void __launch_bounds__(kShortThreads, kTwo ? 2 : 1)
         mma_commit(done);
       }
     }
-    if (__any_sync(kFull, *s_abort)) {  // products in flight end before TMEM is freed
-      volatile int none = 0;
+    if (__any_sync(kFull, s_wait->gave_up)) {  // products in flight end before TMEM is freed
       mma_commit(drain);
-      mbar_wait_warp(drain, 0, &none);
+      mbar_land_warp(drain, 0, s_wait);
     }
   } else {
     // ------------------------------------------------ softmax and its gradient
@@ -264,7 +265,7 @@ __global__ void __launch_bounds__(kShortThreads, kTwo ? 2 : 1)
     bool ok = true;
     for (int i = 0; ok; ++i) {
       const int slot = i % kItemRing;
-      if (!(ok = mbar_wait(item_full + 8 * slot, (i / kItemRing) & 1, s_abort))) break;
+      if (!(ok = mbar_wait_warp(item_full + 8 * slot, (i / kItemRing) & 1, s_wait))) break;
       const ShortItem w = s_item[slot];
       if (w.nq < 0) break;
       mbar_arrive(item_empty + 8 * slot);
@@ -291,14 +292,14 @@ __global__ void __launch_bounds__(kShortThreads, kTwo ? 2 : 1)
             o[c] = (d0 + c) * 8 < a.D ? *reinterpret_cast<const uint4*>(from + (d0 + c) * 8) : make_uint4(0, 0, 0, 0);
           lse = (given() ? a.rows + (int64_t)a.heads * a.n_q : a.lse)[(int64_t)h * a.n_q + w.q_row + q];
         }
-        if (!(ok = mbar_wait(qd_full + 8 * st, (u / kStages) & 1, s_abort))) break;
+        if (!(ok = mbar_wait_warp(qd_full + 8 * st, (u / kStages) & 1, s_wait))) break;
         uint8_t* tile = s_qd + 2 * st * Sh::kTileBytes;
         if (w.nq & 63) {
           clear_rows<Sh::kPanels>(tile, w.nq, w.nq, threadIdx.x, kSoftmaxThreads);
           clear_rows<Sh::kPanels>(tile + Sh::kTileBytes, w.nq, w.nq, threadIdx.x, kSoftmaxThreads);
         }
         if (m == 0 && (w.nk & 63)) {
-          if (!(ok = mbar_wait(kv_full + 8 * ks, (n / kStages) & 1, s_abort))) break;
+          if (!(ok = mbar_wait_warp(kv_full + 8 * ks, (n / kStages) & 1, s_wait))) break;
           clear_rows<Sh::kPanels>(s_kv + 2 * ks * Sh::kTileBytes, w.nk, w.nk, threadIdx.x, kSoftmaxThreads);
         }
         if (q < w.nq) {
@@ -319,8 +320,8 @@ __global__ void __launch_bounds__(kShortThreads, kTwo ? 2 : 1)
         delta += __shfl_xor_sync(kFull, delta, 1);
         s_col[(lane & 1) * kTile + q] = given() ? lse : lane & 1 ? -delta : -lse * kLog2e;
         mbar_arrive(col_full);
-        if (!(ok = mbar_wait(scores_full, u & 1, s_abort))) break;
-        if (!(ok = mbar_wait(col_full, u & 1, s_abort))) break;
+        if (!(ok = mbar_wait_warp(scores_full, u & 1, s_wait))) break;
+        if (!(ok = mbar_wait_warp(col_full, u & 1, s_wait))) break;
         tc_fence_after();
         // 32 queries at a time, to the end of this thread's 64 if there are any:
         // the products take P and dS of all of them
@@ -380,7 +381,7 @@ __global__ void __launch_bounds__(kShortThreads, kTwo ? 2 : 1)
         mbar_arrive(ready);
         // stores: dQ of this head, half of the columns each; after the last
         // head dK and dV
-        if (!(ok = mbar_wait(done, u & 1, s_abort))) break;
+        if (!(ok = mbar_wait_warp(done, u & 1, s_wait))) break;
         tc_fence_after();
         store_row<T, DP / 2>(lanes + Sh::kColDQ + half * (DP / 2), row < w.nq, a.scale, dq + m * a.D + half * (DP / 2),
                              a.D - half * (DP / 2), a.sectors);
@@ -411,7 +412,7 @@ __global__ void __launch_bounds__(kShortThreads, kTwo ? 2 : 1)
     tc_fence_after();
     tmem_free(tmem, Sh::kColumns);
   }
-  if (threadIdx.x == 0 && *s_abort) record_error(a.hdr, kDevWaitTimeout);
+  if (threadIdx.x == 0 && s_wait->gave_up) record_error(a.hdr, kDevWaitTimeout);
 }
 
 template <typename T, int DP, bool kTwo>
@@ -464,6 +465,7 @@ cudaError_t launch_attention_backward_short(const AttnCall& c, const BwdMaps& ma
   a.q_offsets = c.q_offsets;
   a.kv_offsets = c.kv_offsets;
   a.B = c.B;
+  a.test = c.test;
   a.sectors = maps.sectors;
   a.items = items;
   a.hdr = hdr;

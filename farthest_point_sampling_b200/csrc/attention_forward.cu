@@ -58,6 +58,7 @@ struct FwdArgs {
   float* lse;
   const int64_t* q_offsets;
   int B, zero_tail;
+  WaitTest test;
   bool sectors;  // every row of out starts on a 32-byte sector, and ends on one
   const TileItem* items;
   WsHeader* hdr;
@@ -113,7 +114,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
   FwdItem* s_item = reinterpret_cast<FwdItem*>(s_v + Sh::kStages * Sh::kTileBytes);
   uint64_t* s_bar = reinterpret_cast<uint64_t*>(s_item + kItemRing);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_bar + 24);
-  volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
+  volatile WaitState* s_wait = reinterpret_cast<volatile WaitState*>(s_tmem + 1);
   const uint32_t bars = smem_u32(s_bar);
   const uint32_t q_full = bars, k_full = bars + 16, k_empty = bars + 32, v_full = bars + 48, v_empty = bars + 64,
                  s_full = bars + 80, o_full = bars + 88, drain = bars + 96, item_full = bars + 104,
@@ -125,7 +126,8 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     for (int i = 0; i < kItemRing; ++i) mbar_init(item_empty + 8 * i, kSoftmaxThreads + 1);
     mbar_init(p_ready, kSoftmaxThreads);
     for (int i = 0; i < 2; ++i) mbar_init(q_empty + 8 * i, 1);
-    *s_abort = 0;
+    s_wait->gave_up = 0;
+    s_wait->polls = a.test.polls;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     tma_prefetch_map(&map_q);
     tma_prefetch_map(&map_k);
@@ -142,10 +144,11 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     // ------------------------------------------------ items and loads
     {
       ItemClaims claims(&a.hdr->next_item[kQueryTiles], a.items, a.heads, a.hdr->n_items[kQueryTiles]);
-      int i = 0, n = 0, nq = 0;  // items handed out, key tiles and query tiles loaded so far
+      // items handed out; tiles of Q, of K and of V whose loads were issued
+      int i = 0, n = 0, nq = 0, nv = 0;
       for (bool more = true; more; ++i) {
         const int slot = i % kItemRing;
-        if (i >= kItemRing && !mbar_wait_warp(item_empty + 8 * slot, ((i / kItemRing) - 1) & 1, s_abort)) break;
+        if (i >= kItemRing && !mbar_wait_warp(item_empty + 8 * slot, ((i / kItemRing) - 1) & 1, s_wait)) break;
         TileItem entry;
         int h;
         more = claims.take(&entry, &h);
@@ -161,7 +164,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
         mbar_arrive_one(item_full + 8 * slot);
         if (w.count == 0) continue;
         const int qs = nq % Sh::kStages;
-        if (nq >= Sh::kStages && !mbar_wait_warp(q_empty + 8 * qs, ((nq / Sh::kStages) - 1) & 1, s_abort)) break;
+        if (nq >= Sh::kStages && !mbar_wait_warp(q_empty + 8 * qs, ((nq / Sh::kStages) - 1) & 1, s_wait)) break;
         const int q_boxes = (w.rows + 63) / 64;
         mbar_expect(q_full + 8 * qs, q_boxes * 8192 * Sh::kPanels);
 #pragma unroll 1
@@ -172,20 +175,22 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
                      w.q_row + b * 64);
         ++nq;
         const int g = w.h / a.group;
-        for (int j = 0; j < w.count; ++j, ++n) {
+        for (int j = 0; j < w.count; ++j, ++nv) {
           const int st = n % Sh::kStages;
           const uint32_t round = ((n / Sh::kStages) - 1) & 1;
           const int boxes = (w.keys.extent(j) + 63) / 64;
           const int krow = w.k_row + w.keys.start(j);
-          if (n >= Sh::kStages && !(more = mbar_wait_warp(k_empty + 8 * st, round, s_abort))) break;
-          mbar_expect(k_full + 8 * st, boxes * 8192 * Sh::kPanels);
+          if (n >= Sh::kStages && !(more = mbar_wait_warp(k_empty + 8 * st, round, s_wait))) break;
+          const bool skip = (a.test.skip & FPS_SKIP_FORWARD) && blockIdx.x == 0 && n == 0;
+          if (!skip) mbar_expect(k_full + 8 * st, boxes * 8192 * Sh::kPanels);
 #pragma unroll 1
-          for (int b = 0; b < boxes; ++b)
+          for (int b = 0; b < (skip ? 0 : boxes); ++b)
 #pragma unroll
             for (int p = 0; p < Sh::kPanels; ++p)
               tma_load(smem_u32(s_k) + st * Sh::kTileBytes + p * kPanel + b * 8192, &map_k, k_full + 8 * st, p * 64, g,
                        krow + b * 64);
-          if (n >= Sh::kStages && !(more = mbar_wait_warp(v_empty + 8 * st, round, s_abort))) break;
+          ++n;
+          if (nv >= Sh::kStages && !(more = mbar_wait_warp(v_empty + 8 * st, round, s_wait))) break;
           mbar_expect(v_full + 8 * st, boxes * 8192 * Sh::kPanels);
 #pragma unroll 1
           for (int b = 0; b < boxes; ++b)
@@ -195,14 +200,13 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
                        krow + b * 64);
         }
       }
-      // after a wait that gave up: this thread's copies still in flight land first
-      if (__any_sync(kFull, *s_abort)) {
-        volatile int none = 0;
-        for (int b = 0; b < Sh::kStages; ++b) {
-          const int lq = nq - 1 - b, lk = n - b;  // tile n may have its keys loading, not its values
-          if (lq >= 0) mbar_wait_warp(q_full + 8 * (lq % Sh::kStages), (lq / Sh::kStages) & 1, &none);
-          if (lk >= 0) mbar_wait_warp(k_full + 8 * (lk % Sh::kStages), (lk / Sh::kStages) & 1, &none);
-          if (lk >= 1) mbar_wait_warp(v_full + 8 * ((lk - 1) % Sh::kStages), ((lk - 1) / Sh::kStages) & 1, &none);
+      // after a wait that gave up: the copies still in flight land first, at most
+      // the last one of each stage
+      if (__any_sync(kFull, s_wait->gave_up)) {
+        for (int b = 1; b <= Sh::kStages; ++b) {
+          if (nq >= b) mbar_land_warp(q_full + 8 * ((nq - b) % Sh::kStages), ((nq - b) / Sh::kStages) & 1, s_wait);
+          if (n >= b) mbar_land_warp(k_full + 8 * ((n - b) % Sh::kStages), ((n - b) / Sh::kStages) & 1, s_wait);
+          if (nv >= b) mbar_land_warp(v_full + 8 * ((nv - b) % Sh::kStages), ((nv - b) / Sh::kStages) & 1, s_wait);
         }
       }
     }
@@ -214,7 +218,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
       bool ok = true;
       for (int i = 0; ok; ++i) {
         const int slot = i % kItemRing;
-        if (!(ok = mbar_wait_warp(item_full + 8 * slot, (i / kItemRing) & 1, s_abort))) break;
+        if (!(ok = mbar_wait_warp(item_full + 8 * slot, (i / kItemRing) & 1, s_wait))) break;
         const int count = uniform(s_item[slot].count);
         KeyTiles<kTile> keys;
         keys.before = uniform(s_item[slot].keys.before);
@@ -226,13 +230,13 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
         if (count == 0) continue;
         const int qs = nq % Sh::kStages;
         const uint32_t q = smem_desc(smem_u32(s_q) + qs * Sh::kTileBytes, kPanel);
-        if (!(ok = mbar_wait_warp(q_full + 8 * qs, (nq / Sh::kStages) & 1, s_abort))) break;
+        if (!(ok = mbar_wait_warp(q_full + 8 * qs, (nq / Sh::kStages) & 1, s_wait))) break;
         for (int j = 0; j <= count; ++j) {
           if (j > 0) {  // O += P V of tile j - 1
             const int m = n + j - 1, st = m % Sh::kStages;
             const bool both = keys.extent(j - 1) > 64;
-            if (!(ok = mbar_wait_warp(v_full + 8 * st, (m / Sh::kStages) & 1, s_abort))) break;
-            if (!(ok = mbar_wait_warp(p_ready, m & 1, s_abort))) break;
+            if (!(ok = mbar_wait_warp(v_full + 8 * st, (m / Sh::kStages) & 1, s_wait))) break;
+            if (!(ok = mbar_wait_warp(p_ready, m & 1, s_wait))) break;
             tc_fence_after();
             const uint32_t v = smem_desc(smem_u32(s_v) + st * Sh::kTileBytes, kPanel);
             mma_ts(tmem + Sh::kColO, tmem + Sh::kColP, v, pv_desc, j > 1);
@@ -240,12 +244,12 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
             mma_commit(v_empty + 8 * st);
             if (j == count) mma_commit(o_full);
             // products of different shapes are not promised to run in order
-            if (Sh::kOver && !(ok = mbar_wait_warp(v_empty + 8 * st, (m / Sh::kStages) & 1, s_abort))) break;
+            if (Sh::kOver && !(ok = mbar_wait_warp(v_empty + 8 * st, (m / Sh::kStages) & 1, s_wait))) break;
           }
           if (j < count) {  // S = Q K^T of tile j
             const int m = n + j, st = m % Sh::kStages;
             const int cols = (keys.extent(j) + 15) / 16 * 16;
-            if (!(ok = mbar_wait_warp(k_full + 8 * st, (m / Sh::kStages) & 1, s_abort))) break;
+            if (!(ok = mbar_wait_warp(k_full + 8 * st, (m / Sh::kStages) & 1, s_wait))) break;
             tc_fence_after();
             const uint32_t k = smem_desc(smem_u32(s_k) + st * Sh::kTileBytes, kPanel);
             const uint32_t qk_desc = mma_desc(kBf16, false, false, cols);
@@ -260,10 +264,9 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
         n += count;
         ++nq;
       }
-      if (__any_sync(kFull, *s_abort)) {  // products in flight end before TMEM is freed
-        volatile int none = 0;
+      if (__any_sync(kFull, s_wait->gave_up)) {  // products in flight end before TMEM is freed
         mma_commit(drain);
-        mbar_wait_warp(drain, 0, &none);
+        mbar_land_warp(drain, 0, s_wait);
       }
     }
   } else {
@@ -273,7 +276,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     bool ok = true;
     for (int i = 0; ok; ++i) {
       const int slot = i % kItemRing;
-      if (!(ok = mbar_wait(item_full + 8 * slot, (i / kItemRing) & 1, s_abort))) break;
+      if (!(ok = mbar_wait_warp(item_full + 8 * slot, (i / kItemRing) & 1, s_wait))) break;
       const FwdItem& w = s_item[slot];  // read where it is needed: it stays until this thread lets go of the slot
       const int count = w.count;
       if (count < 0) break;
@@ -289,7 +292,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
         const bool some = 32 * lane < extent && warp_rows > 0 && some_seen(a.mask, pa, pb, key);
         const bool all = 32 * lane + 32 <= extent && all_seen(a.mask, pa, pb, key);
         const uint32_t act = __ballot_sync(kFull, some && lane < kChunks), whole = __ballot_sync(kFull, all);
-        if (!(ok = mbar_wait(s_full, n & 1, s_abort))) break;
+        if (!(ok = mbar_wait_warp(s_full, n & 1, s_wait))) break;
         tc_fence_after();
         // Only now is the values' barrier waited for: with one stage, before these
         // scores it may still be in the phase of the tile before, whose end looks
@@ -297,7 +300,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
         const int left = w.nk - k0;
         if (rows_to_clear(extent, left)) {
           const int st = n % Sh::kStages;
-          if (!(ok = mbar_wait(v_full + 8 * st, (n / Sh::kStages) & 1, s_abort))) break;
+          if (!(ok = mbar_wait_warp(v_full + 8 * st, (n / Sh::kStages) & 1, s_wait))) break;
           clear_rows<Sh::kPanels>(s_v + st * Sh::kTileBytes, extent, left, threadIdx.x, kSoftmaxThreads);
           fence_async_smem();
         }
@@ -391,7 +394,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
         }
         continue;
       }
-      if (!(ok = mbar_wait(o_full, nq & 1, s_abort))) break;
+      if (!(ok = mbar_wait_warp(o_full, nq & 1, s_wait))) break;
       ++nq;
       tc_fence_after();
       // O / l.  Where a row saw no key O may hold what masked infinities left, so
@@ -422,7 +425,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     tc_fence_after();
     tmem_free(tmem, kTmemColumns);
   }
-  if (threadIdx.x == 0 && *s_abort) record_error(a.hdr, kDevWaitTimeout);
+  if (threadIdx.x == 0 && s_wait->gave_up) record_error(a.hdr, kDevWaitTimeout);
 }
 
 // Whether a call looks for events with at most kFewRows query rows: when its
@@ -485,6 +488,7 @@ cudaError_t run_forward(const AttnCall& c, const FwdWorkspace& ws, cudaStream_t 
   a.B = c.B;
   a.zero_tail = c.zero_tail && !few_rows(c);  // the other kernel has done it
   a.sectors = reinterpret_cast<uintptr_t>(c.out) % 32 == 0 && c.D % 16 == 0;
+  a.test = c.test;
   a.items = ws.items;
   a.hdr = ws.hdr;
   const auto kernel = k_attn_forward<T, DP>;

@@ -41,7 +41,6 @@ __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
 // A poll sleeps in hardware for up to kWaitNs; polled without that, the waits
 // took half of the softmax warps' issue slots.
 constexpr uint32_t kWaitNs = 20000;
-constexpr int kWaitPolls = 100000;  // 2 s
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -54,21 +53,36 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
-// Every wait ends: after kWaitPolls polls, or once another warp of the block
-// has given up (*abort), it returns false and the caller leaves its loop.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+// Every wait ends: after so many polls as `polls` says, or once another warp of
+// the block has given up, it returns false and the caller leaves its loop.
+struct WaitState {
+  int gave_up, polls;
+};
+// Of one lane.  Lanes may end with different answers, and what follows a wait
+// is for whole warps (TMEM reads and writes, ballots), so only mbar_wait_warp
+// calls it.
+__device__ __forceinline__ bool mbar_wait_lane(uint32_t bar, uint32_t parity, volatile WaitState* state) {
 #pragma unroll 1
   for (int i = 0; !mbar_try(bar, parity); ++i)
-    if (i == kWaitPolls || *abort) {
-      *abort = 1;
+    if (i >= state->polls || state->gave_up) {
+      state->gave_up = 1;
       return false;
     }
   return true;
 }
 
 // By a whole warp, with the same answer for every lane.
-__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile WaitState* state) {
+  return __all_sync(0xffffffffu, mbar_wait_lane(bar, parity, state));
+}
+
+// After a wait gave up: for what is still in flight and ends on `bar`, whether
+// or not the other waits do.
+__device__ __forceinline__ void mbar_land_warp(uint32_t bar, uint32_t parity, volatile WaitState* state) {
+  volatile WaitState own;
+  own.gave_up = 0;
+  own.polls = state->polls;
+  mbar_wait_warp(bar, parity, &own);
 }
 
 // ---------------------------------------------------------------- TMA

@@ -1,5 +1,6 @@
 // C ABI of the packed-token transformer operators (declared in
 // include/fpstok.h): argument checks and launches.
+#include <atomic>
 #include <cmath>
 
 #include "../../include/fpstok.h"
@@ -15,6 +16,9 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 int from_cuda(cudaError_t e) { return e == cudaSuccess ? FPS_OK : FPS_ERR_CUDA; }
 constexpr int64_t kMaxRows = kFar;  // positions, their differences and a window more fit 32 bits
 constexpr int64_t kMaxStride = (int64_t)1 << 38;  // elements; a TMA stride is below 2^40 bytes
+
+constexpr int kWaitPolls = 100000;  // 2 s
+std::atomic<int> g_wait_polls{kWaitPolls}, g_wait_skip{0};
 
 // Sizes only: enough to compute a workspace.
 int check_attention_sizes(const fps_attention_args* a) {
@@ -81,6 +85,7 @@ int make_call(const fps_attention_args* a, AttnCall* c) {
   c->kv_offsets = a->kv_offsets;
   c->scale = a->scale;
   c->zero_tail = a->zero_tail;
+  c->test = {g_wait_polls.load(std::memory_order_relaxed), g_wait_skip.load(std::memory_order_relaxed)};
   return FPS_OK;
 }
 
@@ -185,6 +190,11 @@ int fps_attention_backward(const fps_attention_args* args, const void* out, cons
   c.dk = dk;
   c.dv = dv;
   return from_cuda(launch_attention_backward(c, workspace, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+void fps_set_attention_test(int poll_limit, int skip) {
+  g_wait_polls = poll_limit > 0 ? poll_limit : kWaitPolls;
+  g_wait_skip = skip;
 }
 
 }  // extern "C"

@@ -484,6 +484,22 @@ int fps_device_status(void *workspace, fps_stream_t stream, int *detail);
  */
 void fps_set_exchange_test(int spin_limit, int skip_rank);
 
+/*
+ * Test hook of the attention kernels' bounded waits (host side only; it faults
+ * nothing).  Each wait for a tile polls at most poll_limit times (<= 0: the
+ * default, 100000 polls of up to 20 us), and in the kernels named by `skip` the
+ * first block leaves its first load out, so that the waits for that tile run
+ * out.  That block records FPS_DEV_WAIT_TIMEOUT and ends; the others take the
+ * rest of the work, the launch's results are not valid, the CUDA context stays
+ * usable.  Applies to the launches made after the call;
+ * fps_set_attention_test(0, 0) restores the defaults.
+ */
+#define FPS_SKIP_FORWARD 1 /* forward, events with more rows than the few-query kernel takes */
+#define FPS_SKIP_SHORT 2   /* backward, events of at most 128 queries and 128 keys */
+#define FPS_SKIP_QUERIES 4 /* backward of longer ones, gradient of the queries */
+#define FPS_SKIP_KEYS 8    /* backward of longer ones, gradients of the keys and values */
+void fps_set_attention_test(int poll_limit, int skip);
+
 /* Human-readable name of a status code. */
 const char *fps_status_string(int status);
 
