@@ -178,6 +178,7 @@ cudaError_t launch(const RotaryCall& c, const fps_rotary_table& table, cudaStrea
   sh.copy_rest = c.x != c.y;
   // enough blocks for four on every SM before a block takes more than one token
   const int64_t spread = (int64_t)device_info().sm_count * 4;
+  if (spread <= 0) return cudaErrorNoDevice;
   int64_t tile = (c.T + spread - 1) / spread;
   sh.tile = (int)(tile < 1 ? 1 : tile > kMaxTile ? kMaxTile : tile);
   const unsigned blocks = (unsigned)((c.T + sh.tile - 1) / sh.tile);
