@@ -565,7 +565,8 @@ def rotary_embed(x: torch.Tensor, positions: torch.Tensor, table: RotaryTable, i
     """C ``fps_rotary``: the heads ``x [T, H, D]`` (float32, bfloat16 or
     float16; rows and heads may be strided, e.g. the query and key heads of a
     fused projection) turned by their positions ``[T, axes]`` (float32, e.g.
-    the packed centroids).  ``out`` may be ``x`` itself (in place).  With
+    the packed centroids).  ``out`` may be ``x`` itself (in place) or other
+    heads of the same rows, and is refused where it overlaps otherwise.  With
     ``inverse`` the turn goes back.  Not recorded by autograd: see
     :func:`apply_rotary`."""
     dev = _cuda_device(x)
@@ -674,7 +675,7 @@ def attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, tok_off
     """C ``fps_attention``: returns ``(out [n_q, H, D], lse [H, n_q])`` (lse
     None without ``need_lse``); see :func:`packed_attention`.  Rows of a given
     ``out`` that belong to no event are left as they were; in a new one they
-    are 0.  Not recorded by autograd."""
+    are 0.  ``out`` must not overlap the inputs.  Not recorded by autograd."""
     a, dev = _attention_args(q, k, v, tok_offsets, kv_offsets, scale, causal, window, sinks, max_tokens)
     return _attention_forward(a, dev, q, need_lse, workspace, out, check_device)
 

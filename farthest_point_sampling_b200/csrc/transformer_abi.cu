@@ -20,6 +20,57 @@ constexpr int64_t kMaxStride = (int64_t)1 << 38;  // elements; a TMA stride is b
 constexpr int kWaitPolls = 100000;  // 2 s
 std::atomic<int> g_wait_polls{kWaitPolls}, g_wait_skip{0};
 
+// Rows of `width` bytes, n of each of `heads`; strides in bytes, 0 or more.
+struct Rows {
+  const void* base;
+  int64_t n, heads, token, head, width;
+  int64_t at() const { return (int64_t)reinterpret_cast<uintptr_t>(base); }
+  // bytes from the first to the end of the last
+  int64_t reach() const { return n == 0 ? 0 : (n - 1) * token + (heads - 1) * head + width; }
+};
+Rows rows_of(const void* base, int64_t n, int64_t heads, int64_t token, int64_t head, int64_t values, int64_t size) {
+  // strides that nothing uses may be anything; none reaches beyond 2^60 bytes
+  const auto bytes = [&](int64_t stride, int64_t count) {
+    const int64_t most = ((int64_t)1 << 60) / count;
+    return stride > most / size ? most : stride * size;
+  };
+  return {base, n, heads, n > 1 ? bytes(token, n) : 0, heads > 1 ? bytes(head, heads) : 0, values * size};
+}
+bool apart(const Rows& a, const Rows& b) { return a.at() + a.reach() <= b.at() || b.at() + b.reach() <= a.at(); }
+
+// Whether a row of a set meets one of the same set moved by `by` bytes; the row
+// itself does not count.
+bool rows_meet(const Rows& r, int64_t by) {
+  for (int64_t h = 1 - r.heads; h < r.heads; ++h) {
+    const int64_t at = by + h * r.head;
+    // the two nearest rows of this head
+    const int64_t t0 = r.token > 0 ? (at > 0 ? -((at + r.token - 1) / r.token) : -at / r.token) : 0;
+    for (int64_t t = t0; t <= t0 + 1; ++t) {
+      const int64_t from = at + t * r.token;
+      if (t > -r.n && t < r.n && from > -r.width && from < r.width && !(by == 0 && h == 0 && t == 0)) return true;
+    }
+  }
+  return false;
+}
+bool rows_meet(const Rows& r) {
+  const bool heads_in_rows = r.head >= r.width && r.token >= (r.heads - 1) * r.head + r.width;
+  const bool rows_in_heads = r.token >= r.width && r.head >= (r.n - 1) * r.token + r.width;
+  return !heads_in_rows && !rows_in_heads && rows_meet(r, 0);
+}
+
+// Whether a row meets `bytes` at `base`.
+bool block_meets(const void* base, int64_t bytes, const Rows& r) {
+  const Rows block = {base, 1, 1, 0, 0, bytes};
+  if (bytes == 0 || r.n == 0 || apart(block, r)) return false;
+  for (int64_t h = 0; h < r.heads; ++h) {
+    const int64_t at = r.at() + h * r.head - block.at();  // row 0 of this head; the first that ends behind the block's start
+    const int64_t t = r.token > 0 && at + r.width <= 0 ? -(at + r.width) / r.token + 1 : 0;
+    const int64_t from = at + t * r.token;
+    if (t < r.n && from < bytes && from + r.width > 0) return true;
+  }
+  return false;
+}
+
 // Sizes only: enough to compute a workspace.
 int check_attention_sizes(const fps_attention_args* a) {
   if (!a) return FPS_ERR_ARG;
@@ -89,6 +140,13 @@ int make_call(const fps_attention_args* a, AttnCall* c) {
   return FPS_OK;
 }
 
+// Whether `bytes` that the call writes meet what it reads.
+bool meets_input(const AttnCall& c, const void* base, int64_t bytes) {
+  return block_meets(base, bytes, rows_of(c.q, c.n_q, c.heads, c.q_token, c.q_head, c.D, 2)) ||
+         block_meets(base, bytes, rows_of(c.k, c.n_kv, c.kv_heads, c.k_token, c.k_head, c.D, 2)) ||
+         block_meets(base, bytes, rows_of(c.v, c.n_kv, c.kv_heads, c.v_token, c.v_head, c.D, 2));
+}
+
 }  // namespace
 
 }  // namespace fpstok
@@ -145,6 +203,14 @@ int fps_rotary(const void* x, void* y, int dtype, int64_t T, int H, int D, int64
   if (position_stride < table->axes || x_token_stride < 0 || x_head_stride < 0) return FPS_ERR_ARG;
   if ((T > 1 && y_token_stride < D) || (H > 1 && y_head_stride < D)) return FPS_ERR_ARG;
   if (x == y && (x_token_stride != y_token_stride || x_head_stride != y_head_stride)) return FPS_ERR_ARG;
+  const Rows from = rows_of(x, T, H, x_token_stride, x_head_stride, D, size);
+  const Rows to = rows_of(y, T, H, y_token_stride, y_head_stride, D, size);
+  if (rows_meet(to)) return FPS_ERR_ARG;
+  // x and y among one another with the same strides, such as other heads of the
+  // same rows; with other strides only clear of one another
+  if (x != y && !apart(from, to) &&
+      (from.token != to.token || from.head != to.head || rows_meet(to, from.at() - to.at())))
+    return FPS_ERR_ARG;
   RotaryCall c = {x,           y, dtype, T, H, D, x_token_stride, x_head_stride, y_token_stride, y_head_stride,
                   positions, position_stride, inverse != 0};
   return from_cuda(launch_rotary(c, *table, reinterpret_cast<cudaStream_t>(stream)));
@@ -164,6 +230,7 @@ int fps_attention(const fps_attention_args* args, void* out, float* lse, void* w
   if (c.n_q > 0 && (!out || !aligned(out, 16) || !aligned(lse, 4))) return FPS_ERR_ARG;
   const size_t need = fps_attention_workspace_bytes(args, 0);
   if (!workspace || workspace_bytes < need || !aligned(workspace, 256)) return FPS_ERR_WORKSPACE;
+  if (meets_input(c, out, c.n_q * c.heads * c.D * 2)) return FPS_ERR_ARG;
   c.out = out;
   c.lse = lse;
   return from_cuda(launch_attention_forward(c, workspace, reinterpret_cast<cudaStream_t>(stream)));
@@ -181,6 +248,17 @@ int fps_attention_backward(const fps_attention_args* args, const void* out, cons
   if (c.n_kv > 0 && (!dk || !dv || !aligned(dk, 16) || !aligned(dv, 16))) return FPS_ERR_ARG;
   const size_t need = fps_attention_workspace_bytes(args, 1);
   if (!workspace || workspace_bytes < need || !aligned(workspace, 256)) return FPS_ERR_WORKSPACE;
+  const int64_t q_bytes = c.n_q * c.heads * c.D * 2, kv_bytes = c.n_kv * c.kv_heads * c.D * 2;
+  const Rows of_out = rows_of(out, 1, 1, 0, 0, q_bytes, 1), of_dq = rows_of(dq, 1, 1, 0, 0, q_bytes, 1);
+  const Rows of_dk = rows_of(dk, 1, 1, 0, 0, kv_bytes, 1);
+  const Rows of_dout = rows_of(dout, c.n_q, c.heads, dout_token_stride, dout_head_stride, c.D, 2);
+  for (int i = 0; i < 3; ++i) {
+    const void* base = i == 0 ? dq : i == 1 ? dk : dv;
+    const int64_t bytes = i == 0 ? q_bytes : kv_bytes;
+    if (meets_input(c, base, bytes) || block_meets(base, bytes, of_out) || block_meets(base, bytes, of_dout) ||
+        (i > 0 && block_meets(base, bytes, of_dq)) || (i > 1 && block_meets(base, bytes, of_dk)))
+      return FPS_ERR_ARG;
+  }
   c.out = const_cast<void*>(out);
   c.lse = const_cast<float*>(lse);
   c.dout = dout;

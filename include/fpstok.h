@@ -380,7 +380,9 @@ int fps_rotary_table_init(fps_rotary_table *table, const int *axis_dims, int axe
 /*
  * x, y: [T, H, D] of `dtype`, values of a head contiguous, the other strides
  * in elements.  y may be x with the same strides (in place); otherwise they
- * do not overlap.  positions: float32 [T, table->axes], rows position_stride
+ * do not overlap (with the same strides their rows may lie among one another,
+ * as other heads of the same rows do; with others not), nor do the rows of y.
+ * An argument error where they do.  positions: float32 [T, table->axes], rows position_stride
  * floats apart.  inverse != 0 turns by -theta: the gradient of the forward.
  * 2 * pairs <= D <= FPS_MAX_ROTARY_DIM.  No workspace.
  */

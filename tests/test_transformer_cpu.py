@@ -151,3 +151,50 @@ def test_recorded_traffic_is_of_these_sources():
         sys.path.remove(root)
     with open(os.path.join(root, "profiles", "traffic.md")) as fh:
         assert bench.kernel_source_hash() in fh.read()
+
+
+def test_rotary_refuses_outputs_that_overlap():
+    """Element sizes of 2: a row of D = 16 values takes 32 bytes."""
+    lib = fps.load_library()
+    t = fps.RotaryTable((4, 4)).c
+
+    def call(y, xs, ys, T=5, H=2, x=4096):
+        return lib.fps_rotary(ctypes.c_void_p(x), ctypes.c_void_p(y), 1, T, H, 16, *xs, *ys, X, 2, ctypes.byref(t), 0, None)
+
+    far = 1 << 20
+    # rows of y over one another: both strides D, a head stride that meets the next row, and no stride at all
+    for ys, T, H in (((16, 16), 5, 2), ((48, 40), 5, 2), ((40, 48), 5, 3), ((16, 64), 5, 2), ((16, 32), 3, 2), ((48, 64), 5, 4), ((17, 16), 2, 2)):
+        assert call(far, (32, 16), ys, T, H) == _lib.FPS_ERR_ARG, (ys, T, H)
+    # y a little behind or before x: by values, by heads, by rows
+    for off in (2, 16, 30, -2, 32, -32, 64, -64, 4 * 64, -4 * 64, 4 * 64 + 32 + 30):
+        assert call(4096 + off, (32, 16), (32, 16)) == _lib.FPS_ERR_ARG, off
+    # the heads beside x of the same rows, one too few
+    assert call(4096 + 32, (96, 16), (96, 16)) == _lib.FPS_ERR_ARG
+    # within each other's reach with other strides
+    assert call(4096 + 32, (96, 16), (192, 16)) == _lib.FPS_ERR_ARG
+    assert call(4096 + 64, (0, 0), (32, 16), x=4096 + 64 + 32) == _lib.FPS_ERR_ARG
+
+
+def test_attention_refuses_outputs_over_inputs():
+    lib = fps.load_library()
+    # q [10, 4, 64], k and v [10, 2, 64]: 512 and 256 bytes a row
+    at = dict(q=1 << 16, k=1 << 17, v=1 << 18)
+    a = _args(**at)
+    ref = ctypes.byref(a)
+    ptr = lambda p: ctypes.c_void_p(p)  # noqa: E731
+    far = [ptr((1 << 20) + (i << 16)) for i in range(6)]
+    size = {"q": 5120, "k": 2560, "v": 2560}
+    for name, p in at.items():
+        for out in (p, p + size[name] - 16, p - 5120 + 16):
+            assert lib.fps_attention(ref, ptr(out), far[0], far[1], 1 << 40, None) == _lib.FPS_ERR_ARG, (name, out - p)
+
+    def backward(out=far[0], dout=far[1], dq=far[2], dk=far[3], dv=far[4]):
+        return lib.fps_attention_backward(ref, out, far[5], dout, 256, 64, dq, dk, dv, X, 1 << 40, None)
+
+    for p in (*(ptr(x) for x in at.values()), far[0], far[1]):
+        for name in ("dq", "dk", "dv"):
+            assert backward(**{name: p}) == _lib.FPS_ERR_ARG, (name, p)
+    assert backward(dq=far[3]) == backward(dv=far[3]) == backward(dv=far[2]) == _lib.FPS_ERR_ARG
+    # a head of the queries' own row between two that q reads
+    a = _args(**{**at, "q_token_stride": 1024, "q_head_stride": 128, "n_q": 1, "heads": 2})
+    assert lib.fps_attention(ctypes.byref(a), ptr(at["q"] + 16), far[0], far[1], 1 << 40, None) == _lib.FPS_ERR_ARG
