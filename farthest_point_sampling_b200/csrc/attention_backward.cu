@@ -44,7 +44,8 @@
 // writes.  Short items add the latency of filling the pipeline: 2048 events of up
 // to 256 tokens, 8 heads of 64: 1.79 ms, 2.0 TB/s.
 //
-// Rounding: P and dS are rounded to the input type for their products.  D
+// Rounding: P and dS are rounded to the input type for their products, in
+// float16 scaled into its range (attention_backward_range.cu).  D
 // comes from the rounded output, as the forward left it, but for queries that
 // see few keys, where that would show (attention_backward_rows.cu).
 #include <type_traits>
@@ -72,9 +73,11 @@ struct BwdArgs {
   float scale, scale_log2;
   const void* out;
   const float* lse;
-  // [2][heads, n_q]: -lse log2(e) and -D, written by the queries kernel for the
-  // keys kernel; of queries that see few keys -D is there before
+  // [2][heads, n_q]: -lse log2(e) and -D (float16: the one 14 more, the other
+  // times the event's c), written by the queries kernel for the keys kernel; of
+  // queries that see few keys -D is there before
   float* rows;
+  const float* range;  // float16: see attention_backward_range.cu
   float* partial;  // [slot][key head][128][2 DP]: dK and dV of the pieces of a key tile
   void* d1;      // dQ, or dK
   void* d2;      // dV
@@ -85,8 +88,8 @@ struct BwdArgs {
 };
 
 // One work item as the loading warp hands it to the others.
-template <int kStream>
-struct BwdItem {
+template <int kStream, bool kScaled>
+struct BwdItem : ItemScale<kScaled> {
   int count;            // streamed tiles of one head; -1 ends the work
   int f0, f1;           // which of those of all heads in turn this item takes
   int hd, j;            // the first one's head in the group, and its place among the head's
@@ -98,9 +101,9 @@ struct BwdItem {
   int shift;            // nk - nq: position of query 0
   KeyTiles<kStream> tiles;
 };
-template <bool kKeys, int kStream>
-__device__ __forceinline__ BwdItem<kStream> bwd_item(const BwdArgs& a, int h, const TileItem& e) {
-  BwdItem<kStream> w;
+template <bool kKeys, bool kScaled, int kStream>
+__device__ __forceinline__ BwdItem<kStream, kScaled> bwd_item(const BwdArgs& a, int h, const TileItem& e) {
+  BwdItem<kStream, kScaled> w;
   w.h = h;
   w.at = e.t * kTile;
   w.kept_row = (kKeys ? e.k0 : e.q0) + w.at;
@@ -123,6 +126,8 @@ __device__ __forceinline__ BwdItem<kStream> bwd_item(const BwdArgs& a, int h, co
   w.f1 = w.count * (kKeys ? a.group : 1);
   w.slot = -1;
   w.hd = w.j = 0;
+  if constexpr (kScaled)  // no pair, maybe no first query, and no use of it
+    w.set(w.count > 0 ? range_scale(a.range[e.q0], a.range[a.n_q + e.q0]) : 1.f);
   if (kKeys && e.pad[2] != -1) {  // a piece
     w.f0 = e.pad[0];
     w.f1 = e.pad[1];
@@ -155,7 +160,7 @@ struct BwdShape {
   static constexpr int kAcc = kColAcc + 2 * kAccColumns <= kColumns ? 2 : 1;
   static constexpr size_t kColFloats = kRing * 2 * kStream > 2 * kTile ? kRing * 2 * kStream : 2 * kTile;
   static constexpr size_t kSmem = 1024 + 2 * (kKept * kKeptBytes + kRing * kStreamBytes) + kColFloats * sizeof(float) +
-                                  kItemRing * sizeof(BwdItem<kStream>) + 512;
+                                  kItemRing * sizeof(BwdItem<kStream, true>) + 512;
 };
 
 // 4 bytes from global to shared memory, asynchronously; zero where not real.
@@ -173,7 +178,7 @@ __global__ void __launch_bounds__(BwdShape<DP, kKeys>::kThreads, BwdShape<DP, kK
     k_attn_backward(const BwdArgs a, const __grid_constant__ CUtensorMap map_k1, const __grid_constant__ CUtensorMap map_k2,
                     const __grid_constant__ CUtensorMap map_s1, const __grid_constant__ CUtensorMap map_s2) {
   using Sh = BwdShape<DP, kKeys>;
-  using Item = BwdItem<Sh::kStream>;
+  using Item = BwdItem<Sh::kStream, !std::is_same<T, __nv_bfloat16>::value>;
   constexpr int kStream = Sh::kStream, kSoftmaxThreads = Sh::kSoftmaxThreads;
   constexpr uint32_t kColS = Sh::kColS, kColDP = Sh::kColDP, kColAcc = Sh::kColAcc;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
@@ -247,7 +252,7 @@ __global__ void __launch_bounds__(BwdShape<DP, kKeys>::kThreads, BwdShape<DP, kK
       int h;
       bool more;
       while ((more = claims.take(&entry, &h))) {
-        w = bwd_item<kKeys, kStream>(a, h, entry);
+        w = bwd_item<kKeys, !kBf16, kStream>(a, h, entry);
         if (w.slot == -2) continue;
         if (w.f1 > w.f0) break;
         const int heads = kKeys ? a.kv_heads : a.heads;
@@ -462,7 +467,8 @@ __global__ void __launch_bounds__(BwdShape<DP, kKeys>::kThreads, BwdShape<DP, kK
       const Item& w = s_item[slot];  // read where it is needed: it stays until this thread lets go of the slot
       const int count = w.count;
       if (count < 0) break;
-      float lse2 = 0.f, delta = 0.f;  // -lse log2(e) and -D of this thread's query
+      float lse2 = 0.f, delta = 0.f;  // -lse log2(e) and -D of this thread's query, as in a.rows
+      const uint64_t c2 = pack2(w.c, w.c);
       if constexpr (!kKeys) {
         // D: O as read ahead, dO from its tile; shared with the keys kernel
         // through memory and with the threads of each row through the block's
@@ -488,7 +494,11 @@ __global__ void __launch_bounds__(BwdShape<DP, kKeys>::kThreads, BwdShape<DP, kK
             }
           }
           sum += __shfl_xor_sync(kFull, sum, 1);
-          const float mine = given[r] ? lse[r] : lane & 1 ? -sum : -lse[r] * kLog2e;
+          float mine;
+          if constexpr (kBf16)
+            mine = given[r] ? lse[r] : lane & 1 ? -sum : -lse[r] * kLog2e;
+          else
+            mine = lane & 1 ? (given[r] ? lse[r] : -sum) * w.c : kWeightShift - lse[r] * kLog2e;
           s_col[(lane & 1) * kTile + q] = mine;
           if (q < w.rows) a.rows[((int64_t)(lane & 1) * a.heads + w.h) * a.n_q + w.kept_row + q] = mine;
         }
@@ -587,10 +597,10 @@ __global__ void __launch_bounds__(BwdShape<DP, kKeys>::kThreads, BwdShape<DP, kK
             for (int k = 0; k < 32; k += 4) {
               float4 de = make_float4(delta, delta, delta, delta);
               if constexpr (kKeys) de = *reinterpret_cast<const float4*>(col + kStream + 32 * c + k);
-              const uint64_t y0 = mul2(add2(pack2(y[k], y[k + 1]), pack2(de.x, de.y)),
-                                       pack2(x[32 * c + k], x[32 * c + k + 1]));
-              const uint64_t y1 = mul2(add2(pack2(y[k + 2], y[k + 3]), pack2(de.z, de.w)),
-                                       pack2(x[32 * c + k + 2], x[32 * c + k + 3]));
+              const uint64_t p0 = pack2(y[k], y[k + 1]), p1 = pack2(y[k + 2], y[k + 3]);
+              const uint64_t d0 = pack2(de.x, de.y), d1 = pack2(de.z, de.w);
+              const uint64_t y0 = mul2(kBf16 ? add2(p0, d0) : fma2(p0, c2, d0), pack2(x[32 * c + k], x[32 * c + k + 1]));
+              const uint64_t y1 = mul2(kBf16 ? add2(p1, d1) : fma2(p1, c2, d1), pack2(x[32 * c + k + 2], x[32 * c + k + 3]));
               y[k] = lo2(y0);
               y[k + 1] = hi2(y0);
               y[k + 2] = lo2(y1);
@@ -619,6 +629,7 @@ __global__ void __launch_bounds__(BwdShape<DP, kKeys>::kThreads, BwdShape<DP, kK
       float* sums = kKeys && w.slot >= 0
                         ? a.partial + (((int64_t)w.slot * a.kv_heads + w.h) * kTile + row) * (2 * DP)
                         : nullptr;
+      const float back = w.back;  // a power of two, as kBackP, so that the products with them are exact
       mbar_arrive(item_empty + 8 * slot);
       if (!kKeys && !(ok = ahead(i + 1))) break;
       const int acc = nk % Sh::kAcc;
@@ -635,14 +646,17 @@ __global__ void __launch_bounds__(BwdShape<DP, kKeys>::kThreads, BwdShape<DP, kK
             tmem_ld32(from + x * DP + c, v);
             tmem_wait_ld32(v);
 #pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (!kBf16) v[k] = __float_as_uint(__uint_as_float(v[k]) * (x == 0 ? back : Item::kBackP));
+#pragma unroll
             for (int k = 0; k < 32; k += 4)
               if (live) *reinterpret_cast<uint4*>(sums + x * DP + c + k) = make_uint4(v[k], v[k + 1], v[k + 2], v[k + 3]);
           }
         } else if constexpr (kKeys)
-          store_row<T, DP>(from + x * DP, live, x == 0 ? a.scale : 1.f, static_cast<T*>(x == 0 ? a.d1 : a.d2) + at, a.D,
+          store_row<T, DP>(from + x * DP, live, x == 0 ? a.scale * back : Item::kBackP, static_cast<T*>(x == 0 ? a.d1 : a.d2) + at, a.D,
                            a.sectors);
         else
-          store_row<T, DP / 2>(from + x * (DP / 2), live, a.scale, static_cast<T*>(a.d1) + at + x * (DP / 2),
+          store_row<T, DP / 2>(from + x * (DP / 2), live, a.scale * back, static_cast<T*>(a.d1) + at + x * (DP / 2),
                                a.D - x * (DP / 2), a.sectors);
       }
       tc_fence_before();
@@ -721,7 +735,7 @@ struct BwdWorkspace {
   JoinItem* joins;
   float* partial;
   Pieces pieces;
-  float* rows;
+  float *rows, *range;
   size_t bytes;
 };
 BwdWorkspace carve_backward(void* base, const AttnCall& c) {
@@ -744,6 +758,7 @@ BwdWorkspace carve_backward(void* base, const AttnCall& c) {
       take((size_t)w.pieces.slots * c.kv_heads * kTile * 2 * (c.D <= 64 ? 64 : 128) * sizeof(float)));
   w.shorts = reinterpret_cast<TileItem*>(take((size_t)(B + 1) * sizeof(TileItem)));
   w.rows = reinterpret_cast<float*>(take((size_t)n_q * heads * 2 * sizeof(float)));
+  if (c.dtype == FPS_DTYPE_F16) w.range = reinterpret_cast<float*>(take((size_t)n_q * 2 * sizeof(float)));
   w.bytes = off;
   return w;
 }
@@ -785,6 +800,7 @@ cudaError_t run_tiles(const AttnCall& c, const BwdWorkspace& ws, const BwdMaps& 
   a.out = c.out;
   a.lse = c.lse;
   a.rows = ws.rows;
+  a.range = ws.range;
   a.hdr = ws.hdr;
   a.test = c.test;
   a.sectors = m.sectors;
@@ -839,6 +855,7 @@ cudaError_t launch_attention_backward(const AttnCall& c, void* workspace, cudaSt
   lists.slots = ws.pieces.slots;
   lists.stream = c.D <= 64 ? 64 : 128;
   lists.key_joins = ws.joins;
+  lists.range = ws.range;
   cudaError_t e = launch_attention_plan(c, ws.hdr, lists, s);
   if (e != cudaSuccess || (c.n_q == 0 && c.n_kv == 0)) return e;
   const bool bf16 = c.dtype == FPS_DTYPE_BF16;
@@ -856,7 +873,10 @@ cudaError_t launch_attention_backward(const AttnCall& c, void* workspace, cudaSt
                31) == 0 &&
               c.D % 16 == 0;
   if (c.n_q > 0 && (e = launch_attention_backward_rows(c, ws.rows, s)) != cudaSuccess) return e;
-  if ((e = launch_attention_backward_short(c, m, ws.rows, ws.shorts, ws.hdr, s)) != cudaSuccess) return e;
+  if (ws.range && c.n_q > 0 && c.n_kv > 0 &&
+      (e = launch_attention_backward_range(c, ws.range, ws.queries, ws.keys, ws.shorts, ws.hdr, s)) != cudaSuccess)
+    return e;
+  if ((e = launch_attention_backward_short(c, m, ws.rows, ws.range, ws.shorts, ws.hdr, s)) != cudaSuccess) return e;
   if (c.max_tokens > 0 && c.max_tokens <= kTile) return cudaSuccess;  // every event is short
   if (bf16) return c.D <= 64 ? run_tiles<__nv_bfloat16, 64>(c, ws, m, s) : run_tiles<__nv_bfloat16, 128>(c, ws, m, s);
   return c.D <= 64 ? run_tiles<__half, 64>(c, ws, m, s) : run_tiles<__half, 128>(c, ws, m, s);

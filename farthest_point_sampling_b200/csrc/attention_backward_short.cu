@@ -55,6 +55,7 @@ struct ShortArgs {
   const void* out;
   const float* lse;
   const float* rows;  // [2][heads, n_q]: the second half holds -D of queries that see few keys
+  const float* range;  // float16: see attention_backward_range.cu
   void *dq, *dk, *dv;
   const int64_t *q_offsets, *kv_offsets;
   int B;
@@ -65,7 +66,8 @@ struct ShortArgs {
 };
 
 // One work item as the loading warp hands it to the others; nq = -1 ends the work.
-struct ShortItem {
+template <bool kScaled>
+struct ShortItem : ItemScale<kScaled> {
   int h, q_row, nq, k_row, nk;  // key head; the event's first query and key rows, queries, keys
 };
 
@@ -79,7 +81,7 @@ struct ShortShape {
   static constexpr uint32_t kColDV = 256, kColDK = kTwo ? kColDP : 256 + DP;
   static constexpr uint32_t kColDQ = kTwo ? kColDP + 64 : DP == 64 ? kColDK + DP : kColDP;
   static constexpr size_t kSmem = 1024 + 4 * kStages * kTileBytes + 2 * kPanel + 2 * kTile * sizeof(float) +
-                                  kItemRing * sizeof(ShortItem) + 512;
+                                  kItemRing * sizeof(ShortItem<true>) + 512;
 };
 
 template <typename T, int DP, bool kTwo>
@@ -97,7 +99,8 @@ __global__ void __launch_bounds__(kShortThreads, kTwo ? 2 : 1)
   uint8_t* s_qd = s_kv + 2 * kStages * Sh::kTileBytes;         // [stage][Q, dO]
   uint8_t* s_ds = s_qd + 2 * kStages * Sh::kTileBytes;         // dS: key rows, a panel for each half of the queries
   float* s_col = reinterpret_cast<float*>(s_ds + 2 * kPanel);  // [-lse log2(e), -D][128 queries]
-  ShortItem* s_item = reinterpret_cast<ShortItem*>(s_col + 2 * kTile);
+  using Item = ShortItem<!kBf16>;
+  Item* s_item = reinterpret_cast<Item*>(s_col + 2 * kTile);
   uint64_t* s_bar = reinterpret_cast<uint64_t*>((reinterpret_cast<uintptr_t>(s_item + kItemRing) + 7) & ~(uintptr_t)7);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(s_bar + 32);
   volatile WaitState* s_wait = reinterpret_cast<volatile WaitState*>(s_tmem + 1);
@@ -157,7 +160,14 @@ __global__ void __launch_bounds__(kShortThreads, kTwo ? 2 : 1)
       }
       const int slot = i % kItemRing;
       if (i >= kItemRing && !mbar_wait_warp(item_empty + 8 * slot, ((i / kItemRing) - 1) & 1, s_wait)) break;
-      if (lane == 0) s_item[slot] = more ? ShortItem{h, e.q0, e.nq, e.k0, e.nk} : ShortItem{0, 0, -1, 0, 0};
+      Item w;
+      w.h = h;
+      w.q_row = e.q0;
+      w.nq = more ? e.nq : -1;
+      w.k_row = e.k0;
+      w.nk = e.nk;
+      if constexpr (!kBf16) w.set(more ? range_scale(a.range[e.q0], a.range[a.n_q + e.q0]) : 1.f);
+      if (lane == 0) s_item[slot] = w;
       __syncwarp();
       mbar_arrive_one(item_full + 8 * slot);
       if (!more) break;
@@ -261,12 +271,13 @@ __global__ void __launch_bounds__(kShortThreads, kTwo ? 2 : 1)
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
     const float2 scale2 = make_float2(a.scale_log2, a.scale_log2);
     uint8_t* ds_row = s_ds + half * kPanel + row * 128;
+    constexpr float kBackP = Item::kBackP;
     int n = 0, u = 0;
     bool ok = true;
     for (int i = 0; ok; ++i) {
       const int slot = i % kItemRing;
       if (!(ok = mbar_wait_warp(item_full + 8 * slot, (i / kItemRing) & 1, s_wait))) break;
-      const ShortItem w = s_item[slot];
+      const Item w = s_item[slot];
       if (w.nq < 0) break;
       mbar_arrive(item_empty + 8 * slot);
       T* dq = static_cast<T*>(a.dq) + (((int64_t)w.q_row + row) * a.heads + w.h * a.group) * a.D;
@@ -318,7 +329,10 @@ __global__ void __launch_bounds__(kShortThreads, kTwo ? 2 : 1)
           }
         }
         delta += __shfl_xor_sync(kFull, delta, 1);
-        s_col[(lane & 1) * kTile + q] = given() ? lse : lane & 1 ? -delta : -lse * kLog2e;
+        if constexpr (kBf16)
+          s_col[(lane & 1) * kTile + q] = given() ? lse : lane & 1 ? -delta : -lse * kLog2e;
+        else
+          s_col[(lane & 1) * kTile + q] = lane & 1 ? (given() ? lse : -delta) * w.c : kWeightShift - lse * kLog2e;
         mbar_arrive(col_full);
         if (!(ok = mbar_wait_warp(scores_full, u & 1, s_wait))) break;
         if (!(ok = mbar_wait_warp(col_full, u & 1, s_wait))) break;
@@ -347,8 +361,10 @@ __global__ void __launch_bounds__(kShortThreads, kTwo ? 2 : 1)
               x[k + 1] = exp2_approx(e0.y);
               x[k + 2] = exp2_approx(e1.x);
               x[k + 3] = exp2_approx(e1.y);
-              const uint64_t y0 = mul2(add2(pack2(y[k], y[k + 1]), pack2(de.x, de.y)), pack2(x[k], x[k + 1]));
-              const uint64_t y1 = mul2(add2(pack2(y[k + 2], y[k + 3]), pack2(de.z, de.w)), pack2(x[k + 2], x[k + 3]));
+              const uint64_t p0 = pack2(y[k], y[k + 1]), p1 = pack2(y[k + 2], y[k + 3]);
+              const uint64_t d0 = pack2(de.x, de.y), d1 = pack2(de.z, de.w), c2 = pack2(w.c, w.c);
+              const uint64_t y0 = mul2(kBf16 ? add2(p0, d0) : fma2(p0, c2, d0), pack2(x[k], x[k + 1]));
+              const uint64_t y1 = mul2(kBf16 ? add2(p1, d1) : fma2(p1, c2, d1), pack2(x[k + 2], x[k + 3]));
               y[k] = lo2(y0);
               y[k + 1] = hi2(y0);
               y[k + 2] = lo2(y1);
@@ -383,15 +399,16 @@ __global__ void __launch_bounds__(kShortThreads, kTwo ? 2 : 1)
         // head dK and dV
         if (!(ok = mbar_wait_warp(done, u & 1, s_wait))) break;
         tc_fence_after();
-        store_row<T, DP / 2>(lanes + Sh::kColDQ + half * (DP / 2), row < w.nq, a.scale, dq + m * a.D + half * (DP / 2),
+        const float back = a.scale * w.back;  // of dQ and dK
+        store_row<T, DP / 2>(lanes + Sh::kColDQ + half * (DP / 2), row < w.nq, back, dq + m * a.D + half * (DP / 2),
                              a.D - half * (DP / 2), a.sectors);
         if (kTwo) {  // half of dV's columns are in each half of the scores
-          store_row<T, 32>(lanes + Sh::kColDK + half * 32, row < w.nk, a.scale, static_cast<T*>(a.dk) + key_at + half * 32,
+          store_row<T, 32>(lanes + Sh::kColDK + half * 32, row < w.nk, back, static_cast<T*>(a.dk) + key_at + half * 32,
                            a.D - half * 32, a.sectors);
-          store_row<T, 32>(lanes + kColS + 32 + half * 64, row < w.nk, 1.f, static_cast<T*>(a.dv) + key_at + half * 32,
+          store_row<T, 32>(lanes + kColS + 32 + half * 64, row < w.nk, kBackP, static_cast<T*>(a.dv) + key_at + half * 32,
                            a.D - half * 32, a.sectors);
         } else if (m == a.group - 1) {
-          store_row<T, DP>(lanes + (half == 0 ? Sh::kColDK : Sh::kColDV), row < w.nk, half == 0 ? a.scale : 1.f,
+          store_row<T, DP>(lanes + (half == 0 ? Sh::kColDK : Sh::kColDV), row < w.nk, half == 0 ? back : kBackP,
                            static_cast<T*>(half == 0 ? a.dk : a.dv) + key_at, a.D, a.sectors);
         }
         tc_fence_before();
@@ -444,8 +461,8 @@ cudaError_t run_type(const ShortArgs& a, const BwdMaps& m, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_attention_backward_short(const AttnCall& c, const BwdMaps& maps, const float* rows, const TileItem* items,
-                                            WsHeader* hdr, cudaStream_t s) {
+cudaError_t launch_attention_backward_short(const AttnCall& c, const BwdMaps& maps, const float* rows, const float* range,
+                                            const TileItem* items, WsHeader* hdr, cudaStream_t s) {
   ShortArgs a;
   a.n_q = c.n_q;
   a.n_kv = c.n_kv;
@@ -459,6 +476,7 @@ cudaError_t launch_attention_backward_short(const AttnCall& c, const BwdMaps& ma
   a.out = c.out;
   a.lse = c.lse;
   a.rows = rows;
+  a.range = range;
   a.dq = c.dq;
   a.dk = c.dk;
   a.dv = c.dv;

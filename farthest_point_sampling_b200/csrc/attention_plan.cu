@@ -136,6 +136,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_attn_plan(const int64_t* __res
         e.nq = (int)(q1 - q0);
         e.k0 = (int)k0;
         e.nk = (int)(k1 - k0);
+        if (lists.range && kind == kPlanQueries && e.nq > 0) lists.range[e.q0] = lists.range[n_q + e.q0] = 0.f;
         const bool few = lists.units && (int64_t)e.nq * group <= kFewRows;
         const bool brief = lists.shorts && e.nq <= kTile && e.nk <= kTile;
         if (kind == kPlanQueries) {

@@ -43,6 +43,7 @@ struct PlanLists {
   JoinItem* key_joins;  // per slot: at a tile's first one its rows and how many, else none
   TileItem* shorts;   // the events of at most 128 queries and 128 keys, which then have no tiles of either kind
   PlanRows of_queries, of_keys;  // what the call writes
+  float* range;  // [2][n_q]: set to 0 at every event's first query
 };
 
 // Fills the lists, 1024 events at a time and long ones of these first, their

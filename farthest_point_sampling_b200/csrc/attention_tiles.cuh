@@ -210,6 +210,11 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
       : "l"(pack2(a.x, a.y)), "l"(pack2(b.x, b.y)), "l"(pack2(c.x, c.y)));
   return make_float2(lo2(d), hi2(d));
 }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   const uint64_t d = add2(pack2(a.x, a.y), pack2(b.x, b.y));
   return make_float2(lo2(d), hi2(d));
@@ -228,6 +233,15 @@ __device__ __forceinline__ float rcp_approx(float x) {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+
+// The largest power of two c <= 1 / M, M^2 being the product of an event's
+// largest |dO_i|^2 and |V_j|^2: M < 2^((x + 1) / 2) with x = floor(log2 M^2).
+__device__ __forceinline__ float range_scale(float dout2, float v2) {
+  const float m2 = dout2 * v2;  // from 2^-96 to 2^78 for float16 values
+  if (!(m2 > 0.f)) return 1.f;
+  const int e = (((__float_as_int(m2) >> 23) - 127) + 2) >> 1;
+  return __int_as_float((127 - e) << 23);
+}
 
 // One row's kCols float32 accumulator columns from TMEM to memory, times f,
 // rounded: whole 32-byte sectors per thread where rows start on them, else 16

@@ -411,7 +411,9 @@ int fps_rotary(const void *x, void *y, int dtype, int64_t T, int H, int D, int64
  *
  * Scores, the running maximum and sum, outputs and gradients accumulate in
  * float32; softmax weights and score gradients are rounded to `dtype` for
- * their matrix products; every output is rounded once.
+ * their matrix products (the backward pass in F16: after powers of two that
+ * bring each event's into the type's normal range); every output is rounded
+ * once.
  *
  * Rows of out and lse that belong to no event (behind q_offsets[events]) are
  * left as they were, or out rows set to 0 when zero_tail is set; gradient
