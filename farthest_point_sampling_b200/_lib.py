@@ -32,6 +32,8 @@ FPS_DTYPE_F16 = 2
 FPS_MAX_ROTARY_DIM = 256
 FPS_MAX_ROTARY_AXES = 8
 FPS_MAX_ATTENTION_DIM = 128
+FPS_TAIL_OUT = 1
+FPS_TAIL_LSE = 2
 
 # (name, restype, argtypes) of every exported symbol, mirroring fpstok.h.
 SIGNATURES = [

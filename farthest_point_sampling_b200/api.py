@@ -675,7 +675,7 @@ def attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, tok_off
     """C ``fps_attention``: returns ``(out [n_q, H, D], lse [H, n_q])`` (lse
     None without ``need_lse``); see :func:`packed_attention`.  Rows of a given
     ``out`` that belong to no event are left as they were; in a new one they
-    are 0.  ``out`` must not overlap the inputs.  Not recorded by autograd."""
+    are 0, and their lse is -inf.  ``out`` must not overlap the inputs.  Not recorded by autograd."""
     a, dev = _attention_args(q, k, v, tok_offsets, kv_offsets, scale, causal, window, sinks, max_tokens)
     return _attention_forward(a, dev, q, need_lse, workspace, out, check_device)
 
@@ -689,11 +689,12 @@ def _attention_workspace(nbytes: int, dev: torch.device, workspace: Optional[tor
 def _attention_forward(a, dev, q, need_lse, workspace, out, check_device):
     if out is None:
         out = torch.empty_like(q) if q.is_contiguous() else torch.empty(q.shape, dtype=q.dtype, device=dev)
-        a.zero_tail = 1
+        a.zero_tail = _lib.FPS_TAIL_OUT + _lib.FPS_TAIL_LSE
     else:
         _need(out, "out", q.dtype, 3, dev)
         if out.shape != q.shape or out.data_ptr() % 16:
             raise ValueError("out must have the shape of q and start on 16 bytes")
+        a.zero_tail = _lib.FPS_TAIL_LSE
     lib = _lib.load()
     lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=dev) if need_lse else None
     ref = ctypes.byref(a)

@@ -258,7 +258,8 @@ __global__ void __launch_bounds__(kFewThreads, FewShape<DP>::kBlocks) k_attn_few
         reinterpret_cast<uint4*>(w_o)[e] = make_uint4(0, 0, 0, 0);
     __syncthreads();
   }
-  if (a.zero_tail && rows_known(a.hdr)) zero_rows(a.out, a.B > 0 ? a.q_offsets[a.B] : 0, a.n_q, (int64_t)a.heads * a.D);
+  if (a.zero_tail && rows_known(a.hdr))
+    clear_tail(a.zero_tail, a.out, a.lse, a.B > 0 ? a.q_offsets[a.B] : 0, a.n_q, a.heads, a.D);
 }
 
 // Joins the chunks of one event and head: sum_c 2^(m_c - M) (l_c, O_c); a

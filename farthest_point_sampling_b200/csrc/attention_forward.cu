@@ -417,7 +417,8 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
       if (lse && live) lse[lane] = l == 0.f ? -INFINITY : fmaf(m_used, a.scale, log2_approx(l) * kLn2);
     }
   }
-  if (a.zero_tail && rows_known(a.hdr)) zero_rows(a.out, a.B > 0 ? a.q_offsets[a.B] : 0, a.n_q, (int64_t)a.heads * a.D);
+  if (a.zero_tail && rows_known(a.hdr))
+    clear_tail(a.zero_tail, a.out, a.lse, a.B > 0 ? a.q_offsets[a.B] : 0, a.n_q, a.heads, a.D);
   tc_fence_before();
   __syncthreads();
   if (warp == kSoftmaxWarps + 1) {
@@ -486,7 +487,7 @@ cudaError_t run_forward(const AttnCall& c, const FwdWorkspace& ws, cudaStream_t 
   a.lse = c.lse;
   a.q_offsets = c.q_offsets;
   a.B = c.B;
-  a.zero_tail = c.zero_tail && !few_rows(c);  // the other kernel has done it
+  a.zero_tail = few_rows(c) ? 0 : c.zero_tail;  // the other kernel has done it
   a.sectors = reinterpret_cast<uintptr_t>(c.out) % 32 == 0 && c.D % 16 == 0;
   a.test = c.test;
   a.items = ws.items;

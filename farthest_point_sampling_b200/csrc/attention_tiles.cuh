@@ -345,4 +345,14 @@ __device__ __forceinline__ void zero_rows(void* base, int64_t first, int64_t n, 
     p[e] = make_uint4(0, 0, 0, 0);
 }
 
+// A forward's rows of no event, [first, n): out to 0 and lse to -inf, as
+// FPS_TAIL_* says.
+__device__ __forceinline__ void clear_tail(int which, void* out, float* lse, int64_t first, int64_t n, int heads, int D) {
+  if (which & FPS_TAIL_OUT) zero_rows(out, first, n, (int64_t)heads * D);
+  if (!(which & FPS_TAIL_LSE) || !lse || first < 0 || first >= n) return;
+#pragma unroll 1
+  for (int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; e < (n - first) * heads; e += (int64_t)gridDim.x * blockDim.x)
+    lse[e / (n - first) * n + first + e % (n - first)] = -INFINITY;
+}
+
 }  // namespace fpstok

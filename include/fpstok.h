@@ -391,6 +391,8 @@ int fps_rotary(const void *x, void *y, int dtype, int64_t T, int H, int D, int64
                int64_t position_stride, const fps_rotary_table *table, int inverse, fps_stream_t stream);
 
 #define FPS_MAX_ATTENTION_DIM 128
+#define FPS_TAIL_OUT 1 /* zero_tail: out rows that belong to no event become 0 */
+#define FPS_TAIL_LSE 2 /* and lse rows -inf */
 
 /*
  * Attention of packed events.  Event b holds queries q_offsets[b] ..
@@ -416,7 +418,7 @@ int fps_rotary(const void *x, void *y, int dtype, int64_t T, int H, int D, int64
  * once.
  *
  * Rows of out and lse that belong to no event (behind q_offsets[events]) are
- * left as they were, or out rows set to 0 when zero_tail is set; gradient
+ * left as they were, or set to 0 and to -inf where zero_tail says so; gradient
  * rows that belong to no event are set to 0.  Non-finite values of one event
  * do not reach another; within an event they may reach rows that do not see
  * them.
@@ -442,7 +444,7 @@ typedef struct fps_attention_args {
     int64_t sinks;  /* first keys of an event that every query may see, >= 0 */
     int max_tokens; /* upper bound on the queries and keys of any event, 0 = unknown; an event above it
                        is reported by fps_device_status() and its rows become NaN */
-    int zero_tail;
+    int zero_tail;  /* forward: FPS_TAIL_OUT + FPS_TAIL_LSE, or 0 */
 } fps_attention_args;
 
 /* Workspace bytes of the two calls below for these sizes and this mask

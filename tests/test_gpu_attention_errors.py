@@ -121,3 +121,19 @@ def test_the_backward_pass_reports():
         else:
             out.sum().backward()
             assert all(bool(t.grad.isnan().all()) for t in (q, k, v))
+
+
+@pytest.mark.parametrize("nq,nk", [([100, 30], [100, 30]), ([1, 1, 1], [40, 2000, 0]), ([], []), ([20, 1], [300, 5])])
+@pytest.mark.parametrize("given", [False, True])
+def test_lse_of_rows_behind_the_last_event(nq, nk, given):
+    """They see no key; what the memory held before does not show."""
+    tail = 7
+    qo, ko = _off(nq), _off(nk)
+    q = _rand((sum(nq) + tail, 4, 64), 29)
+    k, v = _rand((sum(nk) + tail, 2, 64), 30), _rand((sum(nk) + tail, 2, 64), 31)
+    for _ in range(3):
+        t = torch.full((4, len(q)), 3.0, device="cuda")
+        del t
+        out, lse = fps.attention_forward(q, k, v, qo, ko, out=torch.full_like(q, 7.0) if given else None)
+        assert bool(torch.isneginf(lse[:, -tail:]).all()) and not bool(lse.isnan().any())
+        assert bool((out[-tail:] == (7.0 if given else 0.0)).all())
