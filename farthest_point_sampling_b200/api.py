@@ -756,7 +756,9 @@ def packed_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, tok_offs
     differentiable with respect to ``q``, ``k`` and ``v``.
 
     ``q [n_q, H, D]``, ``k`` and ``v [n_kv, H_kv, D]`` in bfloat16 or float16
-    (H a multiple of H_kv: shared key heads); rows and heads may be strided.
+    (H a multiple of H_kv: shared key heads); rows and heads may be strided
+    (from 16-byte boundaries, by multiples of 8; an expanded tensor, whose
+    stride is 0, is refused: ``contiguous()`` gives it memory).
     ``tok_offsets [B + 1]`` delimits the events; ``kv_offsets`` when the keys
     have rows of their own (e.g. one summary query per event).  Query i of nq
     stands at position ``p = i + nk - nq`` of its event's nk keys and sees key

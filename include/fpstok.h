@@ -57,7 +57,9 @@
  * library never allocates, frees or synchronises.  Unless stated otherwise
  * pointers are DEVICE pointers and all work is enqueued on `stream`.  Scratch
  * space is the caller's `workspace` (device, 256-byte aligned) of at least the
- * size the matching *_workspace_bytes() call returns.
+ * size the matching *_workspace_bytes() call returns; it serves one call at a
+ * time (calls that may run together, on two streams or in two graphs, need one
+ * each).
  *
  * Errors: every call returns FPS_OK or an FPS_ERR_* code.  Argument errors
  * are found on the host before anything is launched.  Problems only visible
