@@ -20,7 +20,8 @@
 // one block would end last with it.  Such tiles are cut into pieces of their
 // (head, query tile) range; each piece leaves float32 sums, and a second kernel
 // adds a tile's pieces in order.  64 track events of up to 20000 tokens (causal
-// window of 511, 4 sinks, 8 query and 2 key heads of 128): 322 us, whole 385.
+// window of 511, 4 sinks, 8 query and 2 key heads of 128): a sixth less time than
+// with whole tiles.
 //
 // Roles as in the forward kernel: a loading warp, an issuing warp, and softmax
 // warps with a thread for each kept row and 64 streamed rows.  P and dS go
@@ -34,15 +35,17 @@
 // heads they are 64 rows, and two blocks share an SM, each with four softmax
 // warps and 256 columns: where events are a few tiles long one block's loads
 // and stores then run under the other's products (2048 events of up to 256
-// tokens, 8 heads of 64: 1741 us, with tiles and blocks as for 128: 2084).  Where two sets of
-// accumulators fit, a block goes on with the next item while it stores one.
+// tokens, 8 heads of 64; tiles and blocks as for 128 took a fifth longer).
+// Where two sets of accumulators fit, a block goes on with the next item while
+// it stores one.
 //
 // What bounds it: the softmax side.  4 causal events of 4000 to 9000 tokens, 16
-// query and 4 key heads of 128: 2.4 ms, 680 TFLOP/s of five products (seven are
-// done), where the products would take 1.0 ms; the two kernels form each weight
+// query and 4 key heads of 128: 2.46 ms, 662 TFLOP/s of five products (seven are
+// done), where the five would take 0.98 ms; the two kernels form each weight
 // twice and each holds a thread's 64 scores in registers between TMEM reads and
 // writes.  Short items add the latency of filling the pipeline: 2048 events of up
-// to 256 tokens, 8 heads of 64: 1.79 ms, 2.0 TB/s.
+// to 256 tokens, 8 heads of 64: 1.78 ms with the kernel of the short ones, 2.0
+// TB/s.
 //
 // Rounding: P and dS are rounded to the input type for their products, in
 // float16 scaled into its range (attention_backward_range.cu).  D

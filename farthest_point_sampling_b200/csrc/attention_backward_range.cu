@@ -5,7 +5,7 @@
 // times |dO|.  Rounded to float16 for their products as they are, they leave
 // its normal range (from 6e-5 up) for long events or small gradients: 12000
 // keys and |dO| of 0.001 left dQ 14 times the error of rounding it once, 200000
-// and 0.01 43 times (now 1.4).  So the products take
+// and 0.01 43 times (now 1.0 and 1.3).  So the products take
 //   P' = 2^14 P   and   dS' = P' c (dP - D),
 // and the sums are scaled back in float32 where they are stored.  With
 // M = max_i |dO_i| max_j |V_j| over an event, |dP_ij| <= M and |D_i| <= M, so for

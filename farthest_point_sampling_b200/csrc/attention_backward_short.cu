@@ -7,8 +7,8 @@
 // and q, k, v, out and dout are read once and the gradients written once: with
 // 64-wide heads and 128 tokens that traffic, 8 tensors of it, bounds the
 // kernel, not the products.  2048 events of up to 128 tokens, 12 heads of 64:
-// 759 us, 3.6 TB/s; the same events through the kernels of attention_backward.cu
-// 982 us.  What is left is latency: a unit's phases wait for one another.
+// 742 us, 3.7 TB/s; the same events through the kernels of attention_backward.cu
+// took 982.  What is left is latency: a unit's phases wait for one another.
 //
 // A work item is an event and a key head, with a unit for each query head of
 // its group; dK and dV are summed over the units in TMEM.  Warps: a loading
@@ -20,11 +20,11 @@
 // The phases of a unit (scores, weights, gradients, stores) follow one another,
 // so what fills an SM is a second block: with 64-wide heads of their own keys
 // (kTwo) a block makes do with 256 columns of TMEM, dK and dQ in the place of dP
-// and dV in that of the scores that P does not cover (923 us with one block an
-// SM, as above).  Otherwise one block takes
-// the SM, with dV and dK kept over the heads of a group.  The two 32-query
-// chunks of a thread go through one loop body, which keeps the kernel in
-// the instruction cache and a thread at 96 registers.
+// and dV in that of the scores that P does not cover (the same events with one
+// block an SM took 923 us).  Otherwise one block takes the SM, with dV and dK kept
+// over the heads of a group.  The two 32-query chunks of a thread go through one
+// loop body, which keeps the kernel in the instruction cache and a thread at 96
+// registers.
 //
 // Rounding: as in attention_backward.cu.
 #include <type_traits>

@@ -16,15 +16,15 @@
 // products do.  Blocks are persistent; the loader runs ahead into the next
 // items.  Only the 32-key chunks that some of a warp's rows do not see whole
 // pay for masks, so one kernel serves every mask (a second one for calls
-// without any took 514 us where this takes 496).
+// without any took 4% longer).
 //
 // What bounds it: events of a tile or two, memory - 4096 events of up to 128
-// tokens, 12 heads of 64: 496 us, 5.5 TB/s; long events, the softmax - 4 causal
-// events of 4000 to 9000 tokens, 16 query and 4 key heads of 128: 681 us, 958
+// tokens, 12 heads of 64: 493 us, 5.6 TB/s; long events, the softmax - 4 causal
+// events of 4000 to 9000 tokens, 16 query and 4 key heads of 128: 692 us, 942
 // TFLOP/s, where the products alone would take 392 us at the rate of a library's
 // large product and the exponentials 280 us; 8 events of 50000 to 200000 tokens
-// under a window of 128 on both sides: 1750 us, of whose scores (three key tiles
-// for each query tile) a third is masked.
+// under a window of 128 on both sides and 16 sinks: 1756 us, of whose scores
+// (three key tiles for each query tile, and one of the sinks) a third is masked.
 //
 // Rounding: P is rounded to the input type for P V; l sums the unrounded
 // values.  O is rescaled only when m grows by more than 8 / log2 units, which
